@@ -48,13 +48,24 @@
  *   - Dtypes: bf16 is IEEE binary32's upper half, e4m3 is OCP FP8 E4M3,
  *     e2m1 is OCP FP4 E2M1 (weights only; the FP4 experts of "Inference INFRA
  *     methodology (5)", shape-evolution table, DS-V4-Pro row).
+ *     mxfp4 is OCP Microscaling FP4: E2M1 codes in blocks of 32 along the
+ *     reduced dimension that share one UE8M0 scale byte (see "MXFP4" below).
  *     Supported combinations (act / wt / out): F32/F32/F32, BF16/BF16/BF16,
- *     BF16/E4M3/BF16, BF16/E2M1/BF16.  `wt` is the type of the expert
- *     weights; the grouped activations Xg and Hg are of type wt, except that
- *     they are E4M3 when wt is E2M1.  Yg is F32 when wt is F32, else BF16.
+ *     BF16/E4M3/BF16, BF16/E2M1/BF16, BF16/MXFP4/BF16.  `wt` is the type of
+ *     the expert weights; the grouped activations Xg and Hg are of type wt,
+ *     except that they are E4M3 when wt is E2M1.  Yg is F32 when wt is F32,
+ *     else BF16.
  *   - e4m3 and e2m1 scales are fp32: weights one per 128x128 block
  *     ([slots][N/128][K/128]), grouped activations one per 1x128 group
  *     ([rows][cols/128]).  Quantised value = code * scale.
+ *   - MXFP4: rows of K codes, packed as e2m1 weights are (K/2 bytes), and
+ *     K/32 scale bytes per row, row-major ([rows][K/32]).  Scale byte s stands
+ *     for 2^(s - 127); s = 255 stands for NaN.  Value = code * 2^(s - 127).
+ *     Both operands of a product have this form: weights W13 / W2 with scales
+ *     [P+S][2I][H/32] / [P+S][H][I/32], grouped activations Xg / Hg with scales
+ *     [rows][H/32] / [rows][I/32].  The calls below take these byte arrays
+ *     through their `float*` scale arguments.  Codes must be 16-byte aligned
+ *     and scales 4-byte aligned.
  *   - e2m1 weights are packed two codes per byte along the reduced
  *     dimension: byte j of a row holds column 2j in bits 0-3 and column 2j+1
  *     in bits 4-7 (a row of K codes is K/2 bytes).  Their base address must
@@ -86,7 +97,7 @@ typedef enum moe_status {
   MOE_ERR_WORKSPACE = -4    /* workspace smaller than moe_workspace_bytes() */
 } moe_status;
 
-typedef enum moe_dtype { MOE_F32 = 0, MOE_BF16 = 1, MOE_E4M3 = 2, MOE_E2M1 = 3 } moe_dtype;
+typedef enum moe_dtype { MOE_F32 = 0, MOE_BF16 = 1, MOE_E4M3 = 2, MOE_E2M1 = 3, MOE_MXFP4 = 4 } moe_dtype;
 
 typedef enum moe_layout { MOE_LAYOUT_MASKED = 0, MOE_LAYOUT_CONTIG = 1 } moe_layout;
 
@@ -208,8 +219,10 @@ moe_status moe_route_grouped_topk(const moe_problem* p, const float* logits, con
  *   xg [rows][H], dtype p->wt (e4m3 for E2M1 weights): x[t] copied to its
  *     rows; for e4m3 each row is
  *     quantised per 1x128 group: s = amax/448 (fp32 IEEE division, s = 1 for an
- *     all-zero group), code = e4m3(x / s) nearest-even, saturating.
- *   xg_scales [rows][H/128] fp32: the group scales (e4m3 only, else NULL).
+ *     all-zero group), code = e4m3(x / s) nearest-even, saturating; for
+ *     MXFP4 each row is quantised as moe_mx_quantize does.
+ *   xg_scales [rows][H/128] fp32: the group scales (e4m3); [rows][H/32] scale
+ *     bytes (MXFP4); else NULL.
  *   err_flag: device int32, MOE_FLAG_* bits are OR-ed in (never cleared).
  *   workspace: device scratch of moe_workspace_bytes(p) bytes. */
 moe_status moe_permute(const moe_problem* p, const int32_t* ids, const void* x, const int32_t* phys_to_log,
@@ -253,10 +266,14 @@ moe_status moe_permute_no_workspace(const moe_problem* p, const int32_t* ids, co
  *   hg[row][0..I) = h, stored as p->wt (e4m3 for E2M1 weights; e4m3: 1x128
  *   groups as in moe_permute, scales in hg_scales [rows][I/128]; bf16:
  *   nearest-even; f32: as is).
- *   xg_scales / w13_scales / hg_scales: e4m3 / e2m1 weights only, else NULL.
+ *   MXFP4: hg is the MXFP4 form of h (one block per 32 columns of I).
+ *   xg_scales / w13_scales / hg_scales: e4m3 / e2m1 / MXFP4 weights only, else
+ *   NULL.
  *   masked_m [P+S], offsets [P+S+1]: as written by moe_permute (device).
- * bf16 / e4m3 / e2m1 run on the tcgen05 tensor cores and need H, I multiples
- * of 128 (e2m1: e4m3 x e2m1 products, kind::f8f6f4). */
+ * bf16 / e4m3 / e2m1 / MXFP4 run on the tcgen05 tensor cores and need H, I
+ * multiples of 128 (e2m1: e4m3 x e2m1 products, kind::f8f6f4; MXFP4:
+ * block-scaled e2m1 x e2m1 products, kind::mxf4, the scales applied by the
+ * tensor core). */
 moe_status moe_grouped_swiglu_gemm(const moe_problem* p, const void* xg, const float* xg_scales, const void* w13,
                                    const float* w13_scales, const int32_t* masked_m, const int32_t* offsets,
                                    void* hg, float* hg_scales, int32_t* err_flag, void* workspace,
@@ -349,6 +366,103 @@ moe_status moe_eplb_record(const moe_problem* p, const int32_t* masked_m, int64_
 moe_status moe_eplb_rebalance(const moe_problem* p, const int32_t* load_window, int32_t window,
                               const int32_t* phys_to_log, int64_t* logical_load, int32_t* new_phys_to_log,
                               int32_t* err_flag, moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * MXFP4 (the pages describe none; OCP Microscaling Formats v1.0, with the
+ * conversion rule of its section 6.3).  Additions of this library.
+ *
+ * A row of `cols` values (cols a multiple of 32) becomes cols/2 code bytes and
+ * cols/32 scale bytes.  Per block of 32: e = floor(log2(largest magnitude)) - 2
+ * clamped to [-127, 125] (e = 0 for an all-zero block), scale byte = e + 127,
+ * code = E2M1(x * 2^-e), nearest with ties to the even code, saturating at 6;
+ * the sign of a zero is kept.  A block that holds a NaN or an infinity gets the
+ * scale byte 255 and codes 0.
+ * ------------------------------------------------------------------------- */
+
+/* x [rows][cols] (dtype F32 or BF16) -> codes [rows][cols/2], scales
+ * [rows][cols/32].  x 16-byte aligned, codes 4-byte aligned. */
+moe_status moe_mx_quantize(int32_t dtype, int64_t rows, int64_t cols, const void* x, uint8_t* codes, uint8_t* scales,
+                           moe_stream_t stream);
+
+/* codes, scales -> out [rows][cols] (dtype F32 or BF16): code * 2^(s - 127),
+ * exact in both types; NaN where s = 255.  out 16-byte aligned, codes 4-byte
+ * aligned. */
+moe_status moe_mx_dequantize(int32_t dtype, int64_t rows, int64_t cols, const uint8_t* codes, const uint8_t* scales,
+                             void* out, moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Load-balance loss of the router ("MoE inference and expert parallelism" names
+ * the bias-based alternative only; the loss of Switch Transformers, and
+ * DeepSeek-V3's sequence-wise form).  Additions of this library.
+ *
+ * The T tokens fall into nseq segments: token t belongs to segment b when
+ * seq_offsets[b] <= t < seq_offsets[b+1] (ascending; device; NULL with nseq = 1:
+ * one segment of all tokens).  Tokens outside every segment, and tokens with
+ * valid[t] = 0 (valid [T] bytes, device, NULL: all valid), take no part: their
+ * logits and ids are not read and their gradient is 0.  For the n tokens that
+ * are left in a segment:
+ *   p_t = softmax(l_t), or sigmoid(l_t) / sum_e sigmoid(l_te)    (score)
+ *   counts[b][e] = ids equal to e among them,  prob_sum[b][e] = sum_t p_te
+ *   tokens[b] = n,  loss[b] = coef * E / (K n^2) * sum_e counts * prob_sum
+ * A logit of -inf gives p = 0; a token whose logits are all -inf gives a row of
+ * zeros.  An empty segment has zeros everywhere.  Sums are fp32 in a fixed order: the
+ * same inputs give the same bits.
+ * ------------------------------------------------------------------------- */
+typedef enum moe_score { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+
+/* Workspace bytes of moe_balance_loss; 0 for an invalid problem or nseq < 1. */
+size_t moe_balance_workspace_bytes(const moe_problem* p, int32_t nseq);
+
+/* logits [T][E] fp32, ids [T][K] int32 (as written by a router); loss [nseq],
+ * counts [nseq][E] int32, prob_sum [nseq][E], tokens [nseq] int32 (device,
+ * written).  An id outside [0,E) is not counted and sets MOE_FLAG_BAD_EXPERT. */
+moe_status moe_balance_loss(const moe_problem* p, const float* logits, const int32_t* ids, const uint8_t* valid,
+                            const int32_t* seq_offsets, int32_t nseq, int32_t score, float coef, float* loss,
+                            int32_t* counts, float* prob_sum, int32_t* tokens, int32_t* err_flag, void* workspace,
+                            size_t workspace_bytes, moe_stream_t stream);
+
+/* Gradient: dlogits [T][E] = sum_b dloss[b] * d loss[b] / d logits, the counts
+ * held constant (they come from a choice, not from a product).  counts and
+ * tokens as written by moe_balance_loss, dloss [nseq] fp32 (device).  Every
+ * element of dlogits is written. */
+moe_status moe_balance_loss_backward(const moe_problem* p, const float* logits, const uint8_t* valid,
+                                     const int32_t* seq_offsets, int32_t nseq, int32_t score, float coef,
+                                     const int32_t* counts, const int32_t* tokens, const float* dloss,
+                                     float* dlogits, moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The norms around the layer (DeepSeek-V3 Eq. 12 adds the layer's output to its
+ * input u_t, which the pages take normed).  Additions of this library.  Per
+ * token, with rms(v) = v / sqrt(mean(v^2) + eps):
+ *   y  = x + res_scale * gate * rms(block) * w_post     (the norm after)
+ *   xn = rms(y) * w_pre                                 (the norm before the next)
+ * computed in fp32 (xn from the unrounded y) and rounded once.  block = NULL:
+ * y = x (nothing of the norm after is read; y may be NULL).  w_pre and xn =
+ * NULL together: only y.  x, block, y, xn [T][H] and w_post, w_pre [H] are of
+ * `dtype` (F32 or BF16), and so is the gate: none, one value a channel [H], or one a token [T].
+ * 1 <= H <= 16384; any alignment of the type's own size.  Outputs overlap no
+ * input and no other output, except that y may be x.
+ * ------------------------------------------------------------------------- */
+typedef enum moe_gate { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2 } moe_gate;
+
+moe_status moe_block_norm(int32_t dtype, int32_t T, int32_t H, const void* x, const void* block, int32_t gate_kind,
+                          const void* gate, const void* w_post, const void* w_pre, float res_scale, float eps,
+                          void* y, void* xn, moe_stream_t stream);
+
+/* Workspace bytes of moe_block_norm_backward; 0 for sizes out of range. */
+size_t moe_block_norm_workspace_bytes(int32_t T, int32_t H);
+
+/* Gradient of moe_block_norm, from its inputs.  dy [T][H]: gradient of y (NULL:
+ * zero).  dxn [T][H]: gradient of xn (NULL with w_pre: zero).  At least one of
+ * them.  Written: dx [T][H] and, with block, dblock [T][H] (`dtype`); fp32
+ * dw_post [H] (with block), dgate [H] or [T] (with block and a gate), dw_pre [H] (with w_pre).
+ * dw_post, dgate and dw_pre may be NULL.  Sums over tokens are fp32 in a fixed
+ * order.  Outputs overlap no input and no other output, except that dx may be dy. */
+moe_status moe_block_norm_backward(int32_t dtype, int32_t T, int32_t H, const void* x, const void* block,
+                                   int32_t gate_kind, const void* gate, const void* w_post, const void* w_pre,
+                                   float res_scale, float eps, const void* dy, const void* dxn, void* dx,
+                                   void* dblock, float* dgate, float* dw_post, float* dw_pre, void* workspace,
+                                   size_t workspace_bytes, moe_stream_t stream);
 
 /* Diagnostic, an addition of this library (the pages describe none): runs the
  * bounded wait that every kernel here uses on an mbarrier that nothing

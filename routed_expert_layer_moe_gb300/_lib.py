@@ -14,13 +14,16 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe_gb300.so")
 
 MOE_OK, MOE_ERR_INVALID, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA, MOE_ERR_WORKSPACE = 0, -1, -2, -3, -4
-MOE_F32, MOE_BF16, MOE_E4M3, MOE_E2M1 = 0, 1, 2, 3
+MOE_F32, MOE_BF16, MOE_E4M3, MOE_E2M1, MOE_MXFP4 = 0, 1, 2, 3, 4
 MOE_LAYOUT_MASKED, MOE_LAYOUT_CONTIG = 0, 1
 MOE_FLAG_OVERFLOW, MOE_FLAG_BAD_EXPERT, MOE_FLAG_BAD_MAP, MOE_FLAG_TIMEOUT = 1, 2, 4, 8
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_TOKEN = 0, 1, 2
 MOE_STATS_CTAS = 256                        # issue counters at the start of the workspace (include/moe.h)
 MOE_STATS_BYTES = 2 * MOE_STATS_CTAS * 2 * 4
 
-DTYPES = {"f32": MOE_F32, "bf16": MOE_BF16, "e4m3": MOE_E4M3, "e2m1": MOE_E2M1}
+DTYPES = {"f32": MOE_F32, "bf16": MOE_BF16, "e4m3": MOE_E4M3, "e2m1": MOE_E2M1, "mxfp4": MOE_MXFP4}
+SCORES = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
 LAYOUTS = {"masked": MOE_LAYOUT_MASKED, "contig": MOE_LAYOUT_CONTIG}
 
 # every symbol include/moe.h declares
@@ -29,6 +32,9 @@ EXPORTS = ["moe_version", "moe_status_string", "moe_grouped_rows", "moe_workspac
            "moe_route_topk", "moe_route_grouped_topk", "moe_permute", "moe_permute_no_workspace",
            "moe_grouped_swiglu_gemm", "moe_grouped_down_gemm", "moe_grouped_ffn", "moe_combine",
            "moe_route_permute", "moe_ffn_combine",
+           "moe_mx_quantize", "moe_mx_dequantize",
+           "moe_balance_workspace_bytes", "moe_balance_loss", "moe_balance_loss_backward",
+           "moe_block_norm_workspace_bytes", "moe_block_norm", "moe_block_norm_backward",
            "moe_eplb_record", "moe_eplb_rebalance", "moe_eplb_invert", "moe_selftest_bounded_wait"]
 
 
@@ -101,6 +107,23 @@ def lib():
     L.moe_eplb_record.restype = i32
     L.moe_eplb_rebalance.argtypes = [pp, vp, i32, vp, vp, vp, vp, vp]
     L.moe_eplb_rebalance.restype = i32
+    f32 = ctypes.c_float
+    L.moe_mx_quantize.argtypes = [i32, i64, i64, vp, vp, vp, vp]
+    L.moe_mx_quantize.restype = i32
+    L.moe_mx_dequantize.argtypes = [i32, i64, i64, vp, vp, vp, vp]
+    L.moe_mx_dequantize.restype = i32
+    L.moe_balance_workspace_bytes.argtypes = [pp, i32]
+    L.moe_balance_workspace_bytes.restype = sz
+    L.moe_balance_loss.argtypes = [pp] + [vp] * 4 + [i32, i32, f32] + [vp] * 6 + [sz, vp]
+    L.moe_balance_loss.restype = i32
+    L.moe_balance_loss_backward.argtypes = [pp] + [vp] * 3 + [i32, i32, f32] + [vp] * 5
+    L.moe_balance_loss_backward.restype = i32
+    L.moe_block_norm_workspace_bytes.argtypes = [i32, i32]
+    L.moe_block_norm_workspace_bytes.restype = sz
+    L.moe_block_norm.argtypes = [i32, i32, i32, vp, vp, i32, vp, vp, vp, f32, f32, vp, vp, vp]
+    L.moe_block_norm.restype = i32
+    L.moe_block_norm_backward.argtypes = [i32, i32, i32, vp, vp, i32, vp, vp, vp, f32, f32] + [vp] * 8 + [sz, vp]
+    L.moe_block_norm_backward.restype = i32
     L.moe_selftest_bounded_wait.argtypes = [i64, vp, vp]
     L.moe_selftest_bounded_wait.restype = i32
     L.moe_eplb_invert.argtypes = [i32, i32, vp, i32, vp, vp]
@@ -132,6 +155,30 @@ def _stream(stream):
 def _check(status: int, where: str):
     if status != MOE_OK:
         raise MoeError(status, where)
+
+
+_FLOAT_DTYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+
+
+def _arg(t, name: str, dtype, shape):
+    """Device address of a dense tensor of this type and shape (None: no tensor); a ValueError otherwise.
+    The calls below take whole arrays and no strides, so a view that is not dense would be read wrongly."""
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise ValueError("%s: expected a CUDA tensor" % name)
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError("%s: expected %s %s, got %s %s" % (name, dtype, tuple(shape), t.dtype, tuple(t.shape)))
+    if not t.is_contiguous():
+        raise ValueError("%s: expected a dense row-major tensor" % name)
+    return t.data_ptr()
+
+
+def _float_dtype(t, name: str) -> int:
+    d = _FLOAT_DTYPES.get(t.dtype)
+    if d is None:
+        raise ValueError("%s: expected float32 or bfloat16, got %s" % (name, t.dtype))
+    return d
 
 
 def moe_version() -> int:
@@ -228,6 +275,109 @@ def moe_ffn_combine(p: Problem, xg, xg_scales, w13, w13_scales, w2, w2_scales, m
 def moe_combine(p: Problem, yg, row_of, w, out, stream=None) -> None:
     _check(lib().moe_combine(ctypes.byref(p), _ptr(yg), _ptr(row_of), _ptr(w), _ptr(out), _stream(stream)),
            "moe_combine")
+
+
+def _mx_args(values, codes, scales, name: str):
+    """dtype, rows, cols and addresses of an MXFP4 conversion; leading dimensions count as rows."""
+    d = _float_dtype(values, name)
+    if values.dim() < 1:
+        raise ValueError("%s: expected rows of values" % name)
+    lead, cols = values.shape[:-1], values.shape[-1]
+    if cols % 32:
+        raise ValueError("%s: rows of %d values are not whole blocks of 32" % (name, cols))
+    return (d, lead.numel(), cols, _arg(values, name, values.dtype, values.shape),
+            _arg(codes, "codes", torch.uint8, lead + (cols // 2,)),
+            _arg(scales, "scales", torch.uint8, lead + (cols // 32,)))
+
+
+def moe_mx_quantize(x, codes, scales, stream=None) -> None:
+    """x [..., cols] (float32 or bfloat16) -> MXFP4 codes [..., cols/2] and scale bytes [..., cols/32] (uint8)."""
+    d, rows, cols, px, pc, ps = _mx_args(x, codes, scales, "x")
+    _check(lib().moe_mx_quantize(d, rows, cols, px, pc, ps, _stream(stream)), "moe_mx_quantize")
+
+
+def moe_mx_dequantize(codes, scales, out, stream=None) -> None:
+    """MXFP4 codes and scale bytes -> the values they stand for, out [..., cols] (float32 or bfloat16)."""
+    d, rows, cols, po, pc, ps = _mx_args(out, codes, scales, "out")
+    _check(lib().moe_mx_dequantize(d, rows, cols, pc, ps, po, _stream(stream)), "moe_mx_dequantize")
+
+
+def _nseq(p: Problem, seq_offsets) -> int:
+    if seq_offsets is None:
+        return 1
+    if seq_offsets.dim() != 1 or seq_offsets.numel() < 2:
+        raise ValueError("seq_offsets: expected the nseq + 1 offsets of nseq >= 1 segments")
+    return seq_offsets.numel() - 1
+
+
+def moe_balance_workspace_bytes(p: Problem, nseq: int = 1) -> int:
+    return lib().moe_balance_workspace_bytes(ctypes.byref(p), nseq)
+
+
+def moe_balance_loss(p: Problem, logits, ids, valid, seq_offsets, score: str, coef: float, loss, counts, prob_sum,
+                     tokens, err_flag, workspace, stream=None) -> None:
+    """Load-balance loss of the router per segment, with the per-expert counts and score sums (moe.h).
+    valid: uint8 [T] or None; seq_offsets: int32 [nseq + 1] or None (one segment); score: "softmax" or "sigmoid"."""
+    B, i32, f32 = _nseq(p, seq_offsets), torch.int32, torch.float32
+    _check(lib().moe_balance_loss(
+        ctypes.byref(p), _arg(logits, "logits", f32, (p.T, p.E)), _arg(ids, "ids", i32, (p.T, p.K)),
+        _arg(valid, "valid", torch.uint8, (p.T,)), _arg(seq_offsets, "seq_offsets", i32, (B + 1,)), B, SCORES[score],
+        coef, _arg(loss, "loss", f32, (B,)), _arg(counts, "counts", i32, (B, p.E)),
+        _arg(prob_sum, "prob_sum", f32, (B, p.E)), _arg(tokens, "tokens", i32, (B,)), _ptr(err_flag),
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)), "moe_balance_loss")
+
+
+def moe_balance_loss_backward(p: Problem, logits, valid, seq_offsets, score: str, coef: float, counts, tokens, dloss,
+                              dlogits, stream=None) -> None:
+    """Gradient of moe_balance_loss with respect to the logits; counts and tokens as that call wrote them."""
+    B, i32, f32 = _nseq(p, seq_offsets), torch.int32, torch.float32
+    _check(lib().moe_balance_loss_backward(
+        ctypes.byref(p), _arg(logits, "logits", f32, (p.T, p.E)), _arg(valid, "valid", torch.uint8, (p.T,)),
+        _arg(seq_offsets, "seq_offsets", i32, (B + 1,)), B, SCORES[score], coef,
+        _arg(counts, "counts", i32, (B, p.E)), _arg(tokens, "tokens", i32, (B,)), _arg(dloss, "dloss", f32, (B,)),
+        _arg(dlogits, "dlogits", f32, (p.T, p.E)), _stream(stream)), "moe_balance_loss_backward")
+
+
+def _norm_args(x, block, gate, w_post, w_pre):
+    """Common arguments of the norm calls: (dtype, T, H, x, block, gate kind, gate, w_post, w_pre)."""
+    d = _float_dtype(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x: expected [T, H]")
+    T, H = x.shape
+    dt = x.dtype
+    kind = MOE_GATE_NONE
+    if gate is not None:
+        kind = MOE_GATE_TOKEN if gate.dim() == 2 else MOE_GATE_CHANNEL
+    return (d, T, H, _arg(x, "x", dt, (T, H)), _arg(block, "block", dt, (T, H)), kind,
+            _arg(gate, "gate", dt, (T, 1) if kind == MOE_GATE_TOKEN else (H,)), _arg(w_post, "w_post", dt, (H,)),
+            _arg(w_pre, "w_pre", dt, (H,)))
+
+
+def moe_block_norm_workspace_bytes(T: int, H: int) -> int:
+    return lib().moe_block_norm_workspace_bytes(T, H)
+
+
+def moe_block_norm(x, block, gate, w_post, w_pre, res_scale: float, eps: float, y, xn, stream=None) -> None:
+    """y = x + res_scale * gate * rms(block) * w_post, xn = rms(y) * w_pre (moe.h).  x, block, y, xn [T, H];
+    w_post, w_pre [H]; gate None, [H] (a value a channel) or [T, 1] (a value a token); block None: y = x; w_pre and
+    xn None: only y."""
+    a = _norm_args(x, block, gate, w_post, w_pre)
+    _check(lib().moe_block_norm(*a, res_scale, eps, _arg(y, "y", x.dtype, x.shape), _arg(xn, "xn", x.dtype, x.shape),
+                                _stream(stream)), "moe_block_norm")
+
+
+def moe_block_norm_backward(x, block, gate, w_post, w_pre, res_scale: float, eps: float, dy, dxn, dx, dblock, dgate,
+                            dw_post, dw_pre, workspace, stream=None) -> None:
+    """Gradient of moe_block_norm from its inputs: dx, dblock like x; dgate like the gate, dw_post and dw_pre [H],
+    all three float32 and each None where it is not wanted."""
+    a = _norm_args(x, block, gate, w_post, w_pre)
+    H, f32 = a[2], torch.float32
+    _check(lib().moe_block_norm_backward(
+        *a, res_scale, eps, _arg(dy, "dy", x.dtype, x.shape), _arg(dxn, "dxn", x.dtype, x.shape),
+        _arg(dx, "dx", x.dtype, x.shape), _arg(dblock, "dblock", x.dtype, x.shape),
+        _arg(dgate, "dgate", f32, () if gate is None else gate.shape), _arg(dw_post, "dw_post", f32, (H,)),
+        _arg(dw_pre, "dw_pre", f32, (H,)), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        _stream(stream)), "moe_block_norm_backward")
 
 
 def moe_eplb_record(p: Problem, masked_m, pass_index: int, window: int, load_window, stream=None) -> None:

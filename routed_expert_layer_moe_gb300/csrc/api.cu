@@ -39,6 +39,7 @@ EncodeTiledFn encode_fn() {
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 }  // namespace
 
@@ -91,7 +92,7 @@ int check_problem(const moe_problem* p) {
     if (q.M_max <= 0) return MOE_ERR_INVALID;
     if (q.has_shared && q.M_max < q.T) return MOE_ERR_INVALID;
   }
-  if (q.act < MOE_F32 || q.act > MOE_E4M3 || q.wt < MOE_F32 || q.wt > MOE_E2M1 || q.out < MOE_F32 ||
+  if (q.act < MOE_F32 || q.act > MOE_E4M3 || q.wt < MOE_F32 || q.wt > MOE_MXFP4 || q.out < MOE_F32 ||
       q.out > MOE_E4M3)
     return MOE_ERR_INVALID;
   // products that must fit the 32-bit row and element indices used on the device
@@ -102,9 +103,10 @@ int check_problem(const moe_problem* p) {
   const bool f32 = q.act == MOE_F32 && q.wt == MOE_F32 && q.out == MOE_F32;
   const bool bf16 = q.act == MOE_BF16 && q.wt == MOE_BF16 && q.out == MOE_BF16;
   const bool f8 = q.act == MOE_BF16 && fp8_acts(q) && q.out == MOE_BF16;  // FP8 or FP4 weights
-  if (!(f32 || bf16 || f8)) return MOE_ERR_UNSUPPORTED;
+  const bool mx = q.act == MOE_BF16 && q.wt == MOE_MXFP4 && q.out == MOE_BF16;
+  if (!(f32 || bf16 || f8 || mx)) return MOE_ERR_UNSUPPORTED;
   if (f32 && (q.H % 4 || q.I % 4)) return MOE_ERR_UNSUPPORTED;
-  if ((bf16 || f8) && (q.H % 128 || q.I % 128)) return MOE_ERR_UNSUPPORTED;
+  if ((bf16 || f8 || mx) && (q.H % 128 || q.I % 128)) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -123,7 +125,7 @@ moe_status launched(int r) {
 
 extern "C" {
 
-int32_t moe_version(void) { return (1 << 16) | 0; }
+int32_t moe_version(void) { return (1 << 16) | 1; }
 
 const char* moe_status_string(int32_t s) {
   switch (s) {
@@ -187,7 +189,7 @@ moe_status moe_permute(const moe_problem* p, const int32_t* ids, const void* x, 
   if (r) return (moe_status)r;
   if (!masked_m || !offsets || !err_flag || !workspace) return MOE_ERR_INVALID;
   if (p->T > 0 && (!ids || !x || !row_of || !src_of || !xg)) return MOE_ERR_INVALID;
-  if (fp8_acts(*p) && p->T > 0 && !xg_scales) return MOE_ERR_INVALID;
+  if (scaled_acts(*p) && p->T > 0 && !xg_scales) return MOE_ERR_INVALID;
   if (!phys_to_log && p->P != p->E) return MOE_ERR_INVALID;
   if (p->T > 0 && (!aligned16(x) || !aligned16(xg))) return MOE_ERR_UNSUPPORTED;
   if (workspace_bytes < ws_bytes(*p)) return MOE_ERR_WORKSPACE;
@@ -202,9 +204,11 @@ static moe_status gemm_call(const moe_problem* p, int mode, const void* act, con
   int r = check_problem(p);
   if (r) return (moe_status)r;
   if (!act || !w || !masked_m || !offsets || !out || !err_flag) return MOE_ERR_INVALID;
-  if (fp8_acts(*p) && (!act_scales || !w_scales)) return MOE_ERR_INVALID;
-  if (fp8_acts(*p) && mode == MODE_SWIGLU && !out_scales) return MOE_ERR_INVALID;
+  if (scaled_acts(*p) && (!act_scales || !w_scales)) return MOE_ERR_INVALID;
+  if (scaled_acts(*p) && mode == MODE_SWIGLU && !out_scales) return MOE_ERR_INVALID;
   if (!aligned16(act) || !aligned16(w) || !aligned16(out)) return MOE_ERR_UNSUPPORTED;
+  if (p->wt == MOE_MXFP4 && !(aligned4(act_scales) && aligned4(w_scales) && aligned4(out_scales)))
+    return MOE_ERR_UNSUPPORTED;
   // packed 4-bit tensor maps want a 32-byte aligned base
   if (p->wt == MOE_E2M1 && (reinterpret_cast<uintptr_t>(w) & 31u)) return MOE_ERR_UNSUPPORTED;
   if (workspace_bytes < ws_bytes(*p) || (ws_bytes(*p) > 0 && !workspace)) return MOE_ERR_WORKSPACE;
@@ -235,8 +239,10 @@ moe_status moe_grouped_ffn(const moe_problem* p, const void* xg, const float* xg
   int r = check_problem(p);
   if (r) return (moe_status)r;
   if (!xg || !w13 || !w2 || !masked_m || !offsets || !hg || !yg || !err_flag) return MOE_ERR_INVALID;
-  if (fp8_acts(*p) && (!xg_scales || !w13_scales || !w2_scales || !hg_scales)) return MOE_ERR_INVALID;
+  if (scaled_acts(*p) && (!xg_scales || !w13_scales || !w2_scales || !hg_scales)) return MOE_ERR_INVALID;
   if (!aligned16(xg) || !aligned16(w13) || !aligned16(w2) || !aligned16(hg) || !aligned16(yg))
+    return MOE_ERR_UNSUPPORTED;
+  if (p->wt == MOE_MXFP4 && !(aligned4(xg_scales) && aligned4(w13_scales) && aligned4(w2_scales) && aligned4(hg_scales)))
     return MOE_ERR_UNSUPPORTED;
   if (p->wt == MOE_E2M1 && ((reinterpret_cast<uintptr_t>(w13) | reinterpret_cast<uintptr_t>(w2)) & 31u))
     return MOE_ERR_UNSUPPORTED;
@@ -253,7 +259,7 @@ moe_status moe_route_permute(const moe_problem* p, const float* logits, const vo
   if (r) return (moe_status)r;
   if (!masked_m || !offsets || !err_flag || !workspace) return MOE_ERR_INVALID;
   if (p->T > 0 && (!logits || !ids || !w || !x || !row_of || !src_of || !xg)) return MOE_ERR_INVALID;
-  if (fp8_acts(*p) && p->T > 0 && !xg_scales) return MOE_ERR_INVALID;
+  if (scaled_acts(*p) && p->T > 0 && !xg_scales) return MOE_ERR_INVALID;
   if (!phys_to_log && p->P != p->E) return MOE_ERR_INVALID;
   if (p->T > 0 && (!aligned16(x) || !aligned16(xg))) return MOE_ERR_UNSUPPORTED;
   if (workspace_bytes < ws_bytes(*p)) return MOE_ERR_WORKSPACE;
@@ -276,9 +282,11 @@ moe_status moe_ffn_combine(const moe_problem* p, const void* xg, const float* xg
   if (r) return (moe_status)r;
   if (!xg || !w13 || !w2 || !masked_m || !offsets || !hg || !yg || !err_flag) return MOE_ERR_INVALID;
   if (p->T > 0 && (!row_of || !w || !out)) return MOE_ERR_INVALID;
-  if (fp8_acts(*p) && (!xg_scales || !w13_scales || !w2_scales || !hg_scales)) return MOE_ERR_INVALID;
+  if (scaled_acts(*p) && (!xg_scales || !w13_scales || !w2_scales || !hg_scales)) return MOE_ERR_INVALID;
   if (!aligned16(xg) || !aligned16(w13) || !aligned16(w2) || !aligned16(hg) || !aligned16(yg) ||
       (p->T > 0 && !aligned16(out)))
+    return MOE_ERR_UNSUPPORTED;
+  if (p->wt == MOE_MXFP4 && !(aligned4(xg_scales) && aligned4(w13_scales) && aligned4(w2_scales) && aligned4(hg_scales)))
     return MOE_ERR_UNSUPPORTED;
   if (p->wt == MOE_E2M1 && ((reinterpret_cast<uintptr_t>(w13) | reinterpret_cast<uintptr_t>(w2)) & 31u))
     return MOE_ERR_UNSUPPORTED;
@@ -322,6 +330,129 @@ moe_status moe_eplb_rebalance(const moe_problem* p, const int32_t* load_window, 
   if (p->P - p->E > p->E) return MOE_ERR_INVALID;  // each extra slot holds a different expert
   return launched(launch_eplb_rebalance(*p, load_window, window, phys_to_log, logical_load, new_phys_to_log,
                                         err_flag, (cudaStream_t)stream));
+}
+
+static bool float_dtype(int32_t dtype) { return dtype == MOE_F32 || dtype == MOE_BF16; }
+
+static int check_mx(int32_t dtype, int64_t rows, int64_t cols, const void* values, const void* codes,
+                    const void* scales) {
+  if (!float_dtype(dtype) || rows < 0 || cols < 0 || cols % 32) return MOE_ERR_INVALID;
+  if (cols > 0 && rows > (1LL << 40) / cols) return MOE_ERR_INVALID;
+  if (rows * cols == 0) return MOE_OK;
+  if (!values || !codes || !scales) return MOE_ERR_INVALID;
+  if (!aligned16(values) || !aligned4(codes)) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status moe_mx_quantize(int32_t dtype, int64_t rows, int64_t cols, const void* x, uint8_t* codes, uint8_t* scales,
+                           moe_stream_t stream) {
+  const int r = check_mx(dtype, rows, cols, x, codes, scales);
+  if (r) return (moe_status)r;
+  return launched(launch_mx_quantize(dtype, rows, cols, x, codes, scales, (cudaStream_t)stream));
+}
+
+moe_status moe_mx_dequantize(int32_t dtype, int64_t rows, int64_t cols, const uint8_t* codes, const uint8_t* scales,
+                             void* out, moe_stream_t stream) {
+  const int r = check_mx(dtype, rows, cols, out, codes, scales);
+  if (r) return (moe_status)r;
+  return launched(launch_mx_dequantize(dtype, rows, cols, codes, scales, out, (cudaStream_t)stream));
+}
+
+static int check_balance(const moe_problem* p, const int32_t* seq_offsets, int32_t nseq, int32_t score) {
+  const int r = check_problem(p);
+  if (r) return r;
+  if (nseq < 1 || nseq > 65535 || (!seq_offsets && nseq != 1)) return MOE_ERR_INVALID;
+  if (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID) return MOE_ERR_INVALID;
+  return MOE_OK;
+}
+
+size_t moe_balance_workspace_bytes(const moe_problem* p, int32_t nseq) {
+  if (check_problem(p) != MOE_OK || nseq < 1 || nseq > 65535) return 0;
+  return balance_workspace_bytes(*p, nseq);
+}
+
+moe_status moe_balance_loss(const moe_problem* p, const float* logits, const int32_t* ids, const uint8_t* valid,
+                            const int32_t* seq_offsets, int32_t nseq, int32_t score, float coef, float* loss,
+                            int32_t* counts, float* prob_sum, int32_t* tokens, int32_t* err_flag, void* workspace,
+                            size_t workspace_bytes, moe_stream_t stream) {
+  const int r = check_balance(p, seq_offsets, nseq, score);
+  if (r) return (moe_status)r;
+  if (!loss || !counts || !prob_sum || !tokens || !err_flag) return MOE_ERR_INVALID;
+  if (p->T > 0 && (!logits || !ids)) return MOE_ERR_INVALID;
+  if (workspace_bytes < balance_workspace_bytes(*p, nseq) || !workspace) return MOE_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return MOE_ERR_UNSUPPORTED;
+  return launched(launch_balance(*p, logits, ids, valid, seq_offsets, nseq, score, coef, loss, counts, prob_sum,
+                                 tokens, err_flag, workspace, (cudaStream_t)stream));
+}
+
+moe_status moe_balance_loss_backward(const moe_problem* p, const float* logits, const uint8_t* valid,
+                                     const int32_t* seq_offsets, int32_t nseq, int32_t score, float coef,
+                                     const int32_t* counts, const int32_t* tokens, const float* dloss,
+                                     float* dlogits, moe_stream_t stream) {
+  const int r = check_balance(p, seq_offsets, nseq, score);
+  if (r) return (moe_status)r;
+  if (!counts || !tokens || !dloss) return MOE_ERR_INVALID;
+  if (p->T > 0 && (!logits || !dlogits)) return MOE_ERR_INVALID;
+  return launched(launch_balance_backward(*p, logits, valid, seq_offsets, nseq, score, coef, counts, tokens, dloss,
+                                          dlogits, (cudaStream_t)stream));
+}
+
+size_t moe_block_norm_workspace_bytes(int32_t T, int32_t H) { return block_norm_workspace_bytes(T, H); }
+
+static bool aligned_to(int32_t dtype, const void* p) {
+  return (reinterpret_cast<uintptr_t>(p) & (dtype == MOE_F32 ? 3u : 1u)) == 0;
+}
+
+static int check_norm(int32_t dtype, int32_t T, int32_t H, const void* x, const void* block, int32_t gate_kind,
+                      const void* gate, const void* w_post, float eps) {
+  if (!float_dtype(dtype) || T < 0 || H < 1 || block_norm_workspace_bytes(T, H) == 0) return MOE_ERR_INVALID;
+  if (!(eps >= 0.0f) || gate_kind < MOE_GATE_NONE || gate_kind > MOE_GATE_TOKEN) return MOE_ERR_INVALID;
+  if (T > 0 && !x) return MOE_ERR_INVALID;
+  if (T > 0 && block && (!w_post || (gate_kind != MOE_GATE_NONE && !gate))) return MOE_ERR_INVALID;
+  return MOE_OK;
+}
+
+moe_status moe_block_norm(int32_t dtype, int32_t T, int32_t H, const void* x, const void* block, int32_t gate_kind,
+                          const void* gate, const void* w_post, const void* w_pre, float res_scale, float eps,
+                          void* y, void* xn, moe_stream_t stream) {
+  const int r = check_norm(dtype, T, H, x, block, gate_kind, gate, w_post, eps);
+  if (r) return (moe_status)r;
+  if (T == 0) return MOE_OK;
+  if ((!xn) != (!w_pre) || (block && !y) || (!y && !xn)) return MOE_ERR_INVALID;
+  for (const void* q : {x, block, gate, w_post, w_pre, (const void*)y, (const void*)xn})
+    if (!aligned_to(dtype, q)) return MOE_ERR_UNSUPPORTED;
+  NormArgs n{};
+  n.dtype = dtype, n.T = T, n.H = H, n.x = x, n.block = block, n.gate_kind = block ? gate_kind : MOE_GATE_NONE;
+  n.gate = gate, n.w_post = w_post, n.w_pre = w_pre, n.res_scale = res_scale, n.eps = eps, n.y = y, n.xn = xn;
+  return launched(launch_block_norm(n, (cudaStream_t)stream));
+}
+
+moe_status moe_block_norm_backward(int32_t dtype, int32_t T, int32_t H, const void* x, const void* block,
+                                   int32_t gate_kind, const void* gate, const void* w_post, const void* w_pre,
+                                   float res_scale, float eps, const void* dy, const void* dxn, void* dx,
+                                   void* dblock, float* dgate, float* dw_post, float* dw_pre, void* workspace,
+                                   size_t workspace_bytes, moe_stream_t stream) {
+  const int r = check_norm(dtype, T, H, x, block, gate_kind, gate, w_post, eps);
+  if (r) return (moe_status)r;
+  if (T == 0) {  // no rows: the sums over tokens are zeros
+    for (float* sum : {dw_post, dw_pre, gate_kind == MOE_GATE_CHANNEL ? dgate : nullptr})
+      if (sum && cudaMemsetAsync(sum, 0, (size_t)H * sizeof(float), (cudaStream_t)stream) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    return MOE_OK;
+  }
+  if ((!dxn) != (!w_pre) || (!dy && !dxn) || !dx || (!dblock) != (!block)) return MOE_ERR_INVALID;
+  // without what they belong to, gradients would be left unwritten
+  if ((dw_pre && !w_pre) || (!block && (dw_post || dgate)) || (dgate && gate_kind == MOE_GATE_NONE))
+    return MOE_ERR_INVALID;
+  for (const void* q : {x, block, gate, w_post, w_pre, dy, dxn, (const void*)dx, (const void*)dblock})
+    if (!aligned_to(dtype, q)) return MOE_ERR_UNSUPPORTED;
+  if (workspace_bytes < block_norm_workspace_bytes(T, H) || !workspace) return MOE_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return MOE_ERR_UNSUPPORTED;
+  NormArgs n{};
+  n.dtype = dtype, n.T = T, n.H = H, n.x = x, n.block = block, n.gate_kind = block ? gate_kind : MOE_GATE_NONE;
+  n.gate = gate, n.w_post = w_post, n.w_pre = w_pre, n.res_scale = res_scale, n.eps = eps;
+  n.dy = dy, n.dxn = dxn, n.dx = dx, n.dblock = dblock, n.dgate = dgate, n.ws = workspace;
+  return launched(launch_block_norm_backward(n, dw_post, dw_pre, (cudaStream_t)stream));
 }
 
 moe_status moe_selftest_bounded_wait(int64_t cycles, int32_t* err_flag, moe_stream_t stream) {

@@ -65,6 +65,47 @@ int launch_bounded_wait_selftest(long long cycles, int32_t* err, cudaStream_t st
 int launch_combine(const moe_problem& p, const void* yg, const int32_t* row_of, const float* w, void* out,
                    cudaStream_t st);
 
+// The MXFP4 form of launch_gemm and what belongs to it (gemm_mx.cu).
+int launch_gemm_mx(const moe_problem& p, int mode, const void* act, const uint8_t* act_scales, const void* w,
+                   const uint8_t* w_scales, const int32_t* masked_m, const int32_t* offsets, void* out,
+                   uint8_t* out_scales, int32_t* err, void* ws, cudaStream_t st, const CombineArgs* comb);
+size_t gemm_mx_workspace_bytes(const moe_problem& p);
+int gemm_mx_tile_rows(const moe_problem& p, int mode);
+// After a GEMM whose K range was split: part [ksplit][rows][cols] added in split order into
+// out, with the combine in the same kernel when comb is given; ksplit = 1: the combine alone.
+int launch_splitk_reduce(const moe_problem& p, const float* part, int ksplit, int cols, void* out,
+                         const int32_t* masked_m, const int32_t* offsets, cudaStream_t st, const CombineArgs* comb);
+
+int launch_mx_quantize(int dtype, int64_t rows, int64_t cols, const void* x, uint8_t* codes, uint8_t* scales,
+                       cudaStream_t st);
+int launch_mx_dequantize(int dtype, int64_t rows, int64_t cols, const uint8_t* codes, const uint8_t* scales,
+                         void* out, cudaStream_t st);
+
+size_t balance_workspace_bytes(const moe_problem& p, int nseq);
+int launch_balance(const moe_problem& p, const float* logits, const int32_t* ids, const uint8_t* valid,
+                   const int32_t* seq, int nseq, int score, float coef, float* loss, int32_t* counts,
+                   float* prob_sum, int32_t* tokens, int32_t* err, void* ws, cudaStream_t st);
+int launch_balance_backward(const moe_problem& p, const float* logits, const uint8_t* valid, const int32_t* seq,
+                            int nseq, int score, float coef, const int32_t* counts, const int32_t* tokens,
+                            const float* dloss, float* dlogits, cudaStream_t st);
+
+// Arguments of moe_block_norm and moe_block_norm_backward (what one of them lacks is null).
+struct NormArgs {
+  int dtype, T, H;
+  const void *x, *block;
+  int gate_kind;
+  const void *gate, *w_post, *w_pre;
+  float res_scale, eps;
+  void *y, *xn;
+  const void *dy, *dxn;
+  void *dx, *dblock;
+  float* dgate;
+  void* ws;
+};
+size_t block_norm_workspace_bytes(int T, int H);
+int launch_block_norm(const NormArgs& n, cudaStream_t st);
+int launch_block_norm_backward(const NormArgs& n, float* dw_post, float* dw_pre, cudaStream_t st);
+
 enum { MODE_SWIGLU = 0, MODE_DOWN = 1 };
 
 inline int64_t grouped_rows(const moe_problem& p) {
@@ -74,6 +115,9 @@ inline int64_t grouped_rows(const moe_problem& p) {
 
 // Grouped activations (Xg, Hg) are e4m3 with 1x128 scales for FP8 and FP4 experts.
 inline bool fp8_acts(const moe_problem& p) { return p.wt == MOE_E4M3 || p.wt == MOE_E2M1; }
+
+// Grouped activations that carry scales (e4m3 or MXFP4).
+inline bool scaled_acts(const moe_problem& p) { return fp8_acts(p) || p.wt == MOE_MXFP4; }
 
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 

@@ -1380,23 +1380,7 @@ TcParams make_params(const moe_problem& p, const Plan& pl, const int32_t* masked
 // comb is given -- fused into the reduction, or on its own after an unsplit GEMM.
 int launch_reduce(const moe_problem& p, const Plan& pl, const Phase& f, const int32_t* masked_m,
                   const int32_t* offsets, cudaStream_t st, const CombineArgs* comb = nullptr) {
-  if (comb && pl.ksplit > 1) {
-    if (p.T == 0) return MOE_OK;
-    const dim3 grid((unsigned)p.T, (unsigned)((p.H / 8 + 127) / 128));
-    splitk_reduce_combine_kernel<<<grid, 128, 0, st>>>(f.part, pl.ksplit, (long)grouped_rows(p), p.H, comb->row_of,
-                                                       comb->w, p.K, p.K + p.has_shared,
-                                                       static_cast<__nv_bfloat16*>(f.out),
-                                                       static_cast<__nv_bfloat16*>(comb->out));
-    return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
-  }
-  if (comb) return launch_combine(p, f.out, comb->row_of, comb->w, comb->out, st);
-  if (pl.ksplit <= 1) return MOE_OK;
-  const long rows = (long)grouped_rows(p);
-  const dim3 grid((unsigned)rows, (unsigned)((f.out_cols / 4 + 255) / 256));
-  splitk_reduce_kernel<<<grid, 256, 0, st>>>(f.part, pl.ksplit, rows, f.out_cols, masked_m, offsets, pl.nslots,
-                                             p.layout == MOE_LAYOUT_MASKED, p.M_max,
-                                             static_cast<__nv_bfloat16*>(f.out));
-  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return launch_splitk_reduce(p, f.part, pl.ksplit, f.out_cols, f.out, masked_m, offsets, st, comb);
 }
 
 // Clusters of two that the device keeps resident at once for the SM-pair kernel (its shared
@@ -1564,13 +1548,36 @@ __global__ void __launch_bounds__(256) grouped_gemm_f32_kernel(const float* __re
 
 }  // namespace
 
+int launch_splitk_reduce(const moe_problem& p, const float* part, int ksplit, int cols, void* out,
+                         const int32_t* masked_m, const int32_t* offsets, cudaStream_t st, const CombineArgs* comb) {
+  if (comb && ksplit > 1) {
+    if (p.T == 0) return MOE_OK;
+    const dim3 grid((unsigned)p.T, (unsigned)((p.H / 8 + 127) / 128));
+    splitk_reduce_combine_kernel<<<grid, 128, 0, st>>>(part, ksplit, (long)grouped_rows(p), p.H, comb->row_of,
+                                                       comb->w, p.K, p.K + p.has_shared,
+                                                       static_cast<__nv_bfloat16*>(out),
+                                                       static_cast<__nv_bfloat16*>(comb->out));
+    return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  }
+  if (comb) return launch_combine(p, out, comb->row_of, comb->w, comb->out, st);
+  if (ksplit <= 1) return MOE_OK;
+  const long rows = (long)grouped_rows(p);
+  const dim3 grid((unsigned)rows, (unsigned)((cols / 4 + 255) / 256));
+  splitk_reduce_kernel<<<grid, 256, 0, st>>>(part, ksplit, rows, cols, masked_m, offsets, p.P + p.has_shared,
+                                             p.layout == MOE_LAYOUT_MASKED, p.M_max,
+                                             static_cast<__nv_bfloat16*>(out));
+  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
 int gemm_tile_rows(const moe_problem& p, int mode) {
   if (p.wt == MOE_F32) return 0;
+  if (p.wt == MOE_MXFP4) return gemm_mx_tile_rows(p, mode);
   return use_pairs(p, mode, 1) ? 2 * BN : fp8_acts(p) ? DEC_CH : BN;
 }
 
 size_t gemm_workspace_bytes(const moe_problem& p) {
   if (p.wt == MOE_F32) return 0;
+  if (p.wt == MOE_MXFP4) return gemm_mx_workspace_bytes(p);
   // Split-K state depends on the SM count; size it for the largest plausible GPU (up to 256 SMs).
   size_t best = 0;
   for (int mode = 0; mode < 2; ++mode) {
@@ -1605,6 +1612,10 @@ int launch_gemm(const moe_problem& p, int mode, const void* act, const float* ac
     if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
     return comb ? launch_combine(p, out, comb->row_of, comb->w, comb->out, st) : MOE_OK;
   }
+  if (p.wt == MOE_MXFP4)
+    return launch_gemm_mx(p, mode, act, reinterpret_cast<const uint8_t*>(act_scales), w,
+                          reinterpret_cast<const uint8_t*>(w_scales), masked_m, offsets, out,
+                          reinterpret_cast<uint8_t*>(out_scales), err, ws, st, comb);
   const DeviceInfo& di = device_info();
   const Plan pl = make_plan(p, mode, di.sm_count, di.max_smem_optin);
   if (pl.stages == 0) return MOE_ERR_UNSUPPORTED;
@@ -1640,6 +1651,11 @@ int launch_grouped_ffn(const moe_problem& p, const void* xg, const float* xg_sca
     int r = launch_gemm(p, MODE_SWIGLU, xg, nullptr, w13, nullptr, masked_m, offsets, hg, nullptr, err, ws, st);
     if (r) return r;
     return launch_gemm(p, MODE_DOWN, hg, nullptr, w2, nullptr, masked_m, offsets, yg, nullptr, err, ws, st, comb);
+  }
+  if (p.wt == MOE_MXFP4) {  // two launches
+    int r = launch_gemm(p, MODE_SWIGLU, xg, xg_scales, w13, w13_scales, masked_m, offsets, hg, hg_scales, err, ws, st);
+    if (r) return r;
+    return launch_gemm(p, MODE_DOWN, hg, hg_scales, w2, w2_scales, masked_m, offsets, yg, nullptr, err, ws, st, comb);
   }
   const DeviceInfo& di = device_info();
   const Plan pl0 = make_plan(p, MODE_SWIGLU, di.sm_count, di.max_smem_optin, 2);

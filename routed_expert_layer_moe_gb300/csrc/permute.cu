@@ -25,7 +25,7 @@
 // 4096 records, the whole layout in one CTA (replica tables included), then the copy.
 #include <algorithm>
 
-#include "common.cuh"
+#include "mx.cuh"
 #include "route_select.cuh"
 
 namespace moe {
@@ -291,12 +291,15 @@ __global__ void __launch_bounds__(256) slot_scan_kernel(const uint32_t* __restri
   }
 }
 
+// What a copy does to the values on the way.
+enum { QUANT_NONE = 0, QUANT_E4M3 = 1, QUANT_MXFP4 = 2 };
+
 // Part of x[t] to its rows of the grouped buffer (`rows`: the token's K+S rows, -1 = not
 // placed): the 16-byte vectors [v_lo, v_hi) of the token's row; e4m3: quantised per 1x128
-// group on the way (16 vectors per group; v_lo and v_hi are multiples of 16).  Each thread
-// requests up to four vectors (two when quantising) before it stores any.  All threads of the
-// CTA take part.
-template <typename TX, bool QUANT>
+// group on the way (16 vectors per group; v_lo and v_hi are multiples of 16); MXFP4: per block
+// of 32 (four vectors).  Each thread requests up to four vectors (two when quantising) before
+// it stores any.  All threads of the CTA take part.
+template <typename TX, int QUANT>
 __device__ __forceinline__ void copy_token(const TX* __restrict__ x, int t, int H, int KS, const int* rows,
                                            void* __restrict__ xg, float* __restrict__ xg_scales, int v_lo,
                                            int v_hi) {
@@ -331,8 +334,22 @@ __device__ __forceinline__ void copy_token(const TX* __restrict__ x, int t, int 
             f[2 * i + 1] = v.y;
           }
 #pragma unroll
-          for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[i]));
+          for (int i = 0; i < 8; ++i) amax = QUANT == QUANT_MXFP4 ? mx_amax(amax, f[i]) : fmaxf(amax, fabsf(f[i]));
         }
+        if constexpr (QUANT == QUANT_MXFP4) {  // a block of 32: the four threads of a quad
+          amax = mx_amax(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+          amax = mx_amax(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+          if (!live) continue;
+          const uint32_t sb = mx_scale_byte(amax);
+          const uint32_t code = mx_codes8(f, mx_inv_scale(sb));
+          uint8_t* qs = reinterpret_cast<uint8_t*>(xg_scales);
+          for (int k = 0; k < KS; ++k) {
+            const int r = rows[k];
+            if (r < 0) continue;
+            *reinterpret_cast<uint32_t*>(q + (size_t)r * (H / 2) + g * 64 + sub * 4) = code;
+            if ((sub & 3) == 0) qs[(size_t)r * (H / 32) + g * 4 + (sub >> 2)] = (uint8_t)sb;
+          }
+        } else {
 #pragma unroll
         for (int off = 8; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
         if (!live) continue;
@@ -352,6 +369,7 @@ __device__ __forceinline__ void copy_token(const TX* __restrict__ x, int t, int 
           if (r < 0) continue;
           *reinterpret_cast<uint2*>(q + (size_t)r * H + g * 128 + sub * 8) = pv;
           if (sub == 0) xg_scales[(size_t)r * G + g] = sc;
+        }
         }
       }
     }
@@ -390,7 +408,7 @@ __device__ __forceinline__ void copy_range(int H, int esz, int& v_lo, int& v_hi)
 }
 
 // One CTA per token.
-template <typename TX, bool QUANT>
+template <typename TX, int QUANT>
 __global__ void __launch_bounds__(256) scatter_kernel(const TX* __restrict__ x, int H, int T, int K, int P, int S,
                                                       int masked, int M_max, const uint32_t* __restrict__ bits,
                                                       const int32_t* __restrict__ prefix, int W,
@@ -443,7 +461,7 @@ constexpr int kOneLaunchRecords = 256;  // T*K
 constexpr int kSlotsMax = 1024;         // P+S
 constexpr int kSmallThreads = 256;
 
-template <typename TX, bool QUANT, int RPER = 0>
+template <typename TX, int QUANT, int RPER = 0>
 __global__ void __launch_bounds__(kSmallThreads) permute_small_kernel(
     const int32_t* __restrict__ ids, const TX* __restrict__ x, int H, int T, int K, int E, int P, int S, int masked,
     int M_max, int32_t* __restrict__ masked_m, int32_t* __restrict__ offsets, int32_t* __restrict__ row_of,
@@ -738,7 +756,7 @@ __global__ void __launch_bounds__(kLayoutThreads) layout_small_kernel(
 }
 
 // The copy of each token to its rows (row_of written by layout_small_kernel).
-template <typename TX, bool QUANT>
+template <typename TX, int QUANT>
 __global__ void __launch_bounds__(256) copy_rows_kernel(const TX* __restrict__ x, int H, int KS,
                                                         const int32_t* __restrict__ row_of, void* __restrict__ xg,
                                                         float* __restrict__ xg_scales) {
@@ -759,7 +777,7 @@ int copy_splits(const moe_problem& p, int esz) {
   return std::max(1, std::min(want, nv / 128));
 }
 
-template <typename TX, bool QUANT>
+template <typename TX, int QUANT>
 void launch_small(const moe_problem& p, const int32_t* ids, const void* x, const int32_t* p2l, int32_t* masked_m,
                   int32_t* offsets, int32_t* row_of, int32_t* src_of, void* xg, float* xg_scales, int32_t* err,
                   cudaStream_t st) {
@@ -777,7 +795,7 @@ void launch_small(const moe_problem& p, const int32_t* ids, const void* x, const
   }
 }
 
-template <typename TX, bool QUANT, int RPER>
+template <typename TX, int QUANT, int RPER>
 void launch_route_small(const moe_problem& p, const float* logits, const void* x, int32_t* ids, float* w,
                         int32_t* masked_m, int32_t* offsets, int32_t* row_of, int32_t* src_of, void* xg,
                         float* xg_scales, int32_t* err, cudaStream_t st) {
@@ -787,7 +805,7 @@ void launch_route_small(const moe_problem& p, const float* logits, const void* x
       p.M_max, masked_m, offsets, row_of, src_of, xg, xg_scales, err, logits, ids, w);
 }
 
-template <typename TX, bool QUANT>
+template <typename TX, int QUANT>
 void launch_route_small_per(const moe_problem& p, const float* logits, const void* x, int32_t* ids, float* w,
                             int32_t* masked_m, int32_t* offsets, int32_t* row_of, int32_t* src_of, void* xg,
                             float* xg_scales, int32_t* err, cudaStream_t st) {
@@ -812,13 +830,16 @@ int launch_route_permute_small(const moe_problem& p, const float* logits, const 
                                int32_t* masked_m, int32_t* offsets, int32_t* row_of, int32_t* src_of, void* xg,
                                float* xg_scales, int32_t* err, cudaStream_t st) {
   if (fp8_acts(p))
-    launch_route_small_per<__nv_bfloat16, true>(p, logits, x, ids, w, masked_m, offsets, row_of, src_of, xg,
+    launch_route_small_per<__nv_bfloat16, QUANT_E4M3>(p, logits, x, ids, w, masked_m, offsets, row_of, src_of, xg,
                                                 xg_scales, err, st);
+  else if (p.wt == MOE_MXFP4)
+    launch_route_small_per<__nv_bfloat16, QUANT_MXFP4>(p, logits, x, ids, w, masked_m, offsets, row_of, src_of, xg,
+                                                       xg_scales, err, st);
   else if (p.wt == MOE_BF16)
-    launch_route_small_per<__nv_bfloat16, false>(p, logits, x, ids, w, masked_m, offsets, row_of, src_of, xg,
+    launch_route_small_per<__nv_bfloat16, QUANT_NONE>(p, logits, x, ids, w, masked_m, offsets, row_of, src_of, xg,
                                                  xg_scales, err, st);
   else
-    launch_route_small_per<float, false>(p, logits, x, ids, w, masked_m, offsets, row_of, src_of, xg, xg_scales,
+    launch_route_small_per<float, QUANT_NONE>(p, logits, x, ids, w, masked_m, offsets, row_of, src_of, xg, xg_scales,
                                          err, st);
   return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
@@ -840,11 +861,14 @@ int launch_permute(const moe_problem& p, const int32_t* ids, const void* x, cons
   if (p.T > 0 && ((n <= kOneLaunchRecords && !p2l) || (n <= kLayoutRecords && (int64_t)p.P * W <= kLayoutWords))) {
     // decode: one launch, or a one-CTA layout and the copy; no workspace
     if (fp8_acts(p))
-      launch_small<__nv_bfloat16, true>(p, ids, x, p2l, masked_m, offsets, row_of, src_of, xg, xg_scales, err, st);
+      launch_small<__nv_bfloat16, QUANT_E4M3>(p, ids, x, p2l, masked_m, offsets, row_of, src_of, xg, xg_scales, err, st);
+    else if (p.wt == MOE_MXFP4)
+      launch_small<__nv_bfloat16, QUANT_MXFP4>(p, ids, x, p2l, masked_m, offsets, row_of, src_of, xg, xg_scales, err,
+                                               st);
     else if (p.wt == MOE_BF16)
-      launch_small<__nv_bfloat16, false>(p, ids, x, p2l, masked_m, offsets, row_of, src_of, xg, xg_scales, err, st);
+      launch_small<__nv_bfloat16, QUANT_NONE>(p, ids, x, p2l, masked_m, offsets, row_of, src_of, xg, xg_scales, err, st);
     else
-      launch_small<float, false>(p, ids, x, p2l, masked_m, offsets, row_of, src_of, xg, xg_scales, err, st);
+      launch_small<float, QUANT_NONE>(p, ids, x, p2l, masked_m, offsets, row_of, src_of, xg, xg_scales, err, st);
     return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
   }
   if (p.P > 0 && W > 0) {
@@ -865,17 +889,22 @@ int launch_permute(const moe_problem& p, const int32_t* ids, const void* x, cons
   if (p.T > 0) {
     if (fp8_acts(p)) {
       const dim3 grid(p.T, copy_splits(p, 2));
-      scatter_kernel<__nv_bfloat16, true><<<grid, 256, 0, st>>>(
+      scatter_kernel<__nv_bfloat16, QUANT_E4M3><<<grid, 256, 0, st>>>(
+          (const __nv_bfloat16*)x, p.H, p.T, p.K, p.P, p.has_shared, masked, p.M_max, w.bits, w.prefix, W,
+          w.slot_of, offsets, row_of, src_of, xg, xg_scales);
+    } else if (p.wt == MOE_MXFP4) {
+      const dim3 grid(p.T, copy_splits(p, 2));
+      scatter_kernel<__nv_bfloat16, QUANT_MXFP4><<<grid, 256, 0, st>>>(
           (const __nv_bfloat16*)x, p.H, p.T, p.K, p.P, p.has_shared, masked, p.M_max, w.bits, w.prefix, W,
           w.slot_of, offsets, row_of, src_of, xg, xg_scales);
     } else if (p.wt == MOE_BF16) {
       const dim3 grid(p.T, copy_splits(p, 2));
-      scatter_kernel<__nv_bfloat16, false><<<grid, 256, 0, st>>>(
+      scatter_kernel<__nv_bfloat16, QUANT_NONE><<<grid, 256, 0, st>>>(
           (const __nv_bfloat16*)x, p.H, p.T, p.K, p.P, p.has_shared, masked, p.M_max, w.bits, w.prefix, W,
           w.slot_of, offsets, row_of, src_of, xg, nullptr);
     } else {
       const dim3 grid(p.T, copy_splits(p, 4));
-      scatter_kernel<float, false><<<grid, 256, 0, st>>>((const float*)x, p.H, p.T, p.K, p.P, p.has_shared, masked,
+      scatter_kernel<float, QUANT_NONE><<<grid, 256, 0, st>>>((const float*)x, p.H, p.T, p.K, p.P, p.has_shared, masked,
                                                          p.M_max, w.bits, w.prefix, W, w.slot_of, offsets, row_of,
                                                          src_of, xg, nullptr);
     }

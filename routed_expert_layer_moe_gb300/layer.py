@@ -9,7 +9,8 @@ import torch
 
 from . import _lib as L
 
-TORCH_DTYPE = {"f32": torch.float32, "bf16": torch.bfloat16, "e4m3": torch.uint8, "e2m1": torch.uint8}
+TORCH_DTYPE = {"f32": torch.float32, "bf16": torch.bfloat16, "e4m3": torch.uint8, "e2m1": torch.uint8,
+               "mxfp4": torch.uint8}
 
 
 class MoeLayer:
@@ -17,7 +18,10 @@ class MoeLayer:
     device: w13 [P+S, 2I, H], w2 [P+S, H, I] (e4m3: uint8 codes with fp32 block
     scales w13_s [P+S, 2I/128, H/128], w2_s [P+S, H/128, I/128]; e2m1: the same
     with two codes per byte, w13 [P+S, 2I, H/2], w2 [P+S, H, I/2]).  With e4m3
-    or e2m1 weights the grouped activations xg, hg are e4m3 with 1x128 scales."""
+    or e2m1 weights the grouped activations xg, hg are e4m3 with 1x128 scales.
+    mxfp4: uint8 codes, two to a byte, w13 [P+S, 2I, H/2], w2 [P+S, H, I/2], with a
+    scale byte per 32 codes, w13_s [P+S, 2I, H/32], w2_s [P+S, H, I/32] (as
+    moe_mx_quantize writes them); xg and hg have the same form."""
 
     def __init__(self, problem: L.Problem, act: str, wt: str, out: str, w13, w2, w13_s=None, w2_s=None,
                  phys_to_log=None, device="cuda"):
@@ -40,14 +44,16 @@ class MoeLayer:
         self.offsets = torch.empty(p.P + S + 1, **i32)
         self.row_of = torch.empty((p.T, p.K + S), **i32)
         self.src_of = torch.full((rows,), -1, **i32)
-        f8 = wt in ("e4m3", "e2m1")
+        f8, mx = wt in ("e4m3", "e2m1"), wt == "mxfp4"
+        pack = 2 if mx else 1  # MXFP4: two codes a byte
         gd = TORCH_DTYPE[wt]
         yd = torch.float32 if wt == "f32" else torch.bfloat16
-        self.xg = torch.empty((rows, p.H), dtype=gd, device=dev)
-        self.hg = torch.empty((rows, p.I), dtype=gd, device=dev)
+        self.xg = torch.empty((rows, p.H // pack), dtype=gd, device=dev)
+        self.hg = torch.empty((rows, p.I // pack), dtype=gd, device=dev)
         self.yg = torch.empty((rows, p.H), dtype=yd, device=dev)
-        self.xg_s = torch.empty((rows, p.H // 128), dtype=torch.float32, device=dev) if f8 else None
-        self.hg_s = torch.empty((rows, p.I // 128), dtype=torch.float32, device=dev) if f8 else None
+        group, sd = (32, torch.uint8) if mx else (128, torch.float32)
+        self.xg_s = torch.empty((rows, p.H // group), dtype=sd, device=dev) if f8 or mx else None
+        self.hg_s = torch.empty((rows, p.I // group), dtype=sd, device=dev) if f8 or mx else None
         self.out = torch.empty((p.T, p.H), dtype=TORCH_DTYPE[out], device=dev)
         self.err = torch.zeros(1, **i32)
         nbytes = max(L.moe_workspace_bytes(p), 256)
