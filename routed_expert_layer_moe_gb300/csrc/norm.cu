@@ -9,11 +9,15 @@
 //   dw_post = rs sum_t g dx bn,  dw_pre = sum_t dxn yn
 //   dg  = rs w_post sum_t dx bn (a gate per channel),  rs sum_h dx w_post bn (a gate per token)
 //
-// A CTA holds one row in registers, eight columns a vector, so each array is read and written
-// once; the statistics are fp32 sums over the CTA.  Forward: a CTA per row.  Backward: CTAs
-// walk the rows with a fixed stride and keep the sums over tokens in registers (one for
-// dw_post and dg together: a per-channel gate leaves the sum over tokens), write them once, and a
-// second kernel adds the CTAs' sums in order.
+// A CTA works on one row at a time, eight columns a vector, so each array is read and written
+// once; the statistics are fp32 sums over the CTA.  Backward: CTAs walk the rows with a fixed
+// stride and keep the sums over tokens in registers (one for dw_post and dg together: a
+// per-channel gate leaves the sum over tokens), write them once, and a second kernel adds the
+// CTAs' sums in order.  Both directions are bound by HBM.  With a CTA's loads issued at the start
+// of each row, memory idled through the row's two or three reductions: 8192 x 4096 bf16 took 67
+// and 177 us, against 40 and 60 at the memory's rate.  So the rows to come are fetched into
+// shared memory by asynchronous copies, DEPTH rows ahead; a thread copies and reads only its
+// own columns, so these copies need no barrier.
 #include <algorithm>
 #include <type_traits>
 
@@ -26,66 +30,81 @@ constexpr int kMaxH = 16384;
 constexpr int kMaxThreads = 512;
 constexpr int kMaxParts = 512;  // CTAs of the backward pass at most
 
-// Eight consecutive columns c..c+7 of a row: 16-byte accesses (VEC: H a multiple of 8 and every
-// array 16-byte aligned) or single ones within the row; zeros past its end.
-template <bool VEC>
-__device__ __forceinline__ void load8(const float* row, int c, int H, float (&v)[8]) {
-  if constexpr (VEC) {
-    const float4 a = *reinterpret_cast<const float4*>(row + c);
-    const float4 b = *reinterpret_cast<const float4*>(row + c + 4);
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  } else {
+// Eight consecutive columns as four pairs: the arithmetic is on pairs (fp32x2 instructions), for with
+// single ones the backward kernel issued 690 instructions a row and warp and was bound by them.
+struct V8 {
+  float2 v[4];
+};
+
+__device__ __forceinline__ float2 pair(float a) { return make_float2(a, a); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+
+__device__ __forceinline__ V8 zeros() {
+  V8 r;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = c + i < H ? row[c + i] : 0.0f;
-  }
+  for (int i = 0; i < 4; ++i) r.v[i] = make_float2(0.0f, 0.0f);
+  return r;
 }
 
-template <bool VEC>
-__device__ __forceinline__ void load8(const __nv_bfloat16* row, int c, int H, float (&v)[8]) {
-  if constexpr (VEC) {
-    const uint4 raw = *reinterpret_cast<const uint4*>(row + c);
-    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&raw);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = __bfloat1622float2(h[i]);
-      v[2 * i] = f.x;
-      v[2 * i + 1] = f.y;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = c + i < H ? __bfloat162float(row[c + i]) : 0.0f;
-  }
+__device__ __forceinline__ V8 unpack(float4 a, float4 b) {
+  V8 r;
+  r.v[0] = make_float2(a.x, a.y), r.v[1] = make_float2(a.z, a.w);
+  r.v[2] = make_float2(b.x, b.y), r.v[3] = make_float2(b.z, b.w);
+  return r;
 }
 
-template <bool VEC>
-__device__ __forceinline__ void store8(float* row, int c, int H, const float (&v)[8]) {
-  if constexpr (VEC) {
-    *reinterpret_cast<float4*>(row + c) = make_float4(v[0], v[1], v[2], v[3]);
-    *reinterpret_cast<float4*>(row + c + 4) = make_float4(v[4], v[5], v[6], v[7]);
-  } else {
+__device__ __forceinline__ V8 unpack(uint4 raw) {  // eight bf16
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  V8 r;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (c + i < H) row[c + i] = v[i];
-  }
-}
-
-template <bool VEC>
-__device__ __forceinline__ void store8(__nv_bfloat16* row, int c, int H, const float (&v)[8]) {
-  if constexpr (VEC) {
-    uint4 raw;
-    __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&raw);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-    *reinterpret_cast<uint4*>(row + c) = raw;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (c + i < H) row[c + i] = __float2bfloat16_rn(v[i]);
-  }
+  for (int i = 0; i < 4; ++i)
+    r.v[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+  return r;
 }
 
 __device__ __forceinline__ float to_float(float v) { return v; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ void from_float(float* d, float v) { *d = v; }
+__device__ __forceinline__ void from_float(__nv_bfloat16* d, float v) { *d = __float2bfloat16_rn(v); }
+
+// Columns c..c+7 of a row: 16-byte accesses (VEC: H a multiple of 8 and every array 16-byte aligned)
+// or single ones within the row; zeros past its end.
+template <bool VEC, typename T>
+__device__ __forceinline__ V8 load8(const T* row, int c, int H) {
+  if constexpr (VEC && sizeof(T) == 4) {
+    return unpack(*reinterpret_cast<const float4*>(row + c), *reinterpret_cast<const float4*>(row + c + 4));
+  } else if constexpr (VEC) {
+    return unpack(*reinterpret_cast<const uint4*>(row + c));
+  } else {
+    V8 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      r.v[i] = make_float2(c + 2 * i < H ? to_float(row[c + 2 * i]) : 0.0f,
+                           c + 2 * i + 1 < H ? to_float(row[c + 2 * i + 1]) : 0.0f);
+    return r;
+  }
+}
+
+template <bool VEC, typename T>
+__device__ __forceinline__ void store8(T* row, int c, int H, const V8& a) {
+  if constexpr (VEC && sizeof(T) == 4) {
+    *reinterpret_cast<float4*>(row + c) = make_float4(a.v[0].x, a.v[0].y, a.v[1].x, a.v[1].y);
+    *reinterpret_cast<float4*>(row + c + 4) = make_float4(a.v[2].x, a.v[2].y, a.v[3].x, a.v[3].y);
+  } else if constexpr (VEC) {
+    uint4 raw;
+    __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&raw);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __float22bfloat162_rn(a.v[i]);
+    *reinterpret_cast<uint4*>(row + c) = raw;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (c + 2 * i < H) from_float(row + c + 2 * i, a.v[i].x);
+      if (c + 2 * i + 1 < H) from_float(row + c + 2 * i + 1, a.v[i].y);
+    }
+  }
+}
 
 // Sums of N values over the CTA, in the same order in every thread.  `buf` [N][32] is free for
 // the next use after one more barrier: the callers alternate between two.
@@ -121,236 +140,287 @@ struct Args {
   float rs, eps;
 };
 
-template <typename T, int V, bool VEC>
-__global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const Args<T> a) {
+__device__ __forceinline__ void cp_async16(void* smem_dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem_dst)), "l"(src) : "memory");
+}
+
+// The rows of N arrays on their way to one CTA: DEPTH rows ahead in shared memory (DEPTH = 0:
+// read from global memory when wanted).  Vector j of a thread is columns (j * threads + thread) * 8.
+template <typename T, int V, bool VEC, int DEPTH, int N>
+struct Rows {
+  enum { PARTS = 8 * sizeof(T) / 16 };  // 16-byte parts of a vector, in planes of their own
+  const T* a[N];  // null: the array is not there
+  int H;
+  uint8_t* smem;
+
+  __device__ __forceinline__ uint8_t* at(int slot, int n, int part, int j) const {
+    return smem + (size_t)((slot * N + n) * PARTS * V + part * V + j) * (blockDim.x * 16u) + threadIdx.x * 16;
+  }
+  // Requests row r (if there is one) into a slot; every call is one group of copies.
+  __device__ __forceinline__ void request(int r, int rows, int slot) const {
+    if constexpr (DEPTH > 0) {
+      if (r < rows) {
+        const size_t row = (size_t)r * H;
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            const int c = (j * blockDim.x + threadIdx.x) * 8;
+            if (a[n] && c < H) {
+#pragma unroll
+              for (int q = 0; q < PARTS; ++q)
+                cp_async16(at(slot, n, q, j), reinterpret_cast<const uint8_t*>(a[n] + row + c) + 16 * q);
+            }
+          }
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+  }
+  // All but the last DEPTH - 1 requests have arrived (each thread waits for its own).
+  __device__ __forceinline__ void wait() const {
+    if constexpr (DEPTH > 0) asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH > 0 ? DEPTH - 1 : 0) : "memory");
+  }
+  __device__ __forceinline__ V8 get(int n, int r, int slot, int j) const {
+    if constexpr (DEPTH == 0) {
+      return load8<VEC>(a[n] + (size_t)r * H, (j * blockDim.x + threadIdx.x) * 8, H);
+    } else if constexpr (PARTS == 1) {
+      return unpack(*reinterpret_cast<const uint4*>(at(slot, n, 0, j)));
+    } else {
+      return unpack(*reinterpret_cast<const float4*>(at(slot, n, 0, j)),
+                    *reinterpret_cast<const float4*>(at(slot, n, 1, j)));
+    }
+  }
+};
+
+// w_post with a per-channel gate folded in.
+template <bool VEC, typename T>
+__device__ __forceinline__ V8 load_post(const Args<T>& a, int c) {
+  V8 w = load8<VEC>(a.w_post, c, a.H);
+  if (a.gate_kind == MOE_GATE_CHANNEL) {
+    const V8 g = load8<VEC>(a.gate, c, a.H);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w.v[i] = mul2(w.v[i], g.v[i]);
+  }
+  return w;
+}
+
+template <typename T, int V, bool VEC, int DEPTH>
+__global__ void __launch_bounds__(kMaxThreads, V == 1 ? 3 : 1) block_norm_kernel(const Args<T> a) {
+  extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float buf[2][32];
   const int H = a.H, nt = blockDim.x;
-  const size_t at = (size_t)blockIdx.x * H;
-  float y[V][8];
+  const float invH = 1.0f / (float)H;
+  const Rows<T, V, VEC, DEPTH, 2> in{{a.x, a.block}, H, smem};
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const int c = (j * nt + threadIdx.x) * 8;
+  for (int d = 0; d < DEPTH; ++d) in.request(blockIdx.x + d * gridDim.x, a.rows, d);
+  int slot = 0;
+  for (int r = blockIdx.x; r < a.rows; r += gridDim.x) {
+    const size_t at = (size_t)r * H;
+    in.wait();
+    V8 y[V];
+    float2 f = pair(0.0f);
+    if (a.block) {
+      float2 s = pair(0.0f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[j][i] = 0.0f;
-    if (c < H) load8<VEC>(a.x + at, c, H, y[j]);
-  }
-  if (a.block) {
-    float b[V][8];
-    float s[1] = {0.0f};
+      for (int j = 0; j < V; ++j) {
+        if ((j * nt + (int)threadIdx.x) * 8 < H) {
+          y[j] = in.get(1, r, slot, j);
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int c = (j * nt + threadIdx.x) * 8;
-      if (c < H) {
-        load8<VEC>(a.block + at, c, H, b[j]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s[0] = fmaf(b[j][i], b[j][i], s[0]);
-      }
-    }
-    cta_sum(s, buf[0]);
-    float f = a.rs * rsqrtf(s[0] / (float)H + a.eps);
-    if (a.gate_kind == MOE_GATE_TOKEN) f *= to_float(a.gate[blockIdx.x]);
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int c = (j * nt + threadIdx.x) * 8;
-      if (c < H) {
-        float w[8];
-        load8<VEC>(a.w_post, c, H, w);
-        if (a.gate_kind == MOE_GATE_CHANNEL) {
-          float g[8];
-          load8<VEC>(a.gate, c, H, g);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) w[i] *= g[i];
+          for (int i = 0; i < 4; ++i) s = fma2(y[j].v[i], y[j].v[i], s);
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[j][i] = fmaf(f * w[i], b[j][i], y[j][i]);
       }
+      float sum[1] = {s.x + s.y};
+      cta_sum(sum, buf[0]);
+      float g = a.rs * rsqrtf(sum[0] * invH + a.eps);
+      if (a.gate_kind == MOE_GATE_TOKEN) g *= to_float(a.gate[r]);
+      f = pair(g);
     }
-  }
-  if (a.y) {
+    float2 s = pair(0.0f);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int c = (j * nt + threadIdx.x) * 8;
-      if (c < H) store8<VEC>(a.y + at, c, H, y[j]);
+      if (c < H) {
+        const V8 x = in.get(0, r, slot, j);
+        if (a.block) {
+          const V8 w = load_post<VEC>(a, c);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) y[j].v[i] = fma2(f, mul2(w.v[i], y[j].v[i]), x.v[i]);
+        } else {
+          y[j] = x;
+        }
+        if (a.y) store8<VEC>(a.y + at, c, H, y[j]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s = fma2(y[j].v[i], y[j].v[i], s);  // zeros past the row's end
+      }
     }
-  }
-  if (!a.xn) return;
-  float s[1] = {0.0f};
+    in.request(r + DEPTH * gridDim.x, a.rows, slot);
+    if (DEPTH > 0 && ++slot == DEPTH) slot = 0;
+    if (a.xn) {
+      float sum[1] = {s.x + s.y};
+      cta_sum(sum, buf[1]);
+      const float2 ry = pair(rsqrtf(sum[0] * invH + a.eps));
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
+      for (int j = 0; j < V; ++j) {
+        const int c = (j * nt + threadIdx.x) * 8;
+        if (c < H) {
+          V8 w = load8<VEC>(a.w_pre, c, H);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s[0] = fmaf(y[j][i], y[j][i], s[0]);  // zeros past the row's end
-  }
-  cta_sum(s, buf[1]);
-  const float ry = rsqrtf(s[0] / (float)H + a.eps);
-#pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const int c = (j * nt + threadIdx.x) * 8;
-    if (c < H) {
-      float w[8];
-      load8<VEC>(a.w_pre, c, H, w);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] *= y[j][i] * ry;
-      store8<VEC>(a.xn + at, c, H, w);
+          for (int i = 0; i < 4; ++i) w.v[i] = mul2(w.v[i], mul2(y[j].v[i], ry));
+          store8<VEC>(a.xn + at, c, H, w);
+        }
+      }
     }
+    // a buffer is written again only after a barrier on the other one, if both are in use
+    if (!a.block || !a.xn) __syncthreads();
   }
 }
 
-template <typename T, int V, bool VEC>
-__global__ void __launch_bounds__(kMaxThreads) block_norm_backward_kernel(const Args<T> a) {
+template <typename T, int V, bool VEC, int DEPTH>
+__global__ void __launch_bounds__(kMaxThreads, V == 1 ? 2 : 1) block_norm_backward_kernel(const Args<T> a) {
+  extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float buf[3][64];
+  enum { X, B, DY, DXN };
   const int H = a.H, nt = blockDim.x;
   const float invH = 1.0f / (float)H;
-  float acc_post[V][8], acc_pre[V][8];
+  const Rows<T, V, VEC, DEPTH, 4> in{{a.x, a.block, a.dy, a.dxn}, H, smem};
+  V8 acc_post[V], acc_pre[V];
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
+  for (int j = 0; j < V; ++j) acc_post[j] = acc_pre[j] = zeros();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc_post[j][i] = acc_pre[j][i] = 0.0f;
-  }
+  for (int d = 0; d < DEPTH; ++d) in.request(blockIdx.x + d * gridDim.x, a.rows, d);
+  int slot = 0;
   for (int r = blockIdx.x; r < a.rows; r += gridDim.x) {
     const size_t at = (size_t)r * H;
     const float gt = a.gate_kind == MOE_GATE_TOKEN ? to_float(a.gate[r]) : 1.0f;
-    float y[V][8], b[V][8], d[V][8], q[V][8];
+    in.wait();
     float rb = 0.0f;
-    float s[2] = {0.0f, 0.0f};
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int c = (j * nt + threadIdx.x) * 8;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[j][i] = b[j][i] = d[j][i] = q[j][i] = 0.0f;
-      if (c < H) {
-        load8<VEC>(a.x + at, c, H, y[j]);
-        if (a.block) load8<VEC>(a.block + at, c, H, b[j]);
-        if (a.dy) load8<VEC>(a.dy + at, c, H, d[j]);
-        if (a.dxn) load8<VEC>(a.dxn + at, c, H, q[j]);
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s[0] = fmaf(b[j][i], b[j][i], s[0]);
-    }
     if (a.block) {
-      float sb[1] = {s[0]};
-      cta_sum(sb, buf[0]);
-      rb = rsqrtf(sb[0] * invH + a.eps);
+      float2 s = pair(0.0f);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        if ((j * nt + (int)threadIdx.x) * 8 < H) {
+          const V8 b = in.get(B, r, slot, j);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s = fma2(b.v[i], b.v[i], s);
+        }
+      }
+      float sum[1] = {s.x + s.y};
+      cta_sum(sum, buf[0]);
+      rb = rsqrtf(sum[0] * invH + a.eps);
     }
-    s[0] = 0.0f;
+    V8 y[V];
+    float2 s0 = pair(0.0f), s1 = pair(0.0f);  // sums of y^2 and of q y
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int c = (j * nt + threadIdx.x) * 8;
       if (c < H) {
+        y[j] = in.get(X, r, slot, j);
         if (a.block) {
-          float w[8];
-          load8<VEC>(a.w_post, c, H, w);
-          if (a.gate_kind == MOE_GATE_CHANNEL) {
-            float g[8];
-            load8<VEC>(a.gate, c, H, g);
+          const V8 b = in.get(B, r, slot, j), w = load_post<VEC>(a, c);
+          const float2 f = pair(a.rs * gt * rb);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] *= g[i];
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            b[j][i] *= rb;
-            y[j][i] = fmaf(a.rs * gt * w[i], b[j][i], y[j][i]);
-          }
+          for (int i = 0; i < 4; ++i) y[j].v[i] = fma2(f, mul2(w.v[i], b.v[i]), y[j].v[i]);
         }
         if (a.dxn) {
-          float w[8];
-          load8<VEC>(a.w_pre, c, H, w);
+          const V8 q = in.get(DXN, r, slot, j), w = load8<VEC>(a.w_pre, c, H);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            s[0] = fmaf(y[j][i], y[j][i], s[0]);
-            s[1] = fmaf(q[j][i] * w[i], y[j][i], s[1]);
+          for (int i = 0; i < 4; ++i) {
+            s0 = fma2(y[j].v[i], y[j].v[i], s0);
+            s1 = fma2(mul2(q.v[i], w.v[i]), y[j].v[i], s1);
           }
         }
       }
     }
     float ry = 0.0f, m = 0.0f;
     if (a.dxn) {
-      cta_sum(s, buf[1]);
-      ry = rsqrtf(s[0] * invH + a.eps);
-      m = s[1] * ry * ry * invH;  // mean(q yn) / y's factor: yn mean(q yn) = y m
+      float sum[2] = {s0.x + s0.y, s1.x + s1.y};
+      cta_sum(sum, buf[1]);
+      ry = rsqrtf(sum[0] * invH + a.eps);
+      m = -sum[1] * ry * ry * ry * invH;  // -ry yn mean(q yn) = y m
     }
-    float u[1] = {0.0f};
+    float2 u = pair(0.0f);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int c = (j * nt + threadIdx.x) * 8;
       if (c < H) {
+        V8 d = a.dy ? in.get(DY, r, slot, j) : zeros();
         if (a.dxn) {
-          float w[8];
-          load8<VEC>(a.w_pre, c, H, w);
+          const V8 q = in.get(DXN, r, slot, j), w = load8<VEC>(a.w_pre, c, H);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            acc_pre[j][i] = fmaf(q[j][i], y[j][i] * ry, acc_pre[j][i]);
-            d[j][i] = fmaf(ry, fmaf(-y[j][i], m, q[j][i] * w[i]), d[j][i]);
+          for (int i = 0; i < 4; ++i) {
+            acc_pre[j].v[i] = fma2(mul2(q.v[i], y[j].v[i]), pair(ry), acc_pre[j].v[i]);
+            d.v[i] = fma2(pair(m), y[j].v[i], fma2(pair(ry), mul2(q.v[i], w.v[i]), d.v[i]));
           }
         }
-        store8<VEC>(a.dx + at, c, H, d[j]);
+        store8<VEC>(a.dx + at, c, H, d);
         if (a.block) {
-          float w[8];
-          load8<VEC>(a.w_post, c, H, w);
-          if (a.gate_kind == MOE_GATE_CHANNEL) {
-            float g[8];
-            load8<VEC>(a.gate, c, H, g);
+          const V8 b = in.get(B, r, slot, j), w = load_post<VEC>(a, c);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] *= g[i];
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float db = d[j][i] * b[j][i];
-            acc_post[j][i] = fmaf(gt, db, acc_post[j][i]);
-            u[0] = fmaf(w[i], db, u[0]);
-            d[j][i] *= a.rs * w[i];  // q2 without a token's gate
+          for (int i = 0; i < 4; ++i) {
+            const float2 db = mul2(d.v[i], b.v[i]);
+            acc_post[j].v[i] = fma2(pair(gt * rb), db, acc_post[j].v[i]);
+            u = fma2(w.v[i], db, u);
+            y[j].v[i] = mul2(d.v[i], w.v[i]);  // y is done with
           }
         }
       }
     }
     if (a.block) {
-      cta_sum(u, buf[2]);
-      const float mean = a.rs * u[0] * invH, f = rb * gt;
+      float sum[1] = {u.x + u.y};
+      cta_sum(sum, buf[2]);
+      const float dg = a.rs * rb * sum[0];  // sum over the row of rs dx bn w_post
+      const float2 f = pair(a.rs * rb * gt), mean = pair(-rb * rb * gt * dg * invH);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const int c = (j * nt + threadIdx.x) * 8;
         if (c < H) {
+          V8 b = in.get(B, r, slot, j);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) d[j][i] = f * fmaf(-b[j][i], mean, d[j][i]);
-          store8<VEC>(a.dblock + at, c, H, d[j]);
+          for (int i = 0; i < 4; ++i) b.v[i] = fma2(mean, b.v[i], mul2(f, y[j].v[i]));
+          store8<VEC>(a.dblock + at, c, H, b);
         }
       }
-      if (a.dgate && a.gate_kind == MOE_GATE_TOKEN && threadIdx.x == 0) a.dgate[r] = a.rs * u[0];
+      if (a.dgate && a.gate_kind == MOE_GATE_TOKEN && threadIdx.x == 0) a.dgate[r] = dg;
     }
-    __syncthreads();  // the next row writes the buffers again
+    in.request(r + DEPTH * gridDim.x, a.rows, slot);
+    if (DEPTH > 0 && ++slot == DEPTH) slot = 0;
+    // with the block there is a barrier on another buffer between two uses of each
+    if (!a.block) __syncthreads();
   }
   float* part = a.part + (size_t)blockIdx.x * 2 * H;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const int c = (j * nt + threadIdx.x) * 8;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (c + i < H) {
-        part[c + i] = acc_post[j][i];
-        part[H + c + i] = acc_pre[j][i];
-      }
+    if (c < H) {
+      store8<VEC>(part, c, H, acc_post[j]);
+      store8<VEC>(part + H, c, H, acc_pre[j]);
+    }
   }
 }
 
-// The CTAs' sums added in order; a thread per column, four groups of CTAs in flight.
+// The CTAs' sums added in a fixed order: a thread per column and group of CTAs.
+constexpr int kReduceGroups = 16;
+
 template <typename T>
-__global__ void __launch_bounds__(128) block_norm_reduce_kernel(const float* __restrict__ part, int parts, int H,
-                                                               int gate_kind, const T* __restrict__ gate,
-                                                               const T* __restrict__ w_post, float rs,
-                                                               float* __restrict__ dgate,
-                                                               float* __restrict__ dw_post,
-                                                               float* __restrict__ dw_pre) {
-  __shared__ float sum[4][32];
-  const int c = blockIdx.x * 32 + (threadIdx.x & 31), g = threadIdx.x >> 5;
+__global__ void __launch_bounds__(32 * kReduceGroups)
+    block_norm_reduce_kernel(const float* __restrict__ part, int parts, int H, int gate_kind,
+                             const T* __restrict__ gate, const T* __restrict__ w_post, float rs,
+                             float* __restrict__ dgate, float* __restrict__ dw_post, float* __restrict__ dw_pre) {
+  __shared__ float sum[kReduceGroups][32];
+  const int lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane, g = threadIdx.x >> 5;
   const bool pre = blockIdx.y != 0;
   float s = 0.0f;
   if (c < H) {
 #pragma unroll 8
-    for (int i = g; i < parts; i += 4) s += __ldg(part + ((size_t)i * 2 + pre) * H + c);
+    for (int i = g; i < parts; i += kReduceGroups) s += __ldg(part + ((size_t)i * 2 + pre) * H + c);
   }
-  sum[g][threadIdx.x & 31] = s;
+  sum[g][lane] = s;
   __syncthreads();
   if (g != 0 || c >= H) return;
-  s = (sum[0][threadIdx.x] + sum[1][threadIdx.x]) + (sum[2][threadIdx.x] + sum[3][threadIdx.x]);
+  s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kReduceGroups; ++i) s += sum[i][lane];
   if (pre) {
     if (dw_pre) dw_pre[c] = s;
   } else {
@@ -362,31 +432,66 @@ __global__ void __launch_bounds__(128) block_norm_reduce_kernel(const float* __r
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// f(vectors a thread, 16-byte accesses) and the CTA's threads: one vector a thread up to 512
-// threads, then two, four.
-template <typename F>
-int dispatch(int H, bool vec, F f) {
+// How rows of H columns are shared out: vectors and threads, CTAs an SM holds, rows fetched ahead.
+struct Shape {
+  int v, threads, ctas, depth;
+  size_t smem;
+};
+
+// One vector a thread up to 512 threads, then two, four.  `arrays`: how many a row is read from;
+// `most`: CTAs an SM holds with one vector a thread (by their registers).
+Shape shape_of(int H, int esz, bool vec, int arrays, int most, int rows) {
+  Shape s{};
   const int nvec = (H + 7) / 8;
-  auto go = [&](auto v) {
-    constexpr int V = decltype(v)::value;
-    const int threads = (((nvec + V - 1) / V) + 31) / 32 * 32;
-    return vec ? f(v, std::true_type(), threads) : f(v, std::false_type(), threads);
-  };
-  if (nvec <= 512) return go(std::integral_constant<int, 1>());
-  if (nvec <= 1024) return go(std::integral_constant<int, 2>());
-  return go(std::integral_constant<int, 4>());
+  s.v = nvec <= 512 ? 1 : nvec <= 1024 ? 2 : 4;
+  s.threads = ((nvec + s.v - 1) / s.v + 31) / 32 * 32;
+  s.ctas = s.v == 1 ? std::min(512 * most / s.threads, 24) : 1;
+  const DeviceInfo& di = device_info();
+  if (!vec || rows <= di.sm_count * s.ctas) return s;  // a row for each CTA: nothing to fetch ahead
+  const size_t row = (size_t)s.v * s.threads * 8 * esz * arrays;
+  const size_t room = (size_t)di.max_smem_optin - 1024;  // what a CTA's static memory and the system take
+  for (int ctas = s.ctas; ctas >= 1; --ctas)
+    for (int depth = 3; depth >= 2; --depth)
+      if (row * depth <= room / ctas - 1024) {
+        s.ctas = ctas, s.depth = depth, s.smem = row * depth;
+        return s;
+      }
+  return s;
 }
 
-int parts_of(int T) { return std::min(T, std::min(kMaxParts, std::max(2 * device_info().sm_count, 1))); }
+// f(vectors a thread, 16-byte accesses, rows ahead) with compile-time arguments.
+template <typename F>
+int dispatch(const Shape& s, bool vec, F f) {
+  using std::integral_constant;
+  auto go = [&](auto v) {
+    if (!vec) return f(v, std::false_type(), integral_constant<int, 0>());
+    if (s.depth == 3) return f(v, std::true_type(), integral_constant<int, 3>());
+    if (s.depth == 2) return f(v, std::true_type(), integral_constant<int, 2>());
+    return f(v, std::true_type(), integral_constant<int, 0>());
+  };
+  if (s.v == 1) return go(integral_constant<int, 1>());
+  if (s.v == 2) return go(integral_constant<int, 2>());
+  return go(integral_constant<int, 4>());
+}
+
+template <typename K, typename T>
+int launch(K kern, int grid, const Shape& s, const Args<T>& a, cudaStream_t st) {
+  if (s.smem > 40 * 1024 &&  // 48 KB, the static memory counted in, is what a kernel has without asking
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s.smem) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  kern<<<grid, s.threads, s.smem, st>>>(a);
+  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
 
 template <typename T>
 int forward(Args<T> a, cudaStream_t st) {
   const bool vec = a.H % 8 == 0 && aligned16(a.x) && aligned16(a.block) && aligned16(a.w_post) &&
                    aligned16(a.w_pre) && aligned16(a.y) && aligned16(a.xn) &&
                    (a.gate_kind != MOE_GATE_CHANNEL || aligned16(a.gate));
-  return dispatch(a.H, vec, [&](auto v, auto w, int threads) {
-    block_norm_kernel<T, decltype(v)::value, decltype(w)::value><<<a.rows, threads, 0, st>>>(a);
-    return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  const Shape s = shape_of(a.H, (int)sizeof(T), vec, 2, 3, a.rows);
+  const int grid = s.depth ? std::min(a.rows, s.ctas * device_info().sm_count) : a.rows;
+  return dispatch(s, vec, [&](auto v, auto w, auto d) {
+    return launch(block_norm_kernel<T, decltype(v)::value, decltype(w)::value, decltype(d)::value>, grid, s, a, st);
   });
 }
 
@@ -395,18 +500,17 @@ int backward(Args<T> a, float* dw_post, float* dw_pre, cudaStream_t st) {
   const bool vec = a.H % 8 == 0 && aligned16(a.x) && aligned16(a.block) && aligned16(a.w_post) &&
                    aligned16(a.w_pre) && aligned16(a.dy) && aligned16(a.dxn) && aligned16(a.dx) &&
                    aligned16(a.dblock) && (a.gate_kind != MOE_GATE_CHANNEL || aligned16(a.gate));
-  const int parts = parts_of(a.rows);
-  if (parts > 0) {
-    const int r = dispatch(a.H, vec, [&](auto v, auto w, int threads) {
-      block_norm_backward_kernel<T, decltype(v)::value, decltype(w)::value><<<parts, threads, 0, st>>>(a);
-      return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
-    });
-    if (r) return r;
-  }
+  const Shape s = shape_of(a.H, (int)sizeof(T), vec, 4, 2, a.rows);
+  const int parts = std::min({a.rows, kMaxParts, s.ctas * device_info().sm_count});
+  const int r = dispatch(s, vec, [&](auto v, auto w, auto d) {
+    return launch(block_norm_backward_kernel<T, decltype(v)::value, decltype(w)::value, decltype(d)::value>, parts, s,
+                  a, st);
+  });
+  if (r) return r;
   const dim3 grid((a.H + 31) / 32, 2);
-  block_norm_reduce_kernel<T><<<grid, 128, 0, st>>>(a.part, parts, a.H, a.gate_kind, a.gate, a.w_post, a.rs,
-                                                    a.block ? a.dgate : nullptr, a.block ? dw_post : nullptr,
-                                                    a.w_pre ? dw_pre : nullptr);
+  block_norm_reduce_kernel<T><<<grid, 32 * kReduceGroups, 0, st>>>(
+      a.part, parts, a.H, a.gate_kind, a.gate, a.w_post, a.rs, a.block ? a.dgate : nullptr,
+      a.block ? dw_post : nullptr, a.w_pre ? dw_pre : nullptr);
   return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 

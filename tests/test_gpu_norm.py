@@ -198,3 +198,13 @@ def test_gradient_against_differences(gate):
         h = 1e-5
         slope = (value(a[:i] + [a[i] + h * d] + a[i + 1:]) - value(a[:i] + [a[i] - h * d] + a[i + 1:])) / (2 * h)
         assert abs(float((g.double() * d).sum()) - slope) <= 1e-4 * float((g.double() * d).abs().sum()) + 1e-6
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("T,H", [(1000, 4096), (640, 7168), (500, 8200), (900, 384), (3000, 40), (460, 12288)])
+def test_more_rows_than_ctas(T, H, dtype):
+    """Rows fetched ahead: several rows a CTA, at each number of rows in flight."""
+    for gate, block in (("channel", True), ("token", True), ("none", False)):
+        args, dy, dxn = inputs(T, H, dtype, gate, block, seed=T)
+        check_forward(args, forward(args))
+        check_backward(args, dy, dxn, backward(args, dy, dxn))
