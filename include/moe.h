@@ -167,7 +167,9 @@ size_t moe_workspace_bytes(const moe_problem* p);
  * SM holding 128 of the tile's token rows and one of its two 128-row weight
  * tiles, with one cta_group::2 MMA over both; else 64: one CTA per SM with
  * M = 64 MMAs.  moe_grouped_ffn runs on single CTAs: 64-row tiles for FP8 /
- * FP4 experts, 128 for bf16.
+ * FP4 experts, 128 for bf16.  For MXFP4 experts 256 with at least 128 rows per
+ * slot on average (step 4: and H a multiple of 256), on SM pairs as above; else
+ * 128.
  * 0 for an invalid problem or one whose GEMMs run on the CUDA cores (F32).
  * Host only; touches no GPU. */
 int32_t moe_gemm_tile_rows(const moe_problem* p, int32_t step);

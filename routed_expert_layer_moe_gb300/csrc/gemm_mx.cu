@@ -8,23 +8,33 @@
 // memory) and sums the whole K range in fp32, so no partial sum ever leaves tensor memory: the
 // FP8 / FP4 kernels with fp32 scales promote every 128-wide K block on the CUDA cores instead.
 //
-// One CTA per SM, persistent.  A unit is (slot, chunk of at most 128 token rows, pair of 128-row
-// weight tiles, K split); gate/up: the pair is the gate and the up tile of the same columns.
-// Token rows are the MMA's M = 128 side and the pair its N = 256 side, so a token's row lies in
-// one thread of the epilogue: SwiGLU, the MXFP4 form of h (a block is 32 columns of the row) and
-// the stores are row-local.
-//   * Warp 0: TMA producer.  A stage is 256 codes (128 bytes) of K: two weight tiles and the
-//     token box (the smallest of 16 / 32 / 64 / 128 rows that covers the chunk).
-//   * Warps 2-3: scale loaders.  Scales are row-major in global memory; the tensor core wants, for
-//     128 rows and 128 codes, a 512-byte block with the four scale bytes of row r at
-//     16 (r % 32) + 4 (r / 32).  A loader thread reads the 16 scale bytes of 512 codes of a row
-//     and stores them as four words into the blocks of two stages (a group), one group ahead.
-//   * Warp 1: one thread copies a stage's scale blocks from shared to tensor memory
-//     (tcgen05.cp, which runs in order with the MMAs) and issues its four MMAs of K = 64.
-//   * Warps 4-11: epilogue.  Columns 0-255 of tensor memory hold the unit's accumulators, the
-//     columns above them the scales of the stages in flight.  The epilogue first moves the
-//     accumulators to registers and hands them back, so only that move is not overlapped with
-//     the next unit's MMAs; the copies run ahead through it.
+// Persistent CTAs, one per SM.  A unit is (slot, chunk of token rows, pair of weight tiles of 128
+// or 64 rows, K split); gate/up: the pair is the gate and the up tile of the same columns.
+// Token rows are the MMA's M side and the pair its N side, so a token's row lies in one thread of the
+// epilogue: SwiGLU, the MXFP4 form of h (a block is 32 columns of the row) and the stores are
+// row-local.  Two forms:
+//   * One CTA: chunks of at most 128 rows, M = 128.  What decode needs: an expert's weights are
+//     read once, and a chunk's token box is the smallest of 16 / 32 / 64 / 96 / 128 rows.
+//   * SM pairs (PAIR; slots of 128 rows or more on average): clusters of two CTAs, chunks of at
+//     most 256 rows, one cta_group::2 MMA with M = 256 over both CTAs' shared memory.  Each CTA stages
+//     its half of the rows and one of the two weight tiles: 32 KB a stage, not 48, for the
+//     same work of its tensor core.  What bounds large products is the way from L2 to shared memory:
+//     without its MMAs and scales the one-CTA form took 0.50 us a stage of 48 KB (96 GB/s per SM),
+//     against 0.27 us of MMAs.
+// Roles of a CTA:
+//   * Warp 0: TMA producer.  A stage is 256 codes (128 bytes) of K.
+//   * Warp 1: the thread that issues a stage's four MMAs of K = 64.
+//   * Warps 4-7: scales.  Per group of 512 codes (two stages) a thread copies the 16 scale bytes of
+//     its row in each block of 128 rows (row-major in global memory) to shared memory, three
+//     groups ahead; every warp then reads all rows and writes them to its lane quarter of tensor memory
+//     in the order the MMA wants: for 128 rows and 128 codes, four columns, lane i of column q holding
+//     the four bytes of row 32 q + i, the same in each quarter.  Copying them from shared memory
+//     with tcgen05.cp instead put six copies a stage into the tensor core's queue: 0.69 us a stage,
+//     0.62 without them.
+//   * Warps 8-15: epilogue.  Columns 0-255 of tensor memory hold the unit's accumulators, the
+//     columns above them the scales of four groups.  The epilogue first moves the accumulators to
+//     registers and hands them back, so only that move is not overlapped with the next unit's
+//     MMAs; the copies run ahead through it.
 //   * Every wait is bounded; on expiry the CTA drains its copies and MMAs, frees tensor memory,
 //     reports MOE_FLAG_TIMEOUT and returns.
 #include <algorithm>
@@ -37,31 +47,39 @@ namespace {
 
 constexpr int STATS_CTAS = MOE_STATS_CTAS;
 constexpr size_t STATS_BYTES = MOE_STATS_BYTES;
-constexpr int BM = 128;                 // rows of one weight tile
-constexpr int BN = 128;                 // token rows of one chunk at most
+constexpr int BN = 128;                 // token rows of one CTA's chunk at most
 constexpr int ROW_BYTES = 128;          // bytes of a row in one stage (one 128-byte swizzle span)
 constexpr int KB = 256;                 // codes of a row in one stage
-constexpr int TILE_BYTES = 128 * ROW_BYTES;
-constexpr int STAGE_BYTES = 3 * TILE_BYTES;  // weight tile 0 | weight tile 1 | tokens
+constexpr int TOK_BYTES = BN * ROW_BYTES;
 constexpr int GROUP = 2;                // stages whose scales are loaded together (16 bytes of a row)
-constexpr int SF_BLOCK = 512;           // scales of 128 rows and 128 codes
-constexpr int SF_STAGE_TOK = 2 * SF_BLOCK;             // tokens: two blocks along K
-constexpr int SF_STAGE_BYTES = SF_STAGE_TOK + 4 * SF_BLOCK;  // and the weights' two tiles of two blocks
-constexpr int SF_RING = 3;              // groups of scales in flight
-constexpr int SF_COLS = 24;             // tensor-memory columns of one stage's scales: 2 x 4 and 2 x 8
-constexpr uint32_t SF_COL0 = 256;       // first of them
-constexpr int NUM_THREADS = 384;
-constexpr int EPI_THREADS = 256;
-constexpr int EPI_WARP0 = 4;
-constexpr int EPI_WARPS = EPI_THREADS / 32;
-constexpr int LOAD_WARP0 = 2;
-constexpr int LOAD_THREADS = 64;
-// Register split (setmaxnreg): 4*32*ctrl + 8*32*epi <= 384 * (registers at launch), checked
-// before the first launch.
-constexpr int REGS_CTRL = 96, REGS_EPI = 200;
-constexpr int REGS_NEEDED = 4 * 32 * REGS_CTRL + 8 * 32 * REGS_EPI;
+constexpr int SF_RING = 4;              // groups of scales in tensor memory
+constexpr int SF_BUFS = 4;              // and in shared memory: three are on their way while one is read
+constexpr uint32_t SF_COL0 = 256;       // first of their columns
+constexpr int MAX_STAGES = 7;
+constexpr int NUM_THREADS = 512;        // four warpgroups
+constexpr int SF_WARP0 = 4, SF_WARPS = 4;
+constexpr int EPI_WARP0 = 8, EPI_WARPS = 8;
+// Register split (setmaxnreg) of warpgroup 0, the scale warps and the two epilogue warpgroups:
+// 128 * (ctrl + sf + 2 epi) <= 512 * (registers at launch), checked before the first launch.
+constexpr int REGS_CTRL = 72, REGS_SF = 88, REGS_EPI = 176;
+constexpr int REGS_NEEDED = 128 * (REGS_CTRL + REGS_SF + 2 * REGS_EPI);
 constexpr uint32_t TMEM_COLS = 512;
 constexpr long long TIMEOUT = 4000000000LL;  // SM cycles, about 2 s
+// Token boxes of 16, 32, 64, 96 and 128 rows: the smallest that covers a chunk is copied.
+constexpr int NUM_BOXES = 5;
+__host__ __device__ constexpr int box_rows(int i) { return i ? 32 * i : 16; }
+__host__ __device__ constexpr int box_of(int rows) { return rows <= 16 ? 0 : (rows + 31) / 32; }
+
+// Sizes that go with TW, the rows of one weight tile (64 or 128), and the form.
+template <int TW, bool PAIR>
+struct Tile {
+  static constexpr int W_BYTES = TW * ROW_BYTES;
+  static constexpr int W_STAGED = PAIR ? W_BYTES : 2 * W_BYTES;  // weight bytes of this CTA's stage
+  static constexpr int STAGE = W_STAGED + TOK_BYTES;             // weights | tokens
+  static constexpr int NB = 2 * TW / 128;                        // 128-row scale blocks of a pair's rows
+  static constexpr int SF_BUF = (1 + NB) * 128 * 16;             // one group's scales in shared memory
+  static constexpr int SF_COLS = 4 * (4 * NB + 4);               // and in tensor memory: weights, then tokens
+};
 
 struct MxParams {
   int mode;          // MODE_SWIGLU or MODE_DOWN
@@ -90,17 +108,24 @@ struct MxParams {
   uint32_t sf_off, pre_off, bar_off, misc_off;
 };
 
+struct TokenMaps {
+  CUtensorMap box[NUM_BOXES];
+};
+
 struct Unit {
   int s, c, j, q;
-  int nvalid;        // token rows of the chunk
-  int rowB;          // first grouped-buffer row of the chunk
+  int nvalid;        // token rows of this CTA's chunk
+  int most;          // the larger of a pair's two chunks (one CTA: nvalid)
+  int rowB;          // first grouped-buffer row of this CTA's chunk
   int rowA0, rowA1;  // first weight row of each tile
   int kb0, kb1;      // stages
   bool a1;           // the second tile exists
 };
 
+template <bool PAIR>
 __device__ __forceinline__ Unit decode_unit(const MxParams& p, const int* prefix, const int* srows, const int* sbase,
-                                            int u) {
+                                            int u, uint32_t rank) {
+  constexpr int CH = PAIR ? 2 * BN : BN;
   int lo = 0, hi = p.nslots;  // prefix[lo] <= u < prefix[hi]
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -113,7 +138,7 @@ __device__ __forceinline__ Unit decode_unit(const MxParams& p, const int* prefix
   U.s = lo;
   const int r = u - prefix[lo];
   const int m = srows[lo];
-  const int nch = (m + BN - 1) / BN;
+  const int nch = (m + CH - 1) / CH;
   U.q = r % p.ksplit;
   const int rest = r / p.ksplit;
   U.c = rest % nch;
@@ -121,52 +146,99 @@ __device__ __forceinline__ Unit decode_unit(const MxParams& p, const int* prefix
   const int base = m / nch, extra = m - base * nch;  // near-equal chunks
   U.nvalid = base + (U.c < extra ? 1 : 0);
   U.rowB = sbase[lo] + U.c * base + min(U.c, extra);
+  U.most = U.nvalid;
+  if constexpr (PAIR) {  // rank 0 takes the first half of the rows (rounded up)
+    const int n0 = (U.nvalid + 1) >> 1;
+    U.most = n0;
+    if (rank) {
+      U.rowB += n0;
+      U.nvalid -= n0;
+    } else {
+      U.nvalid = n0;
+    }
+  }
   U.rowA0 = lo * p.NA + U.j * p.pair_stride;
   U.rowA1 = U.rowA0 + p.a1_off;
-  U.a1 = p.mode == MODE_SWIGLU || U.j * p.pair_stride + p.a1_off < p.NA;
+  U.a1 = PAIR || p.mode == MODE_SWIGLU || U.j * p.pair_stride + p.a1_off < p.NA;
   U.kb0 = U.q * p.kb_per_split;
   U.kb1 = min(p.kb_total, U.kb0 + p.kb_per_split);
   return U;
 }
 
-// Shared-memory descriptor of a scale block: 32 rows of 16 bytes, no swizzle, 8-row groups 128
-// bytes apart.
-__device__ __forceinline__ uint64_t sf_desc(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)(128 >> 4) << 32;  // stride byte offset
-  d |= (uint64_t)1 << 46;           // descriptor version of the tcgen05 family
-  return d;
-}
-
-// One scale block to four columns of tensor memory, repeated in its four lane quarters.
-__device__ __forceinline__ void sf_copy(uint32_t taddr, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
-}
-
-// D[tmem] (+)= (A sfa) (B sfb)^T over K = 64 codes, issued by one thread.
+// D[tmem] (+)= (A sfa) (B sfb)^T over K = 64 codes, issued by one thread.  PAIR: by the leader for both
+// CTAs; D, sfa and sfb are at the same addresses of both tensor memories.
+template <bool PAIR>
 __device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
                                          uint32_t sfb, uint32_t accumulate) {
-  asm volatile(
-      "{\n"
-      "  .reg .pred p;\n"
-      "  setp.ne.b32 p, %6, 0;\n"
-      "  tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n"
-      "}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-      : "memory");
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n"
+        "  .reg .pred p;\n"
+        "  setp.ne.b32 p, %6, 0;\n"
+        "  tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n"
+        "}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n"
+        "  .reg .pred p;\n"
+        "  setp.ne.b32 p, %6, 0;\n"
+        "  tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n"
+        "}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
 }
 
-// Instruction descriptor of kind::mxf4: E2M1 x E2M1 with UE8M0 scales, K-major, M = 128; the
-// scale factor id (0 or 2) picks the two bytes of a scale word that a K = 64 step uses.
-__device__ __forceinline__ uint32_t mx_idesc(int N, uint32_t sf_id) {
-  return (sf_id << 4)                   // B scale factor id
-         | (1u << 7)                    // A: E2M1
-         | (1u << 10)                   // B: E2M1
-         | ((uint32_t)(N >> 3) << 17)   // N / 8
-         | (1u << 23)                   // scales: UE8M0
-         | ((uint32_t)(BM >> 4) << 24)  // M / 16
-         | (sf_id << 29);               // A scale factor id
+// Instruction descriptor of kind::mxf4: E2M1 x E2M1 with UE8M0 scales, K-major; the scale factor
+// id (0 or 2) picks the two bytes of a scale word that a K = 64 step uses.
+__device__ __forceinline__ uint32_t mx_idesc(int M, int N, uint32_t sf_id) {
+  return (sf_id << 4)                  // B scale factor id
+         | (1u << 7)                   // A: E2M1
+         | (1u << 10)                  // B: E2M1
+         | ((uint32_t)(N >> 3) << 17)  // N / 8
+         | (1u << 23)                  // scales: UE8M0
+         | ((uint32_t)(M >> 4) << 24)  // M / 16
+         | (sf_id << 29);              // A scale factor id
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void cp_async4_at(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// N (32 or 64) columns of this thread's lane of tensor memory, not waited for.
+template <int N>
+__device__ __forceinline__ void tmem_load(uint32_t taddr, float (&v)[N]) {
+#pragma unroll
+  for (int o = 0; o < N; o += 32)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+                 : "=f"(v[o + 0]), "=f"(v[o + 1]), "=f"(v[o + 2]), "=f"(v[o + 3]), "=f"(v[o + 4]), "=f"(v[o + 5]), "=f"(v[o + 6]), "=f"(v[o + 7]), "=f"(v[o + 8]), "=f"(v[o + 9]), "=f"(v[o + 10]), "=f"(v[o + 11]), "=f"(v[o + 12]), "=f"(v[o + 13]), "=f"(v[o + 14]), "=f"(v[o + 15]),
+                   "=f"(v[o + 16]), "=f"(v[o + 17]), "=f"(v[o + 18]), "=f"(v[o + 19]), "=f"(v[o + 20]), "=f"(v[o + 21]), "=f"(v[o + 22]), "=f"(v[o + 23]), "=f"(v[o + 24]), "=f"(v[o + 25]), "=f"(v[o + 26]), "=f"(v[o + 27]), "=f"(v[o + 28]), "=f"(v[o + 29]), "=f"(v[o + 30]), "=f"(v[o + 31])
+                 : "r"(taddr + (uint32_t)o)
+                 : "memory");
+}
+
+// Wait for this thread's loads; v is what one of them wrote.
+template <int N>
+__device__ __forceinline__ void tmem_loaded(float (&v)[N]) {
+#pragma unroll
+  for (int o = 0; o < N; o += 32)
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[o + 0]), "+f"(v[o + 1]), "+f"(v[o + 2]), "+f"(v[o + 3]), "+f"(v[o + 4]), "+f"(v[o + 5]), "+f"(v[o + 6]), "+f"(v[o + 7]), "+f"(v[o + 8]), "+f"(v[o + 9]), "+f"(v[o + 10]), "+f"(v[o + 11]), "+f"(v[o + 12]), "+f"(v[o + 13]), "+f"(v[o + 14]), "+f"(v[o + 15]),
+                   "+f"(v[o + 16]), "+f"(v[o + 17]), "+f"(v[o + 18]), "+f"(v[o + 19]), "+f"(v[o + 20]), "+f"(v[o + 21]), "+f"(v[o + 22]), "+f"(v[o + 23]), "+f"(v[o + 24]), "+f"(v[o + 25]), "+f"(v[o + 26]), "+f"(v[o + 27]), "+f"(v[o + 28]), "+f"(v[o + 29]), "+f"(v[o + 30]), "+f"(v[o + 31])
+                 :
+                 : "memory");
+}
+
+// Four columns of this warp's 32 lanes of tensor memory.
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(a), "r"(b), "r"(c),
+               "r"(d)
+               : "memory");
 }
 
 __device__ __forceinline__ uint32_t bf16x2(float a, float b) {
@@ -186,29 +258,37 @@ __device__ __forceinline__ void store_row(uint8_t* dst, bool wide, F w) {
   }
 }
 
-template <int MODE>
+template <int MODE, int TW, bool PAIR>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
-    grouped_gemm_mx_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB16,
-                           const __grid_constant__ CUtensorMap tmB32, const __grid_constant__ CUtensorMap tmB64,
-                           const __grid_constant__ CUtensorMap tmB128, const MxParams p) {
+    grouped_gemm_mx_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ TokenMaps tmB,
+                           const MxParams p) {
+  using L = Tile<TW, PAIR>;
+  constexpr int TC = TW / 2;  // columns of each tile that an epilogue thread holds
+  constexpr int CH = PAIR ? 2 * BN : BN;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  uint8_t* sf = smem + p.sf_off;                           // [SF_RING][GROUP][SF_STAGE_BYTES]
+  uint8_t* sf = smem + p.sf_off;                           // [SF_BUFS][1 + NB blocks][128 rows][16]
   int* prefix = reinterpret_cast<int*>(smem + p.pre_off);  // [nslots + 1] unit prefix
   int* srows = prefix + p.nslots + 1;                      // [nslots] valid rows per slot
   int* sbase = srows + p.nslots;                           // [nslots] first grouped-buffer row per slot
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + p.bar_off);
   uint64_t* empty = full + p.stages;
-  uint64_t* sfull = empty + p.stages;    // [SF_RING] a group's scales stored
-  uint64_t* sempty = sfull + SF_RING;    // [SF_RING] copied to tensor memory
+  uint64_t* sfull = empty + p.stages;    // [SF_RING] a group's scales are in tensor memory
+  uint64_t* sempty = sfull + SF_RING;    // [SF_RING] and no longer needed
   uint64_t* tfull = sempty + SF_RING;    // accumulators written
   uint64_t* tempty = tfull + 1;          // accumulators read
   uint64_t* drain = tempty + 1;
+  uint64_t* fin = drain + 1;             // pairs: the peer CTA is done with this CTA's memory
   uint32_t* tmem_base_smem = reinterpret_cast<uint32_t*>(smem + p.misc_off);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + p.misc_off + 4);
 
   const int tid = threadIdx.x;
   const int warp = tid >> 5, lane = tid & 31;
+  // pairs: rank 0 (the leader) issues the MMAs; units are dealt per cluster
+  const uint32_t crank = PAIR ? cluster_ctarank() : 0u;
+  const bool leader = crank == 0;
+  const int unit0 = PAIR ? (int)cluster_id_x() : (int)blockIdx.x;
+  const int ustride = PAIR ? (int)nclusters_x() : (int)gridDim.x;
 
   if (tid == 0) {
     for (int i = 0; i < p.stages; ++i) {
@@ -216,18 +296,19 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < SF_RING; ++i) {
-      mbar_init(&sfull[i], LOAD_THREADS);
+      mbar_init(&sfull[i], PAIR ? 2 * SF_WARPS : SF_WARPS);
       mbar_init(&sempty[i], 1);
     }
     mbar_init(tfull, 1);
-    mbar_init(tempty, EPI_WARPS);
+    mbar_init(tempty, PAIR ? 2 * EPI_WARPS : EPI_WARPS);
     mbar_init(drain, 1);
+    mbar_init(fin, 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
-    tmem_alloc(tmem_base_smem, TMEM_COLS);
-    tmem_relinquish();
+    tmem_alloc<PAIR>(tmem_base_smem, TMEM_COLS);
+    tmem_relinquish<PAIR>();
   }
   for (int s = tid; s < p.nslots; s += NUM_THREADS) {
     int m = __ldg(p.masked_m + s);
@@ -235,7 +316,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     m = max(m, 0);
     srows[s] = m;
     sbase[s] = p.masked ? s * p.M_max : __ldg(p.offsets + s);
-    prefix[s + 1] = (m + BN - 1) / BN * p.pairs * p.ksplit;
+    prefix[s + 1] = (m + CH - 1) / CH * p.pairs * p.ksplit;
   }
   if (tid == 0) prefix[0] = 0;
   tc_fence_before_sync();
@@ -255,51 +336,55 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
   }
   __syncthreads();
+  // both CTAs' barriers are initialised before either CTA touches the other's
+  if constexpr (PAIR) cluster_sync_all();
   tc_fence_after_sync();
   const uint32_t tmem_base = *tmem_base_smem;
   const int total = prefix[p.nslots];
+  auto unit = [&](int u) { return decode_unit<PAIR>(p, prefix, srows, sbase, u, crank); };
 
-  if (warp < EPI_WARP0) {
+  if (warp < SF_WARP0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_CTRL));
     if (warp == 0) {
       // ------------------------------------------------------------ producer
       if (lane == 0) {
         tma_prefetch_map(&tmA);
-        tma_prefetch_map(&tmB16);
-        tma_prefetch_map(&tmB32);
-        tma_prefetch_map(&tmB64);
-        tma_prefetch_map(&tmB128);
+        for (int i = 0; i < NUM_BOXES; ++i) tma_prefetch_map(&tmB.box[i]);
         const uint64_t pol = policy_evict_first();
         int stage = 0;
         uint32_t phase = 0;
         long issued = 0;
         bool ok = true;
-        for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
-          const Unit U = decode_unit(p, prefix, srows, sbase, u);
-          const CUtensorMap* mb = &tmB128;
-          int box = 128;
-          if (U.nvalid <= 16) {
-            mb = &tmB16;
-            box = 16;
-          } else if (U.nvalid <= 32) {
-            mb = &tmB32;
-            box = 32;
-          } else if (U.nvalid <= 64) {
-            mb = &tmB64;
-            box = 64;
-          }
-          const uint32_t bytes = (U.a1 ? 2u : 1u) * TILE_BYTES + (uint32_t)box * ROW_BYTES;
+        for (int u = unit0; ok && u < total; u += ustride) {
+          const Unit U = unit(u);
+          const int bi = box_of(U.most);
+          const CUtensorMap* mb = &tmB.box[bi];
+          const uint32_t tok = (uint32_t)box_rows(bi) * ROW_BYTES;
+          // pairs: the leader's stage barrier counts both CTAs' copies
+          const uint32_t bytes = PAIR ? 2u * (L::W_BYTES + tok) : (U.a1 ? 2u : 1u) * L::W_BYTES + tok;
           for (int kb = U.kb0; kb < U.kb1; ++kb) {
             if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, TIMEOUT)) {
               ok = false;
               break;
             }
-            uint8_t* st = smem + (size_t)stage * STAGE_BYTES;
+            uint8_t* st = smem + (size_t)stage * L::STAGE;
             const int x = kb * ROW_BYTES;
-            mbar_arrive_expect_tx(&full[stage], bytes);
-            tma_load_2d_hint(st, &tmA, &full[stage], x, U.rowA0, pol);
-            if (U.a1) tma_load_2d_hint(st + TILE_BYTES, &tmA, &full[stage], x, U.rowA1, pol);
-            tma_load_2d(st + 2 * TILE_BYTES, mb, &full[stage], x, U.rowB);
+            if constexpr (PAIR) {
+              if (leader) {
+                mbar_arrive_expect_tx(&full[stage], bytes);
+                tma_load_2d_hint(st, &tmA, &full[stage], x, U.rowA0, pol);
+                tma_load_2d(st + L::W_STAGED, mb, &full[stage], x, U.rowB);
+              } else {
+                const uint32_t lbar = mapa_shared(&full[stage], 0);
+                tma_load_2d_pair_hint(st, &tmA, lbar, x, U.rowA1, pol);
+                tma_load_2d_pair(st + L::W_STAGED, mb, lbar, x, U.rowB);
+              }
+            } else {
+              mbar_arrive_expect_tx(&full[stage], bytes);
+              tma_load_2d_hint(st, &tmA, &full[stage], x, U.rowA0, pol);
+              if (U.a1) tma_load_2d_hint(st + L::W_BYTES, &tmA, &full[stage], x, U.rowA1, pol);
+              tma_load_2d(st + L::W_STAGED, mb, &full[stage], x, U.rowB);
+            }
             ++issued;
             if (++stage == p.stages) {
               stage = 0;
@@ -307,7 +392,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             }
           }
         }
-        if (!ok) {
+        if (!ok && PAIR && !leader) {
+          // the peer's copies count on the leader's barriers: give those in flight time to land
+          const uint64_t t0 = global_timer_ns();
+          while (global_timer_ns() - t0 < 200000u) {
+          }
+        } else if (!ok) {
           // let the copies already in flight land before the CTA's shared memory is released
           const long first = issued > p.stages ? issued - p.stages : 0;
           for (long i = first; i < issued; ++i) {
@@ -320,65 +410,74 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
       }
     } else if (warp == 1) {
-      // ------------------------------------------------------------ scale copies and MMAs
+      // ------------------------------------------------------------ MMAs
       if (lane == 0) {
+        auto commit = [&](uint64_t* bar) {
+          if constexpr (PAIR)
+            tc_commit_pair(bar, 3);  // both CTAs' barriers
+          else
+            tc_commit(bar);
+        };
         int stage = 0;
-        uint32_t phase = 0, g_it = 0, u_it = 0;
+        uint32_t phase = 0, g = 0, gphase = 0, u_it = 0;
         bool ok = true, any = false;
         int units = 0, tiles = 0;
-        for (int u = blockIdx.x; ok && u < total; u += gridDim.x, ++u_it) {
-          const Unit U = decode_unit(p, prefix, srows, sbase, u);
+        for (int u = unit0; ok && leader && u < total; u += ustride, ++u_it) {
+          const Unit U = unit(u);
           ++units;
           tiles += (U.j == 0 && U.q == 0);  // one unit per (slot, token chunk)
-          const int N = U.a1 ? 2 * BM : BM;
-          const uint32_t id0 = mx_idesc(N, 0), id2 = mx_idesc(N, 2);
-          if (!mbar_wait(tempty, (u_it & 1u) ^ 1u, abort_flag, TIMEOUT)) {
+          const int M = PAIR ? 2 * BN : BN, N = U.a1 ? 2 * TW : TW;
+          const uint32_t id0 = mx_idesc(M, N, 0), id2 = mx_idesc(M, N, 2);
+          if (!mbar_wait<PAIR>(tempty, (u_it & 1u) ^ 1u, abort_flag, TIMEOUT)) {
             ok = false;
             break;
           }
           tc_fence_after_sync();
-          uint32_t g = 0;
+          uint32_t scol = 0;
+          bool second = false;  // stage of the group
           for (int kb = U.kb0; kb < U.kb1; ++kb) {
-            const int in_group = (kb - U.kb0) % GROUP;
-            if (in_group == 0) {
-              g = g_it % SF_RING;
-              if (!mbar_wait(&sfull[g], (g_it / SF_RING) & 1u, abort_flag, TIMEOUT)) {
+            if (!second) {
+              if (!mbar_wait<PAIR>(&sfull[g], gphase, abort_flag, TIMEOUT)) {
                 ok = false;
                 break;
               }
+              scol = tmem_base + SF_COL0 + g * L::SF_COLS;
             }
-            if (!mbar_wait(&full[stage], phase, abort_flag, TIMEOUT)) {
+            if (!mbar_wait<PAIR>(&full[stage], phase, abort_flag, TIMEOUT)) {
               ok = false;
               break;
             }
             tc_fence_after_sync();
-            const int nk = min(4, (p.K - kb * KB) / 64);  // K = 64 steps of this stage: 4, or 2 at the end
-            const uint32_t st = smem_u32(smem + (size_t)stage * STAGE_BYTES);
-            const uint32_t ss = smem_u32(sf + (size_t)(g * GROUP + in_group) * SF_STAGE_BYTES);
-            const uint32_t ta = tmem_base + SF_COL0 + (uint32_t)stage * SF_COLS, tb = ta + 8;
-            const uint64_t dtok = smem_desc_sw128(st + 2 * TILE_BYTES), dw = smem_desc_sw128(st);
+            const uint32_t st = smem_u32(smem + (size_t)stage * L::STAGE);
+            const uint64_t dw = smem_desc_sw128(st), dtok = smem_desc_sw128(st + L::W_STAGED);
+            const uint32_t jb = second ? 2u : 0u;
+            const bool both = p.K - kb * KB > KB / 2;  // a last stage may be half a stage
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              if (2 * j < nk) {
-                sf_copy(ta + 4 * j, sf_desc(ss + j * SF_BLOCK));
-                sf_copy(tb + 8 * j, sf_desc(ss + SF_STAGE_TOK + (2 * j) * SF_BLOCK));
-                if (U.a1) sf_copy(tb + 8 * j + 4, sf_desc(ss + SF_STAGE_TOK + (2 * j + 1) * SF_BLOCK));
-                mma_mxf4(tmem_base, dtok + 4 * j, dw + 4 * j, id0, ta + 4 * j, tb + 8 * j, kb > U.kb0 || j > 0);
-                mma_mxf4(tmem_base, dtok + 4 * j + 2, dw + 4 * j + 2, id2, ta + 4 * j, tb + 8 * j, 1u);
+            for (uint32_t j = 0; j < 2; ++j) {
+              if (j == 0 || both) {
+                const uint32_t sfb = scol + (jb + j) * 4 * L::NB, sfa = scol + 16 * L::NB + (jb + j) * 4;
+                mma_mxf4<PAIR>(tmem_base, dtok + 4 * j, dw + 4 * j, id0, sfa, sfb, kb > U.kb0 || j > 0);
+                mma_mxf4<PAIR>(tmem_base, dtok + 4 * j + 2, dw + 4 * j + 2, id2, sfa, sfb, 1u);
               }
             }
             any = true;
-            tc_commit(&empty[stage]);
-            if (in_group == GROUP - 1 || kb == U.kb1 - 1) {
-              tc_commit(&sempty[g]);
-              ++g_it;
+            commit(&empty[stage]);
+            if (second || kb == U.kb1 - 1) {
+              commit(&sempty[g]);
+              if (++g == SF_RING) {
+                g = 0;
+                gphase ^= 1u;
+              }
+              second = false;
+            } else {
+              second = true;
             }
             if (++stage == p.stages) {
               stage = 0;
               phase ^= 1u;
             }
           }
-          if (ok) tc_commit(tfull);
+          if (ok) commit(tfull);
         }
         if (p.stats) {
           for (int h = 0; h < 2; ++h) {
@@ -395,71 +494,126 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
         if (!ok && any) {
           // all MMAs issued by this thread must finish before tensor memory is freed
-          tc_commit(drain);
+          if constexpr (PAIR)
+            tc_commit_pair(drain, 1);
+          else
+            tc_commit(drain);
           const long long t0 = clock64();
           while (!mbar_try_wait(drain, 0) && clock64() - t0 < TIMEOUT) {
           }
         }
       }
-    } else {
-      // ------------------------------------------------------------ scale loaders
-      const int lt = tid - LOAD_WARP0 * 32;
-      const int words = p.K / 128;             // words of a scale row
-      const size_t row_bytes = (size_t)p.K / 32;
-      // the 16 scale bytes of the codes from word w0 on (zeros past the row's end)
-      auto fetch = [&](const uint8_t* row, int w0, bool vec) -> uint4 {
-        if (vec) return __ldg(reinterpret_cast<const uint4*>(row) + (w0 >> 2));
-        const uint32_t* w = reinterpret_cast<const uint32_t*>(row);
-        return make_uint4(w0 < words ? __ldg(w + w0) : 0u, w0 + 1 < words ? __ldg(w + w0 + 1) : 0u,
-                          w0 + 2 < words ? __ldg(w + w0 + 2) : 0u, w0 + 3 < words ? __ldg(w + w0 + 3) : 0u);
-      };
-      uint32_t g_it = 0;
-      bool ok = true;
-      for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
-        const Unit U = decode_unit(p, prefix, srows, sbase, u);
-        const uint8_t* rw0 = p.w_scales + (size_t)U.rowA0 * row_bytes;
-        const uint8_t* rw1 = p.w_scales + (size_t)U.rowA1 * row_bytes;
-        const uint8_t* rt = p.act_scales + (size_t)U.rowB * row_bytes;
-        for (int kb = U.kb0; ok && kb < U.kb1; kb += GROUP, ++g_it) {
-          const int w0 = kb * 2;
-          uint4 vw[4], vt[2];
+    }
+  } else if (warp < EPI_WARP0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_SF));
+    // ------------------------------------------------------------ scales
+    // These warps run a short serial chain per group and bound the kernel when it is long: addresses
+    // are per unit, the warps meet at a hardware barrier, and a group's stores to tensor memory
+    // are waited for in the next turn.
+    const int lt = tid - SF_WARP0 * 32;  // this thread's row of each 128-row block
+    const uint32_t words = (uint32_t)p.K / 128;  // words of a scale row
+    const size_t row_bytes = (size_t)p.K / 32;
+    const uint32_t t_lane = tmem_base + ((uint32_t)((warp & 3) * 32) << 16) + SF_COL0;
+    // The groups of all units in order, requested SF_BUFS - 1 groups ahead.  Rows past the chunk, a
+    // missing second tile and codes past K keep what shared memory holds: no MMA result that is
+    // used depends on them.
+    int u = unit0, left = 0;  // the next group to request: its unit and the unit's groups that are left
+    const uint8_t *pt = nullptr, *pw[L::NB];
+    uint32_t w0 = 0;  // its first word of a scale row
+    int requested = 0;
+    auto next_unit = [&]() {
+      if (u >= total) return;
+      const Unit U = unit(u);
+      left = (U.kb1 - U.kb0 + GROUP - 1) / GROUP;
+      w0 = (uint32_t)U.kb0 * 2;
+      pt = lt < U.nvalid ? p.act_scales + (size_t)(U.rowB + lt) * row_bytes + 4 * w0 : nullptr;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {  // rows lt, lt + 64 of tile 0, then of tile 1
-            const int r = lt + 64 * (i & 1);
-            vw[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (i < 2 || U.a1) vw[i] = fetch((i < 2 ? rw0 : rw1) + (size_t)r * row_bytes, w0, p.vec_w);
-          }
+      for (int i = 0; i < L::NB; ++i) {
+        const int r = 128 * i + lt;
+        const int row = r >= TW ? U.rowA1 + r - TW : U.rowA0 + r;
+        pw[i] = r < TW || U.a1 ? p.w_scales + (size_t)row * row_bytes + 4 * w0 : nullptr;
+      }
+    };
+    // The 16 scale bytes of a row's codes from word w0 on, those that exist.
+    auto fetch = [&](uint32_t dst, const uint8_t* src, bool vec) {
+      if (vec) {
+        cp_async16(dst, src);
+      } else {
+        for (uint32_t i = 0; i < 4 && w0 + i < words; ++i) cp_async4_at(dst + 4 * i, src + 4 * i);
+      }
+    };
+    const uint32_t sf0 = smem_u32(sf) + (uint32_t)lt * 16;
+    auto request = [&](uint32_t buf) {
+      if (u < total) {
+        const uint32_t dst = sf0 + buf * L::SF_BUF;
+        if (pt) {
+          fetch(dst, pt, p.vec_tok);
+          pt += 16;
+        }
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int r = lt + 64 * i;
-            vt[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (r < U.nvalid) vt[i] = fetch(rt + (size_t)r * row_bytes, w0, p.vec_tok);
+        for (int i = 0; i < L::NB; ++i) {
+          if (pw[i]) {
+            fetch(dst + 2048u * (1 + i), pw[i], p.vec_w);
+            pw[i] += 16;
           }
-          const uint32_t g = g_it % SF_RING;
-          if (!mbar_wait(&sempty[g], ((g_it / SF_RING) & 1u) ^ 1u, abort_flag, TIMEOUT)) {
-            ok = false;
-            break;
-          }
-          uint8_t* dst = sf + (size_t)g * GROUP * SF_STAGE_BYTES;
-          // word w of a row: stage w / 2 of the group, K block w % 2 of the stage
-          auto put = [&](int block0, int block_step, int r, const uint4& v) {
-            uint8_t* d = dst + block0 * SF_BLOCK + (r & 31) * 16 + (r >> 5) * 4;
-            *reinterpret_cast<uint32_t*>(d) = v.x;
-            *reinterpret_cast<uint32_t*>(d + block_step * SF_BLOCK) = v.y;
-            *reinterpret_cast<uint32_t*>(d + SF_STAGE_BYTES) = v.z;
-            *reinterpret_cast<uint32_t*>(d + SF_STAGE_BYTES + block_step * SF_BLOCK) = v.w;
-          };
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            put(0, 1, lt + 64 * i, vt[i]);
-            put(2, 2, lt + 64 * i, vw[i]);
-            put(3, 2, lt + 64 * i, vw[2 + i]);
-          }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before tcgen05.cp reads them
-          mbar_arrive(&sfull[g]);
+        }
+        ++requested;
+        w0 += 4;
+        if (--left == 0) {
+          u += ustride;
+          next_unit();
         }
       }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    next_unit();
+    for (uint32_t i = 0; i < SF_BUFS - 1; ++i) request(i);
+    auto release = [&](uint32_t g) {  // the stores of group g's turn are done: tell the MMA thread
+      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        if (PAIR)
+          mbar_arrive_remote(mapa_shared(&sfull[g], 0));  // the leader's waits for both CTAs
+        else
+          mbar_arrive(&sfull[g]);
+      }
+    };
+    uint32_t buf = 0, g = 0, gphase = 1;
+    bool ok = true;
+    for (int turn = 0; turn < requested; ++turn) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(SF_BUFS - 2) : "memory");  // this turn's group is here
+      // The four warps' rows of the group, and the end of their reads of the buffer before it.  Every
+      // warp takes every turn, after a wait that gave up too, so this barrier always completes.
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      const uint4* src = reinterpret_cast<const uint4*>(sf + buf * L::SF_BUF) + lane;
+      request(buf == 0 ? SF_BUFS - 1 : buf - 1);
+      if (++buf == SF_BUFS) buf = 0;
+      if (!ok) continue;
+      if (turn > 0) release(g == 0 ? SF_RING - 1 : g - 1);
+      // the whole warp goes on or gives up: its stores to tensor memory are warp-wide
+      ok = __all_sync(0xffffffffu, mbar_wait<PAIR>(&sempty[g], gphase, abort_flag, TIMEOUT));
+      if (!ok) continue;
+      tc_fence_after_sync();
+      const uint32_t col = t_lane + g * L::SF_COLS;
+#pragma unroll
+      for (int b = 0; b <= L::NB; ++b) {  // tokens, then the weights' blocks
+        uint4 v[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] = src[128 * b + 32 * q];
+        const uint32_t c0 = b == 0 ? col + 16 * L::NB : col + 4 * (b - 1), step = b == 0 ? 4 : 4 * L::NB;
+        tmem_st4(c0, v[0].x, v[1].x, v[2].x, v[3].x);
+        tmem_st4(c0 + step, v[0].y, v[1].y, v[2].y, v[3].y);
+        tmem_st4(c0 + 2 * step, v[0].z, v[1].z, v[2].z, v[3].z);
+        tmem_st4(c0 + 3 * step, v[0].w, v[1].w, v[2].w, v[3].w);
+      }
+      if (++g == SF_RING) {
+        g = 0;
+        gphase ^= 1u;
+      }
     }
+    if (ok && requested > 0) release(g == 0 ? SF_RING - 1 : g - 1);
+    cp_async_wait_all();  // no copy may land after the CTA has exited
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_EPI));
     // ------------------------------------------------------------ epilogue
@@ -467,40 +621,38 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const int half = (warp - EPI_WARP0) >> 2;  // column half of each tile
     const int lrow = quarter * 32 + lane;      // token row of this thread
     const uint32_t t_lane = tmem_base + ((uint32_t)(quarter * 32) << 16);
-    const int c_lo = half * 64;
+    const int c_lo = half * TC;
     const size_t oc = (size_t)p.out_cols;
     uint32_t u_it = 0;
-    for (int u = blockIdx.x; u < total; u += gridDim.x, ++u_it) {
-      const Unit U = decode_unit(p, prefix, srows, sbase, u);
+    for (int u = unit0; u < total; u += ustride, ++u_it) {
+      const Unit U = unit(u);
       // the whole warp goes on together (its tensor-memory loads are warp-wide) or gives up together
-      if (!__all_sync(0xffffffffu, mbar_wait(tfull, u_it & 1u, abort_flag, TIMEOUT))) break;
+      if (!__all_sync(0xffffffffu, mbar_wait<PAIR>(tfull, u_it & 1u, abort_flag, TIMEOUT))) break;
       tc_fence_after_sync();
-      float acc0[64], acc1[64];
+      float acc0[TC], acc1[TC];
       const bool warp_live = quarter * 32 < U.nvalid;
-      if (warp_live) {
-#pragma unroll
-        for (int pr = 0; pr < 2; ++pr) {
-          float v0[32], v1[32];
-          const uint32_t col = (uint32_t)(c_lo + pr * 32);
-          tmem_ld32x2(t_lane + col, t_lane + col + 128u, v0, v1);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            acc0[pr * 32 + i] = v0[i];
-            acc1[pr * 32 + i] = v1[i];
-          }
-        }
+      if (warp_live) {  // all loads before the wait
+        tmem_load<TC>(t_lane + (uint32_t)c_lo, acc0);
+        tmem_load<TC>(t_lane + (uint32_t)(c_lo + TW), acc1);
+        tmem_loaded<TC>(acc0);
+        tmem_loaded<TC>(acc1);
       }
       tc_fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(tempty);
+      if (lane == 0) {
+        if (PAIR)
+          mbar_arrive_remote(mapa_shared(tempty, 0));
+        else
+          mbar_arrive(tempty);
+      }
       if (lrow >= U.nvalid) continue;  // rows past the chunk: nothing to store
       const size_t row = (size_t)(U.rowB + lrow);
       if constexpr (MODE == MODE_SWIGLU) {
 #pragma unroll
-        for (int i = 0; i < 64; ++i) acc0[i] = silu(acc0[i]) * acc1[i];
-        uint32_t code[16], sb[2];
+        for (int i = 0; i < TC; ++i) acc0[i] = silu(acc0[i]) * acc1[i];
+        uint32_t code[TC / 8], sb[TC / 32];
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < TC / 32; ++b) {
           float amax = 0.0f;
 #pragma unroll
           for (int i = 0; i < 32; ++i) amax = mx_amax(amax, acc0[32 * b + i]);
@@ -509,12 +661,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i) code[4 * b + i] = mx_codes8(acc0 + 32 * b + 8 * i, inv);
         }
-        const size_t col = (size_t)U.j * BM + c_lo;
+        const size_t col = (size_t)U.j * TW + c_lo;
         uint8_t* dst = static_cast<uint8_t*>(p.out) + row * (oc / 2) + col / 2;
-        store_row<1>(dst, (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0, [&](int i) {
-          return make_uint4(code[4 * i], code[4 * i + 1], code[4 * i + 2], code[4 * i + 3]);
-        });
-        *reinterpret_cast<uint16_t*>(p.out_scales + row * (oc / 32) + col / 32) = (uint16_t)(sb[0] | (sb[1] << 8));
+        uint8_t* ds = p.out_scales + row * (oc / 32) + col / 32;
+        if constexpr (TC == 64) {
+          store_row<1>(dst, (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0, [&](int i) {
+            return make_uint4(code[4 * i], code[4 * i + 1], code[4 * i + 2], code[4 * i + 3]);
+          });
+          *reinterpret_cast<uint16_t*>(ds) = (uint16_t)(sb[0] | (sb[1] << 8));
+        } else {
+          *reinterpret_cast<uint4*>(dst) = make_uint4(code[0], code[1], code[2], code[3]);
+          *ds = (uint8_t)sb[0];
+        }
       } else {
         const size_t col = (size_t)U.j * p.pair_stride + c_lo;
         if (p.ksplit > 1) {
@@ -526,8 +684,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                                 __float_as_uint(a[4 * i + 3]));
             };
           };
-          store_row<8>(reinterpret_cast<uint8_t*>(d), wide, f4(acc0));
-          if (U.a1) store_row<8>(reinterpret_cast<uint8_t*>(d + BM), wide, f4(acc1));
+          store_row<TC / 8>(reinterpret_cast<uint8_t*>(d), wide, f4(acc0));
+          if (U.a1) store_row<TC / 8>(reinterpret_cast<uint8_t*>(d + TW), wide, f4(acc1));
         } else {
           __nv_bfloat16* d = static_cast<__nv_bfloat16*>(p.out) + row * oc + col;
           const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
@@ -537,8 +695,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                                 bf16x2(a[8 * i + 4], a[8 * i + 5]), bf16x2(a[8 * i + 6], a[8 * i + 7]));
             };
           };
-          store_row<4>(reinterpret_cast<uint8_t*>(d), wide, h8(acc0));
-          if (U.a1) store_row<4>(reinterpret_cast<uint8_t*>(d + BM), wide, h8(acc1));
+          store_row<TC / 16>(reinterpret_cast<uint8_t*>(d), wide, h8(acc0));
+          if (U.a1) store_row<TC / 16>(reinterpret_cast<uint8_t*>(d + TW), wide, h8(acc1));
         }
       }
     }
@@ -546,9 +704,26 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
   tc_fence_before_sync();
   __syncthreads();
+  if constexpr (PAIR) {
+    // Neither CTA frees its tensor memory or leaves while the other may still use it: the leader's
+    // MMAs read the peer's shared memory and write its tensor memory, the peer's copies and
+    // arrivals land on the leader's barriers.  Each tells the other that it is done and waits,
+    // bounded, for the other's word.
+    if (tid == 0) {
+      mbar_arrive_remote(mapa_shared(fin, crank ^ 1u));
+      const long long t0 = clock64();
+      while (!mbar_try_wait<true>(fin, 0)) {
+        if (clock64() - t0 > TIMEOUT) {
+          *abort_flag = 1;
+          break;
+        }
+      }
+    }
+    __syncthreads();
+  }
   if (warp == 1) {
     tc_fence_after_sync();
-    tmem_dealloc(tmem_base, TMEM_COLS);
+    tmem_dealloc<PAIR>(tmem_base, TMEM_COLS);
   }
   if (tid == 0 && *abort_flag) atomicOr(p.err, MOE_FLAG_TIMEOUT);
 }
@@ -557,39 +732,65 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 // Host side
 // ---------------------------------------------------------------------------
 
+// SM pairs for slots of prefill size: 128 rows or more on average.  The down product needs whole
+// pairs of weight tiles (H a multiple of 256).
+bool use_pairs(const moe_problem& p, int mode) {
+  return (double)p.T * p.K / std::max(1, p.P) >= 128.0 && (mode == MODE_SWIGLU || p.H % 256 == 0);
+}
+
 struct Plan {
-  int kb_total, kb_per_split, ksplit, pairs, stages;
+  bool pair;
+  int tw, kb_total, kb_per_split, ksplit, pairs, stages;
   size_t smem, part_bytes;
   uint32_t sf_off, pre_off, bar_off, misc_off;
 };
+
+// Share of the SMs' time that `units` equal units fill.
+double wave_fill(double units, int sm_count) {
+  const double waves = units / sm_count;
+  return waves > 0 ? waves / std::ceil(waves) : 1.0;
+}
 
 Plan make_plan(const moe_problem& p, int mode, int sm_count, int smem_cap) {
   Plan pl{};
   const int K = (mode == MODE_SWIGLU) ? p.H : p.I;
   const int nslots = p.P + p.has_shared;
+  const size_t out_cols = (mode == MODE_SWIGLU) ? p.I : p.H;
   pl.kb_total = (K + KB - 1) / KB;
-  pl.pairs = (mode == MODE_SWIGLU) ? p.I / BM : (p.H + 2 * BM - 1) / (2 * BM);
-  // upper bound of the token chunks over all slots
+  pl.pair = use_pairs(p, mode);
+  const int ch = pl.pair ? 2 * BN : BN;  // token rows of one chunk at most
+  const int workers = pl.pair ? sm_count / 2 : sm_count;
+  // upper bound of the token chunks over all slots: a slot with rows has at least one of the
+  // records, whose number bounds the chunks of a small batch
+  const long records = (long)p.T * p.K + (long)p.has_shared * ((p.T + ch - 1) / ch);
   long chunks;
   if (p.layout == MOE_LAYOUT_MASKED) {
-    chunks = (long)nslots * ((p.M_max + BN - 1) / BN);
+    chunks = (long)nslots * ((p.M_max + ch - 1) / ch);
   } else {
     const long rows = (long)p.T * p.K + (long)p.has_shared * p.T;
-    chunks = std::min<long>((long)nslots * ((p.T + BN - 1) / BN), nslots + rows / BN);
+    chunks = std::min<long>((long)nslots * ((p.T + ch - 1) / ch), nslots + rows / ch);
   }
+  chunks = std::min(chunks, records);
+  // 128-row weight tiles; 64-row ones where they fill the SMs clearly better (one token of a
+  // Mixtral-shaped layer: 224 pairs of 128-row gate/up tiles are 1.47 waves of 152 SMs)
+  auto pairs_of = [&](int tw) { return (int)((mode == MODE_SWIGLU) ? p.I / tw : (p.H + 2 * tw - 1) / (2 * tw)); };
+  pl.tw = 128;
+  if (mode == MODE_SWIGLU && !pl.pair && chunks > 0 &&
+      wave_fill((double)chunks * pairs_of(64), workers) > 1.1 * wave_fill((double)chunks * pairs_of(128), workers))
+    pl.tw = 64;
+  pl.pairs = pairs_of(pl.tw);
   const long tiles = chunks * pl.pairs;
   pl.ksplit = 1;
-  if (mode == MODE_DOWN && tiles > 0 && tiles < 3L * sm_count) {
+  if (mode == MODE_DOWN && tiles > 0 && tiles < 3L * workers) {
     // split K so the unit count fills whole waves; at least four stages per split
     double best = 0.0;
     for (int ks = 1; ks <= 16 && pl.kb_total / ks >= 4; ++ks) {
-      const double waves = (double)(tiles * ks) / sm_count;
-      const double eff = waves / std::ceil(waves);
+      const double eff = wave_fill((double)tiles * ks, workers);
       if (eff > best + 0.02) {
         best = eff;
         pl.ksplit = ks;
       }
-      if (waves >= 2.0 && eff >= 0.9) {
+      if ((double)tiles * ks >= 2.0 * workers && eff >= 0.9) {
         pl.ksplit = ks;
         break;
       }
@@ -601,20 +802,21 @@ Plan make_plan(const moe_problem& p, int mode, int sm_count, int smem_cap) {
     pl.ksplit = (pl.kb_total + pl.kb_per_split - 1) / pl.kb_per_split;
   };
   split(pl.ksplit);
-  const size_t out_cols = (mode == MODE_SWIGLU) ? p.I : p.H;
   if (pl.ksplit > 1 && (size_t)pl.ksplit * grouped_rows(p) * out_cols * 4 > (size_t(1) << 30)) split(1);
   pl.part_bytes = pl.ksplit > 1 ? (size_t)pl.ksplit * grouped_rows(p) * out_cols * 4 : 0;
-  for (int st = 6; st >= 2; --st) {
-    size_t off = (size_t)st * STAGE_BYTES;
+  const int stage = pl.pair ? Tile<128, true>::STAGE : pl.tw == 128 ? Tile<128, false>::STAGE : Tile<64, false>::STAGE;
+  const int sf_buf = pl.tw == 128 ? Tile<128, false>::SF_BUF : Tile<64, false>::SF_BUF;
+  for (int st = MAX_STAGES; st >= 2; --st) {
+    size_t off = (size_t)st * stage;
     auto carve = [&](size_t bytes, size_t align) {
       off = align_up(off, align);
       const size_t at = off;
       off += bytes;
       return (uint32_t)at;
     };
-    pl.sf_off = carve((size_t)SF_RING * GROUP * SF_STAGE_BYTES, 128);
+    pl.sf_off = carve((size_t)SF_BUFS * sf_buf, 128);
     pl.pre_off = carve((3 * (size_t)nslots + 1) * 4, 16);
-    pl.bar_off = carve((size_t)(2 * st + 2 * SF_RING + 3) * 8, 8);
+    pl.bar_off = carve((size_t)(2 * st + 2 * SF_RING + 4) * 8, 8);
     pl.misc_off = carve(16, 16);
     if ((int)(off + 1024) <= smem_cap) {
       pl.stages = st;
@@ -625,9 +827,9 @@ Plan make_plan(const moe_problem& p, int mode, int sm_count, int smem_cap) {
   return pl;
 }
 
-template <int MODE>
+template <int MODE, int TW, bool PAIR>
 int prepare_kernel() {
-  auto kern = grouped_gemm_mx_kernel<MODE>;
+  auto kern = grouped_gemm_mx_kernel<MODE, TW, PAIR>;
   static bool attr_set[64] = {};
   int dev = 0;
   cudaGetDevice(&dev);
@@ -643,9 +845,61 @@ int prepare_kernel() {
   return MOE_OK;
 }
 
+// Clusters of two that the device keeps resident at once (one CTA per SM), queried once per device and kernel.
+template <int MODE>
+int pair_clusters(size_t smem) {
+  static int n[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 64 && n[dev] > 0) return n[dev];
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(2 * (device_info().sm_count / 2));
+  cfg.blockDim = dim3(NUM_THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int c = 0;
+  if (cudaOccupancyMaxActiveClusters(&c, grouped_gemm_mx_kernel<MODE, 128, true>, &cfg) != cudaSuccess || c <= 0)
+    return 0;
+  c = std::min(c, device_info().sm_count / 2);
+  if (dev < 64) n[dev] = c;
+  return c;
+}
+
+template <int MODE, int TW, bool PAIR>
+int launch_kernel(const Plan& pl, const CUtensorMap& tA, const TokenMaps& tB, const MxParams& prm, cudaStream_t st) {
+  const int r = prepare_kernel<MODE, TW, PAIR>();
+  if (r) return r;
+  cudaLaunchConfig_t cfg{};
+  cfg.blockDim = dim3(NUM_THREADS);
+  cfg.dynamicSmemBytes = pl.smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  if (PAIR) {
+    const int nc = pair_clusters<MODE>(pl.smem);
+    if (nc <= 0) return MOE_ERR_CUDA;
+    cfg.gridDim = dim3(2 * nc);
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+  } else {
+    cfg.gridDim = dim3(device_info().sm_count);
+  }
+  return cudaLaunchKernelEx(&cfg, grouped_gemm_mx_kernel<MODE, TW, PAIR>, tA, tB, prm) == cudaSuccess ? MOE_OK
+                                                                                                    : MOE_ERR_CUDA;
+}
+
 }  // namespace
 
-int gemm_mx_tile_rows(const moe_problem&, int) { return BN; }
+int gemm_mx_tile_rows(const moe_problem& p, int mode) { return use_pairs(p, mode) ? 2 * BN : BN; }
 
 size_t gemm_mx_workspace_bytes(const moe_problem& p) {
   // the split depends on the SM count; sized for the largest plausible GPU (up to 256 SMs)
@@ -661,19 +915,17 @@ int launch_gemm_mx(const moe_problem& p, int mode, const void* act, const uint8_
   const DeviceInfo& di = device_info();
   const Plan pl = make_plan(p, mode, di.sm_count, di.max_smem_optin);
   if (pl.stages == 0) return MOE_ERR_UNSUPPORTED;
-  int r = mode == MODE_SWIGLU ? prepare_kernel<MODE_SWIGLU>() : prepare_kernel<MODE_DOWN>();
-  if (r) return r;
   const int K = (mode == MODE_SWIGLU) ? p.H : p.I;
   const int NA = (mode == MODE_SWIGLU) ? 2 * p.I : p.H;
   const uint64_t rows = (uint64_t)grouped_rows(p);
   if (rows == 0) return MOE_OK;
-  CUtensorMap tA, tB[4];
+  CUtensorMap tA;
+  TokenMaps tB;
   if (encode_tensor_map(&tA, CU_TENSOR_MAP_DATA_TYPE_UINT8, K / 2, (uint64_t)(p.P + p.has_shared) * NA, K / 2,
-                        ROW_BYTES, BM, w) != CUDA_SUCCESS)
+                        ROW_BYTES, pl.tw, w) != CUDA_SUCCESS)
     return MOE_ERR_CUDA;
-  const int boxes[4] = {16, 32, 64, 128};
-  for (int i = 0; i < 4; ++i)
-    if (encode_tensor_map(&tB[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, K / 2, rows, K / 2, ROW_BYTES, boxes[i], act) !=
+  for (int i = 0; i < NUM_BOXES; ++i)
+    if (encode_tensor_map(&tB.box[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, K / 2, rows, K / 2, ROW_BYTES, box_rows(i), act) !=
         CUDA_SUCCESS)
       return MOE_ERR_CUDA;
   MxParams prm{};
@@ -687,8 +939,8 @@ int launch_gemm_mx(const moe_problem& p, int mode, const void* act, const uint8_
   prm.ksplit = pl.ksplit;
   prm.NA = NA;
   prm.pairs = pl.pairs;
-  prm.pair_stride = (mode == MODE_SWIGLU) ? BM : 2 * BM;
-  prm.a1_off = (mode == MODE_SWIGLU) ? p.I : BM;
+  prm.pair_stride = (mode == MODE_SWIGLU) ? pl.tw : 2 * pl.tw;
+  prm.a1_off = (mode == MODE_SWIGLU) ? p.I : pl.tw;
   prm.out_cols = (mode == MODE_SWIGLU) ? p.I : p.H;
   prm.stages = pl.stages;
   prm.vec_tok = K % 512 == 0 && (reinterpret_cast<uintptr_t>(act_scales) & 15u) == 0;
@@ -707,11 +959,16 @@ int launch_gemm_mx(const moe_problem& p, int mode, const void* act, const uint8_
   prm.pre_off = pl.pre_off;
   prm.bar_off = pl.bar_off;
   prm.misc_off = pl.misc_off;
-  if (mode == MODE_SWIGLU)
-    grouped_gemm_mx_kernel<MODE_SWIGLU><<<di.sm_count, NUM_THREADS, pl.smem, st>>>(tA, tB[0], tB[1], tB[2], tB[3], prm);
+  int r;
+  if (mode == MODE_DOWN)
+    r = pl.pair ? launch_kernel<MODE_DOWN, 128, true>(pl, tA, tB, prm, st)
+                : launch_kernel<MODE_DOWN, 128, false>(pl, tA, tB, prm, st);
+  else if (pl.pair)
+    r = launch_kernel<MODE_SWIGLU, 128, true>(pl, tA, tB, prm, st);
   else
-    grouped_gemm_mx_kernel<MODE_DOWN><<<di.sm_count, NUM_THREADS, pl.smem, st>>>(tA, tB[0], tB[1], tB[2], tB[3], prm);
-  if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
+    r = pl.tw == 128 ? launch_kernel<MODE_SWIGLU, 128, false>(pl, tA, tB, prm, st)
+                     : launch_kernel<MODE_SWIGLU, 64, false>(pl, tA, tB, prm, st);
+  if (r) return r;
   return launch_splitk_reduce(p, prm.part, pl.ksplit, prm.out_cols, out, masked_m, offsets, st, comb);
 }
 

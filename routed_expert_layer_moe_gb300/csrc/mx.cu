@@ -27,12 +27,18 @@ __device__ __forceinline__ void load8(const __nv_bfloat16* x, float (&v)[8]) {
   }
 }
 
-__device__ __forceinline__ void store8(float* x, const float (&v)[8]) {
-  reinterpret_cast<float4*>(x)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(x)[1] = make_float4(v[4], v[5], v[6], v[7]);
+__device__ __forceinline__ void store8(float* x, const float (&v)[8], bool wide) {
+  const uint4 a = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+  const uint4 b = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
+  if (wide) {
+    st_global_v8(x, a, b);
+  } else {
+    reinterpret_cast<uint4*>(x)[0] = a;
+    reinterpret_cast<uint4*>(x)[1] = b;
+  }
 }
 
-__device__ __forceinline__ void store8(__nv_bfloat16* x, const float (&v)[8]) {
+__device__ __forceinline__ void store8(__nv_bfloat16* x, const float (&v)[8], bool) {
   uint4 raw;
   __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&raw);
 #pragma unroll
@@ -78,7 +84,7 @@ __global__ void __launch_bounds__(kThreads) mx_dequantize_kernel(const uint8_t* 
     v[2 * j] = f.x * sc;
     v[2 * j + 1] = f.y * sc;
   }
-  store8(out + 8 * i, v);
+  store8(out + 8 * i, v, (reinterpret_cast<uintptr_t>(out) & 31u) == 0);  // whole 32-byte sectors where they can be
 }
 
 }  // namespace

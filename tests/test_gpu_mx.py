@@ -144,7 +144,8 @@ class Grouped:
             if n:
                 yield s, self.first[s], n
 
-    def check_tiles(self, tile=128):
+    def check_tiles(self, step):
+        tile = moe.moe_gemm_tile_rows(self.p, step)
         st = self.ws[:moe.MOE_STATS_BYTES].view(torch.int32).cpu().numpy().reshape(2, moe.MOE_STATS_CTAS, 2)
         assert st[0, :, 1].sum() == sum(-(-n // tile) for _, _, n in self.valid())
 
@@ -167,6 +168,9 @@ SIZES = [
     ([2, 130], 384, 4480, "contig", 0, None),    # split, with a last stage of half a K step, an odd tile
     ([0, 0], 256, 256, "masked", 0, 4),          # nothing at all
     ([9, 3], 256, 256, "masked", 0, 6),          # a slot whose count is above M_max: M_max rows
+    # 144 pairs of 128-row gate/up tiles (fewer take 64-row tiles on 152 SMs)
+    ([16, 15, 31, 32, 33, 63, 64, 65, 127, 128, 1, 2, 0, 100, 90, 17], 256, 1152, "masked", 0, 128),
+    ([16, 15, 31, 32, 33, 63, 64, 65, 127, 128, 1, 2, 0, 100, 90, 17], 384, 1152, "contig", 0, None),
 ]
 
 
@@ -178,7 +182,7 @@ def test_down_product(case):
     moe.moe_grouped_down_gemm(g.p, g.dh[0], g.dh[1], g.d2[0], g.d2[1], g.m, g.off, y, g.err, g.ws)
     torch.cuda.synchronize()
     assert int(g.err) == 0
-    g.check_tiles()
+    g.check_tiles(4)
     got = y.double().cpu().numpy()
     seen = np.zeros(g.rows, bool)
     for s, r, n in g.valid():
@@ -217,7 +221,7 @@ def test_gate_up_product(case):
     moe.moe_grouped_swiglu_gemm(g.p, g.dx[0], g.dx[1], g.d13[0], g.d13[1], g.m, g.off, hq, hs, g.err, g.ws)
     torch.cuda.synchronize()
     assert int(g.err) == 0
-    g.check_tiles()
+    g.check_tiles(3)
     hq, hs = hq.cpu().numpy(), hs.cpu().numpy()
     seen = np.zeros(g.rows, bool)
     for s, r, n in g.valid():
