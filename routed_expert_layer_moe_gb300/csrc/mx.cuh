@@ -40,16 +40,32 @@ __device__ __forceinline__ float mx_amax(float a, float b) {
   return __uint_as_float(max(__float_as_uint(a) & 0x7FFFFFFFu, __float_as_uint(b) & 0x7FFFFFFFu));
 }
 
-// Two codes of a scaled pair, the first in the low nibble (nearest, ties to even, saturating).
-__device__ __forceinline__ uint32_t mx_codes2(float a, float b) {
-  return (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(a, b), __NV_E2M1, cudaRoundNearest);
+// max(|a|, |b|, |c|), NaN if one of them is.
+__device__ __forceinline__ float mx_amax3(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
-// Eight codes (4 bytes) of v[0..7] * inv.  inv = 0 (a block with a NaN or an infinity): zeros.
+// Eight codes (4 bytes) of v[0..7] * inv, the first in the lowest nibble (nearest, ties to even,
+// saturating).  inv = 0 (a block with a NaN or an infinity): zeros.
 __device__ __forceinline__ uint32_t mx_codes8(const float* v, float inv) {
-  if (inv == 0.0f) return 0u;
-  return mx_codes2(v[0] * inv, v[1] * inv) | (mx_codes2(v[2] * inv, v[3] * inv) << 8) |
-         (mx_codes2(v[4] * inv, v[5] * inv) << 16) | (mx_codes2(v[6] * inv, v[7] * inv) << 24);
+  const float2 s = make_float2(inv, inv);
+  float2 a[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) a[i] = __fmul2_rn(make_float2(v[2 * i], v[2 * i + 1]), s);
+  uint32_t r;
+  asm("{\n"
+      "  .reg .b8 b0, b1, b2, b3;\n"
+      "  cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n"
+      "  cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n"
+      "  cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n"
+      "  cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n"
+      "  mov.b32 %0, {b0, b1, b2, b3};\n"
+      "}\n"
+      : "=r"(r)
+      : "f"(a[0].x), "f"(a[0].y), "f"(a[1].x), "f"(a[1].y), "f"(a[2].x), "f"(a[2].y), "f"(a[3].x), "f"(a[3].y));
+  return inv == 0.0f ? 0u : r;
 }
 
 }  // namespace moe
