@@ -300,7 +300,7 @@ moe_status moe_ffn_combine(const moe_problem* p, const void* xg, const float* xg
                   workspace, st);
   if (r) return (moe_status)r;
   return launched(launch_gemm(*p, MODE_DOWN, hg, hg_scales, w2, w2_scales, masked_m, offsets, yg, nullptr, err_flag,
-                              workspace, st, &comb));
+                              workspace, st, &comb, true));
 }
 
 moe_status moe_combine(const moe_problem* p, const void* yg, const int32_t* row_of, const float* w, void* out,

@@ -48,9 +48,12 @@ bool route_permute_one_launch(const moe_problem& p, const int32_t* p2l);
 int launch_route_permute_small(const moe_problem& p, const float* logits, const void* x, int32_t* ids, float* w,
                                int32_t* masked_m, int32_t* offsets, int32_t* row_of, int32_t* src_of, void* xg,
                                float* xg_scales, int32_t* err, cudaStream_t st);
+// after_gate_up: the kernel before this call in the stream is the gate/up GEMM of the same call
+// (MXFP4: the down GEMM then starts on its weights while that one ends).
 int launch_gemm(const moe_problem& p, int mode, const void* a_act, const float* a_act_scales, const void* w,
                 const float* w_scales, const int32_t* masked_m, const int32_t* offsets, void* out,
-                float* out_scales, int32_t* err, void* ws, cudaStream_t st, const CombineArgs* comb = nullptr);
+                float* out_scales, int32_t* err, void* ws, cudaStream_t st, const CombineArgs* comb = nullptr,
+                bool after_gate_up = false);
 size_t gemm_workspace_bytes(const moe_problem& p);
 int gemm_tile_rows(const moe_problem& p, int mode);  // token rows of one MMA tile (0: CUDA-core GEMM)
 int launch_grouped_ffn(const moe_problem& p, const void* xg, const float* xg_scales, const void* w13,
@@ -68,13 +71,24 @@ int launch_combine(const moe_problem& p, const void* yg, const int32_t* row_of, 
 // The MXFP4 form of launch_gemm and what belongs to it (gemm_mx.cu).
 int launch_gemm_mx(const moe_problem& p, int mode, const void* act, const uint8_t* act_scales, const void* w,
                    const uint8_t* w_scales, const int32_t* masked_m, const int32_t* offsets, void* out,
-                   uint8_t* out_scales, int32_t* err, void* ws, cudaStream_t st, const CombineArgs* comb);
+                   uint8_t* out_scales, int32_t* err, void* ws, cudaStream_t st, const CombineArgs* comb,
+                   bool after_gate_up);
 size_t gemm_mx_workspace_bytes(const moe_problem& p);
 int gemm_mx_tile_rows(const moe_problem& p, int mode);
 // After a GEMM whose K range was split: part [ksplit][rows][cols] added in split order into
 // out, with the combine in the same kernel when comb is given; ksplit = 1: the combine alone.
+// overlap: launched while the GEMM's last CTAs run (the kernel waits for them).
 int launch_splitk_reduce(const moe_problem& p, const float* part, int ksplit, int cols, void* out,
-                         const int32_t* masked_m, const int32_t* offsets, cudaStream_t st, const CombineArgs* comb);
+                         const int32_t* masked_m, const int32_t* offsets, cudaStream_t st, const CombineArgs* comb,
+                         bool overlap = false);
+// A launch that may start while the kernel before it in the stream still runs; the kernel calls
+// grid_dependency_wait before it touches what that one reads or writes.
+inline cudaLaunchAttribute overlap_attribute() {
+  cudaLaunchAttribute a{};
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = 1;
+  return a;
+}
 
 int launch_mx_quantize(int dtype, int64_t rows, int64_t cols, const void* x, uint8_t* codes, uint8_t* scales,
                        cudaStream_t st);
@@ -260,6 +274,18 @@ __device__ __forceinline__ void st_global_v8(void* dst, uint4 a, uint4 b) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(a.x), "r"(a.y), "r"(a.z),
                "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
                : "memory");
+}
+
+// ---- programmatic dependent launch ----
+
+// Waits until the kernels before this one in the stream have finished and their writes are visible
+// (at once when this kernel was launched without overlap).
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Lets the next kernel of the stream start, if it was launched with overlap: its CTAs take what room
+// there is and wait as above.
+__device__ __forceinline__ void grid_dependents_launch() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // ---- flags between CTAs ----

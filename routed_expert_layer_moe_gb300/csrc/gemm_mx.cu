@@ -94,6 +94,7 @@ struct MxParams {
   int a1_off;        // row of the pair's second tile relative to the first
   int out_cols;
   int stages;
+  int early;           // the kernel before this one is the gate/up GEMM of the same call
   int vec_tok, vec_w;  // scale rows may be read 16 bytes at a time
   const uint8_t* w_scales;    // [slots * NA][K/32]
   const uint8_t* act_scales;  // [rows][K/32]
@@ -365,12 +366,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     tmem_alloc<PAIR>(tmem_base_smem, TMEM_COLS);
     tmem_relinquish<PAIR>();
   }
+  // Launched while the kernel before it in the stream still runs.  If that one is the gate/up GEMM
+  // of the same call, everything before it has finished (its CTAs wait here, then let this kernel
+  // start), the row counts and the weights among it: only h has to be waited for, below.
+  if (!p.early) grid_dependency_wait();
+  grid_dependents_launch();
   for (int s = tid; s < p.nslots; s += NUM_THREADS) {
-    int m = __ldg(p.masked_m + s);
+    int m = __ldcg(p.masked_m + s);  // not through the read-only path: written while this kernel may have begun
     if (p.masked) m = min(m, p.M_max);
     m = max(m, 0);
     srows[s] = m;
-    sbase[s] = p.masked ? s * p.M_max : __ldg(p.offsets + s);
+    sbase[s] = p.masked ? s * p.M_max : __ldcg(p.offsets + s);
     prefix[s + 1] = (m + CH - 1) / CH * p.pairs * p.ksplit;
   }
   if (tid == 0) prefix[0] = 0;
@@ -410,36 +416,52 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         uint32_t phase = 0;
         long issued = 0;
         bool ok = true;
+        auto token_box = [&](const Unit& U) { return (uint32_t)box_rows(box_of(U.most)) * ROW_BYTES; };
+        // a stage's byte count and its weights; pairs: the leader's barrier counts both CTAs' copies
+        auto load_weights = [&](const Unit& U, int kb, int at) {
+          uint8_t* st = smem + (size_t)at * L::STAGE;
+          const int x = kb * ROW_BYTES;
+          const uint32_t tok = token_box(U);
+          if constexpr (PAIR) {
+            if (leader) {
+              mbar_arrive_expect_tx(&full[at], 2u * (L::W_BYTES + tok));
+              tma_load_2d_hint(st, &tmA, &full[at], x, U.rowA0, pol);
+            } else {
+              tma_load_2d_pair_hint(st, &tmA, mapa_shared(&full[at], 0), x, U.rowA1, pol);
+            }
+          } else {
+            mbar_arrive_expect_tx(&full[at], (U.a1 ? 2u : 1u) * L::W_BYTES + tok);
+            tma_load_2d_hint(st, &tmA, &full[at], x, U.rowA0, pol);
+            if (U.a1) tma_load_2d_hint(st + L::W_BYTES, &tmA, &full[at], x, U.rowA1, pol);
+          }
+        };
+        int ahead = 0;  // stages of the first unit whose weights are on their way before h may be read
+        if (p.early) {
+          if (unit0 < total) {
+            const Unit U = unit(unit0);
+            for (ahead = 0; ahead < p.stages && U.kb0 + ahead < U.kb1; ++ahead) load_weights(U, U.kb0 + ahead, ahead);
+          }
+          grid_dependency_wait();
+        }
         for (int u = unit0; ok && u < total; u += ustride) {
           const Unit U = unit(u);
-          const int bi = box_of(U.most);
-          const CUtensorMap* mb = &tmB.box[bi];
-          const uint32_t tok = (uint32_t)box_rows(bi) * ROW_BYTES;
-          // pairs: the leader's stage barrier counts both CTAs' copies
-          const uint32_t bytes = PAIR ? 2u * (L::W_BYTES + tok) : (U.a1 ? 2u : 1u) * L::W_BYTES + tok;
+          const CUtensorMap* mb = &tmB.box[box_of(U.most)];
           for (int kb = U.kb0; kb < U.kb1; ++kb) {
-            if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, TIMEOUT)) {
-              ok = false;
-              break;
+            if (ahead > 0) {
+              --ahead;
+            } else {
+              if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, TIMEOUT)) {
+                ok = false;
+                break;
+              }
+              load_weights(U, kb, stage);
             }
             uint8_t* st = smem + (size_t)stage * L::STAGE;
             const int x = kb * ROW_BYTES;
-            if constexpr (PAIR) {
-              if (leader) {
-                mbar_arrive_expect_tx(&full[stage], bytes);
-                tma_load_2d_hint(st, &tmA, &full[stage], x, U.rowA0, pol);
-                tma_load_2d(st + L::W_STAGED, mb, &full[stage], x, U.rowB);
-              } else {
-                const uint32_t lbar = mapa_shared(&full[stage], 0);
-                tma_load_2d_pair_hint(st, &tmA, lbar, x, U.rowA1, pol);
-                tma_load_2d_pair(st + L::W_STAGED, mb, lbar, x, U.rowB);
-              }
-            } else {
-              mbar_arrive_expect_tx(&full[stage], bytes);
-              tma_load_2d_hint(st, &tmA, &full[stage], x, U.rowA0, pol);
-              if (U.a1) tma_load_2d_hint(st + L::W_BYTES, &tmA, &full[stage], x, U.rowA1, pol);
+            if (PAIR && !leader)
+              tma_load_2d_pair(st + L::W_STAGED, mb, mapa_shared(&full[stage], 0), x, U.rowB);
+            else
               tma_load_2d(st + L::W_STAGED, mb, &full[stage], x, U.rowB);
-            }
             ++issued;
             if (++stage == p.stages) {
               stage = 0;
@@ -535,6 +557,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           if (ok) commit(tfull);
         }
         if (p.stats) {
+          if (p.early) grid_dependency_wait();  // the kernel ahead writes the same counters
           for (int h = 0; h < 2; ++h) {
             if (blockIdx.x < STATS_CTAS) {
               p.stats[(h * STATS_CTAS + blockIdx.x) * 2] = h ? 0 : units;
@@ -622,6 +645,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
     next_unit();
+    if (p.early) grid_dependency_wait();  // for the scales of h
     for (uint32_t i = 0; i < SF_BUFS - 1; ++i) request(i);
     auto release = [&](uint32_t g) {  // the stores of group g's turn are done: tell the MMA thread
       asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -793,6 +817,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     tmem_dealloc<PAIR>(tmem_base, TMEM_COLS);
   }
   if (tid == 0 && *abort_flag) atomicOr(p.err, MOE_FLAG_TIMEOUT);
+  if (p.early) grid_dependency_wait();  // a CTA without units: this kernel never ends before the one ahead
 }
 
 // ---------------------------------------------------------------------------
@@ -946,17 +971,19 @@ int launch_kernel(const Plan& pl, const CUtensorMap& tA, const TokenMaps& tB, co
   cfg.blockDim = dim3(NUM_THREADS);
   cfg.dynamicSmemBytes = pl.smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
+  attr[0] = overlap_attribute();
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   if (PAIR) {
     const int nc = pair_clusters<MODE>(pl.smem);
     if (nc <= 0) return MOE_ERR_CUDA;
     cfg.gridDim = dim3(2 * nc);
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
   } else {
     cfg.gridDim = dim3(device_info().sm_count);
   }
@@ -978,7 +1005,8 @@ size_t gemm_mx_workspace_bytes(const moe_problem& p) {
 
 int launch_gemm_mx(const moe_problem& p, int mode, const void* act, const uint8_t* act_scales, const void* w,
                    const uint8_t* w_scales, const int32_t* masked_m, const int32_t* offsets, void* out,
-                   uint8_t* out_scales, int32_t* err, void* ws, cudaStream_t st, const CombineArgs* comb) {
+                   uint8_t* out_scales, int32_t* err, void* ws, cudaStream_t st, const CombineArgs* comb,
+                   bool after_gate_up) {
   const DeviceInfo& di = device_info();
   const Plan pl = make_plan(p, mode, di.sm_count, di.max_smem_optin);
   if (pl.stages == 0) return MOE_ERR_UNSUPPORTED;
@@ -1010,6 +1038,7 @@ int launch_gemm_mx(const moe_problem& p, int mode, const void* act, const uint8_
   prm.a1_off = (mode == MODE_SWIGLU) ? p.I : pl.tw;
   prm.out_cols = (mode == MODE_SWIGLU) ? p.I : p.H;
   prm.stages = pl.stages;
+  prm.early = after_gate_up;
   prm.vec_tok = K % 512 == 0 && (reinterpret_cast<uintptr_t>(act_scales) & 15u) == 0;
   prm.vec_w = K % 512 == 0 && (reinterpret_cast<uintptr_t>(w_scales) & 15u) == 0;
   prm.w_scales = w_scales;
@@ -1036,7 +1065,7 @@ int launch_gemm_mx(const moe_problem& p, int mode, const void* act, const uint8_
     r = pl.tw == 128 ? launch_kernel<MODE_SWIGLU, 128, false>(pl, tA, tB, prm, st)
                      : launch_kernel<MODE_SWIGLU, 64, false>(pl, tA, tB, prm, st);
   if (r) return r;
-  return launch_splitk_reduce(p, prm.part, pl.ksplit, prm.out_cols, out, masked_m, offsets, st, comb);
+  return launch_splitk_reduce(p, prm.part, pl.ksplit, prm.out_cols, out, masked_m, offsets, st, comb, true);
 }
 
 }  // namespace moe

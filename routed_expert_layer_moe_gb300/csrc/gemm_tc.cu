@@ -1071,6 +1071,7 @@ __global__ void __launch_bounds__(256) splitk_reduce_kernel(const float* __restr
                                                             int cols, const int32_t* __restrict__ masked_m,
                                                             const int32_t* __restrict__ offsets, int nslots,
                                                             int masked, int M_max, __nv_bfloat16* __restrict__ out) {
+  grid_dependency_wait();
   const long row = blockIdx.x;
   if (masked) {
     const int s = (int)(row / M_max);
@@ -1115,6 +1116,7 @@ __global__ void __launch_bounds__(256) splitk_reduce_kernel(const float* __restr
 __global__ void __launch_bounds__(128) splitk_reduce_combine_kernel(
     const float* __restrict__ part, int ksplit, long rows, int H, const int32_t* __restrict__ row_of,
     const float* __restrict__ w, int K, int KS, __nv_bfloat16* __restrict__ yg, __nv_bfloat16* __restrict__ out) {
+  grid_dependency_wait();
   const int t = blockIdx.x;
   const int c = (int)(blockIdx.y * blockDim.x + threadIdx.x) * 8;
   __shared__ int rws[33];
@@ -1549,24 +1551,33 @@ __global__ void __launch_bounds__(256) grouped_gemm_f32_kernel(const float* __re
 }  // namespace
 
 int launch_splitk_reduce(const moe_problem& p, const float* part, int ksplit, int cols, void* out,
-                         const int32_t* masked_m, const int32_t* offsets, cudaStream_t st, const CombineArgs* comb) {
+                         const int32_t* masked_m, const int32_t* offsets, cudaStream_t st, const CombineArgs* comb,
+                         bool overlap) {
+  cudaLaunchAttribute attr = overlap_attribute();
+  cudaLaunchConfig_t cfg{};
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = overlap ? 1 : 0;
   if (comb && ksplit > 1) {
     if (p.T == 0) return MOE_OK;
-    const dim3 grid((unsigned)p.T, (unsigned)((p.H / 8 + 127) / 128));
-    splitk_reduce_combine_kernel<<<grid, 128, 0, st>>>(part, ksplit, (long)grouped_rows(p), p.H, comb->row_of,
-                                                       comb->w, p.K, p.K + p.has_shared,
-                                                       static_cast<__nv_bfloat16*>(out),
-                                                       static_cast<__nv_bfloat16*>(comb->out));
-    return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    cfg.gridDim = dim3((unsigned)p.T, (unsigned)((p.H / 8 + 127) / 128));
+    cfg.blockDim = dim3(128);
+    return cudaLaunchKernelEx(&cfg, splitk_reduce_combine_kernel, part, ksplit, (long)grouped_rows(p), (int)p.H,
+                              comb->row_of, comb->w, (int)p.K, (int)(p.K + p.has_shared),
+                              static_cast<__nv_bfloat16*>(out), static_cast<__nv_bfloat16*>(comb->out)) == cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
   }
   if (comb) return launch_combine(p, out, comb->row_of, comb->w, comb->out, st);
   if (ksplit <= 1) return MOE_OK;
   const long rows = (long)grouped_rows(p);
-  const dim3 grid((unsigned)rows, (unsigned)((cols / 4 + 255) / 256));
-  splitk_reduce_kernel<<<grid, 256, 0, st>>>(part, ksplit, rows, cols, masked_m, offsets, p.P + p.has_shared,
-                                             p.layout == MOE_LAYOUT_MASKED, p.M_max,
-                                             static_cast<__nv_bfloat16*>(out));
-  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  cfg.gridDim = dim3((unsigned)rows, (unsigned)((cols / 4 + 255) / 256));
+  cfg.blockDim = dim3(256);
+  return cudaLaunchKernelEx(&cfg, splitk_reduce_kernel, part, ksplit, rows, cols, masked_m, offsets,
+                            (int)(p.P + p.has_shared), (int)(p.layout == MOE_LAYOUT_MASKED), (int)p.M_max,
+                            static_cast<__nv_bfloat16*>(out)) == cudaSuccess
+             ? MOE_OK
+             : MOE_ERR_CUDA;
 }
 
 int gemm_tile_rows(const moe_problem& p, int mode) {
@@ -1592,7 +1603,7 @@ size_t gemm_workspace_bytes(const moe_problem& p) {
 
 int launch_gemm(const moe_problem& p, int mode, const void* act, const float* act_scales, const void* w,
                 const float* w_scales, const int32_t* masked_m, const int32_t* offsets, void* out, float* out_scales,
-                int32_t* err, void* ws, cudaStream_t st, const CombineArgs* comb) {
+                int32_t* err, void* ws, cudaStream_t st, const CombineArgs* comb, bool after_gate_up) {
   const int nslots = p.P + p.has_shared;
   if (p.wt == MOE_F32) {
     const int K = (mode == MODE_SWIGLU) ? p.H : p.I;
@@ -1615,7 +1626,7 @@ int launch_gemm(const moe_problem& p, int mode, const void* act, const float* ac
   if (p.wt == MOE_MXFP4)
     return launch_gemm_mx(p, mode, act, reinterpret_cast<const uint8_t*>(act_scales), w,
                           reinterpret_cast<const uint8_t*>(w_scales), masked_m, offsets, out,
-                          reinterpret_cast<uint8_t*>(out_scales), err, ws, st, comb);
+                          reinterpret_cast<uint8_t*>(out_scales), err, ws, st, comb, after_gate_up);
   const DeviceInfo& di = device_info();
   const Plan pl = make_plan(p, mode, di.sm_count, di.max_smem_optin);
   if (pl.stages == 0) return MOE_ERR_UNSUPPORTED;
@@ -1655,7 +1666,8 @@ int launch_grouped_ffn(const moe_problem& p, const void* xg, const float* xg_sca
   if (p.wt == MOE_MXFP4) {  // two launches
     int r = launch_gemm(p, MODE_SWIGLU, xg, xg_scales, w13, w13_scales, masked_m, offsets, hg, hg_scales, err, ws, st);
     if (r) return r;
-    return launch_gemm(p, MODE_DOWN, hg, hg_scales, w2, w2_scales, masked_m, offsets, yg, nullptr, err, ws, st, comb);
+    return launch_gemm(p, MODE_DOWN, hg, hg_scales, w2, w2_scales, masked_m, offsets, yg, nullptr, err, ws, st, comb,
+                       true);
   }
   const DeviceInfo& di = device_info();
   const Plan pl0 = make_plan(p, MODE_SWIGLU, di.sm_count, di.max_smem_optin, 2);

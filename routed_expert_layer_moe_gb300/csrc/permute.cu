@@ -474,6 +474,7 @@ __global__ void __launch_bounds__(kSmallThreads) permute_small_kernel(
   __shared__ int32_t off[kSlotsMax + 1];      // exclusive prefix sum of cnt
   __shared__ int32_t warp_tot[kSmallThreads / 32];
   __shared__ int rows[64];
+  grid_dependents_launch();  // an MXFP4 gate/up GEMM after this kernel sets itself up meanwhile
   const int t = blockIdx.x;
   const int n = T * K, NS = P + S, KS = K + S;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
