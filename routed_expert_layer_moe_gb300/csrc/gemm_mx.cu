@@ -61,8 +61,13 @@ constexpr int SF_WARP0 = 4, SF_WARPS = 4;
 constexpr int EPI_WARP0 = 8, EPI_WARPS = 8;
 // Register split (setmaxnreg) of warpgroup 0, the scale warps and the two epilogue warpgroups:
 // 128 * (ctrl + sf + 2 epi) <= 512 * (registers at launch), checked before the first launch.
-constexpr int REGS_CTRL = 72, REGS_SF = 88, REGS_EPI = 176;
-constexpr int REGS_NEEDED = 128 * (REGS_CTRL + REGS_SF + 2 * REGS_EPI);
+// Next to 220 KB of shared memory there is hardly an L1 to spill to: the split is the one without
+// spills in the epilogue (128 accumulators a thread, or 64 packed to bf16 in an unsplit down product).
+template <bool LEAN>
+struct Regs {
+  static constexpr int ctrl = LEAN ? 96 : 80, sf = LEAN ? 96 : 80, epi = LEAN ? 160 : 176;
+  static constexpr int needed = 128 * (ctrl + sf + 2 * epi);
+};
 constexpr uint32_t TMEM_COLS = 512;
 constexpr long long TIMEOUT = 4000000000LL;  // SM cycles, about 2 s
 // Token boxes of 16, 32, 64, 96 and 128 rows: the smallest that covers a chunk is copied.
@@ -302,23 +307,13 @@ __device__ __forceinline__ void store_quad(uint32_t (&w)[4][8], int lane, int ba
   }
 }
 
-// n 32-byte vectors w(0..2n-1) (16 bytes each), as 32-byte stores when dst allows them.
-template <int N, typename F>
-__device__ __forceinline__ void store_row(uint8_t* dst, bool wide, F w) {
-  if (wide) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) st_global_v8(dst + 32 * i, w(2 * i), w(2 * i + 1));
-  } else {
-#pragma unroll
-    for (int i = 0; i < 2 * N; ++i) reinterpret_cast<uint4*>(dst)[i] = w(i);
-  }
-}
-
-template <int MODE, int TW, bool PAIR>
+// SPLIT: the K range is split (down only); partial sums go to the workspace.
+template <int MODE, int TW, bool PAIR, bool SPLIT>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     grouped_gemm_mx_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ TokenMaps tmB,
                            const MxParams p) {
   using L = Tile<TW, PAIR>;
+  using R = Regs<MODE == MODE_DOWN && !SPLIT>;
   constexpr int TC = TW / 2;  // columns of each tile that an epilogue thread holds
   constexpr int CH = PAIR ? 2 * BN : BN;
   extern __shared__ uint8_t smem_raw[];
@@ -405,7 +400,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   auto unit = [&](int u) { return decode_unit<PAIR>(p, prefix, srows, sbase, u, crank); };
 
   if (warp < SF_WARP0) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_CTRL));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::ctrl));
     if (warp == 0) {
       // ------------------------------------------------------------ producer
       if (lane == 0) {
@@ -583,7 +578,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
     }
   } else if (warp < EPI_WARP0) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_SF));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::sf));
     // ------------------------------------------------------------ scales
     // These warps run a short serial chain per group and bound the kernel when it is long: addresses
     // are per unit, the warps meet at a hardware barrier, and a group's stores to tensor memory
@@ -694,7 +689,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     if (ok && requested > 0) release(g == 0 ? SF_RING - 1 : g - 1);
     cp_async_wait_all();  // no copy may land after the CTA has exited
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_EPI));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R::epi));
     // ------------------------------------------------------------ epilogue
     const int quarter = warp & 3;              // tensor-memory lane quarter this warp may access
     const int half = (warp - EPI_WARP0) >> 2;  // column half of each tile
@@ -708,26 +703,31 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       // the whole warp goes on together (its tensor-memory loads are warp-wide) or gives up together
       if (!__all_sync(0xffffffffu, mbar_wait<PAIR>(tfull, u_it & 1u, abort_flag, TIMEOUT))) break;
       tc_fence_after_sync();
-      float acc0[TC], acc1[TC];
       const bool warp_live = quarter * 32 < U.nvalid;
-      if (warp_live) {  // all loads before the wait
-        tmem_load<TC>(t_lane + (uint32_t)c_lo, acc0);
-        tmem_load<TC>(t_lane + (uint32_t)(c_lo + TW), acc1);
+      const bool live = lrow < U.nvalid;
+      // once per unit: the accumulators are in registers
+      auto release = [&]() {
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          if (PAIR)
+            mbar_arrive_remote(mapa_shared(tempty, 0));
+          else
+            mbar_arrive(tempty);
+        }
+      };
+      if (!warp_live) {  // rows past the chunk: nothing to read or store
+        release();
+        continue;
+      }
+      const uint32_t t0 = t_lane + (uint32_t)c_lo;
+      if constexpr (MODE == MODE_SWIGLU) {
+        float acc0[TC], acc1[TC];
+        tmem_load<TC>(t0, acc0);
+        tmem_load<TC>(t0 + (uint32_t)TW, acc1);
         tmem_loaded<TC>(acc0);
         tmem_loaded<TC>(acc1);
-      }
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) {
-        if (PAIR)
-          mbar_arrive_remote(mapa_shared(tempty, 0));
-        else
-          mbar_arrive(tempty);
-      }
-      if (!warp_live) continue;  // rows past the chunk: nothing to store
-      const bool live = lrow < U.nvalid;
-      const size_t row = (size_t)(U.rowB + lrow);
-      if constexpr (MODE == MODE_SWIGLU) {
+        release();
 #pragma unroll
         for (int i = 0; i < TC; i += 2) {
           const float2 h = silu_mul(make_float2(acc0[i], acc0[i + 1]), make_float2(acc1[i], acc1[i + 1]));
@@ -744,14 +744,19 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i) code[4 * b + i] = mx_codes8(acc0 + 32 * b + 8 * i, inv);
         }
+        if (!live) continue;
+        const size_t row = (size_t)(U.rowB + lrow);
         const size_t col = (size_t)U.j * TW + c_lo;
         uint8_t* dst = static_cast<uint8_t*>(p.out) + row * (oc / 2) + col / 2;
         uint8_t* ds = p.out_scales + row * (oc / 32) + col / 32;
-        if (!live) continue;
         if constexpr (TC == 64) {
-          store_row<1>(dst, (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0, [&](int i) {
-            return make_uint4(code[4 * i], code[4 * i + 1], code[4 * i + 2], code[4 * i + 3]);
-          });
+          const uint4 a = make_uint4(code[0], code[1], code[2], code[3]), b = make_uint4(code[4], code[5], code[6], code[7]);
+          if ((reinterpret_cast<uintptr_t>(p.out) & 31u) == 0) {
+            st_global_v8(dst, a, b);
+          } else {
+            reinterpret_cast<uint4*>(dst)[0] = a;
+            reinterpret_cast<uint4*>(dst)[1] = b;
+          }
           *reinterpret_cast<uint16_t*>(ds) = (uint16_t)(sb[0] | (sb[1] << 8));
         } else {
           *reinterpret_cast<uint4*>(dst) = make_uint4(code[0], code[1], code[2], code[3]);
@@ -761,11 +766,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         static_assert(MODE == MODE_SWIGLU || TC == 64, "64 columns of each tile a thread");
         const size_t col = (size_t)U.j * p.pair_stride + c_lo;
         const int base = lrow & ~3;
-        uint32_t w[4][8];
-        if (p.ksplit > 1) {
+        if constexpr (SPLIT) {
+          float acc0[64], acc1[64];
+          tmem_load<64>(t0, acc0);
+          tmem_load<64>(t0 + (uint32_t)TW, acc1);
+          tmem_loaded<64>(acc0);
+          tmem_loaded<64>(acc1);
+          release();
           float* part = p.part + ((size_t)U.q * p.rows_total + U.rowB) * oc + col;
           const bool wide = (reinterpret_cast<uintptr_t>(p.part) & 31u) == 0;
           auto store = [&](const float* a, int c) {  // 32 columns from column c on
+            uint32_t w[4][8];
 #pragma unroll
             for (int i = 0; i < 32; ++i) w[i / 8][i % 8] = __float_as_uint(a[i]);
             store_quad(w, lane, base, U.nvalid, wide,
@@ -778,16 +789,26 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             store(acc1 + 32, TW + 32);
           }
         } else {
+          // a tile is packed to bf16 before the next one is loaded: with both in registers the compiler
+          // spilled (dense down product 203 us, not 172)
+          uint32_t w[2][4][8];
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            float a[64];
+            tmem_load<64>(t0 + (uint32_t)(t * TW), a);
+            tmem_loaded<64>(a);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) w[t][i / 8][i % 8] = bf16x2(a[2 * i], a[2 * i + 1]);
+          }
+          release();
           __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + (size_t)U.rowB * oc + col;
           const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
-          auto store = [&](const float* a, int c) {  // 64 columns from column c on
 #pragma unroll
-            for (int i = 0; i < 32; ++i) w[i / 8][i % 8] = bf16x2(a[2 * i], a[2 * i + 1]);
-            store_quad(w, lane, base, U.nvalid, wide,
-                       [&](int r) { return reinterpret_cast<uint8_t*>(out + (size_t)r * oc + c); });
-          };
-          store(acc0, 0);
-          if (U.a1) store(acc1, TW);
+          for (int t = 0; t < 2; ++t) {
+            if (t == 0 || U.a1)
+              store_quad(w[t], lane, base, U.nvalid, wide,
+                         [&](int r) { return reinterpret_cast<uint8_t*>(out + (size_t)r * oc + t * TW); });
+          }
         }
       }
     }
@@ -873,7 +894,7 @@ Plan make_plan(const moe_problem& p, int mode, int sm_count, int smem_cap) {
   pl.pairs = pairs_of(pl.tw);
   const long tiles = chunks * pl.pairs;
   pl.ksplit = 1;
-  if (mode == MODE_DOWN && tiles > 0 && tiles < 3L * workers) {
+  if (mode == MODE_DOWN && !pl.pair && tiles > 0 && tiles < 3L * workers) {
     // split K so the unit count fills whole waves; at least four stages per split
     double best = 0.0;
     for (int ks = 1; ks <= 16 && pl.kb_total / ks >= 4; ++ks) {
@@ -919,9 +940,9 @@ Plan make_plan(const moe_problem& p, int mode, int sm_count, int smem_cap) {
   return pl;
 }
 
-template <int MODE, int TW, bool PAIR>
+template <int MODE, int TW, bool PAIR, bool SPLIT>
 int prepare_kernel() {
-  auto kern = grouped_gemm_mx_kernel<MODE, TW, PAIR>;
+  auto kern = grouped_gemm_mx_kernel<MODE, TW, PAIR, SPLIT>;
   static bool attr_set[64] = {};
   int dev = 0;
   cudaGetDevice(&dev);
@@ -929,7 +950,7 @@ int prepare_kernel() {
   // the register split must fit in what the launch provides, or setmaxnreg.inc would wait forever
   cudaFuncAttributes fa{};
   if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return MOE_ERR_CUDA;
-  if (fa.numRegs * NUM_THREADS < REGS_NEEDED) return MOE_ERR_UNSUPPORTED;
+  if (fa.numRegs * NUM_THREADS < Regs<MODE == MODE_DOWN && !SPLIT>::needed) return MOE_ERR_UNSUPPORTED;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, device_info().max_smem_optin) !=
       cudaSuccess)
     return MOE_ERR_CUDA;
@@ -956,16 +977,16 @@ int pair_clusters(size_t smem) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int c = 0;
-  if (cudaOccupancyMaxActiveClusters(&c, grouped_gemm_mx_kernel<MODE, 128, true>, &cfg) != cudaSuccess || c <= 0)
+  if (cudaOccupancyMaxActiveClusters(&c, grouped_gemm_mx_kernel<MODE, 128, true, false>, &cfg) != cudaSuccess || c <= 0)
     return 0;
   c = std::min(c, device_info().sm_count / 2);
   if (dev < 64) n[dev] = c;
   return c;
 }
 
-template <int MODE, int TW, bool PAIR>
+template <int MODE, int TW, bool PAIR, bool SPLIT = false>
 int launch_kernel(const Plan& pl, const CUtensorMap& tA, const TokenMaps& tB, const MxParams& prm, cudaStream_t st) {
-  const int r = prepare_kernel<MODE, TW, PAIR>();
+  const int r = prepare_kernel<MODE, TW, PAIR, SPLIT>();
   if (r) return r;
   cudaLaunchConfig_t cfg{};
   cfg.blockDim = dim3(NUM_THREADS);
@@ -987,7 +1008,7 @@ int launch_kernel(const Plan& pl, const CUtensorMap& tA, const TokenMaps& tB, co
   } else {
     cfg.gridDim = dim3(device_info().sm_count);
   }
-  return cudaLaunchKernelEx(&cfg, grouped_gemm_mx_kernel<MODE, TW, PAIR>, tA, tB, prm) == cudaSuccess ? MOE_OK
+  return cudaLaunchKernelEx(&cfg, grouped_gemm_mx_kernel<MODE, TW, PAIR, SPLIT>, tA, tB, prm) == cudaSuccess ? MOE_OK
                                                                                                     : MOE_ERR_CUDA;
 }
 
@@ -1057,8 +1078,9 @@ int launch_gemm_mx(const moe_problem& p, int mode, const void* act, const uint8_
   prm.misc_off = pl.misc_off;
   int r;
   if (mode == MODE_DOWN)
-    r = pl.pair ? launch_kernel<MODE_DOWN, 128, true>(pl, tA, tB, prm, st)
-                : launch_kernel<MODE_DOWN, 128, false>(pl, tA, tB, prm, st);
+    r = pl.pair        ? launch_kernel<MODE_DOWN, 128, true>(pl, tA, tB, prm, st)
+        : pl.ksplit > 1 ? launch_kernel<MODE_DOWN, 128, false, true>(pl, tA, tB, prm, st)
+                        : launch_kernel<MODE_DOWN, 128, false>(pl, tA, tB, prm, st);
   else if (pl.pair)
     r = launch_kernel<MODE_SWIGLU, 128, true>(pl, tA, tB, prm, st);
   else
