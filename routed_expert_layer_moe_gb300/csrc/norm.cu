@@ -86,6 +86,16 @@ __device__ __forceinline__ V8 load8(const T* row, int c, int H) {
   }
 }
 
+// Eight values as two 16-byte parts, `plane` bytes apart, in shared memory.
+__device__ __forceinline__ void put8(uint8_t* p, uint32_t plane, const V8& a) {
+  *reinterpret_cast<float4*>(p) = make_float4(a.v[0].x, a.v[0].y, a.v[1].x, a.v[1].y);
+  *reinterpret_cast<float4*>(p + plane) = make_float4(a.v[2].x, a.v[2].y, a.v[3].x, a.v[3].y);
+}
+
+__device__ __forceinline__ V8 get8(const uint8_t* p, uint32_t plane) {
+  return unpack(*reinterpret_cast<const float4*>(p), *reinterpret_cast<const float4*>(p + plane));
+}
+
 template <bool VEC, typename T>
 __device__ __forceinline__ void store8(T* row, int c, int H, const V8& a) {
   if constexpr (VEC && sizeof(T) == 4) {
@@ -122,6 +132,14 @@ __device__ __forceinline__ void cta_sum(float (&v)[N], float* buf) {
     for (int i = 0; i < N; ++i) buf[i * 32 + warp] = v[i];
   }
   __syncthreads();
+  if (nwarps == 8) {  // two loads and a tree of adds are shorter than the shuffles
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float4 a = *reinterpret_cast<const float4*>(buf + i * 32), b = *reinterpret_cast<const float4*>(buf + i * 32 + 4);
+      v[i] = ((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w));
+    }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     v[i] = lane < nwarps ? buf[i * 32 + lane] : 0.0f;
@@ -177,9 +195,10 @@ struct Rows {
       asm volatile("cp.async.commit_group;" ::: "memory");
     }
   }
-  // All but the last DEPTH - 1 requests have arrived (each thread waits for its own).
+  // All but the last DEPTH - 1 - BUT requests have arrived (each thread waits for its own).
+  template <int BUT>
   __device__ __forceinline__ void wait() const {
-    if constexpr (DEPTH > 0) asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH > 0 ? DEPTH - 1 : 0) : "memory");
+    if constexpr (DEPTH > 0) asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH > BUT ? DEPTH - 1 - BUT : 0) : "memory");
   }
   __device__ __forceinline__ V8 get(int n, int r, int slot, int j) const {
     if constexpr (DEPTH == 0) {
@@ -205,49 +224,57 @@ __device__ __forceinline__ V8 load_post(const Args<T>& a, int c) {
   return w;
 }
 
-template <typename T, int V, bool VEC, int DEPTH>
-__global__ void __launch_bounds__(kMaxThreads, V == 1 ? 3 : 1) block_norm_kernel(const Args<T> a) {
+// This thread's part of the sum of squares of array n in row r.
+template <int V, typename R>
+__device__ __forceinline__ float sum_squares(const R& in, int n, int r, int slot) {
+  float2 s = pair(0.0f);
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    if ((j * (int)blockDim.x + (int)threadIdx.x) * 8 < in.H) {
+      const V8 b = in.get(n, r, slot, j);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s = fma2(b.v[i], b.v[i], s);
+    }
+  }
+  return s.x + s.y;
+}
+
+// The sum over the block's row is needed before y, the sum over y after it.  The first is taken one
+// row ahead, together with the second one of the row before: one reduction a row, not two.
+template <typename T, int V, bool VEC, int DEPTH, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) block_norm_kernel(const Args<T> a) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float buf[2][32];
+  __shared__ __align__(16) float buf[2][64];
   const int H = a.H, nt = blockDim.x;
   const float invH = 1.0f / (float)H;
   const Rows<T, V, VEC, DEPTH, 2> in{{a.x, a.block}, H, smem};
 #pragma unroll
   for (int d = 0; d < DEPTH; ++d) in.request(blockIdx.x + d * gridDim.x, a.rows, d);
-  int slot = 0;
+  in.template wait<0>();
+  float sb = 0.0f;  // sum of squares of the block's row
+  if (a.block) {
+    float v[1] = {sum_squares<V>(in, 1, blockIdx.x, 0)};
+    cta_sum(v, buf[1]);
+    sb = v[0];
+  }
+  int slot = 0, parity = 0;
   for (int r = blockIdx.x; r < a.rows; r += gridDim.x) {
     const size_t at = (size_t)r * H;
-    in.wait();
+    const int next = r + gridDim.x, next_slot = DEPTH > 0 && slot + 1 < DEPTH ? slot + 1 : 0;
+    float g = a.rs * rsqrtf(sb * invH + a.eps);
+    if (a.gate_kind == MOE_GATE_TOKEN) g *= to_float(a.gate[r]);
+    const float2 f = pair(g);
     V8 y[V];
-    float2 f = pair(0.0f);
-    if (a.block) {
-      float2 s = pair(0.0f);
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        if ((j * nt + (int)threadIdx.x) * 8 < H) {
-          y[j] = in.get(1, r, slot, j);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s = fma2(y[j].v[i], y[j].v[i], s);
-        }
-      }
-      float sum[1] = {s.x + s.y};
-      cta_sum(sum, buf[0]);
-      float g = a.rs * rsqrtf(sum[0] * invH + a.eps);
-      if (a.gate_kind == MOE_GATE_TOKEN) g *= to_float(a.gate[r]);
-      f = pair(g);
-    }
     float2 s = pair(0.0f);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int c = (j * nt + threadIdx.x) * 8;
       if (c < H) {
-        const V8 x = in.get(0, r, slot, j);
+        y[j] = in.get(0, r, slot, j);
         if (a.block) {
-          const V8 w = load_post<VEC>(a, c);
+          const V8 b = in.get(1, r, slot, j), w = load_post<VEC>(a, c);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) y[j].v[i] = fma2(f, mul2(w.v[i], y[j].v[i]), x.v[i]);
-        } else {
-          y[j] = x;
+          for (int i = 0; i < 4; ++i) y[j].v[i] = fma2(f, mul2(w.v[i], b.v[i]), y[j].v[i]);
         }
         if (a.y) store8<VEC>(a.y + at, c, H, y[j]);
 #pragma unroll
@@ -255,11 +282,13 @@ __global__ void __launch_bounds__(kMaxThreads, V == 1 ? 3 : 1) block_norm_kernel
       }
     }
     in.request(r + DEPTH * gridDim.x, a.rows, slot);
-    if (DEPTH > 0 && ++slot == DEPTH) slot = 0;
+    in.template wait<0>();
+    float v[2] = {s.x + s.y, 0.0f};
+    if (a.block && next < a.rows) v[1] = sum_squares<V>(in, 1, next, next_slot);
+    cta_sum(v, buf[parity]);
+    sb = v[1];
     if (a.xn) {
-      float sum[1] = {s.x + s.y};
-      cta_sum(sum, buf[1]);
-      const float2 ry = pair(rsqrtf(sum[0] * invH + a.eps));
+      const float2 ry = pair(rsqrtf(v[0] * invH + a.eps));
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const int c = (j * nt + threadIdx.x) * 8;
@@ -271,44 +300,62 @@ __global__ void __launch_bounds__(kMaxThreads, V == 1 ? 3 : 1) block_norm_kernel
         }
       }
     }
-    // a buffer is written again only after a barrier on the other one, if both are in use
-    if (!a.block || !a.xn) __syncthreads();
+    slot = next_slot;
+    parity ^= 1;  // this row's buffer is written again after the next row's barrier
   }
 }
 
-template <typename T, int V, bool VEC, int DEPTH>
-__global__ void __launch_bounds__(kMaxThreads, V == 1 ? 2 : 1) block_norm_backward_kernel(const Args<T> a) {
+// The reductions of a row: y^2 with q y, then the sum behind dblock with the next row's block^2.
+template <typename T, int V, bool VEC, int DEPTH, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) block_norm_backward_kernel(const Args<T> a) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float buf[3][64];
+  __shared__ __align__(16) float buf[2][64];
   enum { X, B, DY, DXN };
   const int H = a.H, nt = blockDim.x;
   const float invH = 1.0f / (float)H;
   const Rows<T, V, VEC, DEPTH, 4> in{{a.x, a.block, a.dy, a.dxn}, H, smem};
+  // Both weights in fp32, a channel's gate folded in, in this thread's own part of shared memory behind
+  // the rows (when rows are fetched ahead): each is read twice a row, and loaded and unpacked from
+  // global memory they took 33 of 163 us.
+  uint8_t* const wmem = in.at(DEPTH, 0, 0, 0);
+  const uint32_t plane = blockDim.x * 16u;
+  if constexpr (DEPTH > 0) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int c = (j * nt + threadIdx.x) * 8;
+      if (c < H) {
+        if (a.block) put8(wmem + 2 * j * plane, plane, load_post<VEC>(a, c));
+        if (a.dxn) put8(wmem + (2 * V + 2 * j) * plane, plane, load8<VEC>(a.w_pre, c, H));
+      }
+    }
+  }
+  auto post_weight = [&](int j, int c) {
+    if constexpr (DEPTH > 0) return get8(wmem + 2 * j * plane, plane);
+    return load_post<VEC>(a, c);
+  };
+  auto pre_weight = [&](int j, int c) {
+    if constexpr (DEPTH > 0) return get8(wmem + (2 * V + 2 * j) * plane, plane);
+    return load8<VEC>(a.w_pre, c, H);
+  };
   V8 acc_post[V], acc_pre[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) acc_post[j] = acc_pre[j] = zeros();
 #pragma unroll
   for (int d = 0; d < DEPTH; ++d) in.request(blockIdx.x + d * gridDim.x, a.rows, d);
+  in.template wait<0>();
+  float sb = 0.0f;  // sum of squares of the block's row
+  if (a.block) {
+    float v[1] = {sum_squares<V>(in, B, blockIdx.x, 0)};
+    cta_sum(v, buf[1]);
+    sb = v[0];
+    if (!a.dxn) __syncthreads();
+  }
   int slot = 0;
   for (int r = blockIdx.x; r < a.rows; r += gridDim.x) {
     const size_t at = (size_t)r * H;
+    const int next = r + gridDim.x, next_slot = DEPTH > 0 && slot + 1 < DEPTH ? slot + 1 : 0;
     const float gt = a.gate_kind == MOE_GATE_TOKEN ? to_float(a.gate[r]) : 1.0f;
-    in.wait();
-    float rb = 0.0f;
-    if (a.block) {
-      float2 s = pair(0.0f);
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        if ((j * nt + (int)threadIdx.x) * 8 < H) {
-          const V8 b = in.get(B, r, slot, j);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s = fma2(b.v[i], b.v[i], s);
-        }
-      }
-      float sum[1] = {s.x + s.y};
-      cta_sum(sum, buf[0]);
-      rb = rsqrtf(sum[0] * invH + a.eps);
-    }
+    const float rb = rsqrtf(sb * invH + a.eps);
     V8 y[V];
     float2 s0 = pair(0.0f), s1 = pair(0.0f);  // sums of y^2 and of q y
 #pragma unroll
@@ -317,13 +364,13 @@ __global__ void __launch_bounds__(kMaxThreads, V == 1 ? 2 : 1) block_norm_backwa
       if (c < H) {
         y[j] = in.get(X, r, slot, j);
         if (a.block) {
-          const V8 b = in.get(B, r, slot, j), w = load_post<VEC>(a, c);
+          const V8 b = in.get(B, r, slot, j), w = post_weight(j, c);
           const float2 f = pair(a.rs * gt * rb);
 #pragma unroll
           for (int i = 0; i < 4; ++i) y[j].v[i] = fma2(f, mul2(w.v[i], b.v[i]), y[j].v[i]);
         }
         if (a.dxn) {
-          const V8 q = in.get(DXN, r, slot, j), w = load8<VEC>(a.w_pre, c, H);
+          const V8 q = in.get(DXN, r, slot, j), w = pre_weight(j, c);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             s0 = fma2(y[j].v[i], y[j].v[i], s0);
@@ -335,7 +382,7 @@ __global__ void __launch_bounds__(kMaxThreads, V == 1 ? 2 : 1) block_norm_backwa
     float ry = 0.0f, m = 0.0f;
     if (a.dxn) {
       float sum[2] = {s0.x + s0.y, s1.x + s1.y};
-      cta_sum(sum, buf[1]);
+      cta_sum(sum, buf[0]);
       ry = rsqrtf(sum[0] * invH + a.eps);
       m = -sum[1] * ry * ry * ry * invH;  // -ry yn mean(q yn) = y m
     }
@@ -346,7 +393,7 @@ __global__ void __launch_bounds__(kMaxThreads, V == 1 ? 2 : 1) block_norm_backwa
       if (c < H) {
         V8 d = a.dy ? in.get(DY, r, slot, j) : zeros();
         if (a.dxn) {
-          const V8 q = in.get(DXN, r, slot, j), w = load8<VEC>(a.w_pre, c, H);
+          const V8 q = in.get(DXN, r, slot, j), w = pre_weight(j, c);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             acc_pre[j].v[i] = fma2(mul2(q.v[i], y[j].v[i]), pair(ry), acc_pre[j].v[i]);
@@ -355,7 +402,7 @@ __global__ void __launch_bounds__(kMaxThreads, V == 1 ? 2 : 1) block_norm_backwa
         }
         store8<VEC>(a.dx + at, c, H, d);
         if (a.block) {
-          const V8 b = in.get(B, r, slot, j), w = load_post<VEC>(a, c);
+          const V8 b = in.get(B, r, slot, j), w = post_weight(j, c);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float2 db = mul2(d.v[i], b.v[i]);
@@ -367,8 +414,11 @@ __global__ void __launch_bounds__(kMaxThreads, V == 1 ? 2 : 1) block_norm_backwa
       }
     }
     if (a.block) {
-      float sum[1] = {u.x + u.y};
-      cta_sum(sum, buf[2]);
+      in.template wait<1>();
+      float sum[2] = {u.x + u.y, 0.0f};
+      if (next < a.rows) sum[1] = sum_squares<V>(in, B, next, next_slot);
+      cta_sum(sum, buf[1]);
+      sb = sum[1];
       const float dg = a.rs * rb * sum[0];  // sum over the row of rs dx bn w_post
       const float2 f = pair(a.rs * rb * gt), mean = pair(-rb * rb * gt * dg * invH);
 #pragma unroll
@@ -384,9 +434,9 @@ __global__ void __launch_bounds__(kMaxThreads, V == 1 ? 2 : 1) block_norm_backwa
       if (a.dgate && a.gate_kind == MOE_GATE_TOKEN && threadIdx.x == 0) a.dgate[r] = dg;
     }
     in.request(r + DEPTH * gridDim.x, a.rows, slot);
-    if (DEPTH > 0 && ++slot == DEPTH) slot = 0;
-    // with the block there is a barrier on another buffer between two uses of each
-    if (!a.block) __syncthreads();
+    slot = next_slot;
+    if (!a.block) in.template wait<0>();
+    if (!a.block || !a.dxn) __syncthreads();  // else a barrier on the other buffer lies between two uses of each
   }
   float* part = a.part + (size_t)blockIdx.x * 2 * H;
 #pragma unroll
@@ -438,40 +488,45 @@ struct Shape {
   size_t smem;
 };
 
-// One vector a thread up to 512 threads, then two, four.  `arrays`: how many a row is read from;
-// `most`: CTAs an SM holds with one vector a thread (by their registers).
-Shape shape_of(int H, int esz, bool vec, int arrays, int most, int rows) {
+// A thread holds one vector when there are few rows, where a row's latency counts, or few columns; else
+// two, and four beyond 8192 columns: the reductions, the addresses and the loop are then shared
+// by 16 columns.  `arrays`: how many a row is read from; `weights`: fp32 rows kept in shared memory beside
+// those fetched ahead; ctas1, ctas2: CTAs of 512 threads with one vector a thread and of 256 with two
+// that an SM's registers hold (what the kernels are compiled for).
+Shape shape_of(int H, int esz, bool vec, int arrays, int weights, int ctas1, int ctas2, int rows) {
   Shape s{};
   const int nvec = (H + 7) / 8;
-  s.v = nvec <= 512 ? 1 : nvec <= 1024 ? 2 : 4;
+  s.v = nvec > 1024 ? 4 : nvec > 512 || (nvec > 128 && rows > device_info().sm_count) ? 2 : 1;
   s.threads = ((nvec + s.v - 1) / s.v + 31) / 32 * 32;
-  s.ctas = s.v == 1 ? std::min(512 * most / s.threads, 24) : 1;
+  s.ctas = s.v == 1 ? std::min(512 * ctas1 / s.threads, 24) : s.threads <= 256 ? 256 * ctas2 / s.threads : 1;
   const DeviceInfo& di = device_info();
   if (!vec || rows <= di.sm_count * s.ctas) return s;  // a row for each CTA: nothing to fetch ahead
-  const size_t row = (size_t)s.v * s.threads * 8 * esz * arrays;
+  const size_t cols = (size_t)s.v * s.threads * 8;
+  const size_t row = cols * esz * arrays, keep = cols * 4 * weights;
   const size_t room = (size_t)di.max_smem_optin - 1024;  // what a CTA's static memory and the system take
-  for (int ctas = s.ctas; ctas >= 1; --ctas)
+  for (int c = s.ctas; c >= 1; --c)
     for (int depth = 3; depth >= 2; --depth)
-      if (row * depth <= room / ctas - 1024) {
-        s.ctas = ctas, s.depth = depth, s.smem = row * depth;
+      if (row * depth + keep <= room / c - 1024) {
+        s.ctas = c, s.depth = depth, s.smem = row * depth + keep;
         return s;
       }
   return s;
 }
 
-// f(vectors a thread, 16-byte accesses, rows ahead) with compile-time arguments.
+// f(vectors a thread, 16-byte accesses, rows ahead, threads at most) with compile-time arguments.
 template <typename F>
 int dispatch(const Shape& s, bool vec, F f) {
   using std::integral_constant;
-  auto go = [&](auto v) {
-    if (!vec) return f(v, std::false_type(), integral_constant<int, 0>());
-    if (s.depth == 3) return f(v, std::true_type(), integral_constant<int, 3>());
-    if (s.depth == 2) return f(v, std::true_type(), integral_constant<int, 2>());
-    return f(v, std::true_type(), integral_constant<int, 0>());
+  auto go = [&](auto v, auto t) {
+    if (!vec) return f(v, std::false_type(), integral_constant<int, 0>(), t);
+    if (s.depth == 3) return f(v, std::true_type(), integral_constant<int, 3>(), t);
+    if (s.depth == 2) return f(v, std::true_type(), integral_constant<int, 2>(), t);
+    return f(v, std::true_type(), integral_constant<int, 0>(), t);
   };
-  if (s.v == 1) return go(integral_constant<int, 1>());
-  if (s.v == 2) return go(integral_constant<int, 2>());
-  return go(integral_constant<int, 4>());
+  if (s.v == 1) return go(integral_constant<int, 1>(), integral_constant<int, 512>());
+  if (s.v == 2 && s.threads <= 256) return go(integral_constant<int, 2>(), integral_constant<int, 256>());
+  if (s.v == 2) return go(integral_constant<int, 2>(), integral_constant<int, 512>());
+  return go(integral_constant<int, 4>(), integral_constant<int, 512>());
 }
 
 template <typename K, typename T>
@@ -483,15 +538,19 @@ int launch(K kern, int grid, const Shape& s, const Args<T>& a, cudaStream_t st) 
   return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
+constexpr int kForward1 = 3, kForward2 = 5, kBackward1 = 2, kBackward2 = 2;  // CTAs an SM holds, see shape_of
+
 template <typename T>
 int forward(Args<T> a, cudaStream_t st) {
   const bool vec = a.H % 8 == 0 && aligned16(a.x) && aligned16(a.block) && aligned16(a.w_post) &&
                    aligned16(a.w_pre) && aligned16(a.y) && aligned16(a.xn) &&
                    (a.gate_kind != MOE_GATE_CHANNEL || aligned16(a.gate));
-  const Shape s = shape_of(a.H, (int)sizeof(T), vec, 2, 3, a.rows);
+  const Shape s = shape_of(a.H, (int)sizeof(T), vec, 2, 0, kForward1, kForward2, a.rows);
   const int grid = s.depth ? std::min(a.rows, s.ctas * device_info().sm_count) : a.rows;
-  return dispatch(s, vec, [&](auto v, auto w, auto d) {
-    return launch(block_norm_kernel<T, decltype(v)::value, decltype(w)::value, decltype(d)::value>, grid, s, a, st);
+  return dispatch(s, vec, [&](auto v, auto w, auto d, auto t) {
+    constexpr int V = decltype(v)::value, MAXT = decltype(t)::value;
+    constexpr int MINB = V == 1 ? kForward1 : MAXT == 256 ? kForward2 : 1;
+    return launch(block_norm_kernel<T, V, decltype(w)::value, decltype(d)::value, MAXT, MINB>, grid, s, a, st);
   });
 }
 
@@ -500,11 +559,13 @@ int backward(Args<T> a, float* dw_post, float* dw_pre, cudaStream_t st) {
   const bool vec = a.H % 8 == 0 && aligned16(a.x) && aligned16(a.block) && aligned16(a.w_post) &&
                    aligned16(a.w_pre) && aligned16(a.dy) && aligned16(a.dxn) && aligned16(a.dx) &&
                    aligned16(a.dblock) && (a.gate_kind != MOE_GATE_CHANNEL || aligned16(a.gate));
-  const Shape s = shape_of(a.H, (int)sizeof(T), vec, 4, 2, a.rows);
+  const Shape s = shape_of(a.H, (int)sizeof(T), vec, 4, 2, kBackward1, kBackward2, a.rows);
   const int parts = std::min({a.rows, kMaxParts, s.ctas * device_info().sm_count});
-  const int r = dispatch(s, vec, [&](auto v, auto w, auto d) {
-    return launch(block_norm_backward_kernel<T, decltype(v)::value, decltype(w)::value, decltype(d)::value>, parts, s,
-                  a, st);
+  const int r = dispatch(s, vec, [&](auto v, auto w, auto d, auto t) {
+    constexpr int V = decltype(v)::value, MAXT = decltype(t)::value;
+    constexpr int MINB = V == 1 ? kBackward1 : MAXT == 256 ? kBackward2 : 1;
+    return launch(block_norm_backward_kernel<T, V, decltype(w)::value, decltype(d)::value, MAXT, MINB>, parts, s, a,
+                  st);
   });
   if (r) return r;
   const dim3 grid((a.H + 31) / 32, 2);
