@@ -400,9 +400,9 @@ moe_status moe_mx_dequantize(int32_t dtype, int64_t rows, int64_t cols, const ui
  * The T tokens fall into nseq segments: token t belongs to segment b when
  * seq_offsets[b] <= t < seq_offsets[b+1] (ascending; device; NULL with nseq = 1:
  * one segment of all tokens).  Tokens outside every segment, and tokens with
- * valid[t] = 0 (valid [T] bytes, device, NULL: all valid), take no part: their
- * logits and ids are not read and their gradient is 0.  For the n tokens that
- * are left in a segment:
+ * valid[t] = 0 (valid [T] bytes, device, NULL: all valid), take no part, whatever
+ * their logits and ids are, and their gradient is 0.  For the n tokens that are
+ * left in a segment:
  *   p_t = softmax(l_t), or sigmoid(l_t) / sum_e sigmoid(l_te)    (score)
  *   counts[b][e] = ids equal to e among them,  prob_sum[b][e] = sum_t p_te
  *   tokens[b] = n,  loss[b] = coef * E / (K n^2) * sum_e counts * prob_sum

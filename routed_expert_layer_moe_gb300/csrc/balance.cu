@@ -18,7 +18,6 @@
 // every piece, because along the tokens i and b only grow and at least one of them does from
 // one piece to the next.  A second kernel adds each segment's rows in a fixed order.
 #include <algorithm>
-#include <climits>
 #include <type_traits>
 
 #include "common.cuh"
@@ -28,9 +27,8 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kChunk = 8;         // experts of one CTA of the second kernel: a 32-byte sector of a row
-constexpr int kFinishThreads = 512;
-constexpr int kFinishRows = kFinishThreads / kChunk;  // partial rows it reads at a time
+constexpr int kFinishThreads = 512;  // of the second kernel
+constexpr int kMinChunk = 8;         // experts of one of its CTAs at least: a 32-byte sector of a row
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Tokens of one tile: about three tiles per SM, at least 32 (each tile costs the second kernel a row).
@@ -52,16 +50,19 @@ struct Segments {
   int nseq, T;
   __device__ __forceinline__ int lo(int b) const { return off ? max(__ldg(off + b), 0) : 0; }
   __device__ __forceinline__ int hi(int b) const { return off ? min(__ldg(off + b + 1), T) : T; }
-  // The last segment that starts at or before t (the one that holds t, if any does); 0 if none.
+  // The last segment that starts at or before t (the one that holds t, if any does); 0 if none.  By a
+  // whole warp, the same t in every lane: 32 places are looked at together, for one after the other each
+  // costs the memory's latency (six of them for 48 segments).
   __device__ __forceinline__ int find(int t) const {
     if (!off) return 0;
-    int a = 0, z = nseq;
-    while (z - a > 1) {
-      const int m = (a + z) >> 1;
-      if (__ldg(off + m) <= t)
-        a = m;
-      else
-        z = m;
+    const int lane = threadIdx.x & 31;
+    int a = 0, n = nseq;
+    while (n > 1) {
+      const int step = (n + 31) / 32, i = lane * step;
+      const bool before = i < n && __ldg(off + a + i) <= t;
+      const int k = 31 - __clz(__ballot_sync(0xffffffffu, before) | 1u);  // the last place at or before t
+      a += k * step;
+      n = min(step, n - k * step);
     }
     return a;
   }
@@ -88,23 +89,41 @@ __device__ __forceinline__ int expert_of(int j, int sub) {
   return VEC ? (j >> 2) * 4 * L + sub * 4 + (j & 3) : j * L + sub;
 }
 
-// One token's logits, N registers a lane (N L >= E); -inf past the last expert and, without
-// `live`, everywhere.
-template <int N, int L, bool VEC>
-__device__ __forceinline__ void load_row(const float* row, int E, int sub, bool live, float (&l)[N]) {
+// A lane's N values of a row, as pairs: the arithmetic is on pairs (fp32x2 instructions).
+template <int N>
+struct Row {
+  float2 v[N / 2];
+  __device__ __forceinline__ float get(int j) const { return j & 1 ? v[j / 2].y : v[j / 2].x; }
+  __device__ __forceinline__ void set(int j, float x) {
+    if (j & 1)
+      v[j / 2].y = x;
+    else
+      v[j / 2].x = x;
+  }
+  __device__ __forceinline__ void fill(float x) {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) v[i] = make_float2(x, x);
+  }
+};
+
+// One token's logits (N L >= E); -inf past the last expert.  FULL: N L = E, float4 rows.  A masked token's
+// are loaded too (and dropped before use): waiting for its mask first would put two memory
+// latencies one after the other.
+template <int N, int L, bool VEC, bool FULL>
+__device__ __forceinline__ void load_row(const float* row, int E, int sub, Row<N>& l) {
   if constexpr (VEC) {
 #pragma unroll
     for (int c = 0; c < N / 4; ++c) {
       const int e = c * 4 * L + sub * 4;
       float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-      if (live && e < E) v = __ldg(reinterpret_cast<const float4*>(row + e));
-      l[4 * c] = v.x, l[4 * c + 1] = v.y, l[4 * c + 2] = v.z, l[4 * c + 3] = v.w;
+      if (FULL || e < E) v = __ldg(reinterpret_cast<const float4*>(row + e));
+      l.v[2 * c] = make_float2(v.x, v.y), l.v[2 * c + 1] = make_float2(v.z, v.w);
     }
   } else {
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       const int e = j * L + sub;
-      l[j] = live && e < E ? __ldg(row + e) : -INFINITY;
+      l.set(j, e < E ? __ldg(row + e) : -INFINITY);
     }
   }
 }
@@ -123,33 +142,42 @@ __device__ __forceinline__ float fast_rcp(float x) {
   return r;
 }
 
-// l -> unnormalised scores in place; returns 1 / their sum (0 for a row with nothing in it).
+// Unnormalised scores a of the logits l; returns this lane's part of their sum.
 template <int N, int L, bool SIG>
-__device__ __forceinline__ float scores(float (&l)[N]) {
-  float z = 0.0f;
+__device__ __forceinline__ float scores(const Row<N>& l, Row<N>& a) {
+  float2 z = make_float2(0.0f, 0.0f);
   if constexpr (SIG) {
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      l[j] = fast_rcp(1.0f + fast_exp2(-l[j] * kLog2e));
-      z += l[j];
+    for (int i = 0; i < N / 2; ++i) {
+      float2 t = __fmul2_rn(l.v[i], make_float2(-kLog2e, -kLog2e));
+      t = __fadd2_rn(make_float2(fast_exp2(t.x), fast_exp2(t.y)), make_float2(1.0f, 1.0f));
+      a.v[i] = make_float2(fast_rcp(t.x), fast_rcp(t.y));
+      z = __fadd2_rn(z, a.v[i]);
     }
   } else {
     float m = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < N; ++j) m = fmaxf(m, l[j]);
+    for (int i = 0; i < N / 2; ++i) m = fmaxf(m, fmaxf(l.v[i].x, l.v[i].y));
     m = group_max<L>(m);
-    const float b = m == -INFINITY ? 0.0f : m * kLog2e;
+    const float b = m == -INFINITY ? 0.0f : -m * kLog2e;
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      l[j] = fast_exp2(fmaf(l[j], kLog2e, -b));
-      z += l[j];
+    for (int i = 0; i < N / 2; ++i) {
+      const float2 t = __ffma2_rn(l.v[i], make_float2(kLog2e, kLog2e), make_float2(b, b));
+      a.v[i] = make_float2(fast_exp2(t.x), fast_exp2(t.y));
+      z = __fadd2_rn(z, a.v[i]);
     }
   }
+  return z.x + z.y;
+}
+
+// 1 / the sum over the group; 0 for a row with nothing in it.
+template <int L>
+__device__ __forceinline__ float inverse_sum(float z) {
   z = group_sum<L>(z);
   return z == 0.0f ? 0.0f : 1.0f / z;
 }
 
-template <int N, int L, bool VEC, bool SIG>
+template <int N, int L, bool VEC, bool SIG, bool FULL>
 __global__ void __launch_bounds__(kThreads, N > 16 ? 2 : kTilesPerSm)
     balance_partial_kernel(const float* __restrict__ logits, const int32_t* __restrict__ ids,
                            const uint8_t* __restrict__ valid, Segments seg, int E, int K, int tile,
@@ -165,63 +193,65 @@ __global__ void __launch_bounds__(kThreads, N > 16 ? 2 : kTilesPerSm)
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b < seg.nseq; b += kThreads) done[b] = 0;  // the second kernel's counters
   int flags = 0;
-  int t = max(t0, seg.lo(0));
+  int t = t0;
   while (t < t1) {
     const int b = seg.find(t);
+    t = max(t, seg.lo(b));  // tokens before the first segment
     const int end = min(t1, seg.hi(b));
     if (end <= t) break;  // past the last segment
     for (int e = threadIdx.x; e < E; e += kThreads) cnt[e] = 0;
     if (threadIdx.x == 0) ntok = 0;
     __syncthreads();
-    float acc[N];
-#pragma unroll
-    for (int j = 0; j < N; ++j) acc[j] = 0.0f;
+    Row<N> acc;
+    acc.fill(0.0f);
     int mine = 0;
     // u: this lane's token of the step at w; its row and ids are requested while the step before it
-    // is worked on
+    // is worked on (past the piece's end: the last token's, which are not used)
     constexpr int Q = 32 / L;  // ids a lane counts: K <= 32
     bool next_live = false;
-    float next[N];
+    Row<N> next;
     int next_id[Q];
     auto request = [&](int u) {
-      next_live = u < end && !(valid && !__ldg(valid + u));
-      load_row<N, L, VEC>(logits + (size_t)u * E, E, sub, next_live, next);
+      const int r = min(u, end - 1);
+      next_live = u < end && (!valid || __ldg(valid + r));
+      load_row<N, L, VEC, FULL>(logits + (size_t)r * E, E, sub, next);
 #pragma unroll
       for (int q = 0; q < Q; ++q)
-        next_id[q] = next_live && sub + q * L < K ? __ldg(ids + (size_t)u * K + sub + q * L) : INT_MIN;
+        if (sub + q * L < K) next_id[q] = __ldg(ids + (size_t)r * K + sub + q * L);
     };
     const int first = t + warp * G;
     if (first < end) request(first + grp);
     for (int w = first; w < end; w += kWarps * G) {  // the same steps for every lane of a warp
-      float l[N];
+      const bool live = next_live;
+      if (!__all_sync(0xffffffffu, live) && !live) next.fill(-INFINITY);
+      Row<N> a;
+      float z = scores<N, L, SIG>(next, a);
+      mine += live && sub == 0;
       int id[Q];
 #pragma unroll
-      for (int j = 0; j < N; ++j) l[j] = next[j];
-#pragma unroll
       for (int q = 0; q < Q; ++q) id[q] = next_id[q];
-      mine += next_live && sub == 0;
-      const bool live = next_live;
       if (w + kWarps * G < end) request(w + kWarps * G + grp);
 #pragma unroll
       for (int q = 0; q < Q; ++q) {
         if (live && sub + q * L < K) {
-          if (id[q] >= 0 && id[q] < E)
+          if ((unsigned)id[q] < (unsigned)E)
             atomicAdd(&cnt[id[q]], 1);
           else
             flags = MOE_FLAG_BAD_EXPERT;
         }
       }
-      const float inv = scores<N, L, SIG>(l);
+      const float inv = inverse_sum<L>(z);
 #pragma unroll
-      for (int j = 0; j < N; ++j) acc[j] = fmaf(l[j], inv, acc[j]);
+      for (int i = 0; i < N / 2; ++i) acc.v[i] = __ffma2_rn(a.v[i], make_float2(inv, inv), acc.v[i]);
     }
     if (mine) atomicAdd(&ntok, mine);
 #pragma unroll
     for (int j = 0; j < N; ++j) {
+      float sum = acc.get(j);
 #pragma unroll
-      for (int o = L; o < 32; o <<= 1) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], o);
+      for (int o = L; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       const int e = expert_of<L, VEC>(j, sub);
-      if (grp == 0 && e < E) red[warp * E + e] = acc[j];
+      if (grp == 0 && e < E) red[warp * E + e] = sum;
     }
     __syncthreads();
     const size_t row = (size_t)blockIdx.x + b;
@@ -239,26 +269,29 @@ __global__ void __launch_bounds__(kThreads, N > 16 ? 2 : kTilesPerSm)
   if (flags) atomicOr(err, flags);
 }
 
-// One CTA per (segment, kChunk experts): adds the segment's rows; the segment's last CTA adds the
-// chunks' parts of the loss in order.  Few CTAs work when there is one segment, each held by the
-// latency of its loads, so a CTA takes 64 rows at a time (16 rows of 32 experts: 12.6 us for
-// 456 rows of 512 experts).
+// One CTA per (segment, CHUNK experts): adds the segment's rows, ROWS at a time; the segment's last
+// CTA adds the chunks' parts of the loss in order.  Each CTA is held by the latency of its loads: few
+// segments of many rows take 8 experts and 64 rows (with 32 experts and 16 rows 456 rows of 512
+// experts took 12.6 us, not 6.3), many segments of few rows the other way round (4.7 us for 48
+// segments of 256 experts, not 9.2).
+template <int CHUNK>
 __global__ void __launch_bounds__(kFinishThreads)
     balance_finish_kernel(Segments seg, int E, int K, int tile, float coef, const float* __restrict__ part_p,
                           const int32_t* __restrict__ part_c, const int32_t* __restrict__ part_n,
                           float* __restrict__ loss_part, int32_t* done, float* __restrict__ loss,
                           int32_t* __restrict__ counts, float* __restrict__ prob_sum, int32_t* __restrict__ tokens) {
-  __shared__ float sp[kFinishRows][kChunk];
-  __shared__ int sc[kFinishRows][kChunk];
-  __shared__ int sn[kFinishRows];
-  const int b = blockIdx.y, col = threadIdx.x % kChunk, g = threadIdx.x / kChunk;
-  int e = blockIdx.x * kChunk + col;
+  constexpr int ROWS = kFinishThreads / CHUNK;
+  __shared__ float sp[ROWS][CHUNK];
+  __shared__ int sc[ROWS][CHUNK];
+  __shared__ int sn[ROWS];
+  const int b = blockIdx.y, col = threadIdx.x % CHUNK, g = threadIdx.x / CHUNK;
+  int e = blockIdx.x * CHUNK + col;
   const int lo = seg.lo(b), hi = seg.hi(b);
   const int i0 = lo / tile, i1 = hi > lo ? (hi - 1) / tile : i0 - 1;
   float p = 0.0f;
   int c = 0, n = 0;
 #pragma unroll 4
-  for (int i = i0 + g; i <= i1; i += kFinishRows) {
+  for (int i = i0 + g; i <= i1; i += ROWS) {
     const size_t row = (size_t)i + b;
     if (e < E) {
       p += __ldg(part_p + row * E + e);
@@ -271,25 +304,25 @@ __global__ void __launch_bounds__(kFinishThreads)
   if (col == 0) sn[g] = n;
   __syncthreads();
   if (threadIdx.x >= 32) return;
-  // one warp: four groups of rows for each expert, then their sum
+  // one warp: 32 / CHUNK groups of rows for each expert, then their sum
   const int lane = threadIdx.x;
-  p = 0.0f, c = 0;
+  p = 0.0f, c = 0, n = 0;
 #pragma unroll
-  for (int i = 0; i < kFinishRows / 4; ++i) {
-    p += sp[4 * i + g][col];
-    c += sc[4 * i + g][col];
+  for (int i = g; i < ROWS; i += 32 / CHUNK) {
+    p += sp[i][col];
+    c += sc[i][col];
   }
-  n = sn[lane] + sn[lane + 32];
-  static_assert(kFinishRows == 64 && kChunk == 8, "the warp above covers 4 x 8 and 2 x 32 values");
+#pragma unroll
+  for (int i = lane; i < ROWS; i += 32) n += sn[i];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    if (o >= kChunk) {
+    if (o >= CHUNK) {
       p += __shfl_xor_sync(0xffffffffu, p, o);
       c += __shfl_xor_sync(0xffffffffu, c, o);
     }
     n += __shfl_xor_sync(0xffffffffu, n, o);
   }
-  if (lane >= kChunk) e = E;  // the sums are there four times over
+  if (lane >= CHUNK) e = E;  // the sums are there several times over
   if (e < E) {
     counts[(size_t)b * E + e] = c;
     prob_sum[(size_t)b * E + e] = p;
@@ -313,7 +346,7 @@ __global__ void __launch_bounds__(kFinishThreads)
   }
 }
 
-template <int N, int L, bool VEC, bool SIG>
+template <int N, int L, bool VEC, bool SIG, bool FULL>
 __global__ void __launch_bounds__(kThreads, N > 16 ? 2 : kTilesPerSm)
     balance_backward_kernel(const float* __restrict__ logits, const uint8_t* __restrict__ valid, Segments seg, int E,
                             int K, int tile, float coef, const int32_t* __restrict__ counts,
@@ -322,74 +355,88 @@ __global__ void __launch_bounds__(kThreads, N > 16 ? 2 : kTilesPerSm)
   constexpr int G = 32 / L;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % L, grp = lane / L;
   const int t0 = blockIdx.x * tile, t1 = min(seg.T, t0 + tile);
-  float v[N];
-#pragma unroll
-  for (int j = 0; j < N; ++j) v[j] = 0.0f;
+  Row<N> v;
+  v.fill(0.0f);
   int lo = 0, hi = 0;  // the segment that v belongs to
-  auto is_live = [&](int t) { return t < t1 && !(valid && !__ldg(valid + t)); };
+  bool next_live = false;
+  Row<N> next;
+  auto request = [&](int t) {  // past the tile's end: the last token's row, which is not used
+    const int r = min(t, t1 - 1);
+    next_live = t < t1 && (!valid || __ldg(valid + r));
+    load_row<N, L, VEC, FULL>(logits + (size_t)r * E, E, sub, next);
+  };
   const int first = t0 + warp * G;
-  bool next_live = is_live(first + grp);
-  float next[N];
-  if (first < t1) load_row<N, L, VEC>(logits + (size_t)(first + grp) * E, E, sub, next_live, next);
+  if (first < t1) request(first + grp);
   for (int w = first; w < t1; w += kWarps * G) {  // the same steps for every lane of a warp
     const int t = w + grp;
     bool live = next_live;
-    float l[N];
-#pragma unroll
-    for (int j = 0; j < N; ++j) l[j] = next[j];
-    if (w + kWarps * G < t1) {
-      next_live = is_live(t + kWarps * G);
-      load_row<N, L, VEC>(logits + (size_t)(t + kWarps * G) * E, E, sub, next_live, next);
-    }
+    if (!__all_sync(0xffffffffu, live) && !live) next.fill(-INFINITY);
+    Row<N> a;
+    const float z = scores<N, L, SIG>(next, a);
+    if (w + kWarps * G < t1) request(t + kWarps * G);
     const bool move = live && (t < lo || t >= hi);
-    if (__any_sync(0xffffffffu, move)) {
+    unsigned moving = __ballot_sync(0xffffffffu, move);
+    if (moving) {
       int b = 0;
-      if (move) {
-        b = seg.find(t);
-        lo = seg.lo(b), hi = seg.hi(b);
-        if (t < lo || t >= hi) lo = hi = 0;  // in no segment
-      }
+      do {  // the segments of the tokens that left theirs, one token after the other
+        const int other = __shfl_sync(0xffffffffu, t, __ffs(moving) - 1);
+        const int s = seg.find(other), slo = seg.lo(s), shi = seg.hi(s);
+        const bool mine = move && (t == other || (t >= slo && t < shi));
+        if (mine) {
+          b = s;
+          lo = slo, hi = shi;
+          if (t < lo || t >= hi) lo = hi = 0;  // in no segment
+        }
+        moving &= ~__ballot_sync(0xffffffffu, mine);
+      } while (moving);
       const bool fresh = move && hi > lo;
-      float c[N], sum = 0.0f;
+      Row<N> c;
+      float sum = 0.0f;
 #pragma unroll
       for (int j = 0; j < N; ++j) {
         const int e = expert_of<L, VEC>(j, sub);
-        c[j] = fresh && e < E ? (float)__ldg(counts + (size_t)b * E + e) : 0.0f;
-        sum += c[j];
+        c.set(j, fresh && e < E ? (float)__ldg(counts + (size_t)b * E + e) : 0.0f);
+        sum += c.get(j);
       }
       const float mean = group_sum<L>(sum) / (float)E;
       if (fresh) {
         const float fn = (float)max(__ldg(tokens + b), 1);
         const float scale = coef * (float)E / ((float)K * fn * fn) * __ldg(dloss + b);
 #pragma unroll
-        for (int j = 0; j < N; ++j) v[j] = (c[j] - mean) * scale;
+        for (int j = 0; j < N; ++j) v.set(j, (c.get(j) - mean) * scale);
       }
     }
     live = live && t >= lo && t < hi;
-    const float inv = scores<N, L, SIG>(l);
-    float dot = 0.0f;
+    const float inv = inverse_sum<L>(z);
+    float2 d2 = make_float2(0.0f, 0.0f);
+    Row<N> g;  // the scores, then the gradient
 #pragma unroll
-    for (int j = 0; j < N; ++j) dot = fmaf(l[j] * inv, v[j], dot);
-    dot = group_sum<L>(dot);
+    for (int i = 0; i < N / 2; ++i) {
+      g.v[i] = __fmul2_rn(a.v[i], make_float2(inv, inv));
+      d2 = __ffma2_rn(g.v[i], v.v[i], d2);
+    }
+    const float dot = group_sum<L>(d2.x + d2.y);
     if (t >= t1) continue;
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const float d = l[j] * inv * (v[j] - dot);
-      l[j] = live ? (SIG ? d * (1.0f - l[j]) : d) : 0.0f;
+    for (int i = 0; i < N / 2; ++i) {
+      g.v[i] = __fmul2_rn(g.v[i], __fadd2_rn(v.v[i], make_float2(-dot, -dot)));
+      if (SIG) g.v[i] = __fmul2_rn(g.v[i], __ffma2_rn(a.v[i], make_float2(-1.0f, -1.0f), make_float2(1.0f, 1.0f)));
     }
+    if (!live) g.fill(0.0f);
     float* dst = dlogits + (size_t)t * E;
     if constexpr (VEC) {
 #pragma unroll
       for (int c = 0; c < N / 4; ++c) {
         const int e = c * 4 * L + sub * 4;
-        if (e < E)
-          *reinterpret_cast<float4*>(dst + e) = make_float4(l[4 * c], l[4 * c + 1], l[4 * c + 2], l[4 * c + 3]);
+        if (FULL || e < E)
+          *reinterpret_cast<float4*>(dst + e) =
+              make_float4(g.v[2 * c].x, g.v[2 * c].y, g.v[2 * c + 1].x, g.v[2 * c + 1].y);
       }
     } else {
 #pragma unroll
       for (int j = 0; j < N; ++j) {
         const int e = j * L + sub;
-        if (e < E) dst[e] = l[j];
+        if (e < E) dst[e] = g.get(j);
       }
     }
   }
@@ -417,24 +464,31 @@ Work carve(const moe_problem& p, int nseq, void* ws) {
   w.part_p = reinterpret_cast<float*>(take(rows * p.E * 4));
   w.part_c = reinterpret_cast<int32_t*>(take(rows * p.E * 4));
   w.part_n = reinterpret_cast<int32_t*>(take(rows * 4));
-  w.loss_part = reinterpret_cast<float*>(take((size_t)nseq * ((p.E + kChunk - 1) / kChunk) * 4));
+  w.loss_part = reinterpret_cast<float*>(take((size_t)nseq * ((p.E + kMinChunk - 1) / kMinChunk) * 4));
   w.done = reinterpret_cast<int32_t*>(take((size_t)nseq * 4));
   w.bytes = off;
   return w;
 }
 
-// f(registers a lane, lanes a token, float4 rows, sigmoid) with compile-time arguments.  float4
-// rows need E a multiple of 4 and 16-byte aligned arrays.
+// f(registers a lane, lanes a token, float4 rows, sigmoid, rows that fill the registers) with
+// compile-time arguments.  float4 rows need E a multiple of 4 and 16-byte aligned arrays.
 template <typename F>
 int dispatch(int E, bool vec, int score, F f) {
   auto n = [&](auto v, auto s) {
+    constexpr bool V = decltype(v)::value;
+    auto full = [&](auto nn, auto l) {
+      if constexpr (V) {
+        if (E == decltype(nn)::value * decltype(l)::value) return f(nn, l, v, s, std::true_type());
+      }
+      return f(nn, l, v, s, std::false_type());
+    };
     using std::integral_constant;
-    if (E <= 32) return f(integral_constant<int, 4>(), integral_constant<int, 8>(), v, s);
-    if (E <= 64) return f(integral_constant<int, 8>(), integral_constant<int, 8>(), v, s);
-    if (E <= 128) return f(integral_constant<int, 16>(), integral_constant<int, 8>(), v, s);
-    if (E <= 256) return f(integral_constant<int, 16>(), integral_constant<int, 16>(), v, s);
-    if (E <= 512) return f(integral_constant<int, 16>(), integral_constant<int, 32>(), v, s);
-    return f(integral_constant<int, 32>(), integral_constant<int, 32>(), v, s);
+    if (E <= 32) return full(integral_constant<int, 4>(), integral_constant<int, 8>());
+    if (E <= 64) return full(integral_constant<int, 8>(), integral_constant<int, 8>());
+    if (E <= 128) return full(integral_constant<int, 16>(), integral_constant<int, 8>());
+    if (E <= 256) return full(integral_constant<int, 16>(), integral_constant<int, 16>());
+    if (E <= 512) return full(integral_constant<int, 16>(), integral_constant<int, 32>());
+    return full(integral_constant<int, 32>(), integral_constant<int, 32>());
   };
   auto s = [&](auto v) {
     return score == MOE_SCORE_SIGMOID ? n(v, std::true_type()) : n(v, std::false_type());
@@ -457,16 +511,23 @@ int launch_balance(const moe_problem& p, const float* logits, const int32_t* ids
   const int tiles = p.T > 0 ? (p.T + tile - 1) / tile : 1;  // an empty batch: one CTA clears the counters
   const bool vec = p.E % 4 == 0 && aligned16(logits);
   const size_t smem = (size_t)(kWarps + 1) * p.E * 4;
-  const int r = dispatch(p.E, vec, score, [&](auto n, auto l, auto v, auto s) {
-    auto kern = balance_partial_kernel<decltype(n)::value, decltype(l)::value, decltype(v)::value, decltype(s)::value>;
+  const int r = dispatch(p.E, vec, score, [&](auto n, auto l, auto v, auto s, auto full) {
+    auto kern = balance_partial_kernel<decltype(n)::value, decltype(l)::value, decltype(v)::value, decltype(s)::value,
+                                  decltype(full)::value>;
     kern<<<tiles, kThreads, smem, st>>>(
         logits, ids, valid, seg, p.E, p.K, tile, w.part_p, w.part_c, w.part_n, w.done, err);
     return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
   });
   if (r) return r;
-  const dim3 grid((p.E + kChunk - 1) / kChunk, nseq);
-  balance_finish_kernel<<<grid, kFinishThreads, 0, st>>>(seg, p.E, p.K, tile, coef, w.part_p, w.part_c, w.part_n,
-                                                   w.loss_part, w.done, loss, counts, prob_sum, tokens);
+  auto finish = [&](auto chunk) {
+    constexpr int C = decltype(chunk)::value;
+    balance_finish_kernel<C><<<dim3((p.E + C - 1) / C, nseq), kFinishThreads, 0, st>>>(
+        seg, p.E, p.K, tile, coef, w.part_p, w.part_c, w.part_n, w.loss_part, w.done, loss, counts, prob_sum, tokens);
+  };
+  if (tiles / nseq >= 32)
+    finish(std::integral_constant<int, kMinChunk>());
+  else
+    finish(std::integral_constant<int, 32>());
   return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -478,8 +539,9 @@ int launch_balance_backward(const moe_problem& p, const float* logits, const uin
   const int tile = tile_tokens(p.T);
   const int tiles = (p.T + tile - 1) / tile;
   const bool vec = p.E % 4 == 0 && aligned16(logits) && aligned16(dlogits);
-  return dispatch(p.E, vec, score, [&](auto n, auto l, auto v, auto s) {
-    auto kern = balance_backward_kernel<decltype(n)::value, decltype(l)::value, decltype(v)::value, decltype(s)::value>;
+  return dispatch(p.E, vec, score, [&](auto n, auto l, auto v, auto s, auto full) {
+    auto kern = balance_backward_kernel<decltype(n)::value, decltype(l)::value, decltype(v)::value, decltype(s)::value,
+                                  decltype(full)::value>;
     kern<<<tiles, kThreads, 0, st>>>(
         logits, valid, seg, p.E, p.K, tile, coef, counts, tokens, dloss, dlogits);
     return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
