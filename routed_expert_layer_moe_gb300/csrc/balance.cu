@@ -50,21 +50,33 @@ struct Segments {
   int nseq, T;
   __device__ __forceinline__ int lo(int b) const { return off ? max(__ldg(off + b), 0) : 0; }
   __device__ __forceinline__ int hi(int b) const { return off ? min(__ldg(off + b + 1), T) : T; }
-  // The last segment that starts at or before t (the one that holds t, if any does); 0 if none.  By a
-  // whole warp, the same t in every lane: 32 places are looked at together, for one after the other each
-  // costs the memory's latency (six of them for 48 segments).
-  __device__ __forceinline__ int find(int t) const {
-    if (!off) return 0;
+  // The last segment that starts at or before t (the one that holds t, if any does; 0 if none does), with
+  // its bounds.  By a whole warp, the same t in every lane: many places are looked at together, for
+  // one after the other each costs the memory's latency (six of them for 48 segments).
+  __device__ __forceinline__ int find(int t, int& first, int& end) const {
+    if (!off) {
+      first = 0, end = T;
+      return 0;
+    }
     const int lane = threadIdx.x & 31;
     int a = 0, n = nseq;
-    while (n > 1) {
+    while (n > 63) {  // 32 steps through what is left
       const int step = (n + 31) / 32, i = lane * step;
       const bool before = i < n && __ldg(off + a + i) <= t;
       const int k = 31 - __clz(__ballot_sync(0xffffffffu, before) | 1u);  // the last place at or before t
       a += k * step;
       n = min(step, n - k * step);
     }
-    return a;
+    // all that is left, and the end of its last segment
+    const int v0 = lane <= n ? __ldg(off + a + lane) : 0, v1 = lane + 32 <= n ? __ldg(off + a + lane + 32) : 0;
+    const unsigned m0 = __ballot_sync(0xffffffffu, lane < n && v0 <= t);
+    const unsigned m1 = __ballot_sync(0xffffffffu, lane + 32 < n && v1 <= t);
+    const int k = m1 ? 63 - __clz(m1) : 31 - __clz(m0 | 1u);
+    const int lo0 = __shfl_sync(0xffffffffu, v0, k & 31), lo1 = __shfl_sync(0xffffffffu, v1, k & 31);
+    const int hi0 = __shfl_sync(0xffffffffu, v0, (k + 1) & 31), hi1 = __shfl_sync(0xffffffffu, v1, (k + 1) & 31);
+    first = max(k < 32 ? lo0 : lo1, 0);
+    end = min(k + 1 < 32 ? hi0 : hi1, T);
+    return a + k;
   }
 };
 
@@ -192,37 +204,40 @@ __global__ void __launch_bounds__(kThreads, N > 16 ? 2 : kTilesPerSm)
   const int t0 = blockIdx.x * tile, t1 = min(seg.T, t0 + tile);
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b < seg.nseq; b += kThreads) done[b] = 0;  // the second kernel's counters
+  grid_dependents_launch();  // the second kernel's CTAs may wait on the SMs
   int flags = 0;
+  // u: this lane's token of the step at w; its row and ids are requested while the step before it is
+  // worked on, those of the tile's first step while its segment is looked up (past the tile's
+  // end: the last token's, which are not used)
+  constexpr int Q = 32 / L;  // ids a lane counts: K <= 32
+  bool next_valid = false;
+  Row<N> next;
+  int next_id[Q];
+  auto request = [&](int u) {
+    const int r = min(u, t1 - 1);
+    next_valid = !valid || __ldg(valid + r);
+    load_row<N, L, VEC, FULL>(logits + (size_t)r * E, E, sub, next);
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+      if (sub + q * L < K) next_id[q] = __ldg(ids + (size_t)r * K + sub + q * L);
+  };
   int t = t0;
+  if (t < t1) request(t + warp * G + grp);
   while (t < t1) {
-    const int b = seg.find(t);
-    t = max(t, seg.lo(b));  // tokens before the first segment
-    const int end = min(t1, seg.hi(b));
-    if (end <= t) break;  // past the last segment
+    int lo, hi;
+    const int b = seg.find(t, lo, hi);
+    const int from = max(t, lo), end = min(t1, hi);  // from: past the tokens before the first segment
+    if (end <= from) break;                          // past the last segment
+    if (from != t0) request(from + warp * G + grp);  // not the step that is on its way
+    t = from;
     for (int e = threadIdx.x; e < E; e += kThreads) cnt[e] = 0;
     if (threadIdx.x == 0) ntok = 0;
     __syncthreads();
     Row<N> acc;
     acc.fill(0.0f);
     int mine = 0;
-    // u: this lane's token of the step at w; its row and ids are requested while the step before it
-    // is worked on (past the piece's end: the last token's, which are not used)
-    constexpr int Q = 32 / L;  // ids a lane counts: K <= 32
-    bool next_live = false;
-    Row<N> next;
-    int next_id[Q];
-    auto request = [&](int u) {
-      const int r = min(u, end - 1);
-      next_live = u < end && (!valid || __ldg(valid + r));
-      load_row<N, L, VEC, FULL>(logits + (size_t)r * E, E, sub, next);
-#pragma unroll
-      for (int q = 0; q < Q; ++q)
-        if (sub + q * L < K) next_id[q] = __ldg(ids + (size_t)r * K + sub + q * L);
-    };
-    const int first = t + warp * G;
-    if (first < end) request(first + grp);
-    for (int w = first; w < end; w += kWarps * G) {  // the same steps for every lane of a warp
-      const bool live = next_live;
+    for (int w = t + warp * G; w < end; w += kWarps * G) {  // the same steps for every lane of a warp
+      const bool live = next_valid && w + grp < end;
       if (!__all_sync(0xffffffffu, live) && !live) next.fill(-INFINITY);
       Row<N> a;
       float z = scores<N, L, SIG>(next, a);
@@ -276,11 +291,12 @@ __global__ void __launch_bounds__(kThreads, N > 16 ? 2 : kTilesPerSm)
 // segments of 256 experts, not 9.2).
 template <int CHUNK>
 __global__ void __launch_bounds__(kFinishThreads)
-    balance_finish_kernel(Segments seg, int E, int K, int tile, float coef, const float* __restrict__ part_p,
-                          const int32_t* __restrict__ part_c, const int32_t* __restrict__ part_n,
-                          float* __restrict__ loss_part, int32_t* done, float* __restrict__ loss,
+    balance_finish_kernel(Segments seg, int E, int K, int tile, float coef, const float* part_p, const int32_t* part_c,
+                          const int32_t* part_n, float* loss_part, int32_t* done, float* __restrict__ loss,
                           int32_t* __restrict__ counts, float* __restrict__ prob_sum, int32_t* __restrict__ tokens) {
   constexpr int ROWS = kFinishThreads / CHUNK;
+  grid_dependency_wait();
+  grid_dependents_launch();
   __shared__ float sp[ROWS][CHUNK];
   __shared__ int sc[ROWS][CHUNK];
   __shared__ int sn[ROWS];
@@ -294,10 +310,10 @@ __global__ void __launch_bounds__(kFinishThreads)
   for (int i = i0 + g; i <= i1; i += ROWS) {
     const size_t row = (size_t)i + b;
     if (e < E) {
-      p += __ldg(part_p + row * E + e);
-      c += __ldg(part_c + row * E + e);
+      p += __ldcg(part_p + row * E + e);
+      c += __ldcg(part_c + row * E + e);
     }
-    if (col == 0) n += __ldg(part_n + row);
+    if (col == 0) n += __ldcg(part_n + row);
   }
   sp[g][col] = p;
   sc[g][col] = c;
@@ -352,6 +368,7 @@ __global__ void __launch_bounds__(kThreads, N > 16 ? 2 : kTilesPerSm)
                             int K, int tile, float coef, const int32_t* __restrict__ counts,
                             const int32_t* __restrict__ tokens, const float* __restrict__ dloss,
                             float* __restrict__ dlogits) {
+  grid_dependency_wait();
   constexpr int G = 32 / L;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % L, grp = lane / L;
   const int t0 = blockIdx.x * tile, t1 = min(seg.T, t0 + tile);
@@ -380,7 +397,8 @@ __global__ void __launch_bounds__(kThreads, N > 16 ? 2 : kTilesPerSm)
       int b = 0;
       do {  // the segments of the tokens that left theirs, one token after the other
         const int other = __shfl_sync(0xffffffffu, t, __ffs(moving) - 1);
-        const int s = seg.find(other), slo = seg.lo(s), shi = seg.hi(s);
+        int slo, shi;
+        const int s = seg.find(other, slo, shi);
         const bool mine = move && (t == other || (t >= slo && t < shi));
         if (mine) {
           b = s;
@@ -521,14 +539,20 @@ int launch_balance(const moe_problem& p, const float* logits, const int32_t* ids
   if (r) return r;
   auto finish = [&](auto chunk) {
     constexpr int C = decltype(chunk)::value;
-    balance_finish_kernel<C><<<dim3((p.E + C - 1) / C, nseq), kFinishThreads, 0, st>>>(
-        seg, p.E, p.K, tile, coef, w.part_p, w.part_c, w.part_n, w.loss_part, w.done, loss, counts, prob_sum, tokens);
+    cudaLaunchAttribute attr = overlap_attribute();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((p.E + C - 1) / C, nseq);
+    cfg.blockDim = dim3(kFinishThreads);
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, balance_finish_kernel<C>, seg, (int)p.E, (int)p.K, tile, coef,
+                              (const float*)w.part_p, (const int32_t*)w.part_c, (const int32_t*)w.part_n, w.loss_part,
+                              w.done, loss, counts, prob_sum, tokens) == cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
   };
-  if (tiles / nseq >= 32)
-    finish(std::integral_constant<int, kMinChunk>());
-  else
-    finish(std::integral_constant<int, 32>());
-  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return tiles / nseq >= 32 ? finish(std::integral_constant<int, kMinChunk>()) : finish(std::integral_constant<int, 32>());
 }
 
 int launch_balance_backward(const moe_problem& p, const float* logits, const uint8_t* valid, const int32_t* seq,
@@ -542,9 +566,17 @@ int launch_balance_backward(const moe_problem& p, const float* logits, const uin
   return dispatch(p.E, vec, score, [&](auto n, auto l, auto v, auto s, auto full) {
     auto kern = balance_backward_kernel<decltype(n)::value, decltype(l)::value, decltype(v)::value, decltype(s)::value,
                                   decltype(full)::value>;
-    kern<<<tiles, kThreads, 0, st>>>(
-        logits, valid, seg, p.E, p.K, tile, coef, counts, tokens, dloss, dlogits);
-    return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    cudaLaunchAttribute attr = overlap_attribute();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(tiles);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, logits, valid, seg, (int)p.E, (int)p.K, tile, coef, counts, tokens, dloss,
+                              dlogits) == cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
   });
 }
 

@@ -311,6 +311,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_norm_backward_kernel(const A
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ __align__(16) float buf[2][64];
   enum { X, B, DY, DXN };
+  grid_dependents_launch();  // the second kernel's CTAs may wait on the SMs
   const int H = a.H, nt = blockDim.x;
   const float invH = 1.0f / (float)H;
   const Rows<T, V, VEC, DEPTH, 4> in{{a.x, a.block, a.dy, a.dxn}, H, smem};
@@ -454,16 +455,17 @@ constexpr int kReduceGroups = 16;
 
 template <typename T>
 __global__ void __launch_bounds__(32 * kReduceGroups)
-    block_norm_reduce_kernel(const float* __restrict__ part, int parts, int H, int gate_kind,
+    block_norm_reduce_kernel(const float* part, int parts, int H, int gate_kind,
                              const T* __restrict__ gate, const T* __restrict__ w_post, float rs,
                              float* __restrict__ dgate, float* __restrict__ dw_post, float* __restrict__ dw_pre) {
   __shared__ float sum[kReduceGroups][32];
+  grid_dependency_wait();
   const int lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane, g = threadIdx.x >> 5;
   const bool pre = blockIdx.y != 0;
   float s = 0.0f;
   if (c < H) {
 #pragma unroll 8
-    for (int i = g; i < parts; i += kReduceGroups) s += __ldg(part + ((size_t)i * 2 + pre) * H + c);
+    for (int i = g; i < parts; i += kReduceGroups) s += __ldcg(part + ((size_t)i * 2 + pre) * H + c);
   }
   sum[g][lane] = s;
   __syncthreads();
@@ -569,10 +571,18 @@ int backward(Args<T> a, float* dw_post, float* dw_pre, cudaStream_t st) {
   });
   if (r) return r;
   const dim3 grid((a.H + 31) / 32, 2);
-  block_norm_reduce_kernel<T><<<grid, 32 * kReduceGroups, 0, st>>>(
-      a.part, parts, a.H, a.gate_kind, a.gate, a.w_post, a.rs, a.block ? a.dgate : nullptr,
-      a.block ? dw_post : nullptr, a.w_pre ? dw_pre : nullptr);
-  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  cudaLaunchAttribute attr = overlap_attribute();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(32 * kReduceGroups);
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, block_norm_reduce_kernel<T>, (const float*)a.part, parts, a.H, a.gate_kind, a.gate,
+                            a.w_post, a.rs, a.block ? a.dgate : (float*)nullptr, a.block ? dw_post : (float*)nullptr,
+                            a.w_pre ? dw_pre : (float*)nullptr) == cudaSuccess
+             ? MOE_OK
+             : MOE_ERR_CUDA;
 }
 
 template <typename T>
