@@ -50,33 +50,45 @@ struct Segments {
   int nseq, T;
   __device__ __forceinline__ int lo(int b) const { return off ? max(__ldg(off + b), 0) : 0; }
   __device__ __forceinline__ int hi(int b) const { return off ? min(__ldg(off + b + 1), T) : T; }
+  // Offsets that a warp holds: v0, v1 = off[a + lane], off[a + 32 + lane] for the n <= 63 segments from a on.
+  struct Window {
+    int a = 0, n = 0, v0 = 0, v1 = 0;
+    __device__ __forceinline__ int at(int i) const {  // off[a + i], the same i in every lane
+      const int x = __shfl_sync(0xffffffffu, v0, i & 31), y = __shfl_sync(0xffffffffu, v1, i & 31);
+      return i < 32 ? x : y;
+    }
+  };
+
   // The last segment that starts at or before t (the one that holds t, if any does; 0 if none does), with
-  // its bounds.  By a whole warp, the same t in every lane: many places are looked at together, for
-  // one after the other each costs the memory's latency (six of them for 48 segments).
-  __device__ __forceinline__ int find(int t, int& first, int& end) const {
+  // its bounds.  By a whole warp, the same t in every lane and t growing from call to call: many places
+  // are looked at together, for one after the other each costs the memory's latency (six of them
+  // for 48 segments), and kept for the next call: a tile that several short segments meet would pay
+  // for each of them.
+  __device__ __forceinline__ int find(int t, Window& w, int& first, int& end) const {
     if (!off) {
       first = 0, end = T;
       return 0;
     }
     const int lane = threadIdx.x & 31;
-    int a = 0, n = nseq;
-    while (n > 63) {  // 32 steps through what is left
-      const int step = (n + 31) / 32, i = lane * step;
-      const bool before = i < n && __ldg(off + a + i) <= t;
-      const int k = 31 - __clz(__ballot_sync(0xffffffffu, before) | 1u);  // the last place at or before t
-      a += k * step;
-      n = min(step, n - k * step);
+    if (w.n == 0 || (w.a + w.n < nseq && w.at(w.n) <= t)) {
+      int a = w.a, n = nseq - w.a;
+      while (n > 63) {  // 32 steps through what is left
+        const int step = (n + 31) / 32, i = lane * step;
+        const bool before = i < n && __ldg(off + a + i) <= t;
+        const int k = 31 - __clz(__ballot_sync(0xffffffffu, before) | 1u);  // the last place at or before t
+        a += k * step;
+        n = min(step, n - k * step);
+      }
+      w.a = a, w.n = min(63, nseq - a);
+      w.v0 = lane <= w.n ? __ldg(off + a + lane) : 0;
+      w.v1 = lane + 32 <= w.n ? __ldg(off + a + lane + 32) : 0;
     }
-    // all that is left, and the end of its last segment
-    const int v0 = lane <= n ? __ldg(off + a + lane) : 0, v1 = lane + 32 <= n ? __ldg(off + a + lane + 32) : 0;
-    const unsigned m0 = __ballot_sync(0xffffffffu, lane < n && v0 <= t);
-    const unsigned m1 = __ballot_sync(0xffffffffu, lane + 32 < n && v1 <= t);
+    const unsigned m0 = __ballot_sync(0xffffffffu, lane < w.n && w.v0 <= t);
+    const unsigned m1 = __ballot_sync(0xffffffffu, lane + 32 < w.n && w.v1 <= t);
     const int k = m1 ? 63 - __clz(m1) : 31 - __clz(m0 | 1u);
-    const int lo0 = __shfl_sync(0xffffffffu, v0, k & 31), lo1 = __shfl_sync(0xffffffffu, v1, k & 31);
-    const int hi0 = __shfl_sync(0xffffffffu, v0, (k + 1) & 31), hi1 = __shfl_sync(0xffffffffu, v1, (k + 1) & 31);
-    first = max(k < 32 ? lo0 : lo1, 0);
-    end = min(k + 1 < 32 ? hi0 : hi1, T);
-    return a + k;
+    first = max(w.at(k), 0);
+    end = min(w.at(k + 1), T);
+    return w.a + k;
   }
 };
 
@@ -207,8 +219,8 @@ __global__ void __launch_bounds__(kThreads, N > 16 ? 2 : kTilesPerSm)
   grid_dependents_launch();  // the second kernel's CTAs may wait on the SMs
   int flags = 0;
   // u: this lane's token of the step at w; its row and ids are requested while the step before it is
-  // worked on, those of the tile's first step while its segment is looked up (past the tile's
-  // end: the last token's, which are not used)
+  // worked on, those of a piece's first step while its segment is looked up (past the tile's end:
+  // the last token's, which are not used)
   constexpr int Q = 32 / L;  // ids a lane counts: K <= 32
   bool next_valid = false;
   Row<N> next;
@@ -222,13 +234,14 @@ __global__ void __launch_bounds__(kThreads, N > 16 ? 2 : kTilesPerSm)
       if (sub + q * L < K) next_id[q] = __ldg(ids + (size_t)r * K + sub + q * L);
   };
   int t = t0;
+  Segments::Window window;
   if (t < t1) request(t + warp * G + grp);
   while (t < t1) {
     int lo, hi;
-    const int b = seg.find(t, lo, hi);
+    const int b = seg.find(t, window, lo, hi);
     const int from = max(t, lo), end = min(t1, hi);  // from: past the tokens before the first segment
     if (end <= from) break;                          // past the last segment
-    if (from != t0) request(from + warp * G + grp);  // not the step that is on its way
+    if (from != t) request(from + warp * G + grp);   // not the step that is on its way
     t = from;
     for (int e = threadIdx.x; e < E; e += kThreads) cnt[e] = 0;
     if (threadIdx.x == 0) ntok = 0;
@@ -259,6 +272,7 @@ __global__ void __launch_bounds__(kThreads, N > 16 ? 2 : kTilesPerSm)
 #pragma unroll
       for (int i = 0; i < N / 2; ++i) acc.v[i] = __ffma2_rn(a.v[i], make_float2(inv, inv), acc.v[i]);
     }
+    if (end < t1) request(end + warp * G + grp);  // the next piece's first step
     if (mine) atomicAdd(&ntok, mine);
 #pragma unroll
     for (int j = 0; j < N; ++j) {
@@ -398,7 +412,8 @@ __global__ void __launch_bounds__(kThreads, N > 16 ? 2 : kTilesPerSm)
       do {  // the segments of the tokens that left theirs, one token after the other
         const int other = __shfl_sync(0xffffffffu, t, __ffs(moving) - 1);
         int slo, shi;
-        const int s = seg.find(other, slo, shi);
+        Segments::Window window;
+        const int s = seg.find(other, window, slo, shi);
         const bool mine = move && (t == other || (t >= slo && t < shi));
         if (mine) {
           b = s;
