@@ -15,6 +15,7 @@ from ._lib import (EXPORTS, LIB_PATH, MOE_E2M1, MOE_E4M3, MOE_BF16, MOE_F32, MOE
                    moe_permute_no_workspace, moe_route_grouped_topk, moe_route_permute, moe_route_topk, moe_selftest_bounded_wait,
                    moe_version,
                    moe_workspace_bytes, status_string)
+from .block import MoeBlock
 from .layer import MoeLayer
 
 __all__ = [n for n in dir() if not n.startswith("_")]

@@ -1,0 +1,83 @@
+"""The layer inside its transformer block: the norm before it, the router's loss, the layer, and the norm
+after it with gate and residual, which also norms the input of the next block.
+
+    block = MoeBlock(layer, w_pre, w_post, gate, w_next)
+    xn = block.enter(x)                       # rms(x) * w_pre
+    logits = xn.float() @ W_g                 # the router's product is the caller's
+    y, xn_next = block.leave(x, logits)       # x + res_scale * gate * rms(layer(xn)) * w_post, rms(y) * w_next
+
+Buffers are allocated once, every call only enqueues kernels on the stream, so a step is graph-capturable
+after a first eager one."""
+from __future__ import annotations
+
+import torch
+
+from . import _lib as L
+
+
+class MoeBlock:
+    """A MoeLayer with its norms and the balance loss of its router.  w_pre, w_post, w_next [H], gate None, [H] or
+    [T, 1], all of the activations' type; w_next None: no norm of the next block's input.  nseq: segments of
+    the balance loss (moe.h)."""
+
+    def __init__(self, layer, w_pre, w_post, gate=None, w_next=None, res_scale: float = 1.0, eps: float = 1e-6,
+                 score: str = "softmax", coef: float = 0.01, nseq: int = 1):
+        p, x = layer.p, layer.out
+        self.layer, self.p = layer, p
+        self.w_pre, self.w_post, self.gate, self.w_next = w_pre, w_post, gate, w_next
+        self.res_scale, self.eps, self.score, self.coef = res_scale, eps, score, coef
+        f32, i32 = dict(dtype=torch.float32, device=x.device), dict(dtype=torch.int32, device=x.device)
+        self.xn, self.y = torch.empty_like(x), torch.empty_like(x)
+        self.xn_next = None if w_next is None else torch.empty_like(x)
+        self.loss, self.tokens = torch.empty(nseq, **f32), torch.empty(nseq, **i32)
+        self.counts, self.prob_sum = torch.empty((nseq, p.E), **i32), torch.empty((nseq, p.E), **f32)
+        self.dlogits = torch.empty((p.T, p.E), **f32)
+        nbytes = max(L.moe_balance_workspace_bytes(p, nseq), L.moe_block_norm_workspace_bytes(p.T, p.H))
+        self.ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+
+    # -- forward ----------------------------------------------------------------
+    def enter(self, x, stream=None):
+        """The norm before: rms(x) * w_pre, the layer's and the router's input."""
+        L.moe_block_norm(x, None, None, None, self.w_pre, self.res_scale, self.eps, None, self.xn, stream)
+        return self.xn
+
+    def leave(self, x, logits, stream=None):
+        """The layer on enter()'s result, and the norm after it: (y, the next block's normed input or None)."""
+        self.layer.forward(self.xn, logits, stream, fused=True)
+        L.moe_block_norm(x, self.layer.out, self.gate, self.w_post, self.w_next, self.res_scale, self.eps, self.y,
+                         self.xn_next, stream)
+        return self.y, self.xn_next
+
+    # -- the router's loss ------------------------------------------------------
+    def balance(self, logits, valid=None, seq_offsets=None, stream=None):
+        """Balance loss per segment of the routing that leave() made; counts and score sums in counts, prob_sum."""
+        L.moe_balance_loss(self.p, logits, self.layer.ids, valid, seq_offsets, self.score, self.coef, self.loss,
+                           self.counts, self.prob_sum, self.tokens, self.layer.err, self.ws, stream)
+        return self.loss
+
+    def balance_backward(self, logits, dloss, valid=None, seq_offsets=None, stream=None):
+        """Gradient of balance() with respect to the logits."""
+        L.moe_balance_loss_backward(self.p, logits, valid, seq_offsets, self.score, self.coef, self.counts,
+                                    self.tokens, dloss, self.dlogits, stream)
+        return self.dlogits
+
+    # -- gradients of the norms -------------------------------------------------
+    def leave_backward(self, x, dy, dxn_next, stream=None):
+        """Gradients of leave()'s norm: of x, of the layer's output, of gate, w_post and w_next (fp32).  dxn_next is
+        None without w_next."""
+        dx, dout = torch.empty_like(x), torch.empty_like(x)
+        f32 = dict(dtype=torch.float32, device=x.device)
+        dgate = None if self.gate is None else torch.empty(self.gate.shape, **f32)
+        dw_post = torch.empty(self.w_post.shape, **f32)
+        dw_next = None if self.w_next is None else torch.empty(self.w_next.shape, **f32)
+        L.moe_block_norm_backward(x, self.layer.out, self.gate, self.w_post, self.w_next, self.res_scale, self.eps, dy,
+                                  dxn_next, dx, dout, dgate, dw_post, dw_next, self.ws, stream)
+        return dx, dout, dgate, dw_post, dw_next
+
+    def enter_backward(self, x, dxn, dy=None, stream=None):
+        """Gradients of enter(): of x (plus dy, what else reaches x) and of w_pre (fp32)."""
+        dx = torch.empty_like(x)
+        dw_pre = torch.empty(self.w_pre.shape, dtype=torch.float32, device=x.device)
+        L.moe_block_norm_backward(x, None, None, None, self.w_pre, self.res_scale, self.eps, dy, dxn, dx, None, None,
+                                  None, dw_pre, self.ws, stream)
+        return dx, dw_pre

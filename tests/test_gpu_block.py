@@ -1,0 +1,79 @@
+"""The block that runs the norms, the MXFP4 layer and the router's loss together, as examples/mxfp4_block.py does."""
+import importlib.util
+import os
+
+import pytest
+import torch
+
+import operator_reference as ref
+import routed_expert_layer_moe_gb300 as moe
+
+pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module")
+def example():
+    from routed_expert_layer_moe_gb300 import build
+    build.build()
+    spec = importlib.util.spec_from_file_location("mxfp4_block", os.path.join(ROOT, "examples", "mxfp4_block.py"))
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    return m
+
+
+@pytest.mark.parametrize("T", [1, 33])
+def test_block(example, T):
+    H, I, E, K = 256, 384, 8, 2
+    block, w_g = example.make_block(T, H, I, E, K)
+    x = torch.randn(T, H, generator=torch.Generator().manual_seed(T)).bfloat16().cuda()
+    y, xn, logits = (t.clone() for t in example.step(block, w_g, x))
+    out = block.layer.out.clone()
+    torch.cuda.synchronize()
+    assert int(block.layer.err) == 0
+    d = lambda t: t.double().cpu()  # noqa: E731
+    # the norms around the layer's own output, within bf16's rounding (2^-8 allows for a neighbour) and fp32 sums
+    want = ref.block_norm(d(x), None, None, None, d(block.w_pre), 1.0, 1e-6)[1]
+    assert ((d(block.xn) - want).abs() <= 2.0 ** -8 * want.abs() + 1e-6).all()
+    wy, wxn = ref.block_norm(d(x), d(out), d(block.gate), d(block.w_post), d(block.w_next), 1.0, 1e-6)
+    assert ((d(y) - wy).abs() <= 2.0 ** -8 * wy.abs() + 1e-5).all()
+    assert ((d(xn) - wxn).abs() <= 2.0 ** -8 * wxn.abs() + 1e-5).all()
+    # the layer between them ran on the normed input
+    assert torch.equal(block.layer.forward(block.xn, logits), out)
+    # the loss of this routing, and its gradient
+    dloss = torch.tensor([0.7], device="cuda")
+    loss, dl = block.balance(logits), block.balance_backward(logits, dloss)
+    r = ref.balance(logits.cpu(), block.layer.ids.cpu(), None, None, "softmax", 0.01, dloss.cpu())
+    assert torch.equal(block.counts.cpu().long(), r["counts"]) and int(r["counts"].sum()) == T * K
+    assert abs(float(loss) - float(r["loss"][0])) <= 2.0 ** -18 * float(r["loss"][0])
+    scale = r["dlogits"].abs().max()
+    assert (d(dl) - r["dlogits"]).abs().max() <= 2.0 ** -15 * max(float(scale), 1e-30)
+    # gradients of both norms
+    dy, dxn = torch.randn_like(y), torch.randn_like(y)
+    grads = block.leave_backward(x, dy, dxn)
+    want = ref.block_norm_grads([x.cpu(), out.cpu(), block.gate.cpu(), block.w_post.cpu(), block.w_next.cpu()], 1.0, 1e-6,
+                                dy.cpu(), dxn.cpu())
+    for g, w in zip(grads, want):
+        assert (d(g) - w).abs().max() <= 2.0 ** -7 * w.abs().max()
+    dx, dw = block.enter_backward(x, dxn, dy)
+    want = ref.block_norm_grads([x.cpu(), None, None, None, block.w_pre.cpu()], 1.0, 1e-6, dy.cpu(), dxn.cpu())
+    for g, w in ((dx, want[0]), (dw, want[4])):
+        assert (d(g) - w).abs().max() <= 2.0 ** -7 * w.abs().max()
+
+
+def test_block_in_a_graph(example):
+    block, w_g = example.make_block(17, 256, 256, 4, 2)
+    x = torch.randn(17, 256, device="cuda").bfloat16()
+    example.step(block, w_g, x)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, xn, logits = example.step(block, w_g, x)
+        block.balance(logits)
+        dl = block.balance_backward(logits, torch.ones(1, device="cuda"))
+    x.copy_(torch.randn_like(x))
+    graph.replay()
+    got = [t.clone() for t in (y, xn, block.loss, dl)]
+    y, xn, logits = example.step(block, w_g, x)
+    want = [y, xn, block.balance(logits), block.balance_backward(logits, torch.ones(1, device="cuda"))]
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
