@@ -118,9 +118,9 @@ __device__ __forceinline__ void store8(T* row, int c, int H, const V8& a) {
 
 // Sums of N values over the CTA, in the same order in every thread.  `buf` [N][32] is free for
 // the next use after one more barrier: the callers alternate between two.
-template <int N>
+template <int NT, int N>
 __device__ __forceinline__ void cta_sum(float (&v)[N], float* buf) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nwarps = blockDim.x >> 5;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nwarps = (NT ? NT : blockDim.x) >> 5;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
 #pragma unroll
@@ -132,11 +132,12 @@ __device__ __forceinline__ void cta_sum(float (&v)[N], float* buf) {
     for (int i = 0; i < N; ++i) buf[i * 32 + warp] = v[i];
   }
   __syncthreads();
-  if (nwarps == 8) {  // two loads and a tree of adds are shorter than the shuffles
+  if (nwarps == 8 || nwarps == 4) {  // a load or two and a tree of adds are shorter than the shuffles
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const float4 a = *reinterpret_cast<const float4*>(buf + i * 32), b = *reinterpret_cast<const float4*>(buf + i * 32 + 4);
-      v[i] = ((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w));
+      v[i] = (a.x + a.y) + (a.z + a.w);
+      if (nwarps == 8) v[i] += (b.x + b.y) + (b.z + b.w);
     }
     return;
   }
@@ -164,15 +165,18 @@ __device__ __forceinline__ void cp_async16(void* smem_dst, const void* src) {
 
 // The rows of N arrays on their way to one CTA: DEPTH rows ahead in shared memory (DEPTH = 0:
 // read from global memory when wanted).  Vector j of a thread is columns (j * threads + thread) * 8.
-template <typename T, int V, bool VEC, int DEPTH, int N>
+// NT: the CTA's threads, or 0 where only the launch knows.
+template <typename T, int V, bool VEC, int DEPTH, int N, int NT>
 struct Rows {
   enum { PARTS = 8 * sizeof(T) / 16 };  // 16-byte parts of a vector, in planes of their own
   const T* a[N];  // null: the array is not there
   int H;
   uint8_t* smem;
 
+  static __device__ __forceinline__ uint32_t threads() { return NT ? NT : blockDim.x; }
   __device__ __forceinline__ uint8_t* at(int slot, int n, int part, int j) const {
-    return smem + (size_t)((slot * N + n) * PARTS * V + part * V + j) * (blockDim.x * 16u) + threadIdx.x * 16;
+    return smem + (uint32_t)slot * (N * PARTS * V * 16) * threads() + ((n * PARTS * V + part * V + j) * 16) * threads() +
+           threadIdx.x * 16;
   }
   // Requests row r (if there is one) into a slot; every call is one group of copies.
   __device__ __forceinline__ void request(int r, int rows, int slot) const {
@@ -183,7 +187,7 @@ struct Rows {
         for (int n = 0; n < N; ++n) {
 #pragma unroll
           for (int j = 0; j < V; ++j) {
-            const int c = (j * blockDim.x + threadIdx.x) * 8;
+            const int c = (j * threads() + threadIdx.x) * 8;
             if (a[n] && c < H) {
 #pragma unroll
               for (int q = 0; q < PARTS; ++q)
@@ -202,7 +206,7 @@ struct Rows {
   }
   __device__ __forceinline__ V8 get(int n, int r, int slot, int j) const {
     if constexpr (DEPTH == 0) {
-      return load8<VEC>(a[n] + (size_t)r * H, (j * blockDim.x + threadIdx.x) * 8, H);
+      return load8<VEC>(a[n] + (size_t)r * H, (j * threads() + threadIdx.x) * 8, H);
     } else if constexpr (PARTS == 1) {
       return unpack(*reinterpret_cast<const uint4*>(at(slot, n, 0, j)));
     } else {
@@ -230,7 +234,7 @@ __device__ __forceinline__ float sum_squares(const R& in, int n, int r, int slot
   float2 s = pair(0.0f);
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    if ((j * (int)blockDim.x + (int)threadIdx.x) * 8 < in.H) {
+    if ((int)(j * in.threads() + threadIdx.x) * 8 < in.H) {
       const V8 b = in.get(n, r, slot, j);
 #pragma unroll
       for (int i = 0; i < 4; ++i) s = fma2(b.v[i], b.v[i], s);
@@ -241,20 +245,20 @@ __device__ __forceinline__ float sum_squares(const R& in, int n, int r, int slot
 
 // The sum over the block's row is needed before y, the sum over y after it.  The first is taken one
 // row ahead, together with the second one of the row before: one reduction a row, not two.
-template <typename T, int V, bool VEC, int DEPTH, int MAXT, int MINB>
+template <typename T, int V, bool VEC, int DEPTH, int MAXT, int MINB, int NT>
 __global__ void __launch_bounds__(MAXT, MINB) block_norm_kernel(const Args<T> a) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ __align__(16) float buf[2][64];
-  const int H = a.H, nt = blockDim.x;
+  const int H = a.H, nt = NT ? NT : blockDim.x;
   const float invH = 1.0f / (float)H;
-  const Rows<T, V, VEC, DEPTH, 2> in{{a.x, a.block}, H, smem};
+  const Rows<T, V, VEC, DEPTH, 2, NT> in{{a.x, a.block}, H, smem};
 #pragma unroll
   for (int d = 0; d < DEPTH; ++d) in.request(blockIdx.x + d * gridDim.x, a.rows, d);
   in.template wait<0>();
   float sb = 0.0f;  // sum of squares of the block's row
   if (a.block) {
     float v[1] = {sum_squares<V>(in, 1, blockIdx.x, 0)};
-    cta_sum(v, buf[1]);
+    cta_sum<NT>(v, buf[1]);
     sb = v[0];
   }
   int slot = 0, parity = 0;
@@ -285,7 +289,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_norm_kernel(const Args<T> a)
     in.template wait<0>();
     float v[2] = {s.x + s.y, 0.0f};
     if (a.block && next < a.rows) v[1] = sum_squares<V>(in, 1, next, next_slot);
-    cta_sum(v, buf[parity]);
+    cta_sum<NT>(v, buf[parity]);
     sb = v[1];
     if (a.xn) {
       const float2 ry = pair(rsqrtf(v[0] * invH + a.eps));
@@ -306,20 +310,20 @@ __global__ void __launch_bounds__(MAXT, MINB) block_norm_kernel(const Args<T> a)
 }
 
 // The reductions of a row: y^2 with q y, then the sum behind dblock with the next row's block^2.
-template <typename T, int V, bool VEC, int DEPTH, int MAXT, int MINB>
+template <typename T, int V, bool VEC, int DEPTH, int MAXT, int MINB, int NT>
 __global__ void __launch_bounds__(MAXT, MINB) block_norm_backward_kernel(const Args<T> a) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ __align__(16) float buf[2][64];
   enum { X, B, DY, DXN };
   grid_dependents_launch();  // the second kernel's CTAs may wait on the SMs
-  const int H = a.H, nt = blockDim.x;
+  const int H = a.H, nt = NT ? NT : blockDim.x;
   const float invH = 1.0f / (float)H;
-  const Rows<T, V, VEC, DEPTH, 4> in{{a.x, a.block, a.dy, a.dxn}, H, smem};
+  const Rows<T, V, VEC, DEPTH, 4, NT> in{{a.x, a.block, a.dy, a.dxn}, H, smem};
   // Both weights in fp32, a channel's gate folded in, in this thread's own part of shared memory behind
   // the rows (when rows are fetched ahead): each is read twice a row, and loaded and unpacked from
   // global memory they took 33 of 163 us.
   uint8_t* const wmem = in.at(DEPTH, 0, 0, 0);
-  const uint32_t plane = blockDim.x * 16u;
+  const uint32_t plane = nt * 16u;
   if constexpr (DEPTH > 0) {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -347,7 +351,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_norm_backward_kernel(const A
   float sb = 0.0f;  // sum of squares of the block's row
   if (a.block) {
     float v[1] = {sum_squares<V>(in, B, blockIdx.x, 0)};
-    cta_sum(v, buf[1]);
+    cta_sum<NT>(v, buf[1]);
     sb = v[0];
     if (!a.dxn) __syncthreads();
   }
@@ -383,7 +387,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_norm_backward_kernel(const A
     float ry = 0.0f, m = 0.0f;
     if (a.dxn) {
       float sum[2] = {s0.x + s0.y, s1.x + s1.y};
-      cta_sum(sum, buf[0]);
+      cta_sum<NT>(sum, buf[0]);
       ry = rsqrtf(sum[0] * invH + a.eps);
       m = -sum[1] * ry * ry * ry * invH;  // -ry yn mean(q yn) = y m
     }
@@ -418,7 +422,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_norm_backward_kernel(const A
       in.template wait<1>();
       float sum[2] = {u.x + u.y, 0.0f};
       if (next < a.rows) sum[1] = sum_squares<V>(in, B, next, next_slot);
-      cta_sum(sum, buf[1]);
+      cta_sum<NT>(sum, buf[1]);
       sb = sum[1];
       const float dg = a.rs * rb * sum[0];  // sum over the row of rs dx bn w_post
       const float2 f = pair(a.rs * rb * gt), mean = pair(-rb * rb * gt * dg * invH);
@@ -500,6 +504,7 @@ Shape shape_of(int H, int esz, bool vec, int arrays, int weights, int ctas1, int
   const int nvec = (H + 7) / 8;
   s.v = nvec > 1024 ? 4 : nvec > 512 || (nvec > 128 && rows > device_info().sm_count) ? 2 : 1;
   s.threads = ((nvec + s.v - 1) / s.v + 31) / 32 * 32;
+  if (s.v == 2 && s.threads <= 256) s.threads = s.threads <= 128 ? 128 : 256;  // what addresses are compiled for
   s.ctas = s.v == 1 ? std::min(512 * ctas1 / s.threads, 24) : s.threads <= 256 ? 256 * ctas2 / s.threads : 1;
   const DeviceInfo& di = device_info();
   if (!vec || rows <= di.sm_count * s.ctas) return s;  // a row for each CTA: nothing to fetch ahead
@@ -515,7 +520,7 @@ Shape shape_of(int H, int esz, bool vec, int arrays, int weights, int ctas1, int
   return s;
 }
 
-// f(vectors a thread, 16-byte accesses, rows ahead, threads at most) with compile-time arguments.
+// f(vectors a thread, 16-byte accesses, rows ahead, threads) with compile-time arguments; 512 threads: at most.
 template <typename F>
 int dispatch(const Shape& s, bool vec, F f) {
   using std::integral_constant;
@@ -526,7 +531,8 @@ int dispatch(const Shape& s, bool vec, F f) {
     return f(v, std::true_type(), integral_constant<int, 0>(), t);
   };
   if (s.v == 1) return go(integral_constant<int, 1>(), integral_constant<int, 512>());
-  if (s.v == 2 && s.threads <= 256) return go(integral_constant<int, 2>(), integral_constant<int, 256>());
+  if (s.v == 2 && s.threads == 128) return go(integral_constant<int, 2>(), integral_constant<int, 128>());
+  if (s.v == 2 && s.threads == 256) return go(integral_constant<int, 2>(), integral_constant<int, 256>());
   if (s.v == 2) return go(integral_constant<int, 2>(), integral_constant<int, 512>());
   return go(integral_constant<int, 4>(), integral_constant<int, 512>());
 }
@@ -551,8 +557,9 @@ int forward(Args<T> a, cudaStream_t st) {
   const int grid = s.depth ? std::min(a.rows, s.ctas * device_info().sm_count) : a.rows;
   return dispatch(s, vec, [&](auto v, auto w, auto d, auto t) {
     constexpr int V = decltype(v)::value, MAXT = decltype(t)::value;
-    constexpr int MINB = V == 1 ? kForward1 : MAXT == 256 ? kForward2 : 1;
-    return launch(block_norm_kernel<T, V, decltype(w)::value, decltype(d)::value, MAXT, MINB>, grid, s, a, st);
+    constexpr int MINB = V == 1 ? kForward1 : MAXT <= 256 ? kForward2 * 256 / MAXT : 1;
+    return launch(block_norm_kernel<T, V, decltype(w)::value, decltype(d)::value, MAXT, MINB, MAXT <= 256 ? MAXT : 0>,
+                  grid, s, a, st);
   });
 }
 
@@ -565,9 +572,10 @@ int backward(Args<T> a, float* dw_post, float* dw_pre, cudaStream_t st) {
   const int parts = std::min({a.rows, kMaxParts, s.ctas * device_info().sm_count});
   const int r = dispatch(s, vec, [&](auto v, auto w, auto d, auto t) {
     constexpr int V = decltype(v)::value, MAXT = decltype(t)::value;
-    constexpr int MINB = V == 1 ? kBackward1 : MAXT == 256 ? kBackward2 : 1;
-    return launch(block_norm_backward_kernel<T, V, decltype(w)::value, decltype(d)::value, MAXT, MINB>, parts, s, a,
-                  st);
+    constexpr int MINB = V == 1 ? kBackward1 : MAXT <= 256 ? kBackward2 * 256 / MAXT : 1;
+    return launch(
+        block_norm_backward_kernel<T, V, decltype(w)::value, decltype(d)::value, MAXT, MINB, MAXT <= 256 ? MAXT : 0>,
+        parts, s, a, st);
   });
   if (r) return r;
   const dim3 grid((a.H + 31) / 32, 2);
