@@ -35,6 +35,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kTilesPerSm = 3;
 constexpr int kMaxTiles = 512;
 constexpr int kMinTile = 32;
+constexpr int kMaxCluster = 8;  // tiles of a batch that takes one launch
 int tile_tokens(int T) {
   const int tiles = std::min(std::max(kTilesPerSm * device_info().sm_count, 1), kMaxTiles);
   return std::max((T + tiles - 1) / tiles, kMinTile);
@@ -201,12 +202,22 @@ __device__ __forceinline__ float inverse_sum(float z) {
   return z == 0.0f ? 0.0f : 1.0f / z;
 }
 
-template <int N, int L, bool VEC, bool SIG, bool FULL>
+// What the calls write.
+struct Outputs {
+  float* loss;
+  int32_t* counts;
+  float* prob_sum;
+  int32_t* tokens;
+};
+
+// ONE: a batch of at most kMaxCluster tiles and as many segments, the CTAs one cluster, which meets after
+// the partial sums and adds each segment's rows itself: one launch, not two (128 tokens of 256
+// experts: 18.4 us for the loss and its gradient, held by the host's launches).
+template <int N, int L, bool VEC, bool SIG, bool FULL, bool ONE>
 __global__ void __launch_bounds__(kThreads, N > 16 ? 2 : kTilesPerSm)
     balance_partial_kernel(const float* __restrict__ logits, const int32_t* __restrict__ ids,
-                           const uint8_t* __restrict__ valid, Segments seg, int E, int K, int tile,
-                           float* __restrict__ part_p, int32_t* __restrict__ part_c, int32_t* __restrict__ part_n,
-                           int32_t* __restrict__ done, int32_t* err) {
+                           const uint8_t* __restrict__ valid, Segments seg, int E, int K, int tile, float coef,
+                           float* part_p, int32_t* part_c, int32_t* part_n, int32_t* done, Outputs out, int32_t* err) {
   extern __shared__ float smem[];
   float* red = smem;                                             // [kWarps][E]
   int32_t* cnt = reinterpret_cast<int32_t*>(smem + kWarps * E);  // [E]
@@ -214,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, N > 16 ? 2 : kTilesPerSm)
   constexpr int G = 32 / L;  // tokens of a warp
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % L, grp = lane / L;
   const int t0 = blockIdx.x * tile, t1 = min(seg.T, t0 + tile);
-  if (blockIdx.x == 0)
+  if (!ONE && blockIdx.x == 0)
     for (int b = threadIdx.x; b < seg.nseq; b += kThreads) done[b] = 0;  // the second kernel's counters
   grid_dependents_launch();  // the second kernel's CTAs may wait on the SMs
   int flags = 0;
@@ -296,6 +307,42 @@ __global__ void __launch_bounds__(kThreads, N > 16 ? 2 : kTilesPerSm)
     t = end;
   }
   if (flags) atomicOr(err, flags);
+  if constexpr (ONE) {
+    cluster_sync_all();  // every CTA's rows are visible
+    for (int b = blockIdx.x; b < seg.nseq; b += gridDim.x) {
+      const int lo = seg.lo(b), hi = seg.hi(b);
+      const int i0 = lo / tile, i1 = hi > lo ? (hi - 1) / tile : i0 - 1;
+      int n = 0;
+      for (int i = i0; i <= i1; ++i) n += __ldcg(part_n + i + b);
+      float s = 0.0f;
+      for (int e = threadIdx.x; e < E; e += kThreads) {
+        float p = 0.0f;
+        int c = 0;
+#pragma unroll
+        for (int k = 0; k < kMaxCluster; ++k) {
+          if (i0 + k <= i1) {
+            p += __ldcg(part_p + (size_t)(i0 + k + b) * E + e);
+            c += __ldcg(part_c + (size_t)(i0 + k + b) * E + e);
+          }
+        }
+        out.counts[(size_t)b * E + e] = c;
+        out.prob_sum[(size_t)b * E + e] = p;
+        s = fmaf((float)c, p, s);
+      }
+      s = group_sum<32>(s);
+      __syncthreads();  // red is free
+      if (lane == 0) red[warp] = s;
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        s = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) s += red[w];
+        const float fn = (float)max(n, 1);
+        out.loss[b] = coef * (float)E / ((float)K * fn * fn) * s;
+        out.tokens[b] = n;
+      }
+    }
+  }
 }
 
 // One CTA per (segment, CHUNK experts): adds the segment's rows, ROWS at a time; the segment's last
@@ -306,8 +353,7 @@ __global__ void __launch_bounds__(kThreads, N > 16 ? 2 : kTilesPerSm)
 template <int CHUNK>
 __global__ void __launch_bounds__(kFinishThreads)
     balance_finish_kernel(Segments seg, int E, int K, int tile, float coef, const float* part_p, const int32_t* part_c,
-                          const int32_t* part_n, float* loss_part, int32_t* done, float* __restrict__ loss,
-                          int32_t* __restrict__ counts, float* __restrict__ prob_sum, int32_t* __restrict__ tokens) {
+                          const int32_t* part_n, float* loss_part, int32_t* done, Outputs out) {
   constexpr int ROWS = kFinishThreads / CHUNK;
   grid_dependency_wait();
   grid_dependents_launch();
@@ -354,8 +400,8 @@ __global__ void __launch_bounds__(kFinishThreads)
   }
   if (lane >= CHUNK) e = E;  // the sums are there several times over
   if (e < E) {
-    counts[(size_t)b * E + e] = c;
-    prob_sum[(size_t)b * E + e] = p;
+    out.counts[(size_t)b * E + e] = c;
+    out.prob_sum[(size_t)b * E + e] = p;
   }
   const float part = group_sum<32>(e < E ? (float)c * p : 0.0f);
   int last = 0;
@@ -371,8 +417,8 @@ __global__ void __launch_bounds__(kFinishThreads)
   s = group_sum<32>(s);
   if (lane == 0) {
     const float fn = (float)max(n, 1);
-    loss[b] = coef * (float)E / ((float)K * fn * fn) * s;
-    tokens[b] = n;
+    out.loss[b] = coef * (float)E / ((float)K * fn * fn) * s;
+    out.tokens[b] = n;
   }
 }
 
@@ -544,14 +590,38 @@ int launch_balance(const moe_problem& p, const float* logits, const int32_t* ids
   const int tiles = p.T > 0 ? (p.T + tile - 1) / tile : 1;  // an empty batch: one CTA clears the counters
   const bool vec = p.E % 4 == 0 && aligned16(logits);
   const size_t smem = (size_t)(kWarps + 1) * p.E * 4;
+  const Outputs out{loss, counts, prob_sum, tokens};
+  const bool one = tiles <= kMaxCluster && nseq <= kMaxCluster;
   const int r = dispatch(p.E, vec, score, [&](auto n, auto l, auto v, auto s, auto full) {
-    auto kern = balance_partial_kernel<decltype(n)::value, decltype(l)::value, decltype(v)::value, decltype(s)::value,
-                                  decltype(full)::value>;
-    kern<<<tiles, kThreads, smem, st>>>(
-        logits, ids, valid, seg, p.E, p.K, tile, w.part_p, w.part_c, w.part_n, w.done, err);
-    return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    auto go = [&](auto o) {
+      constexpr bool ONE = decltype(o)::value;
+      auto kern = balance_partial_kernel<decltype(n)::value, decltype(l)::value, decltype(v)::value, decltype(s)::value,
+                                         decltype(full)::value, ONE>;
+      cudaLaunchAttribute attr{};
+      cudaLaunchConfig_t cfg{};
+      cfg.gridDim = dim3(tiles);
+      cfg.blockDim = dim3(kThreads);
+      cfg.dynamicSmemBytes = smem;
+      cfg.stream = st;
+      if (ONE) {  // a whole cluster: CTAs past the last token only meet the others
+        int c = 1;
+        while (c < tiles) c *= 2;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = c;
+        attr.val.clusterDim.y = 1;
+        attr.val.clusterDim.z = 1;
+        cfg.gridDim = dim3(c);
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+      }
+      return cudaLaunchKernelEx(&cfg, kern, logits, ids, valid, seg, (int)p.E, (int)p.K, tile, coef, w.part_p, w.part_c,
+                                w.part_n, w.done, out, err) == cudaSuccess
+                 ? MOE_OK
+                 : MOE_ERR_CUDA;
+    };
+    return one ? go(std::true_type()) : go(std::false_type());
   });
-  if (r) return r;
+  if (r || one) return r;
   auto finish = [&](auto chunk) {
     constexpr int C = decltype(chunk)::value;
     cudaLaunchAttribute attr = overlap_attribute();
@@ -563,7 +633,7 @@ int launch_balance(const moe_problem& p, const float* logits, const int32_t* ids
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, balance_finish_kernel<C>, seg, (int)p.E, (int)p.K, tile, coef,
                               (const float*)w.part_p, (const int32_t*)w.part_c, (const int32_t*)w.part_n, w.loss_part,
-                              w.done, loss, counts, prob_sum, tokens) == cudaSuccess
+                              w.done, out) == cudaSuccess
                ? MOE_OK
                : MOE_ERR_CUDA;
   };
