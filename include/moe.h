@@ -442,7 +442,7 @@ moe_status moe_balance_loss_backward(const moe_problem* p, const float* logits, 
  * y = x (nothing of the norm after is read; y may be NULL).  w_pre and xn =
  * NULL together: only y.  x, block, y, xn [T][H] and w_post, w_pre [H] are of
  * `dtype` (F32 or BF16), and so is the gate: none, one value a channel [H], or one a token [T].
- * 1 <= H <= 16384; any alignment of the type's own size.  Outputs overlap no
+ * 1 <= H <= 16384, T <= 2^30; any alignment of the type's own size.  Outputs overlap no
  * input and no other output, except that y may be x.
  * ------------------------------------------------------------------------- */
 typedef enum moe_gate { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2 } moe_gate;

@@ -148,12 +148,13 @@ def _ptr(t):
 
 # The current stream's handle without a stream object (2.8 us of a call's 10 us on a Grace core), where torch has it.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream):
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -180,11 +181,14 @@ def _arg(t, name: str, dtype, shape):
     raise ValueError("%s: expected %s %s, got %s %s" % (name, dtype, tuple(shape), t.dtype, tuple(t.shape)))
 
 
-def _float_dtype(t, name: str) -> int:
+def _values(t, name: str):
+    """(moe_dtype, device address) of a dense float32 or bfloat16 tensor."""
     d = _FLOAT_DTYPES.get(t.dtype)
     if d is None:
         raise ValueError("%s: expected float32 or bfloat16, got %s" % (name, t.dtype))
-    return d
+    if t.is_cuda and t.is_contiguous():
+        return d, t.data_ptr()
+    return d, _arg(t, name, t.dtype, t.shape)
 
 
 def moe_version() -> int:
@@ -285,15 +289,20 @@ def moe_combine(p: Problem, yg, row_of, w, out, stream=None) -> None:
 
 def _mx_args(values, codes, scales, name: str):
     """dtype, rows, cols and addresses of an MXFP4 conversion; leading dimensions count as rows."""
-    d = _float_dtype(values, name)
-    if values.dim() < 1:
+    d, addr = _values(values, name)
+    if values.dim() == 2:
+        rows, cols = values.shape
+        lead = (rows,)
+    elif values.dim() > 0:
+        *lead, cols = values.shape
+        lead = tuple(lead)
+        rows = torch.Size(lead).numel()
+    else:
         raise ValueError("%s: expected rows of values" % name)
-    lead, cols = values.shape[:-1], values.shape[-1]
     if cols % 32:
         raise ValueError("%s: rows of %d values are not whole blocks of 32" % (name, cols))
-    return (d, lead.numel(), cols, _arg(values, name, values.dtype, values.shape),
-            _arg(codes, "codes", torch.uint8, lead + (cols // 2,)),
-            _arg(scales, "scales", torch.uint8, lead + (cols // 32,)))
+    return (d, rows, cols, addr, _arg(codes, "codes", torch.uint8, (*lead, cols // 2)),
+            _arg(scales, "scales", torch.uint8, (*lead, cols // 32)))
 
 
 def moe_mx_quantize(x, codes, scales, stream=None) -> None:
@@ -345,18 +354,19 @@ def moe_balance_loss_backward(p: Problem, logits, valid, seq_offsets, score: str
 
 
 def _norm_args(x, block, gate, w_post, w_pre):
-    """Common arguments of the norm calls: (dtype, T, H, x, block, gate kind, gate, w_post, w_pre)."""
-    d = _float_dtype(x, "x")
+    """Common arguments of the norm calls: their type and shapes, and (dtype, T, H, x, block, gate kind, gate, w_post,
+    w_pre)."""
+    d, addr = _values(x, "x")
     if x.dim() != 2:
         raise ValueError("x: expected [T, H]")
-    T, H = x.shape
-    dt = x.dtype
+    TH = T, H = x.shape
+    dt, one = x.dtype, (H,)
     kind = MOE_GATE_NONE
     if gate is not None:
         kind = MOE_GATE_TOKEN if gate.dim() == 2 else MOE_GATE_CHANNEL
-    return (d, T, H, _arg(x, "x", dt, (T, H)), _arg(block, "block", dt, (T, H)), kind,
-            _arg(gate, "gate", dt, (T, 1) if kind == MOE_GATE_TOKEN else (H,)), _arg(w_post, "w_post", dt, (H,)),
-            _arg(w_pre, "w_pre", dt, (H,)))
+    return dt, TH, (d, T, H, addr, _arg(block, "block", dt, TH), kind,
+                    _arg(gate, "gate", dt, (T, 1) if kind == MOE_GATE_TOKEN else one),
+                    _arg(w_post, "w_post", dt, one), _arg(w_pre, "w_pre", dt, one))
 
 
 def moe_block_norm_workspace_bytes(T: int, H: int) -> int:
@@ -367,23 +377,22 @@ def moe_block_norm(x, block, gate, w_post, w_pre, res_scale: float, eps: float, 
     """y = x + res_scale * gate * rms(block) * w_post, xn = rms(y) * w_pre (moe.h).  x, block, y, xn [T, H];
     w_post, w_pre [H]; gate None, [H] (a value a channel) or [T, 1] (a value a token); block None: y = x; w_pre and
     xn None: only y."""
-    a = _norm_args(x, block, gate, w_post, w_pre)
-    _check(lib().moe_block_norm(*a, res_scale, eps, _arg(y, "y", x.dtype, x.shape), _arg(xn, "xn", x.dtype, x.shape),
-                                _stream(stream)), "moe_block_norm")
+    dt, TH, a = _norm_args(x, block, gate, w_post, w_pre)
+    _check(lib().moe_block_norm(*a, res_scale, eps, _arg(y, "y", dt, TH), _arg(xn, "xn", dt, TH), _stream(stream)),
+           "moe_block_norm")
 
 
 def moe_block_norm_backward(x, block, gate, w_post, w_pre, res_scale: float, eps: float, dy, dxn, dx, dblock, dgate,
                             dw_post, dw_pre, workspace, stream=None) -> None:
     """Gradient of moe_block_norm from its inputs: dx, dblock like x; dgate like the gate, dw_post and dw_pre [H],
     all three float32 and each None where it is not wanted."""
-    a = _norm_args(x, block, gate, w_post, w_pre)
-    H, f32 = a[2], torch.float32
+    dt, TH, a = _norm_args(x, block, gate, w_post, w_pre)
+    one, f32 = TH[1:], torch.float32
     _check(lib().moe_block_norm_backward(
-        *a, res_scale, eps, _arg(dy, "dy", x.dtype, x.shape), _arg(dxn, "dxn", x.dtype, x.shape),
-        _arg(dx, "dx", x.dtype, x.shape), _arg(dblock, "dblock", x.dtype, x.shape),
-        _arg(dgate, "dgate", f32, () if gate is None else gate.shape), _arg(dw_post, "dw_post", f32, (H,)),
-        _arg(dw_pre, "dw_pre", f32, (H,)), _ptr(workspace), workspace.numel() * workspace.element_size(),
-        _stream(stream)), "moe_block_norm_backward")
+        *a, res_scale, eps, _arg(dy, "dy", dt, TH), _arg(dxn, "dxn", dt, TH), _arg(dx, "dx", dt, TH),
+        _arg(dblock, "dblock", dt, TH), _arg(dgate, "dgate", f32, () if gate is None else gate.shape),
+        _arg(dw_post, "dw_post", f32, one), _arg(dw_pre, "dw_pre", f32, one), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream)), "moe_block_norm_backward")
 
 
 def moe_eplb_record(p: Problem, masked_m, pass_index: int, window: int, load_window, stream=None) -> None:

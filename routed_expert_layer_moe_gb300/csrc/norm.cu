@@ -27,6 +27,7 @@ namespace moe {
 namespace {
 
 constexpr int kMaxH = 16384;
+constexpr int kMaxT = 1 << 30;  // row numbers a few strides past the last one stay in 32 bits
 constexpr int kMaxThreads = 512;
 constexpr int kMaxParts = 512;  // CTAs of the backward pass at most
 
@@ -620,7 +621,7 @@ Args<T> make_args(const NormArgs& n) {
 }  // namespace
 
 size_t block_norm_workspace_bytes(int T, int H) {
-  if (T < 0 || H < 1 || H > kMaxH) return 0;
+  if (T < 0 || T > kMaxT || H < 1 || H > kMaxH) return 0;
   return std::max<size_t>((size_t)std::min(T, kMaxParts) * 2 * H * sizeof(float), 256);
 }
 

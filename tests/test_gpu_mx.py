@@ -168,6 +168,10 @@ SIZES = [
     ([2, 130], 384, 4480, "contig", 0, None),    # split, with a last stage of half a K step, an odd tile
     ([0, 0], 256, 256, "masked", 0, 4),          # nothing at all
     ([9, 3], 256, 256, "masked", 0, 6),          # a slot whose count is above M_max: M_max rows
+    # slots of 128 rows or more on average: SM pairs, chunks of up to 256 rows in two unequal halves
+    ([300, 256, 513, 1, 130], 512, 384, "contig", 0, None),
+    ([600, 0, 255, 257], 768, 1024, "masked", 0, 600),
+    ([700, 3, 700], 256, 640, "contig", 1, None),
     # 144 pairs of 128-row gate/up tiles (fewer take 64-row tiles on 152 SMs)
     ([16, 15, 31, 32, 33, 63, 64, 65, 127, 128, 1, 2, 0, 100, 90, 17], 256, 1152, "masked", 0, 128),
     ([16, 15, 31, 32, 33, 63, 64, 65, 127, 128, 1, 2, 0, 100, 90, 17], 384, 1152, "contig", 0, None),

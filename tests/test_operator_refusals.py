@@ -96,7 +96,7 @@ def test_block_norm(lib):
         return lib.moe_block_norm(dtype, T, H, x, block, kind, gate, w_post, w_pre, 1.0, eps, y, xn, None)
 
     assert fwd(T=0, x=None, block=None, y=None, xn=None) == moe.MOE_OK
-    for kw in (dict(dtype=2), dict(T=-1), dict(H=0), dict(H=16385), dict(x=None), dict(kind=3), dict(kind=-1),
+    for kw in (dict(dtype=2), dict(T=-1), dict(H=0), dict(H=16385), dict(T=(1 << 30) + 1), dict(x=None), dict(kind=3), dict(kind=-1),
                dict(gate=None), dict(w_post=None), dict(w_pre=None), dict(xn=None), dict(y=None), dict(eps=-1.0),
                dict(eps=float("nan")), dict(block=None, y=None, xn=None, w_pre=None)):
         assert fwd(**kw) == INVALID, kw
