@@ -211,7 +211,8 @@ static moe_status gemm_call(const moe_problem* p, int mode, const void* act, con
     return MOE_ERR_UNSUPPORTED;
   // packed 4-bit tensor maps want a 32-byte aligned base
   if (p->wt == MOE_E2M1 && (reinterpret_cast<uintptr_t>(w) & 31u)) return MOE_ERR_UNSUPPORTED;
-  if (workspace_bytes < ws_bytes(*p) || (ws_bytes(*p) > 0 && !workspace)) return MOE_ERR_WORKSPACE;
+  const size_t need = ws_bytes(*p);
+  if (workspace_bytes < need || (need > 0 && !workspace)) return MOE_ERR_WORKSPACE;
   return launched(launch_gemm(*p, mode, act, act_scales, w, w_scales, masked_m, offsets, out, out_scales, err_flag,
                               workspace, (cudaStream_t)stream));
 }
@@ -246,7 +247,8 @@ moe_status moe_grouped_ffn(const moe_problem* p, const void* xg, const float* xg
     return MOE_ERR_UNSUPPORTED;
   if (p->wt == MOE_E2M1 && ((reinterpret_cast<uintptr_t>(w13) | reinterpret_cast<uintptr_t>(w2)) & 31u))
     return MOE_ERR_UNSUPPORTED;
-  if (workspace_bytes < ws_bytes(*p) || (ws_bytes(*p) > 0 && !workspace)) return MOE_ERR_WORKSPACE;
+  const size_t need = ws_bytes(*p);
+  if (workspace_bytes < need || (need > 0 && !workspace)) return MOE_ERR_WORKSPACE;
   return launched(launch_grouped_ffn(*p, xg, xg_scales, w13, w13_scales, w2, w2_scales, masked_m, offsets, hg,
                                      hg_scales, yg, err_flag, workspace, (cudaStream_t)stream));
 }
@@ -290,7 +292,8 @@ moe_status moe_ffn_combine(const moe_problem* p, const void* xg, const float* xg
     return MOE_ERR_UNSUPPORTED;
   if (p->wt == MOE_E2M1 && ((reinterpret_cast<uintptr_t>(w13) | reinterpret_cast<uintptr_t>(w2)) & 31u))
     return MOE_ERR_UNSUPPORTED;
-  if (workspace_bytes < ws_bytes(*p) || (ws_bytes(*p) > 0 && !workspace)) return MOE_ERR_WORKSPACE;
+  const size_t need = ws_bytes(*p);
+  if (workspace_bytes < need || (need > 0 && !workspace)) return MOE_ERR_WORKSPACE;
   const cudaStream_t st = (cudaStream_t)stream;
   const CombineArgs comb{row_of, w, out};
   if (p->wt == MOE_BF16)  // one launch for both GEMMs

@@ -99,6 +99,7 @@ struct MxParams {
   int a1_off;        // row of the pair's second tile relative to the first
   int out_cols;
   int stages;
+  int boxes;           // token boxes with a tensor map: enough for any chunk
   int early;           // the kernel before this one is the gate/up GEMM of the same call
   int vec_tok, vec_w;  // scale rows may be read 16 bytes at a time
   const uint8_t* w_scales;    // [slots * NA][K/32]
@@ -405,18 +406,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       // ------------------------------------------------------------ producer
       if (lane == 0) {
         tma_prefetch_map(&tmA);
-        for (int i = 0; i < NUM_BOXES; ++i) tma_prefetch_map(&tmB.box[i]);
+        for (int i = 0; i < p.boxes; ++i) tma_prefetch_map(&tmB.box[i]);
         const uint64_t pol = policy_evict_first();
         int stage = 0;
         uint32_t phase = 0;
         long issued = 0;
         bool ok = true;
-        auto token_box = [&](const Unit& U) { return (uint32_t)box_rows(box_of(U.most)) * ROW_BYTES; };
+        auto box = [&](const Unit& U) { return min(box_of(U.most), p.boxes - 1); };
         // a stage's byte count and its weights; pairs: the leader's barrier counts both CTAs' copies
         auto load_weights = [&](const Unit& U, int kb, int at) {
           uint8_t* st = smem + (size_t)at * L::STAGE;
           const int x = kb * ROW_BYTES;
-          const uint32_t tok = token_box(U);
+          const uint32_t tok = (uint32_t)box_rows(box(U)) * ROW_BYTES;
           if constexpr (PAIR) {
             if (leader) {
               mbar_arrive_expect_tx(&full[at], 2u * (L::W_BYTES + tok));
@@ -440,7 +441,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
         for (int u = unit0; ok && u < total; u += ustride) {
           const Unit U = unit(u);
-          const CUtensorMap* mb = &tmB.box[box_of(U.most)];
+          const CUtensorMap* mb = &tmB.box[box(U)];
           for (int kb = U.kb0; kb < U.kb1; ++kb) {
             if (ahead > 0) {
               --ahead;
@@ -864,7 +865,8 @@ double wave_fill(double units, int sm_count) {
   return waves > 0 ? waves / std::ceil(waves) : 1.0;
 }
 
-Plan make_plan(const moe_problem& p, int mode, int sm_count, int smem_cap) {
+// The part of a plan that the workspace depends on.
+Plan plan_units(const moe_problem& p, int mode, int sm_count) {
   Plan pl{};
   const int K = (mode == MODE_SWIGLU) ? p.H : p.I;
   const int nslots = p.P + p.has_shared;
@@ -917,6 +919,12 @@ Plan make_plan(const moe_problem& p, int mode, int sm_count, int smem_cap) {
   split(pl.ksplit);
   if (pl.ksplit > 1 && (size_t)pl.ksplit * grouped_rows(p) * out_cols * 4 > (size_t(1) << 30)) split(1);
   pl.part_bytes = pl.ksplit > 1 ? (size_t)pl.ksplit * grouped_rows(p) * out_cols * 4 : 0;
+  return pl;
+}
+
+Plan make_plan(const moe_problem& p, int mode, int sm_count, int smem_cap) {
+  Plan pl = plan_units(p, mode, sm_count);
+  const int nslots = p.P + p.has_shared;
   const int stage = pl.pair ? Tile<128, true>::STAGE : pl.tw == 128 ? Tile<128, false>::STAGE : Tile<64, false>::STAGE;
   const int sf_buf = pl.tw == 128 ? Tile<128, false>::SF_BUF : Tile<64, false>::SF_BUF;
   for (int st = MAX_STAGES; st >= 2; --st) {
@@ -1017,10 +1025,11 @@ int launch_kernel(const Plan& pl, const CUtensorMap& tA, const TokenMaps& tB, co
 int gemm_mx_tile_rows(const moe_problem& p, int mode) { return use_pairs(p, mode) ? 2 * BN : BN; }
 
 size_t gemm_mx_workspace_bytes(const moe_problem& p) {
-  // the split depends on the SM count; sized for the largest plausible GPU (up to 256 SMs)
+  // the split (of the down product alone) depends on the SM count; sized for the largest plausible
+  // GPU (up to 256 SMs)
   size_t best = 0;
-  for (int mode = 0; mode < 2; ++mode)
-    for (int sms : {132, 148, 152, 160, 170, 188, 256}) best = std::max(best, make_plan(p, mode, sms, 232448).part_bytes);
+  for (int sms : {132, 148, 152, 160, 170, 188, 256})
+    best = std::max(best, plan_units(p, MODE_DOWN, sms).part_bytes);
   return STATS_BYTES + align_up(best, 256);
 }
 
@@ -1040,7 +1049,9 @@ int launch_gemm_mx(const moe_problem& p, int mode, const void* act, const uint8_
   if (encode_tensor_map(&tA, CU_TENSOR_MAP_DATA_TYPE_UINT8, K / 2, (uint64_t)(p.P + p.has_shared) * NA, K / 2,
                         ROW_BYTES, pl.tw, w) != CUDA_SUCCESS)
     return MOE_ERR_CUDA;
-  for (int i = 0; i < NUM_BOXES; ++i)
+  // boxes for the rows that a chunk may have (the kernel takes no larger one, whatever the counts say)
+  const int boxes = box_of((int)std::min<uint64_t>(p.layout == MOE_LAYOUT_MASKED ? p.M_max : rows, BN)) + 1;
+  for (int i = 0; i < boxes; ++i)
     if (encode_tensor_map(&tB.box[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, K / 2, rows, K / 2, ROW_BYTES, box_rows(i), act) !=
         CUDA_SUCCESS)
       return MOE_ERR_CUDA;
@@ -1059,6 +1070,7 @@ int launch_gemm_mx(const moe_problem& p, int mode, const void* act, const uint8_
   prm.a1_off = (mode == MODE_SWIGLU) ? p.I : pl.tw;
   prm.out_cols = (mode == MODE_SWIGLU) ? p.I : p.H;
   prm.stages = pl.stages;
+  prm.boxes = boxes;
   prm.early = after_gate_up;
   prm.vec_tok = K % 512 == 0 && (reinterpret_cast<uintptr_t>(act_scales) & 15u) == 0;
   prm.vec_w = K % 512 == 0 && (reinterpret_cast<uintptr_t>(w_scales) & 15u) == 0;

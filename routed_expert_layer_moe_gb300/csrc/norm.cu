@@ -28,7 +28,6 @@ namespace {
 
 constexpr int kMaxH = 16384;
 constexpr int kMaxT = 1 << 30;  // row numbers a few strides past the last one stay in 32 bits
-constexpr int kMaxThreads = 512;
 constexpr int kMaxParts = 512;  // CTAs of the backward pass at most
 
 // Eight consecutive columns as four pairs: the arithmetic is on pairs (fp32x2 instructions), for with
@@ -133,20 +132,17 @@ __device__ __forceinline__ void cta_sum(float (&v)[N], float* buf) {
     for (int i = 0; i < N; ++i) buf[i * 32 + warp] = v[i];
   }
   __syncthreads();
-  if (nwarps == 8 || nwarps == 4) {  // a load or two and a tree of adds are shorter than the shuffles
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
+  for (int i = 0; i < N; ++i) {
+    if (nwarps == 8 || nwarps == 4) {  // a load or two and a tree of adds are shorter than the shuffles
       const float4 a = *reinterpret_cast<const float4*>(buf + i * 32), b = *reinterpret_cast<const float4*>(buf + i * 32 + 4);
       v[i] = (a.x + a.y) + (a.z + a.w);
       if (nwarps == 8) v[i] += (b.x + b.y) + (b.z + b.w);
+    } else {
+      v[i] = lane < nwarps ? buf[i * 32 + lane] : 0.0f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
     }
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    v[i] = lane < nwarps ? buf[i * 32 + lane] : 0.0f;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
   }
 }
 
