@@ -31,8 +31,11 @@
 //     the four bytes of row 32 q + i, the same in each quarter.  Copying them from shared memory
 //     with tcgen05.cp instead put six copies a stage into the tensor core's queue: 0.69 us a stage,
 //     0.62 without them.
+//     A stage's scales are counted on the barrier of its copies and freed with them: with barriers of
+//     their own, two more operations a group, the issuing thread became the bottleneck (dense gate/up 328
+//     us instead of 269 without epilogue).
 //   * Warps 8-15: epilogue.  Columns 0-255 of tensor memory hold the unit's accumulators, the
-//     columns above them the scales of four groups.  The epilogue first moves the accumulators to
+//     columns above them the stages' scales.  The epilogue first moves the accumulators to
 //     registers and hands them back, so only that move is not overlapped with the next unit's
 //     MMAs; the copies run ahead through it.
 //   * Every wait is bounded; on expiry the CTA drains its copies and MMAs, frees tensor memory,
@@ -52,10 +55,9 @@ constexpr int ROW_BYTES = 128;          // bytes of a row in one stage (one 128-
 constexpr int KB = 256;                 // codes of a row in one stage
 constexpr int TOK_BYTES = BN * ROW_BYTES;
 constexpr int GROUP = 2;                // stages whose scales are loaded together (16 bytes of a row)
-constexpr int SF_RING = 4;              // groups of scales in tensor memory
-constexpr int SF_BUFS = 4;              // and in shared memory: three are on their way while one is read
-constexpr uint32_t SF_COL0 = 256;       // first of their columns
-constexpr int MAX_STAGES = 7;
+constexpr int SF_BUFS = 4;              // groups of scales in shared memory: three on their way while one is read
+constexpr uint32_t SF_COL0 = 256;       // first tensor-memory column of the stages' scales
+constexpr int MAX_STAGES = 6;           // their scales: 24 columns each at most
 constexpr int NUM_THREADS = 512;        // four warpgroups
 constexpr int SF_WARP0 = 4, SF_WARPS = 4;
 constexpr int EPI_WARP0 = 8, EPI_WARPS = 8;
@@ -83,7 +85,7 @@ struct Tile {
   static constexpr int STAGE = W_STAGED + TOK_BYTES;             // weights | tokens
   static constexpr int NB = 2 * TW / 128;                        // 128-row scale blocks of a pair's rows
   static constexpr int SF_BUF = (1 + NB) * 128 * 16;             // one group's scales in shared memory
-  static constexpr int SF_COLS = 4 * (4 * NB + 4);               // and in tensor memory: weights, then tokens
+  static constexpr int SF_COLS = 2 * (4 * NB + 4);               // one stage's in tensor memory: weights, then tokens
 };
 
 struct MxParams {
@@ -325,9 +327,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   int* sbase = srows + p.nslots;                           // [nslots] first grouped-buffer row per slot
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + p.bar_off);
   uint64_t* empty = full + p.stages;
-  uint64_t* sfull = empty + p.stages;    // [SF_RING] a group's scales are in tensor memory
-  uint64_t* sempty = sfull + SF_RING;    // [SF_RING] and no longer needed
-  uint64_t* tfull = sempty + SF_RING;    // accumulators written
+  uint64_t* tfull = empty + p.stages;    // accumulators written
   uint64_t* tempty = tfull + 1;          // accumulators read
   uint64_t* drain = tempty + 1;
   uint64_t* fin = drain + 1;             // pairs: the peer CTA is done with this CTA's memory
@@ -344,12 +344,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
   if (tid == 0) {
     for (int i = 0; i < p.stages; ++i) {
-      mbar_init(&full[i], 1);
+      mbar_init(&full[i], 1 + (PAIR ? 2 * SF_WARPS : SF_WARPS));  // the copies, and the scale warps
       mbar_init(&empty[i], 1);
-    }
-    for (int i = 0; i < SF_RING; ++i) {
-      mbar_init(&sfull[i], PAIR ? 2 * SF_WARPS : SF_WARPS);
-      mbar_init(&sempty[i], 1);
     }
     mbar_init(tfull, 1);
     mbar_init(tempty, PAIR ? 2 * EPI_WARPS : EPI_WARPS);
@@ -465,20 +461,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             }
           }
         }
-        if (!ok && PAIR && !leader) {
-          // the peer's copies count on the leader's barriers: give those in flight time to land
+        if (!ok && issued > 0) {
+          // let the copies already in flight land before the CTA's shared memory is released
           const uint64_t t0 = global_timer_ns();
           while (global_timer_ns() - t0 < 200000u) {
-          }
-        } else if (!ok) {
-          // let the copies already in flight land before the CTA's shared memory is released
-          const long first = issued > p.stages ? issued - p.stages : 0;
-          for (long i = first; i < issued; ++i) {
-            const int st = (int)(i % p.stages);
-            const uint32_t ph = (uint32_t)((i / p.stages) & 1);
-            const long long t0 = clock64();
-            while (!mbar_try_wait(&full[st], ph) && clock64() - t0 < TIMEOUT) {
-            }
           }
         }
       }
@@ -492,7 +478,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             tc_commit(bar);
         };
         int stage = 0;
-        uint32_t phase = 0, g = 0, gphase = 0, u_it = 0;
+        uint32_t phase = 0, u_it = 0;
         bool ok = true, any = false;
         int units = 0, tiles = 0;
         for (int u = unit0; ok && leader && u < total; u += ustride, ++u_it) {
@@ -506,16 +492,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             break;
           }
           tc_fence_after_sync();
-          uint32_t scol = 0;
-          bool second = false;  // stage of the group
           for (int kb = U.kb0; kb < U.kb1; ++kb) {
-            if (!second) {
-              if (!mbar_wait<PAIR>(&sfull[g], gphase, abort_flag, TIMEOUT)) {
-                ok = false;
-                break;
-              }
-              scol = tmem_base + SF_COL0 + g * L::SF_COLS;
-            }
             if (!mbar_wait<PAIR>(&full[stage], phase, abort_flag, TIMEOUT)) {
               ok = false;
               break;
@@ -523,28 +500,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             tc_fence_after_sync();
             const uint32_t st = smem_u32(smem + (size_t)stage * L::STAGE);
             const uint64_t dw = smem_desc_sw128(st), dtok = smem_desc_sw128(st + L::W_STAGED);
-            const uint32_t jb = second ? 2u : 0u;
+            const uint32_t scol = tmem_base + SF_COL0 + (uint32_t)stage * L::SF_COLS;
             const bool both = p.K - kb * KB > KB / 2;  // a last stage may be half a stage
 #pragma unroll
             for (uint32_t j = 0; j < 2; ++j) {
               if (j == 0 || both) {
-                const uint32_t sfb = scol + (jb + j) * 4 * L::NB, sfa = scol + 16 * L::NB + (jb + j) * 4;
+                const uint32_t sfb = scol + 4 * L::NB * j, sfa = scol + 8 * L::NB + 4 * j;
                 mma_mxf4<PAIR>(tmem_base, dtok + 4 * j, dw + 4 * j, id0, sfa, sfb, kb > U.kb0 || j > 0);
                 mma_mxf4<PAIR>(tmem_base, dtok + 4 * j + 2, dw + 4 * j + 2, id2, sfa, sfb, 1u);
               }
             }
             any = true;
             commit(&empty[stage]);
-            if (second || kb == U.kb1 - 1) {
-              commit(&sempty[g]);
-              if (++g == SF_RING) {
-                g = 0;
-                gphase ^= 1u;
-              }
-              second = false;
-            } else {
-              second = true;
-            }
             if (++stage == p.stages) {
               stage = 0;
               phase ^= 1u;
@@ -591,14 +558,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     // The groups of all units in order, requested SF_BUFS - 1 groups ahead.  Rows past the chunk, a
     // missing second tile and codes past K keep what shared memory holds: no MMA result that is
     // used depends on them.
-    int u = unit0, left = 0;  // the next group to request: its unit and the unit's groups that are left
+    int u = unit0, left = 0;  // the next group to request: its unit and the unit's stages that are left
     const uint8_t *pt = nullptr, *pw[L::NB];
     uint32_t w0 = 0;  // its first word of a scale row
     int requested = 0;
+    uint32_t single = 0;  // bit r % 32: group r, at the end of its unit, has one stage
     auto next_unit = [&]() {
       if (u >= total) return;
       const Unit U = unit(u);
-      left = (U.kb1 - U.kb0 + GROUP - 1) / GROUP;
+      left = U.kb1 - U.kb0;
       w0 = (uint32_t)U.kb0 * 2;
       pt = lt < U.nvalid ? p.act_scales + (size_t)(U.rowB + lt) * row_bytes + 4 * w0 : nullptr;
 #pragma unroll
@@ -631,9 +599,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             pw[i] += 16;
           }
         }
+        const uint32_t bit = 1u << (requested & 31);
+        single = left == 1 ? single | bit : single & ~bit;
         ++requested;
         w0 += 4;
-        if (--left == 0) {
+        left -= GROUP;
+        if (left <= 0) {
           u += ustride;
           next_unit();
         }
@@ -643,51 +614,70 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     next_unit();
     if (p.early) grid_dependency_wait();  // for the scales of h
     for (uint32_t i = 0; i < SF_BUFS - 1; ++i) request(i);
-    auto release = [&](uint32_t g) {  // the stores of group g's turn are done: tell the MMA thread
+    // The stores of a turn are done: tell the MMA thread, through the barrier of the stage that also
+    // counts its copies (the leader's, for both CTAs of a pair).
+    auto arrive = [&](uint64_t* bar) {
+      if (PAIR)
+        mbar_arrive_remote(mapa_shared(bar, 0));
+      else
+        mbar_arrive(bar);
+    };
+    auto release = [&](int stage, bool two) {
       asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) {
-        if (PAIR)
-          mbar_arrive_remote(mapa_shared(&sfull[g], 0));  // the leader's waits for both CTAs
-        else
-          mbar_arrive(&sfull[g]);
+        arrive(&full[stage]);
+        if (two) arrive(&full[stage + 1 == p.stages ? 0 : stage + 1]);
       }
     };
-    uint32_t buf = 0, g = 0, gphase = 1;
-    bool ok = true;
+    uint32_t buf = 0, phase = 0;
+    int stage = 0, last_stage = 0;
+    bool ok = true, last_two = false;
     for (int turn = 0; turn < requested; ++turn) {
       asm volatile("cp.async.wait_group %0;" ::"n"(SF_BUFS - 2) : "memory");  // this turn's group is here
       // The four warps' rows of the group, and the end of their reads of the buffer before it.  Every
       // warp takes every turn, after a wait that gave up too, so this barrier always completes.
       asm volatile("bar.sync 1, 128;" ::: "memory");
+      const bool two = !(single >> (turn & 31) & 1u);
       const uint4* src = reinterpret_cast<const uint4*>(sf + buf * L::SF_BUF) + lane;
       request(buf == 0 ? SF_BUFS - 1 : buf - 1);
       if (++buf == SF_BUFS) buf = 0;
       if (!ok) continue;
-      if (turn > 0) release(g == 0 ? SF_RING - 1 : g - 1);
-      // the whole warp goes on or gives up: its stores to tensor memory are warp-wide
-      ok = __all_sync(0xffffffffu, mbar_wait<PAIR>(&sempty[g], gphase, abort_flag, TIMEOUT));
+      if (turn > 0) release(last_stage, last_two);
+      // the group's last stage is free, and with it the one before; the whole warp goes on or gives
+      // up: its stores to tensor memory are warp-wide
+      const bool wraps = stage + 1 == p.stages;
+      const int s1 = wraps ? 0 : stage + 1;
+      const int end = two ? s1 : stage;
+      const uint32_t ephase = two && wraps ? phase ^ 1u : phase;
+      ok = __all_sync(0xffffffffu, mbar_wait<PAIR>(&empty[end], ephase ^ 1u, abort_flag, TIMEOUT));
       if (!ok) continue;
       tc_fence_after_sync();
-      const uint32_t col = t_lane + g * L::SF_COLS;
+      const uint32_t c0 = t_lane + (uint32_t)stage * L::SF_COLS, c1 = t_lane + (uint32_t)s1 * L::SF_COLS;
 #pragma unroll
       for (int b = 0; b <= L::NB; ++b) {  // tokens, then the weights' blocks
         uint4 v[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) v[q] = src[128 * b + 32 * q];
-        const uint32_t c0 = b == 0 ? col + 16 * L::NB : col + 4 * (b - 1), step = b == 0 ? 4 : 4 * L::NB;
-        tmem_st4(c0, v[0].x, v[1].x, v[2].x, v[3].x);
-        tmem_st4(c0 + step, v[0].y, v[1].y, v[2].y, v[3].y);
-        tmem_st4(c0 + 2 * step, v[0].z, v[1].z, v[2].z, v[3].z);
-        tmem_st4(c0 + 3 * step, v[0].w, v[1].w, v[2].w, v[3].w);
+        const uint32_t at = b == 0 ? 8 * L::NB : 4 * (b - 1), step = b == 0 ? 4 : 4 * L::NB;
+        tmem_st4(c0 + at, v[0].x, v[1].x, v[2].x, v[3].x);
+        tmem_st4(c0 + at + step, v[0].y, v[1].y, v[2].y, v[3].y);
+        if (two) {
+          tmem_st4(c1 + at, v[0].z, v[1].z, v[2].z, v[3].z);
+          tmem_st4(c1 + at + step, v[0].w, v[1].w, v[2].w, v[3].w);
+        }
       }
-      if (++g == SF_RING) {
-        g = 0;
-        gphase ^= 1u;
+      last_stage = stage, last_two = two;
+      const int next = two ? s1 + 1 : stage + 1;  // the stage after the group's last
+      if (two && wraps) phase ^= 1u;
+      stage = next;
+      if (stage == p.stages) {
+        stage = 0;
+        phase ^= 1u;
       }
     }
-    if (ok && requested > 0) release(g == 0 ? SF_RING - 1 : g - 1);
+    if (ok && requested > 0) release(last_stage, last_two);
     cp_async_wait_all();  // no copy may land after the CTA has exited
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R::epi));
@@ -937,7 +927,7 @@ Plan make_plan(const moe_problem& p, int mode, int sm_count, int smem_cap) {
     };
     pl.sf_off = carve((size_t)SF_BUFS * sf_buf, 128);
     pl.pre_off = carve((3 * (size_t)nslots + 1) * 4, 16);
-    pl.bar_off = carve((size_t)(2 * st + 2 * SF_RING + 4) * 8, 8);
+    pl.bar_off = carve((size_t)(2 * st + 4) * 8, 8);
     pl.misc_off = carve(16, 16);
     if ((int)(off + 1024) <= smem_cap) {
       pl.stages = st;
