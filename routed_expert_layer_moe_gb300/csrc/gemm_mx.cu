@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   constexpr int TC = TW / 2;  // columns of each tile that an epilogue thread holds
   constexpr int CH = PAIR ? 2 * BN : BN;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);  // pointer arithmetic: it stays in the shared space
   uint8_t* sf = smem + p.sf_off;                           // [SF_BUFS][1 + NB blocks][128 rows][16]
   int* prefix = reinterpret_cast<int*>(smem + p.pre_off);  // [nslots + 1] unit prefix
   int* srows = prefix + p.nslots + 1;                      // [nslots] valid rows per slot
@@ -480,20 +480,23 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         int stage = 0;
         uint32_t phase = 0, u_it = 0;
         bool ok = true, any = false;
-        int units = 0, tiles = 0;
+        // whole K and always two weight tiles: a unit need not be looked up between its MMAs and the next's
+        constexpr bool ALIKE = MODE == MODE_SWIGLU;
+        int kb0 = 0, kb1 = p.kb_total, N = 2 * TW;
         for (int u = unit0; ok && leader && u < total; u += ustride, ++u_it) {
-          const Unit U = unit(u);
-          ++units;
-          tiles += (U.j == 0 && U.q == 0);  // one unit per (slot, token chunk)
-          const int M = PAIR ? 2 * BN : BN, N = U.a1 ? 2 * TW : TW;
-          const uint32_t id0 = mx_idesc(M, N, 0), id2 = mx_idesc(M, N, 2);
-          if (!mbar_wait<PAIR>(tempty, (u_it & 1u) ^ 1u, abort_flag, TIMEOUT)) {
+          if constexpr (!ALIKE) {
+            const Unit U = unit(u);
+            kb0 = U.kb0, kb1 = U.kb1;
+            N = U.a1 ? 2 * TW : TW;
+          }
+          const uint32_t id0 = mx_idesc(PAIR ? 2 * BN : BN, N, 0), id2 = mx_idesc(PAIR ? 2 * BN : BN, N, 2);
+          if (!mbar_wait(tempty, (u_it & 1u) ^ 1u, abort_flag, TIMEOUT)) {
             ok = false;
             break;
           }
           tc_fence_after_sync();
-          for (int kb = U.kb0; kb < U.kb1; ++kb) {
-            if (!mbar_wait<PAIR>(&full[stage], phase, abort_flag, TIMEOUT)) {
+          for (int kb = kb0; kb < kb1; ++kb) {
+            if (!mbar_wait(&full[stage], phase, abort_flag, TIMEOUT)) {
               ok = false;
               break;
             }
@@ -506,7 +509,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             for (uint32_t j = 0; j < 2; ++j) {
               if (j == 0 || both) {
                 const uint32_t sfb = scol + 4 * L::NB * j, sfa = scol + 8 * L::NB + 4 * j;
-                mma_mxf4<PAIR>(tmem_base, dtok + 4 * j, dw + 4 * j, id0, sfa, sfb, kb > U.kb0 || j > 0);
+                mma_mxf4<PAIR>(tmem_base, dtok + 4 * j, dw + 4 * j, id0, sfa, sfb, kb > kb0 || j > 0);
                 mma_mxf4<PAIR>(tmem_base, dtok + 4 * j + 2, dw + 4 * j + 2, id2, sfa, sfb, 1u);
               }
             }
@@ -519,20 +522,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           }
           if (ok) commit(tfull);
         }
-        if (p.stats) {
-          if (p.early) grid_dependency_wait();  // the kernel ahead writes the same counters
-          for (int h = 0; h < 2; ++h) {
-            if (blockIdx.x < STATS_CTAS) {
-              p.stats[(h * STATS_CTAS + blockIdx.x) * 2] = h ? 0 : units;
-              p.stats[(h * STATS_CTAS + blockIdx.x) * 2 + 1] = h ? 0 : tiles;
-            }
-            if (blockIdx.x == 0)
-              for (int c = gridDim.x; c < STATS_CTAS; ++c) {
-                p.stats[(h * STATS_CTAS + c) * 2] = 0;
-                p.stats[(h * STATS_CTAS + c) * 2 + 1] = 0;
-              }
-          }
-        }
         if (!ok && any) {
           // all MMAs issued by this thread must finish before tensor memory is freed
           if constexpr (PAIR)
@@ -542,6 +531,28 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           const long long t0 = clock64();
           while (!mbar_try_wait(drain, 0) && clock64() - t0 < TIMEOUT) {
           }
+        }
+      }
+    } else if (warp == 2) {
+      // ------------------------------------------------------------ statistics
+      if (lane == 0 && p.stats) {
+        int units = 0, tiles = 0;
+        for (int u = unit0; leader && u < total; u += ustride) {
+          const Unit U = unit(u);
+          ++units;
+          tiles += (U.j == 0 && U.q == 0);  // one unit per (slot, token chunk)
+        }
+        if (p.early) grid_dependency_wait();  // the kernel ahead writes the same counters
+        for (int h = 0; h < 2; ++h) {
+          if (blockIdx.x < STATS_CTAS) {
+            p.stats[(h * STATS_CTAS + blockIdx.x) * 2] = h ? 0 : units;
+            p.stats[(h * STATS_CTAS + blockIdx.x) * 2 + 1] = h ? 0 : tiles;
+          }
+          if (blockIdx.x == 0)
+            for (int c = gridDim.x; c < STATS_CTAS; ++c) {
+              p.stats[(h * STATS_CTAS + c) * 2] = 0;
+              p.stats[(h * STATS_CTAS + c) * 2 + 1] = 0;
+            }
         }
       }
     }
@@ -641,17 +652,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       asm volatile("bar.sync 1, 128;" ::: "memory");
       const bool two = !(single >> (turn & 31) & 1u);
       const uint4* src = reinterpret_cast<const uint4*>(sf + buf * L::SF_BUF) + lane;
-      request(buf == 0 ? SF_BUFS - 1 : buf - 1);
+      const uint32_t nb = buf == 0 ? SF_BUFS - 1 : buf - 1;
       if (++buf == SF_BUFS) buf = 0;
+      if (ok && turn > 0) release(last_stage, last_two);
+      request(nb);
       if (!ok) continue;
-      if (turn > 0) release(last_stage, last_two);
       // the group's last stage is free, and with it the one before; the whole warp goes on or gives
       // up: its stores to tensor memory are warp-wide
       const bool wraps = stage + 1 == p.stages;
       const int s1 = wraps ? 0 : stage + 1;
       const int end = two ? s1 : stage;
       const uint32_t ephase = two && wraps ? phase ^ 1u : phase;
-      ok = __all_sync(0xffffffffu, mbar_wait<PAIR>(&empty[end], ephase ^ 1u, abort_flag, TIMEOUT));
+      ok = __all_sync(0xffffffffu, mbar_wait(&empty[end], ephase ^ 1u, abort_flag, TIMEOUT));
       if (!ok) continue;
       tc_fence_after_sync();
       const uint32_t c0 = t_lane + (uint32_t)stage * L::SF_COLS, c1 = t_lane + (uint32_t)s1 * L::SF_COLS;
@@ -692,7 +704,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     for (int u = unit0; u < total; u += ustride, ++u_it) {
       const Unit U = unit(u);
       // the whole warp goes on together (its tensor-memory loads are warp-wide) or gives up together
-      if (!__all_sync(0xffffffffu, mbar_wait<PAIR>(tfull, u_it & 1u, abort_flag, TIMEOUT))) break;
+      if (!__all_sync(0xffffffffu, mbar_wait(tfull, u_it & 1u, abort_flag, TIMEOUT))) break;
       tc_fence_after_sync();
       const bool warp_live = quarter * 32 < U.nvalid;
       const bool live = lrow < U.nvalid;
