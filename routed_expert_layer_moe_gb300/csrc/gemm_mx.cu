@@ -61,15 +61,11 @@ constexpr int MAX_STAGES = 6;           // their scales: 24 columns each at most
 constexpr int NUM_THREADS = 512;        // four warpgroups
 constexpr int SF_WARP0 = 4, SF_WARPS = 4;
 constexpr int EPI_WARP0 = 8, EPI_WARPS = 8;
-// Register split (setmaxnreg) of warpgroup 0, the scale warps and the two epilogue warpgroups:
-// 128 * (ctrl + sf + 2 epi) <= 512 * (registers at launch), checked before the first launch.
-// Next to 220 KB of shared memory there is hardly an L1 to spill to: the split is the one without
-// spills in the epilogue (128 accumulators a thread, or 64 packed to bf16 in an unsplit down product).
-template <bool LEAN>
-struct Regs {
-  static constexpr int ctrl = LEAN ? 96 : 80, sf = LEAN ? 96 : 80, epi = LEAN ? 160 : 176;
-  static constexpr int needed = 128 * (ctrl + sf + 2 * epi);
-};
+// Register split (setmaxnreg) of warpgroup 0, the scale warps and the two epilogue warpgroups (128
+// accumulators a thread): what they add up to must be there at launch, which is checked before the first one.
+// None of the forms spills with it; next to 220 KB of shared memory there is hardly an L1 to spill to.
+constexpr int CTRL_REGS = 104, SF_REGS = 104, EPI_REGS = 152;
+constexpr int SPLIT_REGS = 128 * (CTRL_REGS + SF_REGS + 2 * EPI_REGS);
 constexpr uint32_t TMEM_COLS = 512;
 constexpr long long TIMEOUT = 4000000000LL;  // SM cycles, about 2 s
 // Token boxes of 16, 32, 64, 96 and 128 rows: the smallest that covers a chunk is copied.
@@ -172,6 +168,25 @@ __device__ __forceinline__ Unit decode_unit(const MxParams& p, const int* prefix
   U.kb0 = U.q * p.kb_per_split;
   U.kb1 = min(p.kb_total, U.kb0 + p.kb_per_split);
   return U;
+}
+
+__device__ __forceinline__ uint64_t policy_evict_normal() {
+  uint64_t pol;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
+  return pol;
+}
+
+// One lane of a converged warp, the same at every call.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n"
+      "  .reg .pred p;\n"
+      "  elect.sync _|p, 0xffffffff;\n"
+      "  selp.u32 %0, 1, 0, p;\n"
+      "}\n"
+      : "=r"(one));
+  return one;
 }
 
 // D[tmem] (+)= (A sfa) (B sfb)^T over K = 64 codes, issued by one thread.  PAIR: by the leader for both
@@ -316,7 +331,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     grouped_gemm_mx_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ TokenMaps tmB,
                            const MxParams p) {
   using L = Tile<TW, PAIR>;
-  using R = Regs<MODE == MODE_DOWN && !SPLIT>;
   constexpr int TC = TW / 2;  // columns of each tile that an epilogue thread holds
   constexpr int CH = PAIR ? 2 * BN : BN;
   extern __shared__ uint8_t smem_raw[];
@@ -335,7 +349,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + p.misc_off + 4);
 
   const int tid = threadIdx.x;
-  const int warp = tid >> 5, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;  // the warp number is uniform
   // pairs: rank 0 (the leader) issues the MMAs; units are dealt per cluster
   const uint32_t crank = PAIR ? cluster_ctarank() : 0u;
   const bool leader = crank == 0;
@@ -397,13 +411,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   auto unit = [&](int u) { return decode_unit<PAIR>(p, prefix, srows, sbase, u, crank); };
 
   if (warp < SF_WARP0) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::ctrl));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(CTRL_REGS));
     if (warp == 0) {
       // ------------------------------------------------------------ producer
       if (lane == 0) {
         tma_prefetch_map(&tmA);
         for (int i = 0; i < p.boxes; ++i) tma_prefetch_map(&tmB.box[i]);
-        const uint64_t pol = policy_evict_first();
+        // Weights give way in L2 to what is used again, but not in the down product of SM pairs: with 512 experts of
+        // 1024 x 4096 it took 319 us so and 267 without (one expert of 14336 x 4096: 145 and 147).
+        const uint64_t pol = PAIR && MODE == MODE_DOWN ? policy_evict_normal() : policy_evict_first();
         int stage = 0;
         uint32_t phase = 0;
         long issued = 0;
@@ -470,69 +486,72 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
     } else if (warp == 1) {
       // ------------------------------------------------------------ MMAs
-      if (lane == 0) {
-        auto commit = [&](uint64_t* bar) {
-          if constexpr (PAIR)
-            tc_commit_pair(bar, 3);  // both CTAs' barriers
-          else
-            tc_commit(bar);
-        };
-        int stage = 0;
-        uint32_t phase = 0, u_it = 0;
-        bool ok = true, any = false;
-        // whole K and always two weight tiles: a unit need not be looked up between its MMAs and the next's
-        constexpr bool ALIKE = MODE == MODE_SWIGLU;
-        int kb0 = 0, kb1 = p.kb_total, N = 2 * TW;
-        for (int u = unit0; ok && leader && u < total; u += ustride, ++u_it) {
-          if constexpr (!ALIKE) {
-            const Unit U = unit(u);
-            kb0 = U.kb0, kb1 = U.kb1;
-            N = U.a1 ? 2 * TW : TW;
-          }
-          const uint32_t id0 = mx_idesc(PAIR ? 2 * BN : BN, N, 0), id2 = mx_idesc(PAIR ? 2 * BN : BN, N, 2);
-          if (!mbar_wait(tempty, (u_it & 1u) ^ 1u, abort_flag, TIMEOUT)) {
-            ok = false;
-            break;
-          }
+      // The whole warp runs the loop and one elected lane issues: the operands then stay in uniform
+      // registers.  In a loop that only lane 0 ran, each MMA took its eight operands there one by one, 85
+      // cycles an MMA and 680 a stage of 528 cycles of MMAs.
+      auto commit = [&](uint64_t* bar) {
+        if constexpr (PAIR)
+          tc_commit_pair(bar, 3);  // both CTAs' barriers
+        else
+          tc_commit(bar);
+      };
+      const uint32_t acc = __shfl_sync(0xffffffffu, tmem_base, 0);
+      const uint64_t desc_w = smem_desc_sw128(smem_u32(smem)), desc_t = smem_desc_sw128(smem_u32(smem) + L::W_STAGED);
+      int stage = 0;
+      uint32_t phase = 0, u_it = 0;
+      bool ok = true, any = false;
+      // whole K and always two weight tiles: a unit need not be looked up between its MMAs and the next's
+      constexpr bool ALIKE = MODE == MODE_SWIGLU;
+      int kb0 = 0, kb1 = p.kb_total, N = 2 * TW;
+      for (int u = unit0; ok && leader && u < total; u += ustride, ++u_it) {
+        if constexpr (!ALIKE) {
+          const Unit U = unit(u);
+          kb0 = __shfl_sync(0xffffffffu, U.kb0, 0), kb1 = __shfl_sync(0xffffffffu, U.kb1, 0);
+          N = __shfl_sync(0xffffffffu, U.a1 ? 2 * TW : TW, 0);
+        }
+        const uint32_t id0 = mx_idesc(PAIR ? 2 * BN : BN, N, 0), id2 = mx_idesc(PAIR ? 2 * BN : BN, N, 2);
+        ok = __all_sync(0xffffffffu, mbar_wait(tempty, (u_it & 1u) ^ 1u, abort_flag, TIMEOUT));
+        if (!ok) break;
+        tc_fence_after_sync();
+        for (int kb = kb0; kb < kb1; ++kb) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&full[stage], phase, abort_flag, TIMEOUT));
+          if (!ok) break;
           tc_fence_after_sync();
-          for (int kb = kb0; kb < kb1; ++kb) {
-            if (!mbar_wait(&full[stage], phase, abort_flag, TIMEOUT)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after_sync();
-            const uint32_t st = smem_u32(smem + (size_t)stage * L::STAGE);
-            const uint64_t dw = smem_desc_sw128(st), dtok = smem_desc_sw128(st + L::W_STAGED);
-            const uint32_t scol = tmem_base + SF_COL0 + (uint32_t)stage * L::SF_COLS;
-            const bool both = p.K - kb * KB > KB / 2;  // a last stage may be half a stage
+          const uint64_t dw = desc_w + (uint32_t)stage * (L::STAGE >> 4), dtok = desc_t + (uint32_t)stage * (L::STAGE >> 4);
+          const uint32_t scol = acc + SF_COL0 + (uint32_t)stage * L::SF_COLS;
+          const bool both = p.K - kb * KB > KB / 2;  // a last stage may be half a stage
+          if (elect_one()) {
 #pragma unroll
             for (uint32_t j = 0; j < 2; ++j) {
               if (j == 0 || both) {
                 const uint32_t sfb = scol + 4 * L::NB * j, sfa = scol + 8 * L::NB + 4 * j;
-                mma_mxf4<PAIR>(tmem_base, dtok + 4 * j, dw + 4 * j, id0, sfa, sfb, kb > kb0 || j > 0);
-                mma_mxf4<PAIR>(tmem_base, dtok + 4 * j + 2, dw + 4 * j + 2, id2, sfa, sfb, 1u);
+                mma_mxf4<PAIR>(acc, dtok + 4 * j, dw + 4 * j, id0, sfa, sfb, kb > kb0 || j > 0);
+                mma_mxf4<PAIR>(acc, dtok + 4 * j + 2, dw + 4 * j + 2, id2, sfa, sfb, 1u);
               }
             }
-            any = true;
             commit(&empty[stage]);
-            if (++stage == p.stages) {
-              stage = 0;
-              phase ^= 1u;
-            }
           }
-          if (ok) commit(tfull);
+          __syncwarp();
+          any = true;
+          if (++stage == p.stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
         }
-        if (!ok && any) {
-          // all MMAs issued by this thread must finish before tensor memory is freed
-          if constexpr (PAIR)
-            tc_commit_pair(drain, 1);
-          else
-            tc_commit(drain);
-          const long long t0 = clock64();
-          while (!mbar_try_wait(drain, 0) && clock64() - t0 < TIMEOUT) {
-          }
+        if (ok && elect_one()) commit(tfull);
+        __syncwarp();
+      }
+      if (!ok && any && elect_one()) {
+        // all MMAs issued by this thread must finish before tensor memory is freed
+        if constexpr (PAIR)
+          tc_commit_pair(drain, 1);
+        else
+          tc_commit(drain);
+        const long long t0 = clock64();
+        while (!mbar_try_wait(drain, 0) && clock64() - t0 < TIMEOUT) {
         }
       }
+      __syncwarp();
     } else if (warp == 2) {
       // ------------------------------------------------------------ statistics
       if (lane == 0 && p.stats) {
@@ -557,7 +576,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
     }
   } else if (warp < EPI_WARP0) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::sf));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(SF_REGS));
     // ------------------------------------------------------------ scales
     // These warps run a short serial chain per group and bound the kernel when it is long: addresses
     // are per unit, the warps meet at a hardware barrier, and a group's stores to tensor memory
@@ -692,7 +711,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     if (ok && requested > 0) release(last_stage, last_two);
     cp_async_wait_all();  // no copy may land after the CTA has exited
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R::epi));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(EPI_REGS));
     // ------------------------------------------------------------ epilogue
     const int quarter = warp & 3;              // tensor-memory lane quarter this warp may access
     const int half = (warp - EPI_WARP0) >> 2;  // column half of each tile
@@ -960,7 +979,7 @@ int prepare_kernel() {
   // the register split must fit in what the launch provides, or setmaxnreg.inc would wait forever
   cudaFuncAttributes fa{};
   if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return MOE_ERR_CUDA;
-  if (fa.numRegs * NUM_THREADS < Regs<MODE == MODE_DOWN && !SPLIT>::needed) return MOE_ERR_UNSUPPORTED;
+  if (fa.numRegs * NUM_THREADS < SPLIT_REGS) return MOE_ERR_UNSUPPORTED;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, device_info().max_smem_optin) !=
       cudaSuccess)
     return MOE_ERR_CUDA;
