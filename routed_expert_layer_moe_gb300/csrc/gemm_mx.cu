@@ -23,7 +23,7 @@
 //     against 0.27 us of MMAs.
 // Roles of a CTA:
 //   * Warp 0: TMA producer.  A stage is 256 codes (128 bytes) of K.
-//   * Warp 1: the thread that issues a stage's four MMAs of K = 64.
+//   * Warp 1: issues a stage's four MMAs of K = 64.
 //   * Warps 4-7: scales.  Per group of 512 codes (two stages) a thread copies the 16 scale bytes of
 //     its row in each block of 128 rows (row-major in global memory) to shared memory, three
 //     groups ahead; every warp then reads all rows and writes them to its lane quarter of tensor memory
@@ -31,9 +31,9 @@
 //     the four bytes of row 32 q + i, the same in each quarter.  Copying them from shared memory
 //     with tcgen05.cp instead put six copies a stage into the tensor core's queue: 0.69 us a stage,
 //     0.62 without them.
-//     A stage's scales are counted on the barrier of its copies and freed with them: with barriers of
-//     their own, two more operations a group, the issuing thread became the bottleneck (dense gate/up 328
-//     us instead of 269 without epilogue).
+//     A stage's scales are counted on the barrier of its copies and freed with them: with barriers
+//     of their own, two more operations a group for the MMA warp, a dense gate/up product (8192 x 4096
+//     by 28672 columns) took 391 us instead of 338.
 //   * Warps 8-15: epilogue.  Columns 0-255 of tensor memory hold the unit's accumulators, the
 //     columns above them the stages' scales.  The epilogue first moves the accumulators to
 //     registers and hands them back, so only that move is not overlapped with the next unit's
@@ -127,7 +127,7 @@ struct Unit {
   bool a1;           // the second tile exists
 };
 
-template <bool PAIR>
+template <bool PAIR, bool SPLIT>
 __device__ __forceinline__ Unit decode_unit(const MxParams& p, const int* prefix, const int* srows, const int* sbase,
                                             int u, uint32_t rank) {
   constexpr int CH = PAIR ? 2 * BN : BN;
@@ -144,8 +144,8 @@ __device__ __forceinline__ Unit decode_unit(const MxParams& p, const int* prefix
   const int r = u - prefix[lo];
   const int m = srows[lo];
   const int nch = (m + CH - 1) / CH;
-  U.q = r % p.ksplit;
-  const int rest = r / p.ksplit;
+  U.q = SPLIT ? r % p.ksplit : 0;
+  const int rest = SPLIT ? r / p.ksplit : r;
   U.c = rest % nch;
   U.j = rest / nch;
   const int base = m / nch, extra = m - base * nch;  // near-equal chunks
@@ -165,8 +165,8 @@ __device__ __forceinline__ Unit decode_unit(const MxParams& p, const int* prefix
   U.rowA0 = lo * p.NA + U.j * p.pair_stride;
   U.rowA1 = U.rowA0 + p.a1_off;
   U.a1 = PAIR || p.mode == MODE_SWIGLU || U.j * p.pair_stride + p.a1_off < p.NA;
-  U.kb0 = U.q * p.kb_per_split;
-  U.kb1 = min(p.kb_total, U.kb0 + p.kb_per_split);
+  U.kb0 = SPLIT ? U.q * p.kb_per_split : 0;
+  U.kb1 = SPLIT ? min(p.kb_total, U.kb0 + p.kb_per_split) : p.kb_total;
   return U;
 }
 
@@ -406,9 +406,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   // both CTAs' barriers are initialised before either CTA touches the other's
   if constexpr (PAIR) cluster_sync_all();
   tc_fence_after_sync();
-  const uint32_t tmem_base = *tmem_base_smem;
+  const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_base_smem, 0);  // uniform, as the tensor core's operands are
   const int total = prefix[p.nslots];
-  auto unit = [&](int u) { return decode_unit<PAIR>(p, prefix, srows, sbase, u, crank); };
+  auto unit = [&](int u) { return decode_unit<PAIR, SPLIT>(p, prefix, srows, sbase, u, crank); };
 
   if (warp < SF_WARP0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(CTRL_REGS));
@@ -495,7 +495,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         else
           tc_commit(bar);
       };
-      const uint32_t acc = __shfl_sync(0xffffffffu, tmem_base, 0);
       const uint64_t desc_w = smem_desc_sw128(smem_u32(smem)), desc_t = smem_desc_sw128(smem_u32(smem) + L::W_STAGED);
       int stage = 0;
       uint32_t phase = 0, u_it = 0;
@@ -518,15 +517,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           if (!ok) break;
           tc_fence_after_sync();
           const uint64_t dw = desc_w + (uint32_t)stage * (L::STAGE >> 4), dtok = desc_t + (uint32_t)stage * (L::STAGE >> 4);
-          const uint32_t scol = acc + SF_COL0 + (uint32_t)stage * L::SF_COLS;
+          const uint32_t scol = tmem_base + SF_COL0 + (uint32_t)stage * L::SF_COLS;
           const bool both = p.K - kb * KB > KB / 2;  // a last stage may be half a stage
           if (elect_one()) {
 #pragma unroll
             for (uint32_t j = 0; j < 2; ++j) {
               if (j == 0 || both) {
                 const uint32_t sfb = scol + 4 * L::NB * j, sfa = scol + 8 * L::NB + 4 * j;
-                mma_mxf4<PAIR>(acc, dtok + 4 * j, dw + 4 * j, id0, sfa, sfb, kb > kb0 || j > 0);
-                mma_mxf4<PAIR>(acc, dtok + 4 * j + 2, dw + 4 * j + 2, id2, sfa, sfb, 1u);
+                mma_mxf4<PAIR>(tmem_base, dtok + 4 * j, dw + 4 * j, id0, sfa, sfb, kb > kb0 || j > 0);
+                mma_mxf4<PAIR>(tmem_base, dtok + 4 * j + 2, dw + 4 * j + 2, id2, sfa, sfb, 1u);
               }
             }
             commit(&empty[stage]);
@@ -578,9 +577,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   } else if (warp < EPI_WARP0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(SF_REGS));
     // ------------------------------------------------------------ scales
-    // These warps run a short serial chain per group and bound the kernel when it is long: addresses
-    // are per unit, the warps meet at a hardware barrier, and a group's stores to tensor memory
-    // are waited for in the next turn.
+    // These warps run a serial chain per group, and it bounds large products: 1200-1400 cycles a turn
+    // against 1056 of the group's MMAs.  So addresses are per unit, all reads of a turn come before its
+    // stores, the next copies are requested while those are on their way, and the next unit is
+    // looked up after the MMA thread has been told (dense gate/up 294 -> 286 us).
     const int lt = tid - SF_WARP0 * 32;  // this thread's row of each 128-row block
     const uint32_t words = (uint32_t)p.K / 128;  // words of a scale row
     const size_t row_bytes = (size_t)p.K / 32;
@@ -634,16 +634,21 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         ++requested;
         w0 += 4;
         left -= GROUP;
-        if (left <= 0) {
-          u += ustride;
-          next_unit();
-        }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
+    auto look_up = [&]() {  // the unit of the next request
+      if (left <= 0 && u < total) {
+        u += ustride;
+        next_unit();
+      }
+    };
     next_unit();
     if (p.early) grid_dependency_wait();  // for the scales of h
-    for (uint32_t i = 0; i < SF_BUFS - 1; ++i) request(i);
+    for (uint32_t i = 0; i < SF_BUFS - 1; ++i) {
+      request(i);
+      look_up();
+    }
     // The stores of a turn are done: tell the MMA thread, through the barrier of the stage that also
     // counts its copies (the leader's, for both CTAs of a pair).
     auto arrive = [&](uint64_t* bar) {
@@ -662,8 +667,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
     };
     uint32_t buf = 0, phase = 0;
-    int stage = 0, last_stage = 0;
-    bool ok = true, last_two = false;
+    int stage = 0;
+    bool ok = true;
     for (int turn = 0; turn < requested; ++turn) {
       asm volatile("cp.async.wait_group %0;" ::"n"(SF_BUFS - 2) : "memory");  // this turn's group is here
       // The four warps' rows of the group, and the end of their reads of the buffer before it.  Every
@@ -673,33 +678,42 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const uint4* src = reinterpret_cast<const uint4*>(sf + buf * L::SF_BUF) + lane;
       const uint32_t nb = buf == 0 ? SF_BUFS - 1 : buf - 1;
       if (++buf == SF_BUFS) buf = 0;
-      if (ok && turn > 0) release(last_stage, last_two);
-      request(nb);
-      if (!ok) continue;
+      uint4 v[1 + L::NB][4];  // all of the group's reads before its first store
+#pragma unroll
+      for (int b = 0; b <= L::NB; ++b)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[b][q] = src[128 * b + 32 * q];
       // the group's last stage is free, and with it the one before; the whole warp goes on or gives
       // up: its stores to tensor memory are warp-wide
       const bool wraps = stage + 1 == p.stages;
       const int s1 = wraps ? 0 : stage + 1;
       const int end = two ? s1 : stage;
       const uint32_t ephase = two && wraps ? phase ^ 1u : phase;
-      ok = __all_sync(0xffffffffu, mbar_wait(&empty[end], ephase ^ 1u, abort_flag, TIMEOUT));
-      if (!ok) continue;
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&empty[end], ephase ^ 1u, abort_flag, TIMEOUT));
+      if (!ok) {
+        request(nb);
+        look_up();
+        continue;
+      }
       tc_fence_after_sync();
       const uint32_t c0 = t_lane + (uint32_t)stage * L::SF_COLS, c1 = t_lane + (uint32_t)s1 * L::SF_COLS;
+      auto at = [](int b) { return (uint32_t)(b == 0 ? 8 * L::NB : 4 * (b - 1)); };  // tokens, then the weights' blocks
+      auto step = [](int b) { return (uint32_t)(b == 0 ? 4 : 4 * L::NB); };
 #pragma unroll
-      for (int b = 0; b <= L::NB; ++b) {  // tokens, then the weights' blocks
-        uint4 v[4];
+      for (int b = 0; b <= L::NB; ++b) {
+        tmem_st4(c0 + at(b), v[b][0].x, v[b][1].x, v[b][2].x, v[b][3].x);
+        tmem_st4(c0 + at(b) + step(b), v[b][0].y, v[b][1].y, v[b][2].y, v[b][3].y);
+      }
+      if (two) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = src[128 * b + 32 * q];
-        const uint32_t at = b == 0 ? 8 * L::NB : 4 * (b - 1), step = b == 0 ? 4 : 4 * L::NB;
-        tmem_st4(c0 + at, v[0].x, v[1].x, v[2].x, v[3].x);
-        tmem_st4(c0 + at + step, v[0].y, v[1].y, v[2].y, v[3].y);
-        if (two) {
-          tmem_st4(c1 + at, v[0].z, v[1].z, v[2].z, v[3].z);
-          tmem_st4(c1 + at + step, v[0].w, v[1].w, v[2].w, v[3].w);
+        for (int b = 0; b <= L::NB; ++b) {
+          tmem_st4(c1 + at(b), v[b][0].z, v[b][1].z, v[b][2].z, v[b][3].z);
+          tmem_st4(c1 + at(b) + step(b), v[b][0].w, v[b][1].w, v[b][2].w, v[b][3].w);
         }
       }
-      last_stage = stage, last_two = two;
+      request(nb);  // while the stores are on their way
+      release(stage, two);
+      look_up();  // a few hundred cycles: after the group that the MMA thread waits for
       const int next = two ? s1 + 1 : stage + 1;  // the stage after the group's last
       if (two && wraps) phase ^= 1u;
       stage = next;
@@ -708,7 +722,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         phase ^= 1u;
       }
     }
-    if (ok && requested > 0) release(last_stage, last_two);
     cp_async_wait_all();  // no copy may land after the CTA has exited
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(EPI_REGS));
