@@ -13,11 +13,14 @@
 // once; the statistics are fp32 sums over the CTA.  Backward: CTAs walk the rows with a fixed
 // stride and keep the sums over tokens in registers (one for dw_post and dg together: a
 // per-channel gate leaves the sum over tokens), write them once, and a second kernel adds the
-// CTAs' sums in order.  Both directions are bound by HBM.  With a CTA's loads issued at the start
+// CTAs' sums in order.  With a CTA's loads issued at the start
 // of each row, memory idled through the row's two or three reductions: 8192 x 4096 bf16 took 67
 // and 177 us, against 40 and 60 at the memory's rate.  So the rows to come are fetched into
 // shared memory by asynchronous copies, DEPTH rows ahead; a thread copies and reads only its
-// own columns, so these copies need no barrier.
+// own columns, so these copies need no barrier.  Now 42 and 88 us: forward at the memory's rate (6.4 TB/s),
+// backward (4.6 TB/s) held by its instructions and the latency of two reductions a row.  Rows that
+// are not 16-byte aligned are read when wanted: 2018 x 6290 bf16 takes 75 us forward and 200
+// backward, 15 and 23 at the memory's rate.
 #include <algorithm>
 #include <type_traits>
 
@@ -68,8 +71,20 @@ __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162f
 __device__ __forceinline__ void from_float(float* d, float v) { *d = v; }
 __device__ __forceinline__ void from_float(__nv_bfloat16* d, float v) { *d = __float2bfloat16_rn(v); }
 
-// Columns c..c+7 of a row: 16-byte accesses (VEC: H a multiple of 8 and every array 16-byte aligned)
-// or single ones within the row; zeros past its end.
+// The eight columns of the thread whose vector begins at c = 8 * (a number whose last five bits are the lane):
+// c..c+7 by 16-byte accesses (VEC: H a multiple of 8 and every array 16-byte aligned), or by single ones the lane's
+// of the warp's 256 columns with a stride of 32, so that a warp's access is one contiguous piece (4000 x 1111
+// fp32 in both directions 71 us, 123 with columns c..c+7; 2018 x 6290 bf16 forward 75 and 103).  Zeros past
+// the row's end.
+template <bool VEC>
+__device__ __forceinline__ int column(int c, int i) {
+  return VEC ? c + i : (c & ~255) + ((c >> 3) & 31) + 32 * i;
+}
+template <bool VEC>
+__device__ __forceinline__ bool inside(int c, int H) {  // one of a vector's columns may be in the row
+  return (VEC ? c : c & ~255) < H;
+}
+
 template <bool VEC, typename T>
 __device__ __forceinline__ V8 load8(const T* row, int c, int H) {
   if constexpr (VEC && sizeof(T) == 4) {
@@ -79,9 +94,10 @@ __device__ __forceinline__ V8 load8(const T* row, int c, int H) {
   } else {
     V8 r;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      r.v[i] = make_float2(c + 2 * i < H ? to_float(row[c + 2 * i]) : 0.0f,
-                           c + 2 * i + 1 < H ? to_float(row[c + 2 * i + 1]) : 0.0f);
+    for (int i = 0; i < 4; ++i) {
+      const int c0 = column<false>(c, 2 * i), c1 = column<false>(c, 2 * i + 1);
+      r.v[i] = make_float2(c0 < H ? to_float(row[c0]) : 0.0f, c1 < H ? to_float(row[c1]) : 0.0f);
+    }
     return r;
   }
 }
@@ -110,8 +126,9 @@ __device__ __forceinline__ void store8(T* row, int c, int H, const V8& a) {
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (c + 2 * i < H) from_float(row + c + 2 * i, a.v[i].x);
-      if (c + 2 * i + 1 < H) from_float(row + c + 2 * i + 1, a.v[i].y);
+      const int c0 = column<false>(c, 2 * i), c1 = column<false>(c, 2 * i + 1);
+      if (c0 < H) from_float(row + c0, a.v[i].x);
+      if (c1 < H) from_float(row + c1, a.v[i].y);
     }
   }
 }
@@ -166,6 +183,7 @@ __device__ __forceinline__ void cp_async16(void* smem_dst, const void* src) {
 template <typename T, int V, bool VEC, int DEPTH, int N, int NT>
 struct Rows {
   enum { PARTS = 8 * sizeof(T) / 16 };  // 16-byte parts of a vector, in planes of their own
+  static constexpr bool kVec = VEC;
   const T* a[N];  // null: the array is not there
   int H;
   uint8_t* smem;
@@ -231,7 +249,7 @@ __device__ __forceinline__ float sum_squares(const R& in, int n, int r, int slot
   float2 s = pair(0.0f);
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    if ((int)(j * in.threads() + threadIdx.x) * 8 < in.H) {
+    if (inside<R::kVec>((int)(j * in.threads() + threadIdx.x) * 8, in.H)) {
       const V8 b = in.get(n, r, slot, j);
 #pragma unroll
       for (int i = 0; i < 4; ++i) s = fma2(b.v[i], b.v[i], s);
@@ -270,7 +288,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_norm_kernel(const Args<T> a)
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int c = (j * nt + threadIdx.x) * 8;
-      if (c < H) {
+      if (inside<VEC>(c, H)) {
         y[j] = in.get(0, r, slot, j);
         if (a.block) {
           const V8 b = in.get(1, r, slot, j), w = load_post<VEC>(a, c);
@@ -293,7 +311,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_norm_kernel(const Args<T> a)
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const int c = (j * nt + threadIdx.x) * 8;
-        if (c < H) {
+        if (inside<VEC>(c, H)) {
           V8 w = load8<VEC>(a.w_pre, c, H);
 #pragma unroll
           for (int i = 0; i < 4; ++i) w.v[i] = mul2(w.v[i], mul2(y[j].v[i], ry));
@@ -325,7 +343,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_norm_backward_kernel(const A
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int c = (j * nt + threadIdx.x) * 8;
-      if (c < H) {
+      if (inside<VEC>(c, H)) {
         if (a.block) put8(wmem + 2 * j * plane, plane, load_post<VEC>(a, c));
         if (a.dxn) put8(wmem + (2 * V + 2 * j) * plane, plane, load8<VEC>(a.w_pre, c, H));
       }
@@ -363,7 +381,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_norm_backward_kernel(const A
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int c = (j * nt + threadIdx.x) * 8;
-      if (c < H) {
+      if (inside<VEC>(c, H)) {
         y[j] = in.get(X, r, slot, j);
         if (a.block) {
           const V8 b = in.get(B, r, slot, j), w = post_weight(j, c);
@@ -392,7 +410,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_norm_backward_kernel(const A
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int c = (j * nt + threadIdx.x) * 8;
-      if (c < H) {
+      if (inside<VEC>(c, H)) {
         V8 d = a.dy ? in.get(DY, r, slot, j) : zeros();
         if (a.dxn) {
           const V8 q = in.get(DXN, r, slot, j), w = pre_weight(j, c);
@@ -426,7 +444,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_norm_backward_kernel(const A
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const int c = (j * nt + threadIdx.x) * 8;
-        if (c < H) {
+        if (inside<VEC>(c, H)) {
           V8 b = in.get(B, r, slot, j);
 #pragma unroll
           for (int i = 0; i < 4; ++i) b.v[i] = fma2(mean, b.v[i], mul2(f, y[j].v[i]));
@@ -444,7 +462,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_norm_backward_kernel(const A
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const int c = (j * nt + threadIdx.x) * 8;
-    if (c < H) {
+    if (inside<VEC>(c, H)) {
       store8<VEC>(part, c, H, acc_post[j]);
       store8<VEC>(part + H, c, H, acc_pre[j]);
     }
