@@ -60,10 +60,11 @@ struct Segments {
     }
   };
 
-  // The last segment that starts at or before t (the one that holds t, if any does; 0 if none does), with
-  // its bounds.  By a whole warp, the same t in every lane and t growing from call to call: many places
-  // are looked at together, for one after the other each costs the memory's latency (six of them
-  // for 48 segments), and kept for the next call: a tile that several short segments meet would pay
+  // The last segment that starts at or before t (the one that holds t, if any does), with its bounds; for a t
+  // before all segments the last one that starts where the first does (those before it are empty, so it
+  // is the next with tokens, if any has).  By a whole warp, the same t in every lane and t growing from call
+  // to call: many places are looked at together, for one after the other each costs the memory's latency (six
+  // of them for 48 segments), and kept for the next call: a tile that several short segments meet would pay
   // for each of them.
   __device__ __forceinline__ int find(int t, Window& w, int& first, int& end) const {
     if (!off) {
@@ -71,21 +72,27 @@ struct Segments {
       return 0;
     }
     const int lane = threadIdx.x & 31;
-    if (w.n == 0 || (w.a + w.n < nseq && w.at(w.n) <= t)) {
-      int a = w.a, n = nseq - w.a;
-      while (n > 63) {  // 32 steps through what is left
-        const int step = (n + 31) / 32, i = lane * step;
-        const bool before = i < n && __ldg(off + a + i) <= t;
-        const int k = 31 - __clz(__ballot_sync(0xffffffffu, before) | 1u);  // the last place at or before t
-        a += k * step;
-        n = min(step, n - k * step);
+    unsigned m0, m1;
+    for (int pass = 0;; ++pass) {
+      if (w.n == 0 || (w.a + w.n < nseq && w.at(w.n) <= t)) {
+        int a = w.a, n = nseq - w.a;
+        while (n > 63) {  // 32 steps through what is left
+          const int step = (n + 31) / 32, i = lane * step;
+          const bool before = i < n && __ldg(off + a + i) <= t;
+          const int k = 31 - __clz(__ballot_sync(0xffffffffu, before) | 1u);  // the last place at or before t
+          a += k * step;
+          n = min(step, n - k * step);
+        }
+        w.a = a, w.n = min(63, nseq - a);
+        w.v0 = lane <= w.n ? __ldg(off + a + lane) : 0;
+        w.v1 = lane + 32 <= w.n ? __ldg(off + a + lane + 32) : 0;
       }
-      w.a = a, w.n = min(63, nseq - a);
-      w.v0 = lane <= w.n ? __ldg(off + a + lane) : 0;
-      w.v1 = lane + 32 <= w.n ? __ldg(off + a + lane + 32) : 0;
+      m0 = __ballot_sync(0xffffffffu, lane < w.n && w.v0 <= t);
+      m1 = __ballot_sync(0xffffffffu, lane + 32 < w.n && w.v1 <= t);
+      if (m0 | m1 || pass) break;
+      t = w.at(0);  // no segment starts at or before t: look up the first one's start instead
+      w.n = 0;
     }
-    const unsigned m0 = __ballot_sync(0xffffffffu, lane < w.n && w.v0 <= t);
-    const unsigned m1 = __ballot_sync(0xffffffffu, lane + 32 < w.n && w.v1 <= t);
     const int k = m1 ? 63 - __clz(m1) : 31 - __clz(m0 | 1u);
     first = max(w.at(k), 0);
     end = min(w.at(k + 1), T);

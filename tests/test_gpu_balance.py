@@ -181,3 +181,22 @@ def test_unaligned_rows_other_streams_and_repeats():
             assert a[k] == other[k] if k == "err" else torch.equal(a[k], other[k]), k
     b = run(*args, offset=1)  # 4-byte aligned rows
     check(b, ref.balance(*args), *args)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,seq", [
+    (10, [5, 5, 10]), (10, [3, 3, 3, 10]), (80, [7, 7, 30, 80]),  # one launch
+    (100, [40, 40, 40, 100]), (200, [100, 100, 170]),             # the first segment with tokens in a later tile
+    (50, [20, 20]), (50, [50, 50, 50]),                           # no segment has tokens
+    (900, [7, 7, 30, 880]), (900, [400, 400, 400, 900]),          # two kernels
+    (900, [33] * 80 + [500, 500, 501, 890]),                      # more empty segments than a look-up holds
+])
+def test_empty_segments_behind_tokens_of_no_segment(T, seq, score):
+    """Tokens before the first segment, and that one empty: the segments after it keep their tokens."""
+    logits, ids, g = inputs(T, 24, 3, seed=T)
+    dloss = torch.randn(len(seq) - 1, generator=g)
+    for valid in (None, (torch.rand(T, generator=g) < 0.7).to(torch.uint8)):
+        args = (logits, ids, valid, seq, score, 0.01, dloss)
+        got = run(*args)
+        assert got["err"] == 0
+        check(got, ref.balance(*args), *args)
