@@ -9,6 +9,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "moe.h"
 
 namespace moe {
@@ -22,6 +24,21 @@ struct DeviceInfo {
   int max_smem_optin;
 };
 const DeviceInfo& device_info();  // of the current device, cached
+
+// The most that bytes(SM count) comes to over GPUs of common sizes and the present device, if there is one.  A plan that
+// splits K to fill whole waves is not monotone in the SM count, so the counts listed do not bound those between
+// them; they are there so that a workspace also serves the other devices of a machine.
+template <typename F>
+size_t max_over_sm_counts(F bytes) {
+  const int own = device_info().sm_count;
+  bool done = own == 0;
+  size_t best = 0;
+  for (int sms : {132, 148, 152, 160, 170, 188, 256}) {
+    best = std::max<size_t>(best, bytes(sms));
+    done = done || sms == own;
+  }
+  return done ? best : std::max<size_t>(best, bytes(own));
+}
 
 // cuTensorMapEncodeTiled, resolved once through the runtime's driver entry point.
 CUresult encode_tensor_map(CUtensorMap* map, CUtensorMapDataType dtype, uint64_t inner, uint64_t outer,

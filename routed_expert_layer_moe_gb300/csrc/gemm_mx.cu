@@ -1062,11 +1062,8 @@ int launch_kernel(const Plan& pl, const CUtensorMap& tA, const TokenMaps& tB, co
 int gemm_mx_tile_rows(const moe_problem& p, int mode) { return use_pairs(p, mode) ? 2 * BN : BN; }
 
 size_t gemm_mx_workspace_bytes(const moe_problem& p) {
-  // the split (of the down product alone) depends on the SM count; sized for the largest plausible
-  // GPU (up to 256 SMs)
-  size_t best = 0;
-  for (int sms : {132, 148, 152, 160, 170, 188, 256})
-    best = std::max(best, plan_units(p, MODE_DOWN, sms).part_bytes);
+  // the split (of the down product alone) depends on the SM count
+  const size_t best = max_over_sm_counts([&](int sms) { return plan_units(p, MODE_DOWN, sms).part_bytes; });
   return STATS_BYTES + align_up(best, 256);
 }
 

@@ -1589,14 +1589,8 @@ int gemm_tile_rows(const moe_problem& p, int mode) {
 size_t gemm_workspace_bytes(const moe_problem& p) {
   if (p.wt == MOE_F32) return 0;
   if (p.wt == MOE_MXFP4) return gemm_mx_workspace_bytes(p);
-  // Split-K state depends on the SM count; size it for the largest plausible GPU (up to 256 SMs).
-  size_t best = 0;
-  for (int mode = 0; mode < 2; ++mode) {
-    for (int sms : {132, 148, 152, 160, 170, 188, 256}) {
-      const Plan pl = make_plan(p, mode, sms, 232448);
-      best = std::max(best, pl.part_bytes);
-    }
-  }
+  // the split (of the down GEMM alone) depends on the SM count
+  const size_t best = max_over_sm_counts([&](int sms) { return make_plan(p, MODE_DOWN, sms, 232448).part_bytes; });
   // issue counters first, then the split-K partial sums, then (two-phase launch) one counter per slot
   return STATS_BYTES + align_up(best, 256) + align_up(sizeof(int) * (size_t)(p.P + p.has_shared), 256);
 }
