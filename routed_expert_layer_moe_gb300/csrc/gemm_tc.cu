@@ -1231,7 +1231,9 @@ Plan make_plan(const moe_problem& p, int mode, int sm_count, int smem_cap, int n
   }
   const long tiles = chunks * pl.pairs;
   pl.ksplit = 1;
-  if (mode == MODE_DOWN && !pl.pair && tiles > 0 && tiles < 3L * sm_count) {
+  // The one-launch FFN splits where the separate down GEMM does and nowhere else (not where that one runs on SM
+  // pairs): the workspace is sized for one split, and yg has the same bits from both.
+  if (mode == MODE_DOWN && !use_pairs(p, mode, 1) && tiles > 0 && tiles < 3L * sm_count) {
     // split K so the unit count fills whole waves; keep >= 4 K blocks per split
     double best = 0.0;
     for (int ks = 1; ks <= 16 && pl.kb_total / ks >= 4; ++ks) {

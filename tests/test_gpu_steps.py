@@ -686,3 +686,26 @@ def test_bounded_wait_expires_with_a_flag():
     assert float(x.sum().item()) == 28.0
     with pytest.raises(moe.MoeError):
         moe.moe_selftest_bounded_wait(0, err)
+
+
+@pytest.mark.parametrize("base", ["e4m3_contig_pair", "e2m1_contig_pair"])
+def test_grouped_ffn_of_prefill_slots_with_few_units(base):
+    """Slots of 128 rows whose down GEMM has too few units for the SMs: nothing past the workspace is written, and yg has the
+    separate calls' bits."""
+    wl = Workload(SMALL[base].replace(T=640, E=5, K=1, H=512, I=1024))
+    cfg = wl.cfg
+    lay, xg, xgs, *_ = gemm_inputs(wl)
+    L = wl.layer()
+    n = L.ws.numel()
+    room = torch.full((n + (16 << 20),), 0x5A, dtype=torch.uint8, device="cuda")
+    L.ws = room[:n]
+    L.xg.copy_(to_dev(xg)), L.xg_s.copy_(to_dev(xgs))
+    L.masked_m.copy_(to_dev(lay["masked_m"])), L.offsets.copy_(to_dev(lay["offsets"]))
+    L.swiglu(), L.down()
+    want = L.yg.clone()
+    L.yg.fill_(-3.0)
+    L.ffn()
+    torch.cuda.synchronize()
+    assert int(to_host(L.err)[0]) == 0
+    assert torch.equal(L.yg, want)
+    assert (room[n:] == 0x5A).all()

@@ -15,23 +15,45 @@ FAKE = r"""
 #include <stdio.h>
 #include <stdlib.h>
 #include <stddef.h>
+#include <string.h>
 typedef struct { unsigned x, y, z; } dim3_;
+typedef struct { dim3_ grid, block; size_t smem; } config_;  /* how cudaLaunchConfig_t begins */
 int cudaGetDevice(int* d) { *d = 0; return 0; }
 int cudaDeviceGetAttribute(int* v, int attr, int dev) {
   *v = attr == 16 ? atoi(getenv("FAKE_SMS")) : attr == 97 ? 232448 : 0;  /* SMs, shared memory a block may ask for */
   return 0;
 }
+int cudaOccupancyMaxActiveClusters(int* n, const void* f, const void* config) {
+  *n = atoi(getenv("FAKE_SMS")) / 2;
+  return 0;
+}
+int cudaFuncGetAttributes(char* a, const void* f) {  /* three sizes, the most threads, the registers */
+  int regs = 255;
+  memset(a, 0, 32);
+  memcpy(a + 28, &regs, 4);
+  return 0;
+}
 int cudaFuncSetAttribute(const void* f, int attr, int v) {
-  printf("limit %p %d %d\n", f, attr, v);
+  printf("limit %p %d\n", f, v);
   fflush(stdout);
   return 0;
 }
-int cudaLaunchKernel(const void* f, dim3_ grid, dim3_ block, void** args, size_t smem, void* stream) {
+static int launch(const void* f, size_t smem) {
   printf("launch %p %zu\n", f, smem);
   fflush(stdout);
   return 0;
 }
+int __cudaGetKernel(void** k, const void* f) { *k = (void*)f; return 0; }
+int __cudaLaunchKernel(void* k, dim3_ grid, dim3_ block, void** args, size_t smem, void* stream) { return launch(k, smem); }
+int cudaLaunchKernelExC(const config_* c, const void* f, void** args) { return launch(f, c->smem); }
+int cudaMemsetAsync(void* p, int v, size_t n, void* stream) { return 0; }
 int cudaGetLastError(void) { return 0; }
+static int encode(void) { return 0; }
+int cudaGetDriverEntryPointByVersion(const char* name, void** f, unsigned version, unsigned long long flags, int* result) {
+  *f = (void*)encode;
+  *result = 0;
+  return 0;
+}
 """
 
 
@@ -51,7 +73,7 @@ def run(tmp_path_factory):
     def call(sms, code):
         env = dict(os.environ, LD_PRELOAD=str(so), FAKE_SMS=str(sms), PYTHONPATH=ROOT)
         head = "import ctypes, routed_expert_layer_moe_gb300 as moe\nlib = moe.lib()\n"
-        r = subprocess.run([sys.executable, "-c", head + textwrap.dedent(code)], env=env, capture_output=True, text=True,
+        r = subprocess.run([sys.executable, "-u", "-c", head + textwrap.dedent(code)], env=env, capture_output=True, text=True,
                            timeout=300)
         assert r.returncode == 0, r.stderr
         return r.stdout.splitlines()
@@ -75,3 +97,23 @@ def test_workspace_holds_the_split_of_any_device(run, wt, sms, splits, T, K, E, 
     out = run(sms, "print('bytes', moe.moe_workspace_bytes(moe.Problem.make(T=%d, K=%d, E=%d, H=%d, I=%d, "
                    "layout='contig', wt='%s')))" % (T, K, E, H, I, wt))
     assert int(out[-1].split()[1]) >= STATS + splits * T * K * H * 4
+
+
+@pytest.mark.parametrize("wt,T,E,H,I,M_max", [
+    ("e4m3", 640, 5, 1536, 6016, 0), ("e2m1", 768, 6, 1280, 6016, 0), ("e4m3", 640, 5, 1792, 1408, 640),
+    ("e4m3", 64, 4, 1792, 1408, 64)])
+def test_one_launch_ffn_splits_as_the_separate_down_product(run, wt, T, E, H, I, M_max):
+    """128 rows a slot and H a multiple of 256: the separate down GEMM runs on SM pairs, not split, and the workspace has no
+    room for a split.  moe_grouped_ffn runs it on single CTAs and must not split it either (5 slots + 640 / 64 = 15 chunks
+    x 6 tile pairs are 90 units for 152 SMs).  With few rows a slot both are split: one more launch, the reduction."""
+    out = run(152, """
+        p = moe.Problem.make(T=%d, K=1, E=%d, H=%d, I=%d, M_max=%d, layout='%s', wt='%s')
+        A, n, q = 4096, moe.moe_workspace_bytes(p), ctypes.byref(p)  # an address that is never followed
+        print("down", lib.moe_grouped_down_gemm(q, A, A, A, A, A, A, A, A, A, n, None))
+        print("ffn", lib.moe_grouped_ffn(q, A, A, A, A, A, A, A, A, A, A, A, A, A, n, None))
+        """ % (T, E, H, I, M_max, "masked" if M_max else "contig", wt))
+    kinds = [line.split()[0] for line in out if not line.startswith("limit")]
+    launches = kinds.index("down")
+    assert "down 0" in out and out[-1] == "ffn 0"
+    assert launches == (1 if T * 1 / E >= 128 else 2)
+    assert kinds[launches + 1:] == ["launch"] * launches + ["ffn"]
