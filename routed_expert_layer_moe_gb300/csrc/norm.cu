@@ -22,6 +22,7 @@
 // are not 16-byte aligned are read when wanted: 2018 x 6290 bf16 takes 75 us forward and 200
 // backward, 15 and 23 at the memory's rate.
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "common.cuh"
@@ -503,6 +504,8 @@ __global__ void __launch_bounds__(32 * kReduceGroups)
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+constexpr int kReserved = 1024;  // shared memory that a CTA's static arrays and the system take
+
 // How rows of H columns are shared out: vectors and threads, CTAs an SM holds, rows fetched ahead.
 struct Shape {
   int v, threads, ctas, depth;
@@ -525,10 +528,10 @@ Shape shape_of(int H, int esz, bool vec, int arrays, int weights, int ctas1, int
   if (!vec || rows <= di.sm_count * s.ctas) return s;  // a row for each CTA: nothing to fetch ahead
   const size_t cols = (size_t)s.v * s.threads * 8;
   const size_t row = cols * esz * arrays, keep = cols * 4 * weights;
-  const size_t room = (size_t)di.max_smem_optin - 1024;  // what a CTA's static memory and the system take
+  const size_t room = (size_t)di.max_smem_optin - kReserved;
   for (int c = s.ctas; c >= 1; --c)
     for (int depth = 3; depth >= 2; --depth)
-      if (row * depth + keep <= room / c - 1024) {
+      if (row * depth + keep <= room / c - kReserved) {
         s.ctas = c, s.depth = depth, s.smem = row * depth + keep;
         return s;
       }
@@ -552,11 +555,26 @@ int dispatch(const Shape& s, bool vec, F f) {
   return go(integral_constant<int, 4>(), integral_constant<int, 512>());
 }
 
-template <typename K, typename T>
-int launch(K kern, int grid, const Shape& s, const Args<T>& a, cudaStream_t st) {
-  if (s.smem > 40 * 1024 &&  // 48 KB, the static memory counted in, is what a kernel has without asking
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s.smem) != cudaSuccess)
-    return MOE_ERR_CUDA;
+// A kernel's limit on dynamic shared memory is raised once per device, to all that a call may ask for: a call that set it
+// to its own need could do so between another host thread's setting and launch.
+template <auto kern>
+bool raise_limit() {
+  static std::atomic<bool> raised[64];
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const bool keep = dev >= 0 && dev < 64;
+  if (keep && raised[dev].load(std::memory_order_acquire)) return true;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, device_info().max_smem_optin - kReserved) !=
+      cudaSuccess)
+    return false;
+  if (keep) raised[dev].store(true, std::memory_order_release);
+  return true;
+}
+
+template <auto kern, typename T>
+int launch(int grid, const Shape& s, const Args<T>& a, cudaStream_t st) {
+  // 48 KB, the static memory counted in, is what a kernel has without asking
+  if (s.smem > 40 * 1024 && !raise_limit<kern>()) return MOE_ERR_CUDA;
   kern<<<grid, s.threads, s.smem, st>>>(a);
   return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
@@ -573,8 +591,8 @@ int forward(Args<T> a, cudaStream_t st) {
   return dispatch(s, vec, [&](auto v, auto w, auto d, auto t) {
     constexpr int V = decltype(v)::value, MAXT = decltype(t)::value;
     constexpr int MINB = V == 1 ? kForward1 : MAXT <= 256 ? kForward2 * 256 / MAXT : 1;
-    return launch(block_norm_kernel<T, V, decltype(w)::value, decltype(d)::value, MAXT, MINB, MAXT <= 256 ? MAXT : 0>,
-                  grid, s, a, st);
+    return launch<block_norm_kernel<T, V, decltype(w)::value, decltype(d)::value, MAXT, MINB, MAXT <= 256 ? MAXT : 0>>(
+        grid, s, a, st);
   });
 }
 
@@ -588,8 +606,8 @@ int backward(Args<T> a, float* dw_post, float* dw_pre, cudaStream_t st) {
   const int r = dispatch(s, vec, [&](auto v, auto w, auto d, auto t) {
     constexpr int V = decltype(v)::value, MAXT = decltype(t)::value;
     constexpr int MINB = V == 1 ? kBackward1 : MAXT <= 256 ? kBackward2 * 256 / MAXT : 1;
-    return launch(
-        block_norm_backward_kernel<T, V, decltype(w)::value, decltype(d)::value, MAXT, MINB, MAXT <= 256 ? MAXT : 0>,
+    return launch<
+        block_norm_backward_kernel<T, V, decltype(w)::value, decltype(d)::value, MAXT, MINB, MAXT <= 256 ? MAXT : 0>>(
         parts, s, a, st);
   });
   if (r) return r;

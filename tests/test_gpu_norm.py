@@ -208,3 +208,36 @@ def test_more_rows_than_ctas(T, H, dtype):
         args, dy, dxn = inputs(T, H, dtype, gate, block, seed=T)
         check_forward(args, forward(args))
         check_backward(args, dy, dxn, backward(args, dy, dxn))
+
+
+def test_two_host_threads_of_different_row_lengths():
+    """Rows of two lengths that one kernel serves with different amounts of shared memory, called from two threads."""
+    import threading
+    T, calls = 160, 4000  # more rows than SMs: they are fetched ahead into shared memory
+    jobs = []
+    for H in (8192, 4352):
+        g = torch.Generator(device="cuda").manual_seed(H)
+        x = torch.randn(T, H, generator=g, device="cuda")
+        w = torch.randn(H, generator=g, device="cuda")
+        y, xn = torch.empty_like(x), torch.empty_like(x)
+        moe.moe_block_norm(x, x, None, w, w, 1.0, 1e-6, y, xn)
+        jobs.append((x, w, y, xn, y.clone(), xn.clone(), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(x, w, y, xn, want_y, want_xn, stream):
+        try:
+            for _ in range(calls):
+                moe.moe_block_norm(x, x, None, w, w, 1.0, 1e-6, y, xn, stream)
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=j) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed, failed
+    for x, w, y, xn, want_y, want_xn, _ in jobs:
+        assert torch.equal(y, want_y) and torch.equal(xn, want_xn)

@@ -117,3 +117,32 @@ def test_one_launch_ffn_splits_as_the_separate_down_product(run, wt, T, E, H, I,
     assert "down 0" in out and out[-1] == "ffn 0"
     assert launches == (1 if T * 1 / E >= 128 else 2)
     assert kinds[launches + 1:] == ["launch"] * launches + ["ffn"]
+
+
+@pytest.mark.parametrize("backward", [False, True])
+def test_norm_calls_never_lower_a_kernels_shared_memory_limit(run, backward):
+    """One kernel serves many row lengths, and its limit is the process's: a call that lowered it to its own need would
+    make a launch of another host thread fail that has set its own just before."""
+    out = run(152, """
+        A, F = 4096, ctypes.c_float
+        for rep in range(2):
+            for dtype, H in ((0, 8192), (0, 4352), (1, 8192), (1, 5632), (1, 4352), (0, 2048), (0, 1200), (0, 16384), (0, 9000)):
+                a = (dtype, 5000, H, A, A, 0, None, A, A, F(1.0), F(1e-6))
+                if %d:
+                    n = moe.moe_block_norm_workspace_bytes(5000, H)
+                    print("call", lib.moe_block_norm_backward(*a, A, A, A, A, None, A, A, A, n, None))
+                else:
+                    print("call", lib.moe_block_norm(*a, A, A, None))
+        """ % backward)
+    limit, launched = {}, set()
+    for line in out:
+        kind, *v = line.split()
+        if kind == "limit":
+            assert int(v[1]) >= limit.get(v[0], 0)
+            limit[v[0]] = int(v[1])
+        elif kind == "launch":
+            assert int(v[1]) <= max(limit.get(v[0], 0), 48 * 1024)
+            launched.add(int(v[1]))
+        else:
+            assert v == ["0"]
+    assert len(launched) > 4  # calls of different needs
