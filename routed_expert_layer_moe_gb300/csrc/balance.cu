@@ -191,10 +191,12 @@ __device__ __forceinline__ float scores(const Row<N>& l, Row<N>& a) {
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) m = fmaxf(m, fmaxf(l.v[i].x, l.v[i].y));
     m = group_max<L>(m);
-    const float b = m == -INFINITY ? 0.0f : -m * kLog2e;
+    // the difference first: l log2 e - m log2 e as one multiply-add has the rounding of m log2 e in every term, which
+    // is a power of two too many from |m| = 2^24 on and infinite for a row of the type's lowest value
+    const float b = m == -INFINITY ? 0.0f : -m;
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) {
-      const float2 t = __ffma2_rn(l.v[i], make_float2(kLog2e, kLog2e), make_float2(b, b));
+      const float2 t = __fmul2_rn(__fadd2_rn(l.v[i], make_float2(b, b)), make_float2(kLog2e, kLog2e));
       a.v[i] = make_float2(fast_exp2(t.x), fast_exp2(t.y));
       z = __fadd2_rn(z, a.v[i]);
     }

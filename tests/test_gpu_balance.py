@@ -200,3 +200,23 @@ def test_empty_segments_behind_tokens_of_no_segment(T, seq, score):
         got = run(*args)
         assert got["err"] == 0
         check(got, ref.balance(*args), *args)
+
+
+@pytest.mark.parametrize("E", [6, 64, 257, 512, 1000])
+def test_softmax_rows_of_large_logits(E):
+    """Logits of any finite size, the type's lowest value in a whole row among them: a row of equal ones is uniform."""
+    big = torch.finfo(torch.float32).max
+    tops = [big, 1e30, 1e10, 2.0 ** 25, 1e5, -1e5, -(2.0 ** 25), -1e10, -1e30, -big]
+    T, K = 3 * len(tops), min(E, 4)
+    g = torch.Generator().manual_seed(E)
+    logits = torch.empty(T, E)
+    for i, top in enumerate(tops):
+        logits[3 * i] = top
+        logits[3 * i + 1] = max(top, -big) - torch.rand(E, generator=g) * 20.0
+        logits[3 * i + 2] = -big                   # masked with the lowest value, a few experts left
+        logits[3 * i + 2, :3] = top
+    ids = torch.stack([torch.randperm(E, generator=g)[:K] for _ in range(T)]).int()
+    args = (logits, ids, None, [0, 17, T], "softmax", 0.01, torch.tensor([1.0, -2.0]))
+    got = run(*args)
+    assert got["err"] == 0
+    check(got, ref.balance(*args), *args)
