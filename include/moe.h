@@ -410,7 +410,8 @@ moe_status moe_mx_dequantize(int32_t dtype, int64_t rows, int64_t cols, const ui
  *   counts[b][e] = ids equal to e among them,  prob_sum[b][e] = sum_t p_te
  *   tokens[b] = n,  loss[b] = coef * E / (K n^2) * sum_e counts * prob_sum
  * A logit of -inf gives p = 0; a token whose logits are all -inf gives a row of
- * zeros.  An empty segment has zeros everywhere.  Sums are fp32 in a fixed order: the
+ * zeros.  Finite logits may have any size; a score that is below 2^-46 of its
+ * row's sum may count as 0.  An empty segment has zeros everywhere.  Sums are fp32 in a fixed order: the
  * same inputs give the same bits.
  * ------------------------------------------------------------------------- */
 typedef enum moe_score { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;

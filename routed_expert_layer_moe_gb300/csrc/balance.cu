@@ -160,8 +160,8 @@ __device__ __forceinline__ void load_row(const float* row, int E, int sub, Row<N
   }
 }
 
-// 2^x and 1/x with the special-function unit's own error (2 ulp and 1 ulp; results under 2^-126 are 0, which
-// no sum of scores notices).
+// 2^x and 1/x with the special-function unit's own error (2 ulp and 1 ulp; results under 2^-126 are 0).  The
+// scores' error is within 8e-8 of 64 bits so, against 1e-8 with expf and an IEEE division: fp32's own rounding.
 __device__ __forceinline__ float fast_exp2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -174,34 +174,58 @@ __device__ __forceinline__ float fast_rcp(float x) {
   return r;
 }
 
-// Unnormalised scores a of the logits l; returns this lane's part of their sum.
-template <int N, int L, bool SIG>
-__device__ __forceinline__ float scores(const Row<N>& l, Row<N>& a) {
+// e^(l - the row's largest logit) in the lanes that `take` it (every lane of the warp takes part); returns this
+// lane's part of their sum.
+template <int N, int L>
+__device__ __forceinline__ float exponentials(const Row<N>& l, bool take, Row<N>& a) {
+  float m = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) m = fmaxf(m, fmaxf(l.v[i].x, l.v[i].y));
+  m = group_max<L>(m);
+  // the difference first: l log2 e - m log2 e as one multiply-add has the rounding of m log2 e in every term, which
+  // is a power of two too many from |m| = 2^24 on and infinite for a row of the type's lowest value
+  const float b = m == -INFINITY ? 0.0f : -m;
   float2 z = make_float2(0.0f, 0.0f);
-  if constexpr (SIG) {
 #pragma unroll
-    for (int i = 0; i < N / 2; ++i) {
-      float2 t = __fmul2_rn(l.v[i], make_float2(-kLog2e, -kLog2e));
-      t = __fadd2_rn(make_float2(fast_exp2(t.x), fast_exp2(t.y)), make_float2(1.0f, 1.0f));
-      a.v[i] = make_float2(fast_rcp(t.x), fast_rcp(t.y));
-      z = __fadd2_rn(z, a.v[i]);
-    }
-  } else {
-    float m = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < N / 2; ++i) m = fmaxf(m, fmaxf(l.v[i].x, l.v[i].y));
-    m = group_max<L>(m);
-    // the difference first: l log2 e - m log2 e as one multiply-add has the rounding of m log2 e in every term, which
-    // is a power of two too many from |m| = 2^24 on and infinite for a row of the type's lowest value
-    const float b = m == -INFINITY ? 0.0f : -m;
-#pragma unroll
-    for (int i = 0; i < N / 2; ++i) {
-      const float2 t = __fmul2_rn(__fadd2_rn(l.v[i], make_float2(b, b)), make_float2(kLog2e, kLog2e));
-      a.v[i] = make_float2(fast_exp2(t.x), fast_exp2(t.y));
-      z = __fadd2_rn(z, a.v[i]);
-    }
+  for (int i = 0; i < N / 2; ++i) {
+    const float2 t = __fmul2_rn(__fadd2_rn(l.v[i], make_float2(b, b)), make_float2(kLog2e, kLog2e));
+    const float2 e = make_float2(fast_exp2(t.x), fast_exp2(t.y));
+    a.v[i] = take ? e : a.v[i];
+    z = __fadd2_rn(z, e);
   }
   return z.x + z.y;
+}
+
+// Unnormalised scores a of the logits l of a token that takes part (live); returns this lane's part of their
+// sum.  Sigmoid scores whose sum in every lane is below kLowSum are tiny or 0, but their ratios are not: the largest logit
+// is below -51 there, sigmoid(l) = e^l to 2^-75 of it, and the scores are taken relative to the largest one
+// instead (ratio).  In any other row some lane has kLowSum or more, next to which the at most 1024 scores below 2^-126
+// that were taken as 0 are 2^-36.
+constexpr float kLowSum = 0x1p-80f;
+
+template <int N, int L, bool SIG>
+__device__ __forceinline__ float scores(const Row<N>& l, bool live, Row<N>& a, bool& ratio) {
+  ratio = false;
+  if constexpr (!SIG) return exponentials<N, L>(l, true, a);
+  float2 z2 = make_float2(0.0f, 0.0f);
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    float2 t = __fmul2_rn(l.v[i], make_float2(-kLog2e, -kLog2e));
+    t = __fadd2_rn(make_float2(fast_exp2(t.x), fast_exp2(t.y)), make_float2(1.0f, 1.0f));
+    a.v[i] = make_float2(fast_rcp(t.x), fast_rcp(t.y));
+    z2 = __fadd2_rn(z2, a.v[i]);
+  }
+  const float z = z2.x + z2.y;
+  const unsigned low = __ballot_sync(0xffffffffu, live && z < kLowSum);
+  if (low) {  // lanes of experts that are off, and rarely a whole row
+    const unsigned group = (0xffffffffu >> (32 - L)) << (threadIdx.x & 31 & ~(L - 1));
+    ratio = (low & group) == group;
+    if (__any_sync(0xffffffffu, ratio)) {
+      const float y = exponentials<N, L>(l, ratio, a);
+      return ratio ? y : z;
+    }
+  }
+  return z;
 }
 
 // 1 / the sum over the group; 0 for a row with nothing in it.
@@ -273,7 +297,8 @@ __global__ void __launch_bounds__(kThreads, N > 16 ? 2 : kTilesPerSm)
       const bool live = next_valid && w + grp < end;
       if (!__all_sync(0xffffffffu, live) && !live) next.fill(-INFINITY);
       Row<N> a;
-      float z = scores<N, L, SIG>(next, a);
+      bool ratio;
+      const float z = scores<N, L, SIG>(next, live, a, ratio);
       mine += live && sub == 0;
       int id[Q];
 #pragma unroll
@@ -458,7 +483,8 @@ __global__ void __launch_bounds__(kThreads, N > 16 ? 2 : kTilesPerSm)
     bool live = next_live;
     if (!__all_sync(0xffffffffu, live) && !live) next.fill(-INFINITY);
     Row<N> a;
-    const float z = scores<N, L, SIG>(next, a);
+    bool ratio;
+    const float z = scores<N, L, SIG>(next, live, a, ratio);
     if (w + kWarps * G < t1) request(t + kWarps * G);
     const bool move = live && (t < lo || t >= hi);
     unsigned moving = __ballot_sync(0xffffffffu, move);
@@ -505,10 +531,11 @@ __global__ void __launch_bounds__(kThreads, N > 16 ? 2 : kTilesPerSm)
     }
     const float dot = group_sum<L>(d2.x + d2.y);
     if (t >= t1) continue;
+    const float minus = ratio ? 0.0f : -1.0f;  // 1 - sigmoid(l) is 1 where the scores are ratios
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) {
       g.v[i] = __fmul2_rn(g.v[i], __fadd2_rn(v.v[i], make_float2(-dot, -dot)));
-      if (SIG) g.v[i] = __fmul2_rn(g.v[i], __ffma2_rn(a.v[i], make_float2(-1.0f, -1.0f), make_float2(1.0f, 1.0f)));
+      if (SIG) g.v[i] = __fmul2_rn(g.v[i], __ffma2_rn(a.v[i], make_float2(minus, minus), make_float2(1.0f, 1.0f)));
     }
     if (!live) g.fill(0.0f);
     float* dst = dlogits + (size_t)t * E;

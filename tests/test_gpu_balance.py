@@ -220,3 +220,46 @@ def test_softmax_rows_of_large_logits(E):
     got = run(*args)
     assert got["err"] == 0
     check(got, ref.balance(*args), *args)
+
+
+@pytest.mark.parametrize("E", [5, 48, 256, 300, 700])
+def test_sigmoid_rows_of_low_logits(E):
+    """Rows whose largest logit is far below zero, where sigmoid(l) itself is below the smallest normal number: the scores
+    still sum to one.  Bound: 2^-16.  Where the sigmoid is taken directly its exponential's argument is at most 126,
+    rounded to 2^-18 and with log2 e's own rounding 2^-20 off; times ln 2, with the exponential, the reciprocal, the
+    sum and the division, under 2^-17.  Ratios of exponentials of differences up to 30 are better than that."""
+    tops = [-20.0, -52.0, -55.0, -55.4, -56.0, -60.0, -80.0, -87.0, -88.0, -100.0, -104.0, -150.0, -1e4, -1e30]
+    T, K = len(tops) * 3, min(E, 4)
+    g = torch.Generator().manual_seed(E)
+    logits = torch.empty(T, E)
+    for i, top in enumerate(tops):
+        spread = torch.rand(E, generator=g) * 30.0
+        logits[3 * i] = top                       # all alike
+        logits[3 * i + 1] = top - spread          # the largest and others below it
+        logits[3 * i + 1, i % E] = top
+        logits[3 * i + 2] = top - spread
+        logits[3 * i + 2, ::2] = -float("inf")    # and experts that are off
+        logits[3 * i + 2, -1 if E % 2 == 0 else 1] = top
+    ids = torch.stack([torch.randperm(E, generator=g)[:K] for _ in range(T)]).int()
+    perm = torch.randperm(T, generator=g)         # neighbours of every kind in a warp
+    logits, ids = logits[perm], ids[perm]
+    dloss = torch.tensor([1.0, -2.0])
+    seq = [0, T // 2, T]
+    # the reference's sigmoid in 64 bits underflows below -745: there its ratios are those of the differences
+    exact_logits, top = logits.double(), logits.double().amax(1, keepdim=True)
+    exact_logits = torch.where(top < -700, exact_logits - top - 100.0, exact_logits)
+    for valid in (None, (torch.rand(T, generator=g) < 0.7).to(torch.uint8)):
+        got = run(logits, ids, valid, seq, "sigmoid", 0.01, dloss)
+        want = ref.balance(exact_logits, ids, valid, seq, "sigmoid", 0.01, dloss)
+        assert got["err"] == 0 and torch.equal(got["counts"].long(), want["counts"])
+        for k in ("prob_sum", "loss"):
+            assert ((got[k].double() - want[k]).abs() <= 2.0 ** -16 * want[k].abs() + 1e-37).all(), k
+        p = torch.sigmoid(exact_logits)
+        p = p / p.sum(1, keepdim=True)
+        for b in range(2):
+            rows, n = slice(seq[b], seq[b + 1]), max(int(want["tokens"][b]), 1)
+            v = want["counts"][b].double()
+            v = (v - v.mean()).abs().max() * 0.01 * E / (K * n * n) * abs(float(dloss[b]))
+            # p and the difference v - sum v p each carry the scores' error, the difference of both signs
+            d = (got["dlogits"][rows].double() - want["dlogits"][rows]).abs()
+            assert (d <= 2.0 ** -14 * p[rows] * v + 1e-37).all()
