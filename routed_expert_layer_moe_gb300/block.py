@@ -32,8 +32,10 @@ class MoeBlock:
         self.loss, self.tokens = torch.empty(nseq, **f32), torch.empty(nseq, **i32)
         self.counts, self.prob_sum = torch.empty((nseq, p.E), **i32), torch.empty((nseq, p.E), **f32)
         self.dlogits = torch.empty((p.T, p.E), **f32)
-        nbytes = max(L.moe_balance_workspace_bytes(p, nseq), L.moe_block_norm_workspace_bytes(p.T, p.H))
-        self.ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+        scratch = lambda n: torch.empty(n, dtype=torch.uint8, device=x.device)  # noqa: E731
+        # one for each call that may run beside the others on a stream of its own
+        self.ws_balance = scratch(L.moe_balance_workspace_bytes(p, nseq))
+        self.ws_leave, self.ws_enter = (scratch(L.moe_block_norm_workspace_bytes(p.T, p.H)) for _ in range(2))
 
     # -- forward ----------------------------------------------------------------
     def enter(self, x, stream=None):
@@ -52,7 +54,7 @@ class MoeBlock:
     def balance(self, logits, valid=None, seq_offsets=None, stream=None):
         """Balance loss per segment of the routing that leave() made; counts and score sums in counts, prob_sum."""
         L.moe_balance_loss(self.p, logits, self.layer.ids, valid, seq_offsets, self.score, self.coef, self.loss,
-                           self.counts, self.prob_sum, self.tokens, self.layer.err, self.ws, stream)
+                           self.counts, self.prob_sum, self.tokens, self.layer.err, self.ws_balance, stream)
         return self.loss
 
     def balance_backward(self, logits, dloss, valid=None, seq_offsets=None, stream=None):
@@ -71,7 +73,7 @@ class MoeBlock:
         dw_post = torch.empty(self.w_post.shape, **f32)
         dw_next = None if self.w_next is None else torch.empty(self.w_next.shape, **f32)
         L.moe_block_norm_backward(x, self.layer.out, self.gate, self.w_post, self.w_next, self.res_scale, self.eps, dy,
-                                  dxn_next, dx, dout, dgate, dw_post, dw_next, self.ws, stream)
+                                  dxn_next, dx, dout, dgate, dw_post, dw_next, self.ws_leave, stream)
         return dx, dout, dgate, dw_post, dw_next
 
     def enter_backward(self, x, dxn, dy=None, stream=None):
@@ -79,5 +81,5 @@ class MoeBlock:
         dx = torch.empty_like(x)
         dw_pre = torch.empty(self.w_pre.shape, dtype=torch.float32, device=x.device)
         L.moe_block_norm_backward(x, None, None, None, self.w_pre, self.res_scale, self.eps, dy, dxn, dx, None, None,
-                                  None, dw_pre, self.ws, stream)
+                                  None, dw_pre, self.ws_enter, stream)
         return dx, dw_pre

@@ -77,3 +77,65 @@ def test_block_in_a_graph(example):
     y, xn, logits = example.step(block, w_g, x)
     want = [y, xn, block.balance(logits), block.balance_backward(logits, torch.ones(1, device="cuda"))]
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def wide_block(T=4096, H=1024, E=64, score="softmax", nseq=1, gate="token"):
+    """A block of many tokens and a thin layer, so that its norms and its loss take long enough to overlap."""
+    g = torch.Generator(device="cuda").manual_seed(T + E)
+    r = lambda *s, std=1.0, mean=0.0: torch.randn(*s, generator=g, device="cuda") * std + mean  # noqa: E731
+    q = []
+    for s in ((E, 256, H), (E, H, 128)):
+        w = r(*s, std=0.05)
+        q.append((torch.empty(*s[:2], s[2] // 2, dtype=torch.uint8, device="cuda"),
+                  torch.empty(*s[:2], s[2] // 32, dtype=torch.uint8, device="cuda")))
+        moe.moe_mx_quantize(w, *q[-1])
+    p = moe.Problem.make(T=T, H=H, I=128, E=E, K=4, wt="mxfp4", layout="contig")
+    layer = moe.MoeLayer(p, "bf16", "mxfp4", "bf16", q[0][0], q[1][0], q[0][1], q[1][1])
+    norm = lambda: r(H, std=0.1, mean=1.0).bfloat16()  # noqa: E731
+    gt = {"token": torch.sigmoid(r(T, 1)).bfloat16(), "channel": r(H, std=0.1, mean=0.3).bfloat16(), None: None}[gate]
+    return moe.MoeBlock(layer, norm(), norm(), gt, norm(), score=score, nseq=nseq), r
+
+
+def test_loss_and_norm_gradients_on_their_own_streams(example):
+    """balance(), leave_backward() and enter_backward() on three streams at once give what they give in turn."""
+    block, r = wide_block()
+    T, H, E = block.p.T, block.p.H, block.p.E
+    x, logits = r(T, H).bfloat16(), r(T, E)
+    dy, dxn = r(T, H).bfloat16(), r(T, H).bfloat16()
+    block.enter(x)
+    block.leave(x, logits)
+
+    def calls(a=None, b=None, c=None):
+        return [block.balance(logits, stream=a), *block.leave_backward(x, dy, dxn, stream=b),
+                *block.enter_backward(x, dxn, dy, stream=c)]
+
+    want = [t.clone() for t in calls()]
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for _ in range(20):
+        torch.cuda.synchronize()
+        got = calls(*streams)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_calls_of_a_block_share_no_scratch(example, monkeypatch):
+    """balance(), leave_backward() and enter_backward() may run at once on streams of their own."""
+    block, r = wide_block(T=40, H=256)
+    x, logits, d = r(40, 256).bfloat16(), r(40, 64), r(40, 256).bfloat16()
+    block.enter(x)
+    block.leave(x, logits)
+    spans = []
+    from routed_expert_layer_moe_gb300 import _lib
+
+    def recorded(f, at):
+        def call(*a):
+            spans.append((a[at].data_ptr(), a[at].data_ptr() + a[at].numel()))
+            return f(*a)
+        return call
+
+    monkeypatch.setattr(_lib, "moe_balance_loss", recorded(_lib.moe_balance_loss, 12))
+    monkeypatch.setattr(_lib, "moe_block_norm_backward", recorded(_lib.moe_block_norm_backward, 14))
+    block.balance(logits), block.leave_backward(x, d, d), block.enter_backward(x, d)
+    assert len(spans) == 3
+    spans.sort()
+    assert all(a[1] <= b[0] for a, b in zip(spans, spans[1:]))
