@@ -5,6 +5,7 @@ a cudaStream_t.  Every step runs in the library's CUDA kernels; there is no
 other implementation to fall back to, so a missing library is an error."""
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -157,6 +158,18 @@ def _stream(stream):
             return _raw_stream(_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _allocate_on(stream):
+    """Context in which torch allocates on the stream of a call: memory of a result that is dropped then goes back to
+    that stream, behind the kernel that writes it.  stream: as the calls take it (None: the current one)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)
+        # 0 and 1 are the default stream's handles
+        stream = torch.cuda.ExternalStream(handle) if handle > 1 else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
 
 
 def _check(status: int, where: str):

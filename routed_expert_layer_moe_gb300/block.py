@@ -6,8 +6,10 @@ after it with gate and residual, which also norms the input of the next block.
     logits = xn.float() @ W_g                 # the router's product is the caller's
     y, xn_next = block.leave(x, logits)       # x + res_scale * gate * rms(layer(xn)) * w_post, rms(y) * w_next
 
-Buffers are allocated once, every call only enqueues kernels on the stream, so a step is graph-capturable
-after a first eager one."""
+The buffers of the forward calls and of the loss are allocated once and every call only enqueues kernels on the
+stream, so a step is graph-capturable after a first eager one.  leave_backward() and enter_backward() return new
+tensors, allocated on the stream of the call: a caller that uses them on another stream orders the two streams, and
+calls record_stream on what it drops there, as with any tensor of another stream."""
 from __future__ import annotations
 
 import torch
@@ -67,19 +69,21 @@ class MoeBlock:
     def leave_backward(self, x, dy, dxn_next, stream=None):
         """Gradients of leave()'s norm: of x, of the layer's output, of gate, w_post and w_next (fp32).  dxn_next is
         None without w_next."""
-        dx, dout = torch.empty_like(x), torch.empty_like(x)
         f32 = dict(dtype=torch.float32, device=x.device)
-        dgate = None if self.gate is None else torch.empty(self.gate.shape, **f32)
-        dw_post = torch.empty(self.w_post.shape, **f32)
-        dw_next = None if self.w_next is None else torch.empty(self.w_next.shape, **f32)
+        with L._allocate_on(stream):
+            dx, dout = torch.empty_like(x), torch.empty_like(x)
+            dgate = None if self.gate is None else torch.empty(self.gate.shape, **f32)
+            dw_post = torch.empty(self.w_post.shape, **f32)
+            dw_next = None if self.w_next is None else torch.empty(self.w_next.shape, **f32)
         L.moe_block_norm_backward(x, self.layer.out, self.gate, self.w_post, self.w_next, self.res_scale, self.eps, dy,
                                   dxn_next, dx, dout, dgate, dw_post, dw_next, self.ws_leave, stream)
         return dx, dout, dgate, dw_post, dw_next
 
     def enter_backward(self, x, dxn, dy=None, stream=None):
         """Gradients of enter(): of x (plus dy, what else reaches x) and of w_pre (fp32)."""
-        dx = torch.empty_like(x)
-        dw_pre = torch.empty(self.w_pre.shape, dtype=torch.float32, device=x.device)
+        with L._allocate_on(stream):
+            dx = torch.empty_like(x)
+            dw_pre = torch.empty(self.w_pre.shape, dtype=torch.float32, device=x.device)
         L.moe_block_norm_backward(x, None, None, None, self.w_pre, self.res_scale, self.eps, dy, dxn, dx, None, None,
                                   None, dw_pre, self.ws_enter, stream)
         return dx, dw_pre

@@ -139,3 +139,22 @@ def test_calls_of_a_block_share_no_scratch(example, monkeypatch):
     assert len(spans) == 3
     spans.sort()
     assert all(a[1] <= b[0] for a, b in zip(spans, spans[1:]))
+
+
+def test_results_belong_to_the_stream_that_writes_them(example):
+    """Memory of a dropped result is not handed out on another stream while its kernel may still write it."""
+    block, r = wide_block(T=64, H=256)
+    x, logits, d = r(64, 256).bfloat16(), r(64, 64), r(64, 256).bfloat16()
+    block.enter(x)
+    block.leave(x, logits)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        for call in (lambda: block.leave_backward(x, d, d, stream=stream), lambda: block.enter_backward(x, d, stream=stream)):
+            grads = call()
+            sizes = [(g.shape, g.dtype) for g in grads]
+            at = {g.data_ptr() for g in grads}
+            del grads
+            again = [torch.empty(s, dtype=t, device="cuda") for s, t in sizes]
+            assert not at & {g.data_ptr() for g in again}
+            torch.cuda.synchronize()
