@@ -9,7 +9,13 @@ after it with gate and residual, which also norms the input of the next block.
 The buffers of the forward calls and of the loss are allocated once and every call only enqueues kernels on the
 stream, so a step is graph-capturable after a first eager one.  leave_backward() and enter_backward() return new
 tensors, allocated on the stream of the call: a caller that uses them on another stream orders the two streams, and
-calls record_stream on what it drops there, as with any tensor of another stream."""
+calls record_stream on what it drops there, as with any tensor of another stream.
+
+What one pass leaves for its gradients is overwritten by the next one: layer.out and layer.ids by any forward pass of
+the layer (of another block on it too), the results of a method of the block by its next call.  Where another
+pass comes between a forward and its gradients (micro-batches, two blocks on one layer), keep copies and hand
+them in: ids to balance(), counts and tokens to balance_backward(), out to leave_backward().  Calls that use each
+other's results are ordered by the caller if they run on different streams, and so are two calls of one method."""
 from __future__ import annotations
 
 import torch
@@ -53,30 +59,38 @@ class MoeBlock:
         return self.y, self.xn_next
 
     # -- the router's loss ------------------------------------------------------
-    def balance(self, logits, valid=None, seq_offsets=None, stream=None):
-        """Balance loss per segment of the routing that leave() made; counts and score sums in counts, prob_sum."""
-        L.moe_balance_loss(self.p, logits, self.layer.ids, valid, seq_offsets, self.score, self.coef, self.loss,
-                           self.counts, self.prob_sum, self.tokens, self.layer.err, self.ws_balance, stream)
+    def balance(self, logits, valid=None, seq_offsets=None, stream=None, ids=None):
+        """Balance loss per segment of the routing that leave() made; counts and score sums in counts, prob_sum.
+        ids: that routing, if it is not the layer's last one any more."""
+        L.moe_balance_loss(self.p, logits, self.layer.ids if ids is None else ids, valid, seq_offsets, self.score,
+                           self.coef, self.loss, self.counts, self.prob_sum, self.tokens, self.layer.err,
+                           self.ws_balance, stream)
         return self.loss
 
-    def balance_backward(self, logits, dloss, valid=None, seq_offsets=None, stream=None):
-        """Gradient of balance() with respect to the logits."""
-        L.moe_balance_loss_backward(self.p, logits, valid, seq_offsets, self.score, self.coef, self.counts,
-                                    self.tokens, dloss, self.dlogits, stream)
+    def balance_backward(self, logits, dloss, valid=None, seq_offsets=None, stream=None, counts=None, tokens=None):
+        """Gradient of balance() with respect to the logits.  counts, tokens: as that call left them, if another one
+        came since."""
+        if (counts is None) != (tokens is None):
+            raise ValueError("counts and tokens belong together")
+        if counts is None:
+            counts, tokens = self.counts, self.tokens
+        L.moe_balance_loss_backward(self.p, logits, valid, seq_offsets, self.score, self.coef, counts, tokens, dloss,
+                                    self.dlogits, stream)
         return self.dlogits
 
     # -- gradients of the norms -------------------------------------------------
-    def leave_backward(self, x, dy, dxn_next, stream=None):
+    def leave_backward(self, x, dy, dxn_next, stream=None, out=None):
         """Gradients of leave()'s norm: of x, of the layer's output, of gate, w_post and w_next (fp32).  dxn_next is
-        None without w_next."""
+        None without w_next.  out: the layer's output in that leave(), if it is not the layer's last one any more."""
         f32 = dict(dtype=torch.float32, device=x.device)
         with L._allocate_on(stream):
             dx, dout = torch.empty_like(x), torch.empty_like(x)
             dgate = None if self.gate is None else torch.empty(self.gate.shape, **f32)
             dw_post = torch.empty(self.w_post.shape, **f32)
             dw_next = None if self.w_next is None else torch.empty(self.w_next.shape, **f32)
-        L.moe_block_norm_backward(x, self.layer.out, self.gate, self.w_post, self.w_next, self.res_scale, self.eps, dy,
-                                  dxn_next, dx, dout, dgate, dw_post, dw_next, self.ws_leave, stream)
+        L.moe_block_norm_backward(x, self.layer.out if out is None else out, self.gate, self.w_post, self.w_next,
+                                  self.res_scale, self.eps, dy, dxn_next, dx, dout, dgate, dw_post, dw_next,
+                                  self.ws_leave, stream)
         return dx, dout, dgate, dw_post, dw_next
 
     def enter_backward(self, x, dxn, dy=None, stream=None):

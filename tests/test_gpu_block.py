@@ -158,3 +158,34 @@ def test_results_belong_to_the_stream_that_writes_them(example):
             again = [torch.empty(s, dtype=t, device="cuda") for s, t in sizes]
             assert not at & {g.data_ptr() for g in again}
             torch.cuda.synchronize()
+
+
+def test_gradients_of_an_earlier_pass(example):
+    """Two micro-batches forward, then both backward, from what the caller kept of the first."""
+    block, r = wide_block(T=300, H=256, score="sigmoid", nseq=2)
+    T, H, E = block.p.T, block.p.H, block.p.E
+    seq = torch.tensor([0, 120, T], dtype=torch.int32, device="cuda")
+    batches = [(r(T, H).bfloat16(), r(T, E), r(T, H).bfloat16(), r(T, H).bfloat16()) for _ in range(2)]
+    dloss = torch.tensor([1.0, 0.5], device="cuda")
+    want = []
+    for x, logits, dy, dxn in batches:  # one after the other
+        block.enter(x)
+        block.leave(x, logits)
+        block.balance(logits, None, seq)
+        want.append([t.clone() for t in (block.loss, block.balance_backward(logits, dloss, None, seq),
+                                         *block.leave_backward(x, dy, dxn))])
+    kept = []
+    for x, logits, dy, dxn in batches:
+        block.enter(x)
+        block.leave(x, logits)
+        kept.append((block.layer.out.clone(), block.layer.ids.clone()))
+    sums = []
+    for (x, logits, dy, dxn), (out, ids) in zip(batches, kept):
+        block.balance(logits, None, seq, ids=ids)
+        sums.append((block.loss.clone(), block.counts.clone(), block.tokens.clone()))
+    for (x, logits, dy, dxn), (out, ids), (loss, counts, tokens), w in zip(batches, kept, sums, want):
+        got = [loss, block.balance_backward(logits, dloss, None, seq, counts=counts, tokens=tokens),
+               *block.leave_backward(x, dy, dxn, out=out)]
+        assert all(torch.equal(a, b) for a, b in zip(got, w))
+    with pytest.raises(ValueError, match="belong together"):
+        block.balance_backward(logits, dloss, None, seq, counts=counts)
