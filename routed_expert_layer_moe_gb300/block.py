@@ -6,6 +6,11 @@ after it with gate and residual, which also norms the input of the next block.
     logits = xn.float() @ W_g                 # the router's product is the caller's
     y, xn_next = block.leave(x, logits)       # x + res_scale * gate * rms(layer(xn)) * w_post, rms(y) * w_next
 
+With sigmoid scores and groups of experts the router's call comes between:
+
+    block.layer.route_grouped(logits, n_group, topk_group, bias, scale=2.5)
+    y, xn_next = block.leave(x, logits, routed=True)
+
 The buffers of the forward calls and of the loss are allocated once and every call only enqueues kernels on the
 stream, so a step is graph-capturable after a first eager one.  leave_backward() and enter_backward() return new
 tensors, allocated on the stream of the call: a caller that uses them on another stream orders the two streams, and
@@ -25,8 +30,8 @@ from . import _lib as L
 
 class MoeBlock:
     """A MoeLayer with its norms and the balance loss of its router.  w_pre, w_post, w_next [H], gate None, [H] or
-    [T, 1], all of the activations' type; w_next None: no norm of the next block's input.  nseq: segments of
-    the balance loss (moe.h)."""
+    [T, 1], all of the activations' type; w_next None: no norm of the next block's input.  score, coef, nseq: the scores,
+    the factor and the segments of the balance loss (moe.h); they choose no router, see leave()."""
 
     def __init__(self, layer, w_pre, w_post, gate=None, w_next=None, res_scale: float = 1.0, eps: float = 1e-6,
                  score: str = "softmax", coef: float = 0.01, nseq: int = 1):
@@ -51,9 +56,15 @@ class MoeBlock:
         L.moe_block_norm(x, None, None, None, self.w_pre, self.res_scale, self.eps, None, self.xn, stream)
         return self.xn
 
-    def leave(self, x, logits, stream=None):
-        """The layer on enter()'s result, and the norm after it: (y, the next block's normed input or None)."""
-        self.layer.forward(self.xn, logits, stream, fused=True)
+    def leave(self, x, logits, stream=None, routed=False):
+        """The layer on enter()'s result, and the norm after it: (y, the next block's normed input or None).  The layer
+        routes by softmax top-k of the logits; routed: it takes the ids and weights that it holds, of a routing
+        that the caller made (layer.route_grouped, or any that writes layer.ids and layer.w)."""
+        if routed:
+            self.layer.permute(self.xn, stream)
+            self.layer.ffn_combine(stream)
+        else:
+            self.layer.forward(self.xn, logits, stream, fused=True)
         L.moe_block_norm(x, self.layer.out, self.gate, self.w_post, self.w_next, self.res_scale, self.eps, self.y,
                          self.xn_next, stream)
         return self.y, self.xn_next

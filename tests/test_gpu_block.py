@@ -189,3 +189,25 @@ def test_gradients_of_an_earlier_pass(example):
         assert all(torch.equal(a, b) for a, b in zip(got, w))
     with pytest.raises(ValueError, match="belong together"):
         block.balance_backward(logits, dloss, None, seq, counts=counts)
+
+
+def test_a_routing_of_the_callers_own(example):
+    """leave(routed=True) runs the layer on the routing that the layer holds: here the grouped sigmoid router's."""
+    block, r = wide_block(T=50, H=256, E=16, score="sigmoid", gate="channel")
+    layer, x, logits = block.layer, r(50, 256).bfloat16(), r(50, 16)
+    xn = block.enter(x).clone()
+    layer.route_grouped(logits, 4, 2, scale=2.5)
+    ids, w = layer.ids.clone(), layer.w.clone()
+    y, xn_next = (t.clone() for t in block.leave(x, logits, routed=True))
+    assert torch.equal(layer.ids, ids) and torch.equal(layer.w, w)
+    out = layer.out.clone()
+    layer.permute(xn), layer.swiglu(), layer.down(), layer.combine()
+    assert torch.equal(layer.out, out) and int(layer.err) == 0
+    d = lambda t: t.double().cpu()  # noqa: E731
+    wy, wxn = ref.block_norm(d(x), d(out), d(block.gate), d(block.w_post), d(block.w_next), 1.0, 1e-6)
+    for got, want in ((y, wy), (xn_next, wxn)):
+        assert ((d(got) - want).abs() <= 2.0 ** -8 * want.abs() + 1e-5).all()
+    loss = block.balance(logits)
+    want = ref.balance(logits.cpu(), ids.cpu(), None, None, "sigmoid", 0.01, torch.ones(1))
+    assert torch.equal(block.counts.cpu().long(), want["counts"])
+    assert abs(float(loss) - float(want["loss"][0])) <= 2.0 ** -18 * float(want["loss"][0])
