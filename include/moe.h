@@ -142,8 +142,8 @@ int64_t moe_grouped_rows(const moe_problem* p);
  * One workspace may serve every call of a layer as long as the calls are
  * ordered on one stream.  The bytes depend on the current device's SM count:
  * ask with the device current that runs the calls (a call that is given less
- * than it needs there answers MOE_ERR_WORKSPACE).  Returns 0 for an invalid
- * problem. */
+ * than it needs there answers MOE_ERR_WORKSPACE).  A workspace is 16-byte
+ * aligned.  Returns 0 for an invalid problem. */
 size_t moe_workspace_bytes(const moe_problem* p);
 
 /* Issue counters ("Inference INFRA methodology (5)", section "DeepGEMM": a tile

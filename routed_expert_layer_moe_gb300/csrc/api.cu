@@ -38,7 +38,6 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 }  // namespace
@@ -213,6 +212,8 @@ static moe_status gemm_call(const moe_problem* p, int mode, const void* act, con
   if (p->wt == MOE_E2M1 && (reinterpret_cast<uintptr_t>(w) & 31u)) return MOE_ERR_UNSUPPORTED;
   const size_t need = ws_bytes(*p);
   if (workspace_bytes < need || (need > 0 && !workspace)) return MOE_ERR_WORKSPACE;
+  if (mode == MODE_DOWN && !aligned16(workspace) && gemm_splits(*p))
+    return MOE_ERR_UNSUPPORTED;  // partial sums, 16 bytes at a time
   return launched(launch_gemm(*p, mode, act, act_scales, w, w_scales, masked_m, offsets, out, out_scales, err_flag,
                               workspace, (cudaStream_t)stream));
 }
@@ -249,6 +250,7 @@ moe_status moe_grouped_ffn(const moe_problem* p, const void* xg, const float* xg
     return MOE_ERR_UNSUPPORTED;
   const size_t need = ws_bytes(*p);
   if (workspace_bytes < need || (need > 0 && !workspace)) return MOE_ERR_WORKSPACE;
+  if (!aligned16(workspace) && gemm_splits(*p)) return MOE_ERR_UNSUPPORTED;  // partial sums, 16 bytes at a time
   return launched(launch_grouped_ffn(*p, xg, xg_scales, w13, w13_scales, w2, w2_scales, masked_m, offsets, hg,
                                      hg_scales, yg, err_flag, workspace, (cudaStream_t)stream));
 }
@@ -294,6 +296,7 @@ moe_status moe_ffn_combine(const moe_problem* p, const void* xg, const float* xg
     return MOE_ERR_UNSUPPORTED;
   const size_t need = ws_bytes(*p);
   if (workspace_bytes < need || (need > 0 && !workspace)) return MOE_ERR_WORKSPACE;
+  if (!aligned16(workspace) && gemm_splits(*p)) return MOE_ERR_UNSUPPORTED;  // partial sums, 16 bytes at a time
   const cudaStream_t st = (cudaStream_t)stream;
   const CombineArgs comb{row_of, w, out};
   if (p->wt == MOE_BF16)  // one launch for both GEMMs

@@ -611,8 +611,6 @@ int dispatch(int E, bool vec, int score, F f) {
   return vec ? s(std::true_type()) : s(std::false_type());
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 }  // namespace
 
 size_t balance_workspace_bytes(const moe_problem& p, int nseq) { return carve(p, nseq, nullptr).bytes; }

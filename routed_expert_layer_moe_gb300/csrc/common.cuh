@@ -40,6 +40,8 @@ size_t max_over_sm_counts(F bytes) {
   return done ? best : std::max<size_t>(best, bytes(own));
 }
 
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
 // cuTensorMapEncodeTiled, resolved once through the runtime's driver entry point.
 CUresult encode_tensor_map(CUtensorMap* map, CUtensorMapDataType dtype, uint64_t inner, uint64_t outer,
                            uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, const void* base);
@@ -72,6 +74,7 @@ int launch_gemm(const moe_problem& p, int mode, const void* a_act, const float* 
                 float* out_scales, int32_t* err, void* ws, cudaStream_t st, const CombineArgs* comb = nullptr,
                 bool after_gate_up = false);
 size_t gemm_workspace_bytes(const moe_problem& p);
+bool gemm_splits(const moe_problem& p);  // the down GEMM leaves partial sums in the workspace
 int gemm_tile_rows(const moe_problem& p, int mode);  // token rows of one MMA tile (0: CUDA-core GEMM)
 int launch_grouped_ffn(const moe_problem& p, const void* xg, const float* xg_scales, const void* w13,
                        const float* w13_scales, const void* w2, const float* w2_scales, const int32_t* masked_m,
@@ -91,6 +94,7 @@ int launch_gemm_mx(const moe_problem& p, int mode, const void* act, const uint8_
                    uint8_t* out_scales, int32_t* err, void* ws, cudaStream_t st, const CombineArgs* comb,
                    bool after_gate_up);
 size_t gemm_mx_workspace_bytes(const moe_problem& p);
+bool gemm_mx_splits(const moe_problem& p);
 int gemm_mx_tile_rows(const moe_problem& p, int mode);
 // After a GEMM whose K range was split: part [ksplit][rows][cols] added in split order into
 // out, with the combine in the same kernel when comb is given; ksplit = 1: the combine alone.

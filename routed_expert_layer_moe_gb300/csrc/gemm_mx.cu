@@ -1067,6 +1067,8 @@ size_t gemm_mx_workspace_bytes(const moe_problem& p) {
   return STATS_BYTES + align_up(best, 256);
 }
 
+bool gemm_mx_splits(const moe_problem& p) { return plan_units(p, MODE_DOWN, device_info().sm_count).ksplit > 1; }
+
 int launch_gemm_mx(const moe_problem& p, int mode, const void* act, const uint8_t* act_scales, const void* w,
                    const uint8_t* w_scales, const int32_t* masked_m, const int32_t* offsets, void* out,
                    uint8_t* out_scales, int32_t* err, void* ws, cudaStream_t st, const CombineArgs* comb,

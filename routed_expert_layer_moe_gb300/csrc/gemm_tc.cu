@@ -1597,6 +1597,13 @@ size_t gemm_workspace_bytes(const moe_problem& p) {
   return STATS_BYTES + align_up(best, 256) + align_up(sizeof(int) * (size_t)(p.P + p.has_shared), 256);
 }
 
+bool gemm_splits(const moe_problem& p) {
+  if (p.wt == MOE_F32) return false;
+  if (p.wt == MOE_MXFP4) return gemm_mx_splits(p);
+  const DeviceInfo& di = device_info();
+  return make_plan(p, MODE_DOWN, di.sm_count, di.max_smem_optin).ksplit > 1;
+}
+
 int launch_gemm(const moe_problem& p, int mode, const void* act, const float* act_scales, const void* w,
                 const float* w_scales, const int32_t* masked_m, const int32_t* offsets, void* out, float* out_scales,
                 int32_t* err, void* ws, cudaStream_t st, const CombineArgs* comb, bool after_gate_up) {

@@ -502,8 +502,6 @@ __global__ void __launch_bounds__(32 * kReduceGroups)
   }
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 constexpr int kReserved = 1024;  // shared memory that a CTA's static arrays and the system take
 
 // How rows of H columns are shared out: vectors and threads, CTAs an SM holds, rows fetched ahead.

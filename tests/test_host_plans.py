@@ -146,3 +146,22 @@ def test_norm_calls_never_lower_a_kernels_shared_memory_limit(run, backward):
         else:
             assert v == ["0"]
     assert len(launched) > 4  # calls of different needs
+
+
+@pytest.mark.parametrize("wt", ["bf16", "e4m3", "mxfp4"])
+def test_unaligned_workspace_of_a_split_product_is_refused(run, wt):
+    """Partial sums of a split down product are written and read 16 bytes at a time."""
+    out = run(152, """
+        for I in (4096, 256):  # enough of K to split, and not
+            p = moe.Problem.make(T=8, K=2, E=4, H=512, I=I, M_max=8, wt='%s')
+            A, n, q = 4096, moe.moe_workspace_bytes(p), ctypes.byref(p)
+            for ws in (A, A + 4):
+                print("status", I, ws - A,
+                      lib.moe_grouped_swiglu_gemm(q, A, A, A, A, A, A, A, A, A, ws, n, None),
+                      lib.moe_grouped_down_gemm(q, A, A, A, A, A, A, A, A, ws, n, None),
+                      lib.moe_grouped_ffn(q, A, A, A, A, A, A, A, A, A, A, A, A, ws, n, None),
+                      lib.moe_ffn_combine(q, A, A, A, A, A, A, A, A, A, A, A, A, A, A, A, ws, n, None))
+        """ % wt)
+    got = {tuple(line.split()[1:3]): line.split()[3:] for line in out if line.startswith("status")}
+    assert got == {("4096", "0"): ["0"] * 4, ("4096", "4"): ["0", "-2", "-2", "-2"],
+                   ("256", "0"): ["0"] * 4, ("256", "4"): ["0"] * 4}
