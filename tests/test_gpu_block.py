@@ -211,3 +211,31 @@ def test_a_routing_of_the_callers_own(example):
     want = ref.balance(logits.cpu(), ids.cpu(), None, None, "sigmoid", 0.01, torch.ones(1))
     assert torch.equal(block.counts.cpu().long(), want["counts"])
     assert abs(float(loss) - float(want["loss"][0])) <= 2.0 ** -18 * float(want["loss"][0])
+
+
+@pytest.mark.parametrize("gate", ["token", "channel", None])
+def test_block_with_segments_and_masked_tokens(example, gate):
+    """Packed sequences with padding: the block's outputs, its loss per segment and the gradients, with each gate."""
+    block, r = wide_block(T=70, H=256, E=16, nseq=3, gate=gate)
+    T, H, E = 70, 256, 16
+    x, logits, dy, dxn = r(T, H).bfloat16(), r(T, E), r(T, H).bfloat16(), r(T, H).bfloat16()
+    seq = torch.tensor([4, 4, 40, 66], dtype=torch.int32, device="cuda")
+    valid = (r(T) > -1.0).to(torch.uint8)
+    dloss = torch.tensor([1.0, 0.5, -2.0], device="cuda")
+    block.enter(x)
+    y, xn = block.leave(x, logits)
+    loss, dl = block.balance(logits, valid, seq), block.balance_backward(logits, dloss, valid, seq)
+    want = ref.balance(logits.cpu(), block.layer.ids.cpu(), valid.cpu(), seq.tolist(), "softmax", 0.01, dloss.cpu())
+    d = lambda t: t.double().cpu()  # noqa: E731
+    assert torch.equal(block.counts.cpu().long(), want["counts"]) and torch.equal(block.tokens.cpu().long(), want["tokens"])
+    assert ((d(loss) - want["loss"]).abs() <= 2.0 ** -18 * want["loss"]).all()
+    assert (d(dl) - want["dlogits"]).abs().max() <= 2.0 ** -15 * want["dlogits"].abs().max()
+    out = block.layer.out
+    host = [None if t is None else t.cpu() for t in (x, out, block.gate, block.w_post, block.w_next)]
+    wy, wxn = ref.block_norm(*[None if t is None else t.double() for t in host], 1.0, 1e-6)
+    for got, w in ((y, wy), (xn, wxn)):
+        assert ((d(got) - w).abs() <= 2.0 ** -8 * w.abs() + 1e-5).all()
+    for g, w in zip(block.leave_backward(x, dy, dxn), ref.block_norm_grads(host, 1.0, 1e-6, dy.cpu(), dxn.cpu())):
+        assert (g is None) == (w is None)
+        if g is not None:
+            assert (d(g) - w).abs().max() <= 2.0 ** -7 * w.abs().max()

@@ -360,3 +360,85 @@ def test_layer_in_a_graph():
     L.out.zero_()
     graph.replay()
     assert torch.equal(L.out, want)
+
+
+def test_overflowing_h_marks_its_blocks():
+    """Columns of h that are infinite or NaN give their blocks of 32 the scale byte 255 and codes 0, the others keep theirs;
+    single CTAs with tiles of 64 and of 128 weight rows, and SM pairs."""
+    for sizes, I in (([9, 3], 256), ([16, 15, 31, 32, 33, 63, 64, 65, 127, 128, 1, 2, 0, 100, 90, 17], 1152),
+                     ([300, 256, 513, 1, 130], 384)):
+        H = 256
+        g = Grouped(sizes, H, I, "contig", seed=I)
+
+        def h():
+            hq = torch.full((g.rows, I // 2), 0x5A, dtype=torch.uint8, device="cuda")
+            hs = torch.full((g.rows, I // 32), 0x5A, dtype=torch.uint8, device="cuda")
+            moe.moe_grouped_swiglu_gemm(g.p, g.dx[0], g.dx[1], g.d13[0], g.d13[1], g.m, g.off, hq, hs, g.err, g.ws)
+            return hq, hs
+
+        hq, hs = h()
+        bad = [1, I // 32 - 2]  # blocks of 32 columns
+        g.d13[1][:, 40] = 255                     # a NaN in a row of W1
+        g.d13[1][:, I + I - 40] = 254             # a row of W3 whose products with x pass the largest fp32
+        g.d13[0][:, I + I - 40] = 0x77            # all 6
+        first = next(g.valid())[1]
+        g.dx[0][first] = 0x77
+        g.dx[1][first] = 160                      # x = 6 * 2^33: certainly infinite
+        want_q, want_s = hq.clone(), hs.clone()
+        hq, hs = h()
+        torch.cuda.synchronize()
+        assert int(g.err) == 0
+        for s, r, n in g.valid():
+            rows = slice(r, r + n)
+            assert (hs[rows, 1] == 255).all() and (hq[rows, 16:32] == 0).all()
+        assert int(hs[first, bad[1]]) == 255 and (hq[first, 16 * bad[1]:16 * bad[1] + 16] == 0).all()
+        keep = [b for b in range(I // 32) if b not in bad]
+        others = torch.tensor([r for s, a, n in g.valid() for r in range(a, a + n) if r != first], device="cuda")
+        cols = torch.tensor([16 * b + i for b in keep for i in range(16)], device="cuda")
+        keep = torch.tensor(keep, device="cuda")
+        assert torch.equal(hs[others][:, keep], want_s[others][:, keep])
+        assert torch.equal(hq[others][:, cols], want_q[others][:, cols])
+
+
+def random_layer(T, H, I, E, K, layout, seed):
+    g = torch.Generator().manual_seed(seed)
+    p = moe.Problem.make(T=T, H=H, I=I, E=E, K=K, M_max=T if layout == "masked" else 0, wt="mxfp4", layout=layout)
+    q13, q2 = (quantize((torch.randn(E, *s, generator=g) * 0.05).cuda()) for s in ((2 * I, H), (H, I)))
+    L = moe.MoeLayer(p, "bf16", "mxfp4", "bf16", q13[0], q2[0], q13[1], q2[1])
+    return L, torch.randn(T, H, generator=g).bfloat16(), torch.randn(T, E, generator=g)
+
+
+@pytest.mark.parametrize("T,H,I,E,K,layout", [
+    (3, 256, 384, 8, 2, "masked"), (40, 256, 256, 8, 4, "contig"), (600, 512, 256, 4, 2, "contig"),
+    (1100, 256, 128, 8, 4, "masked")])
+def test_non_finite_tokens_stay_in_their_rows(T, H, I, E, K, layout):
+    """A NaN or an infinity in a token makes its own output NaN and no other token's."""
+    L, x, logits = random_layer(T, H, I, E, K, layout, T)
+    want = L.forward(x.cuda(), logits.cuda(), fused=True).clone()
+    bad = [0, T // 2, T - 1]
+    for t, (c, v) in zip(bad, ((5, float("nan")), (H - 1, float("inf")), (H // 2, -float("inf")))):
+        x[t, c] = v
+    for fused in (True, False):
+        out = L.forward(x.cuda(), logits.cuda(), fused=fused)
+        torch.cuda.synchronize()
+        assert int(L.err) == 0
+        assert torch.isnan(out[bad]).all()
+        rest = torch.ones(T, dtype=torch.bool)
+        rest[bad] = False
+        assert torch.equal(out[rest.cuda()], want[rest.cuda()])
+
+
+@pytest.mark.parametrize("T,H,I,E,K,layout", [(600, 512, 256, 4, 2, "contig"), (1100, 256, 128, 8, 4, "masked"),
+                                              (1030, 256, 256, 16, 3, "contig")])
+def test_layer_of_prefill_size(T, H, I, E, K, layout):
+    """The whole layer on SM pairs against 64 bits, 48 of its tokens.  h is stored in four bits: next
+    to a tie its code may be the neighbour of the exact one's, a relative error of up to 1/2 in one of I terms, so the
+    bound on an output is 3e-2 of the largest, as in test_layer."""
+    L, x, logits = random_layer(T, H, I, E, K, layout, T + 1)
+    out = L.forward(x.cuda(), logits.cuda(), fused=True).double().cpu().numpy()
+    assert int(L.err) == 0
+    tokens = np.random.default_rng(T).choice(T, 48, replace=False)
+    sub = moe.Problem.make(T=48, H=H, I=I, E=E, K=K, M_max=48, wt="mxfp4")
+    want = layer_reference(type("S", (), dict(p=sub, w13=L.w13, w13_s=L.w13_s, w2=L.w2, w2_s=L.w2_s)), x[tokens],
+                           logits[tokens])
+    assert np.abs(out[tokens] - want).max() <= 3e-2 * np.abs(want).max()
