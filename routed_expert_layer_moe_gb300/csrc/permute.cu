@@ -351,25 +351,25 @@ __device__ __forceinline__ void copy_token(const TX* __restrict__ x, int t, int 
           }
         } else {
 #pragma unroll
-        for (int off = 8; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-        if (!live) continue;
-        const float sc = (amax == 0.0f) ? 1.0f : __fdiv_rn(amax, 448.0f);
-        uint32_t packed[2];
+          for (int off = 8; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+          if (!live) continue;
+          const float sc = (amax == 0.0f) ? 1.0f : __fdiv_rn(amax, 448.0f);
+          uint32_t packed[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(
-              make_float2(__fdiv_rn(f[4 * i], sc), __fdiv_rn(f[4 * i + 1], sc)), __NV_SATFINITE, __NV_E4M3);
-          const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(
-              make_float2(__fdiv_rn(f[4 * i + 2], sc), __fdiv_rn(f[4 * i + 3], sc)), __NV_SATFINITE, __NV_E4M3);
-          packed[i] = (uint32_t)lo | ((uint32_t)hi << 16);
-        }
-        const uint2 pv = make_uint2(packed[0], packed[1]);
-        for (int k = 0; k < KS; ++k) {
-          const int r = rows[k];
-          if (r < 0) continue;
-          *reinterpret_cast<uint2*>(q + (size_t)r * H + g * 128 + sub * 8) = pv;
-          if (sub == 0) xg_scales[(size_t)r * G + g] = sc;
-        }
+          for (int i = 0; i < 2; ++i) {
+            const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(
+                make_float2(__fdiv_rn(f[4 * i], sc), __fdiv_rn(f[4 * i + 1], sc)), __NV_SATFINITE, __NV_E4M3);
+            const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(
+                make_float2(__fdiv_rn(f[4 * i + 2], sc), __fdiv_rn(f[4 * i + 3], sc)), __NV_SATFINITE, __NV_E4M3);
+            packed[i] = (uint32_t)lo | ((uint32_t)hi << 16);
+          }
+          const uint2 pv = make_uint2(packed[0], packed[1]);
+          for (int k = 0; k < KS; ++k) {
+            const int r = rows[k];
+            if (r < 0) continue;
+            *reinterpret_cast<uint2*>(q + (size_t)r * H + g * 128 + sub * 8) = pv;
+            if (sub == 0) xg_scales[(size_t)r * G + g] = sc;
+          }
         }
       }
     }
