@@ -156,8 +156,8 @@ size_t moe_workspace_bytes(const moe_problem* p);
  * on SM pairs counts each pair's units once, in its first CTA).  Summed over
  * CTAs, the token tiles of a GEMM equal the sum over slots of
  * ceil(masked_m[s] / BM).  Phase 1 is the down GEMM of moe_grouped_ffn and
- * zero otherwise.  The counters stay valid until the next call that uses the
- * workspace. */
+ * zero otherwise (MXFP4: two launches, and phase 0 is the down GEMM's).  The
+ * counters stay valid until the next call that uses the workspace. */
 #define MOE_STATS_CTAS 256
 #define MOE_STATS_BYTES (2 * MOE_STATS_CTAS * 2 * 4)
 
@@ -291,20 +291,22 @@ moe_status moe_grouped_down_gemm(const moe_problem* p, const void* hg, const flo
                                  void* yg, int32_t* err_flag, void* workspace, size_t workspace_bytes,
                                  moe_stream_t stream);
 
-/* Steps 3 and 4 in one launch (the fused path of "MoE inference and expert
+/* Steps 3 and 4 in one call (the fused path of "MoE inference and expert
  * parallelism", routing section: "fused MoE" runs the grouped gate/up, the
  * activation and the grouped down GEMM as one unit of work).  Same arguments,
  * outputs and numerics as moe_grouped_swiglu_gemm followed by
  * moe_grouped_down_gemm (hg/hg_scales are still written; yg is bit-identical
- * to the two separate calls).  On the tensor cores it is one persistent
+ * to the two separate calls).  For bf16, e4m3 and e2m1 weights it is one persistent
  * cooperative launch in which a CTA moves on to down tiles as soon as every
  * gate/up tile of that slot has released its rows of h, so the down GEMM's
  * weight streaming overlaps the end of gate/up (plus the split-K reduction
- * kernel when the down GEMM is split); fp32 problems run the two CUDA-core
- * GEMMs one after the other.  All CTAs must be resident at once: the launch
- * fails (MOE_ERR_CUDA) if the device cannot co-schedule them.  workspace:
- * moe_workspace_bytes(p) bytes (it holds the per-slot ready counters, cleared
- * by this call). */
+ * kernel when the down GEMM is split).  All CTAs of it must be resident at once:
+ * the launch fails (MOE_ERR_CUDA) if the device cannot co-schedule them.  MXFP4
+ * problems run the two GEMMs as two launches (and the reduction when the down
+ * GEMM is split), the second of which starts on its weights while the first
+ * ends; fp32 problems run the two CUDA-core GEMMs one after the other.
+ * workspace: moe_workspace_bytes(p) bytes (for the cooperative launch it holds
+ * the per-slot ready counters, cleared by this call). */
 moe_status moe_grouped_ffn(const moe_problem* p, const void* xg, const float* xg_scales, const void* w13,
                            const float* w13_scales, const void* w2, const float* w2_scales, const int32_t* masked_m,
                            const int32_t* offsets, void* hg, float* hg_scales, void* yg, int32_t* err_flag,
@@ -339,8 +341,8 @@ moe_status moe_route_permute(const moe_problem* p, const float* logits, const vo
  * moe_grouped_swiglu_gemm, moe_grouped_down_gemm and moe_combine in that order
  * (row_of and w as written by moe_permute and the router; hg, hg_scales and
  * yg are written as by those calls; out is bit-identical to moe_combine's).
- * bf16 experts run both GEMMs in one launch (as moe_grouped_ffn); FP8 / FP4
- * experts in two.  When the down GEMM is split along K (decode-sized slots),
+ * bf16 experts run both GEMMs in one launch (as moe_grouped_ffn); FP8, FP4 and
+ * MXFP4 experts in two.  When the down GEMM is split along K (decode-sized slots),
  * the combine runs inside the split-K reduction: each record's row is
  * reduced over the splits and enters its token's k-order sum in the same
  * kernel; otherwise the combine kernel follows the down GEMM.
@@ -390,7 +392,8 @@ moe_status moe_mx_quantize(int32_t dtype, int64_t rows, int64_t cols, const void
                            moe_stream_t stream);
 
 /* codes, scales -> out [rows][cols] (dtype F32 or BF16): code * 2^(s - 127),
- * exact in both types; NaN where s = 255.  out 16-byte aligned, codes 4-byte
+ * exact in both types (infinite where that passes their largest value, which
+ * scale bytes 253 and 254 can); NaN where s = 255.  out 16-byte aligned, codes 4-byte
  * aligned. */
 moe_status moe_mx_dequantize(int32_t dtype, int64_t rows, int64_t cols, const uint8_t* codes, const uint8_t* scales,
                              void* out, moe_stream_t stream);

@@ -11,7 +11,8 @@
 // or 32 lanes, so a warp works on up to four tokens at a time and its shuffles serve all of
 // them, and the next rows are requested before this step's arithmetic.  65536 x 256 sigmoid scores:
 // a warp per token and no request ahead took 64 and 52 us, held by the latency of one row at a
-// time; groups of lanes 20 and 21 us; 10 and 20 us is the memory's rate, 2-3 us of each go to start and end.
+// time; groups of lanes 21.7 and 25.4 us (0.6 of the first for the rows of low sigmoids, see `scores`); 10 and 20 us is
+// the memory's rate, 2-3 us of each go to start and end.
 // The sums over tokens use no float
 // atomics: the token range is cut into `ntiles` equal tiles, a tile meets the segments in
 // pieces, and the piece of tile i in segment b is row i + b of the partial sums -- distinct for

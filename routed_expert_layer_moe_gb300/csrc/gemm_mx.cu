@@ -274,7 +274,10 @@ __device__ __forceinline__ uint32_t bf16x2(float a, float b) {
 }
 
 // h = SiLU(g) u of a pair, with the special-function unit's exponential and reciprocal (2 ulp and 1 ulp): for
-// g -> -inf the exponential is inf and the product -0 u.
+// g -> -inf the exponential is inf and the product -0 u.  h is rounded to four bits next; a value within those ulps of
+// a tie may take the neighbouring code, as it may after another order of the fp32 sum behind g and u.  Against 64
+// bits one expert of 14336 is as far off as a plain form with expf and an IEEE division (1.68e-3 both; 8e-5 between
+// the two).
 __device__ __forceinline__ float2 silu_mul(float2 g, float2 u) {
   const float2 t = __fmul2_rn(g, make_float2(-1.4426950408889634f, -1.4426950408889634f));
   float2 e;

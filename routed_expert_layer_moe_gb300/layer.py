@@ -81,7 +81,8 @@ class MoeLayer:
                                 self.yg, self.err, self.ws, stream)
 
     def ffn(self, stream=None):
-        """gate/up + SwiGLU and down in one launch (moe_grouped_ffn); same outputs as swiglu() + down()."""
+        """gate/up + SwiGLU and down in one call (moe_grouped_ffn; one launch, but two for mxfp4 and f32); same outputs as
+        swiglu() + down()."""
         L.moe_grouped_ffn(self.p, self.xg, self.xg_s, self.w13, self.w13_s, self.w2, self.w2_s, self.masked_m,
                           self.offsets, self.hg, self.hg_s, self.yg, self.err, self.ws, stream)
 
