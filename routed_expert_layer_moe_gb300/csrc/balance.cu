@@ -11,7 +11,7 @@
 // or 32 lanes, so a warp works on up to four tokens at a time and its shuffles serve all of
 // them, and the next rows are requested before this step's arithmetic.  65536 x 256 sigmoid scores:
 // a warp per token and no request ahead took 64 and 52 us, held by the latency of one row at a
-// time; groups of lanes 21.7 and 25.4 us (0.6 of the first for the rows of low sigmoids, see `scores`); 10 and 20 us is
+// time; groups of lanes 21.7 and 25.3 us (0.6 of the first for the rows of low sigmoids, see `scores`); 10 and 20 us is
 // the memory's rate, 2-3 us of each go to start and end.
 // The sums over tokens use no float
 // atomics: the token range is cut into `ntiles` equal tiles, a tile meets the segments in
@@ -61,12 +61,13 @@ struct Segments {
     }
   };
 
-  // The last segment that starts at or before t (the one that holds t, if any does), with its bounds; for a t
-  // before all segments the last one that starts where the first does (those before it are empty, so it
-  // is the next with tokens, if any has).  By a whole warp, the same t in every lane and t growing from call
+  // The last segment that starts at or before t (the one that holds t, if any does), with its bounds.  For a t before
+  // all segments: NEXT: the last one that starts where the first does (those before it are empty, so it is the
+  // next with tokens, if any has); else any one, which does not hold t.  By a whole warp, the same t in every lane and t growing from call
   // to call: many places are looked at together, for one after the other each costs the memory's latency (six
   // of them for 48 segments), and kept for the next call: a tile that several short segments meet would pay
   // for each of them.
+  template <bool NEXT>
   __device__ __forceinline__ int find(int t, Window& w, int& first, int& end) const {
     if (!off) {
       first = 0, end = T;
@@ -90,7 +91,7 @@ struct Segments {
       }
       m0 = __ballot_sync(0xffffffffu, lane < w.n && w.v0 <= t);
       m1 = __ballot_sync(0xffffffffu, lane + 32 < w.n && w.v1 <= t);
-      if (m0 | m1 || pass) break;
+      if (!NEXT || m0 | m1 || pass) break;
       t = w.at(0);  // no segment starts at or before t: look up the first one's start instead
       w.n = 0;
     }
@@ -283,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, N > 16 ? 2 : kTilesPerSm)
   if (t < t1) request(t + warp * G + grp);
   while (t < t1) {
     int lo, hi;
-    const int b = seg.find(t, window, lo, hi);
+    const int b = seg.find<true>(t, window, lo, hi);
     const int from = max(t, lo), end = min(t1, hi);  // from: past the tokens before the first segment
     if (end <= from) break;                          // past the last segment
     if (from != t) request(from + warp * G + grp);   // not the step that is on its way
@@ -495,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, N > 16 ? 2 : kTilesPerSm)
         const int other = __shfl_sync(0xffffffffu, t, __ffs(moving) - 1);
         int slo, shi;
         Segments::Window window;
-        const int s = seg.find(other, window, slo, shi);
+        const int s = seg.find<false>(other, window, slo, shi);
         const bool mine = move && (t == other || (t >= slo && t < shi));
         if (mine) {
           b = s;
