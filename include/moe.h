@@ -473,6 +473,110 @@ moe_status moe_block_norm_backward(int32_t dtype, int32_t T, int32_t H, const vo
                                    void* dblock, float* dgate, float* dw_post, float* dw_pre, void* workspace,
                                    size_t workspace_bytes, moe_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Activation checkpoints in 8 bits.  Additions of this library.
+ *
+ * A row of `cols` values becomes cols E4M3 codes and ceil(cols / 128) fp32
+ * scales, one per group of 128 values (a row's last group may be shorter): s =
+ * largest magnitude * fp32(1/448) (rounded to fp32; 1 where it is 0), code =
+ * E4M3(x / s), the nearest to the exact quotient with ties to the even code,
+ * saturating at 448; the sign of a zero is kept.  A group that holds a NaN or an infinity gets a NaN scale and
+ * codes 0.  Value = code * s, rounded once; it is within 2^-4 of x, relative,
+ * where |x| >= 2^-6 s, and within 2^-10 s below that.
+ * ------------------------------------------------------------------------- */
+
+/* x [rows][cols] (dtype F32 or BF16, any alignment of the type's own size) ->
+ * codes [rows][cols], scales [rows][ceil(cols / 128)]. */
+moe_status moe_fp8_quantize(int32_t dtype, int64_t rows, int64_t cols, const void* x, uint8_t* codes, float* scales,
+                            moe_stream_t stream);
+
+/* codes, scales -> out [rows][cols] (dtype F32 or BF16). */
+moe_status moe_fp8_dequantize(int32_t dtype, int64_t rows, int64_t cols, const uint8_t* codes, const float* scales,
+                              void* out, moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Training the experts (the pages treat inference alone).  Additions of this
+ * library, for bf16 experts (BF16/BF16/BF16; others answer
+ * MOE_ERR_UNSUPPORTED).  A training pass is the forward pass with step 3 in the
+ * form that keeps its results:
+ *
+ *   moe_route_topk, moe_permute, moe_grouped_swiglu_gemm_save,
+ *   moe_grouped_down_gemm, moe_combine
+ *
+ * and its gradient, in this order on one stream:
+ *
+ *   moe_combine_backward      dout -> dyg, wg, dw
+ *   moe_grouped_ffn_backward  dyg -> dxg and the weights' gradients
+ *   moe_permute_backward      dxg -> dx
+ *   moe_route_backward        dw -> dlogits
+ *
+ * What the gradient reads of the forward pass: ids, w, row_of, masked_m,
+ * offsets, xg, yg and the checkpoint gu.  Rows at or past masked_m[s] are
+ * neither read into a result nor written, whatever they hold; a record that was
+ * not placed (row_of = -1) contributes nothing and has dw = 0.  Weights'
+ * gradients are per slot: replicas of one expert each have their own.  Sums are
+ * fp32 in a fixed order: the same inputs give the same bits.  No workspace.
+ * ------------------------------------------------------------------------- */
+
+/* Step 3 that also keeps g and u for the gradient: with (g, u) the products of
+ * a row with W13's gate and up rows,
+ *   hg [rows][I] bf16: SiLU(g) * u,
+ *   gu [rows][2I]: the codes of the row (g, u) as moe_fp8_quantize has them (of
+ *     the fp32 sums; a code whose quotient lies within the sums' rounding of the
+ *     middle of two may be either), gu_scales [rows][2I/128] the scales.
+ * xg, w13, hg and gu 16-byte aligned. */
+moe_status moe_grouped_swiglu_gemm_save(const moe_problem* p, const void* xg, const void* w13, const int32_t* masked_m,
+                                        const int32_t* offsets, void* hg, uint8_t* gu, float* gu_scales,
+                                        int32_t* err_flag, moe_stream_t stream);
+
+/* Gradient of moe_combine: for every placed record (t, k) with grouped row r,
+ *   the gradient of yg[r] is wg[r] * dyg[r] with dyg[r] = dout[t] and wg[r] =
+ *     w[t,k] (the shared expert's: 1), kept apart so that the product is not
+ *     rounded to bf16,
+ *   dw[t,k] = sum_h dout[t,h] * yg[r,h]  (fp32; the shared expert has none).
+ * dout [T][H], yg and dyg [rows][H] bf16, wg [rows] fp32; dyg may be yg.  dw
+ * [T][K], or NULL: it is not computed and yg is not read (and may be NULL). */
+moe_status moe_combine_backward(const moe_problem* p, const void* dout, const void* yg, const int32_t* row_of,
+                                const float* w, void* dyg, float* wg, float* dw, moe_stream_t stream);
+
+/* Gradient of steps 3 and 4.  With g, u the values of the checkpoint and s =
+ * sigmoid(g), for every valid row:
+ *   dh = wg[row] * W2[s]^T . dyg[row],  hg[row] = wg[row] * g s u,
+ *   dgu[row] = (dh u s (1 + g (1 - s)), dh g s),
+ *   dxg[row] = W13[s]^T . dgu[row]
+ * and for every slot, summed over its valid rows,
+ *   dw13[s] = dgu^T xg [2I][H],  dw2[s] = dyg^T hg [H][I].
+ * dgu [rows][2I], hg [rows][I] and dxg [rows][H] are bf16 (written; products
+ * take them in that form).  wg NULL: every row has weight 1.  dw13, dw2: dw_dtype BF16 or F32; `accumulate` (F32
+ * alone, else MOE_ERR_UNSUPPORTED) adds to what they hold, otherwise every
+ * element is written, zeros for a slot without rows.  dxg, dw13 and dw2 may each
+ * be NULL where they are not wanted (then w13, xg are not read).  All but wg and
+ * gu_scales 16-byte aligned; outputs overlap no input and no other output. */
+moe_status moe_grouped_ffn_backward(const moe_problem* p, const void* dyg, const float* wg, const void* xg,
+                                    const void* w13, const void* w2, const uint8_t* gu, const float* gu_scales,
+                                    const int32_t* masked_m, const int32_t* offsets, void* dgu, void* hg, void* dxg, void* dw13, void* dw2,
+                                    int32_t dw_dtype, int32_t accumulate, int32_t* err_flag, moe_stream_t stream);
+
+/* Gradient of the dispatch: dx[t] = sum over the token's placed records of
+ * dxg[row], in fp32 in k order (the shared expert's last), rounded once.  dxg
+ * [rows][H], dx [T][H] bf16, 16-byte aligned. */
+moe_status moe_permute_backward(const moe_problem* p, const void* dxg, const int32_t* row_of, void* dx,
+                                moe_stream_t stream);
+
+/* Gradient of the router's weights with the choice held constant; any problem
+ * type.  dlogits [T][E] = add (or zeros), plus at expert ids[t,k]:
+ *   SOFTMAX (moe_route_topk):  w_k (dw_k - sum_j w_j dw_j); w as that call wrote
+ *     it, logits are not read;
+ *   SIGMOID (moe_route_grouped_topk): s_k (1 - s_k) ds_k with s = sigmoid(logits),
+ *     ds_k = scale (dw_k - sum_j s_j dw_j / S) / S with S = sum_j s_j when
+ *     `renormalize`, else scale dw_k; w is not read.  A token whose S is 0 has 0.
+ * renormalize and scale: as in that call (SOFTMAX ignores them).  add [T][E]
+ * fp32 or NULL, for instance the gradient of moe_balance_loss; dlogits may be
+ * add.  Ids outside [0,E) are skipped. */
+moe_status moe_route_backward(const moe_problem* p, int32_t score, const float* logits, const int32_t* ids,
+                              const float* w, const float* dw, int32_t renormalize, float scale, const float* add,
+                              float* dlogits, moe_stream_t stream);
+
 /* Diagnostic, an addition of this library (the pages describe none): runs the
  * bounded wait that every kernel here uses on an mbarrier that nothing
  * completes, with a limit of `cycles` SM cycles (1 .. 4e9), so that the expiry

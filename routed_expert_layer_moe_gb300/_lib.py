@@ -36,6 +36,8 @@ EXPORTS = ["moe_version", "moe_status_string", "moe_grouped_rows", "moe_workspac
            "moe_mx_quantize", "moe_mx_dequantize",
            "moe_balance_workspace_bytes", "moe_balance_loss", "moe_balance_loss_backward",
            "moe_block_norm_workspace_bytes", "moe_block_norm", "moe_block_norm_backward",
+           "moe_fp8_quantize", "moe_fp8_dequantize", "moe_grouped_swiglu_gemm_save", "moe_combine_backward",
+           "moe_grouped_ffn_backward", "moe_permute_backward", "moe_route_backward",
            "moe_eplb_record", "moe_eplb_rebalance", "moe_eplb_invert", "moe_selftest_bounded_wait"]
 
 
@@ -125,6 +127,20 @@ def lib():
     L.moe_block_norm.restype = i32
     L.moe_block_norm_backward.argtypes = [i32, i32, i32, vp, vp, i32, vp, vp, vp, f32, f32] + [vp] * 8 + [sz, vp]
     L.moe_block_norm_backward.restype = i32
+    L.moe_fp8_quantize.argtypes = [i32, i64, i64, vp, vp, vp, vp]
+    L.moe_fp8_quantize.restype = i32
+    L.moe_fp8_dequantize.argtypes = [i32, i64, i64, vp, vp, vp, vp]
+    L.moe_fp8_dequantize.restype = i32
+    L.moe_grouped_swiglu_gemm_save.argtypes = [pp] + [vp] * 9
+    L.moe_grouped_swiglu_gemm_save.restype = i32
+    L.moe_combine_backward.argtypes = [pp] + [vp] * 8
+    L.moe_combine_backward.restype = i32
+    L.moe_grouped_ffn_backward.argtypes = [pp] + [vp] * 14 + [i32, i32, vp, vp]
+    L.moe_grouped_ffn_backward.restype = i32
+    L.moe_permute_backward.argtypes = [pp] + [vp] * 4
+    L.moe_permute_backward.restype = i32
+    L.moe_route_backward.argtypes = [pp, i32] + [vp] * 4 + [i32, f32] + [vp] * 3
+    L.moe_route_backward.restype = i32
     L.moe_selftest_bounded_wait.argtypes = [i64, vp, vp]
     L.moe_selftest_bounded_wait.restype = i32
     L.moe_eplb_invert.argtypes = [i32, i32, vp, i32, vp, vp]
@@ -406,6 +422,106 @@ def moe_block_norm_backward(x, block, gate, w_post, w_pre, res_scale: float, eps
         _arg(dblock, "dblock", dt, TH), _arg(dgate, "dgate", f32, () if gate is None else gate.shape),
         _arg(dw_post, "dw_post", f32, one), _arg(dw_pre, "dw_pre", f32, one), _ptr(workspace),
         workspace.numel() * workspace.element_size(), _stream(stream)), "moe_block_norm_backward")
+
+
+FP8_GROUP = 128  # values that share a scale of an 8-bit checkpoint
+
+
+def _fp8_args(values, codes, scales, name: str):
+    """dtype, rows, cols and addresses of an 8-bit conversion; leading dimensions count as rows."""
+    d, addr = _values(values, name)
+    if values.dim() < 1:
+        raise ValueError("%s: expected rows of values" % name)
+    *lead, cols = values.shape
+    return (d, torch.Size(lead).numel(), cols, addr, _arg(codes, "codes", torch.uint8, values.shape),
+            _arg(scales, "scales", torch.float32, (*lead, -(-cols // FP8_GROUP))))
+
+
+def moe_fp8_quantize(x, codes, scales, stream=None) -> None:
+    """x [..., cols] (float32 or bfloat16) -> E4M3 codes [..., cols] (uint8) and scales [..., ceil(cols / 128)]."""
+    d, rows, cols, px, pc, ps = _fp8_args(x, codes, scales, "x")
+    _check(lib().moe_fp8_quantize(d, rows, cols, px, pc, ps, _stream(stream)), "moe_fp8_quantize")
+
+
+def moe_fp8_dequantize(codes, scales, out, stream=None) -> None:
+    """E4M3 codes and scales -> the values they stand for, out [..., cols] (float32 or bfloat16)."""
+    d, rows, cols, po, pc, ps = _fp8_args(out, codes, scales, "out")
+    _check(lib().moe_fp8_dequantize(d, rows, cols, pc, ps, po, _stream(stream)), "moe_fp8_dequantize")
+
+
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+
+
+def _train_sizes(p: Problem):
+    """rows, slots of a problem whose experts can be trained; a MoeError for one that is none."""
+    rows = moe_grouped_rows(p)
+    if rows < 0 or p.wt != MOE_BF16:
+        st = moe_check_problem(p)
+        raise MoeError(MOE_ERR_UNSUPPORTED if st == MOE_OK else st, "problem")
+    return rows, p.P + p.has_shared
+
+
+def moe_grouped_swiglu_gemm_save(p: Problem, xg, w13, masked_m, offsets, hg, gu, gu_scales, err_flag,
+                                 stream=None) -> None:
+    """Step 3 that also keeps g and u for the gradient, in 8 bits: gu [rows, 2I] uint8, gu_scales [rows, 2I/128]."""
+    rows, n = _train_sizes(p)
+    _check(lib().moe_grouped_swiglu_gemm_save(
+        ctypes.byref(p), _arg(xg, "xg", _BF16, (rows, p.H)), _arg(w13, "w13", _BF16, (n, 2 * p.I, p.H)),
+        _arg(masked_m, "masked_m", _I32, (n,)), _arg(offsets, "offsets", _I32, (n + 1,)),
+        _arg(hg, "hg", _BF16, (rows, p.I)), _arg(gu, "gu", _U8, (rows, 2 * p.I)),
+        _arg(gu_scales, "gu_scales", _F32, (rows, 2 * p.I // FP8_GROUP)), _ptr(err_flag), _stream(stream)),
+        "moe_grouped_swiglu_gemm_save")
+
+
+def moe_combine_backward(p: Problem, dout, yg, row_of, w, dyg, wg, dw, stream=None) -> None:
+    """Gradient of moe_combine: that of yg as wg [rows] times dyg [rows, H] (may be yg), and dw [T, K] (None: not
+    computed, yg not read)."""
+    rows, _ = _train_sizes(p)
+    _check(lib().moe_combine_backward(
+        ctypes.byref(p), _arg(dout, "dout", _BF16, (p.T, p.H)), _arg(yg, "yg", _BF16, (rows, p.H)),
+        _arg(row_of, "row_of", _I32, (p.T, p.K + p.has_shared)), _arg(w, "w", _F32, (p.T, p.K)),
+        _arg(dyg, "dyg", _BF16, (rows, p.H)), _arg(wg, "wg", _F32, (rows,)), _arg(dw, "dw", _F32, (p.T, p.K)),
+        _stream(stream)), "moe_combine_backward")
+
+
+def moe_grouped_ffn_backward(p: Problem, dyg, wg, xg, w13, w2, gu, gu_scales, masked_m, offsets, dgu, hg, dxg, dw13,
+                             dw2, err_flag, accumulate=False, stream=None) -> None:
+    """Gradient of steps 3 and 4 from the checkpoint gu (moe.h).  wg None: every row has weight 1.  dxg, dw13, dw2: each None where it is not wanted;
+    dw13 [slots, 2I, H] and dw2 [slots, H, I] are both bfloat16 or both float32; accumulate (float32): added to what
+    they hold."""
+    rows, n = _train_sizes(p)
+    dt = next((t.dtype for t in (dw13, dw2) if t is not None), _BF16)
+    if dt not in _FLOAT_DTYPES:
+        raise ValueError("dw13, dw2: expected float32 or bfloat16, got %s" % dt)
+    _check(lib().moe_grouped_ffn_backward(
+        ctypes.byref(p), _arg(dyg, "dyg", _BF16, (rows, p.H)), _arg(wg, "wg", _F32, (rows,)), _arg(xg, "xg", _BF16, (rows, p.H)),
+        _arg(w13, "w13", _BF16, (n, 2 * p.I, p.H)), _arg(w2, "w2", _BF16, (n, p.H, p.I)),
+        _arg(gu, "gu", _U8, (rows, 2 * p.I)), _arg(gu_scales, "gu_scales", _F32, (rows, 2 * p.I // FP8_GROUP)),
+        _arg(masked_m, "masked_m", _I32, (n,)), _arg(offsets, "offsets", _I32, (n + 1,)),
+        _arg(dgu, "dgu", _BF16, (rows, 2 * p.I)), _arg(hg, "hg", _BF16, (rows, p.I)),
+        _arg(dxg, "dxg", _BF16, (rows, p.H)), _arg(dw13, "dw13", dt, (n, 2 * p.I, p.H)),
+        _arg(dw2, "dw2", dt, (n, p.H, p.I)), _FLOAT_DTYPES[dt], int(bool(accumulate)), _ptr(err_flag),
+        _stream(stream)), "moe_grouped_ffn_backward")
+
+
+def moe_permute_backward(p: Problem, dxg, row_of, dx, stream=None) -> None:
+    """Gradient of the dispatch: dx [T, H] = the sum of a token's rows of dxg."""
+    rows, _ = _train_sizes(p)
+    _check(lib().moe_permute_backward(
+        ctypes.byref(p), _arg(dxg, "dxg", _BF16, (rows, p.H)),
+        _arg(row_of, "row_of", _I32, (p.T, p.K + p.has_shared)), _arg(dx, "dx", _BF16, (p.T, p.H)), _stream(stream)),
+        "moe_permute_backward")
+
+
+def moe_route_backward(p: Problem, score: str, logits, ids, w, dw, dlogits, add=None, renormalize=True,
+                       scale: float = 1.0, stream=None) -> None:
+    """Gradient of the router's weights (moe.h): score "softmax" (moe_route_topk; logits may be None) or "sigmoid"
+    (moe_route_grouped_topk; w may be None).  add [T, E]: added to the result; dlogits may be add."""
+    _check(lib().moe_route_backward(
+        ctypes.byref(p), SCORES[score], _arg(logits, "logits", _F32, (p.T, p.E)), _arg(ids, "ids", _I32, (p.T, p.K)),
+        _arg(w, "w", _F32, (p.T, p.K)), _arg(dw, "dw", _F32, (p.T, p.K)), int(bool(renormalize)), float(scale),
+        _arg(add, "add", _F32, (p.T, p.E)), _arg(dlogits, "dlogits", _F32, (p.T, p.E)), _stream(stream)),
+        "moe_route_backward")
 
 
 def moe_eplb_record(p: Problem, masked_m, pass_index: int, window: int, load_window, stream=None) -> None:

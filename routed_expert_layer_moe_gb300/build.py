@@ -16,7 +16,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe_gb300.so")
 SOURCES = ["api.cu", "route.cu", "permute.cu", "permute_static.cu", "gemm_tc.cu", "combine.cu", "eplb.cu",
-           "gemm_mx.cu", "mx.cu", "balance.cu", "norm.cu"]
+           "gemm_mx.cu", "mx.cu", "balance.cu", "norm.cu", "fp8.cu", "gemm_train.cu", "gradient.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

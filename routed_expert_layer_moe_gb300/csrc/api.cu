@@ -461,6 +461,109 @@ moe_status moe_block_norm_backward(int32_t dtype, int32_t T, int32_t H, const vo
   return launched(launch_block_norm_backward(n, dw_post, dw_pre, (cudaStream_t)stream));
 }
 
+static int check_fp8(int32_t dtype, int64_t rows, int64_t cols, const void* values, const void* codes,
+                     const void* scales) {
+  // groups of all rows, a warp each, and the values' index
+  if (!float_dtype(dtype) || rows < 0 || cols < 0 || rows > (1LL << 33) || cols > (1LL << 33) ||
+      (cols > 0 && rows > (1LL << 40) / cols) || rows * ((cols + 127) / 128) > (1LL << 33))
+    return MOE_ERR_INVALID;
+  if (rows == 0 || cols == 0) return MOE_OK;
+  if (!values || !codes || !scales) return MOE_ERR_INVALID;
+  if (!aligned_to(dtype, values) || !aligned4(scales)) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status moe_fp8_quantize(int32_t dtype, int64_t rows, int64_t cols, const void* x, uint8_t* codes, float* scales,
+                            moe_stream_t stream) {
+  const int r = check_fp8(dtype, rows, cols, x, codes, scales);
+  if (r) return (moe_status)r;
+  return launched(launch_fp8_quantize(dtype, rows, cols, x, codes, scales, (cudaStream_t)stream));
+}
+
+moe_status moe_fp8_dequantize(int32_t dtype, int64_t rows, int64_t cols, const uint8_t* codes, const float* scales,
+                              void* out, moe_stream_t stream) {
+  const int r = check_fp8(dtype, rows, cols, out, codes, scales);
+  if (r) return (moe_status)r;
+  return launched(launch_fp8_dequantize(dtype, rows, cols, codes, scales, out, (cudaStream_t)stream));
+}
+
+// The experts that can be trained: bf16, and rows of weights that the copies' 32-bit coordinates reach.
+static int check_training(const moe_problem* p) {
+  const int r = check_problem(p);
+  if (r) return r;
+  if (p->wt != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if ((int64_t)(p->P + p->has_shared) * std::max<int64_t>(2 * (int64_t)p->I, p->H) >= (1LL << 31))
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status moe_grouped_swiglu_gemm_save(const moe_problem* p, const void* xg, const void* w13, const int32_t* masked_m,
+                                        const int32_t* offsets, void* hg, uint8_t* gu, float* gu_scales,
+                                        int32_t* err_flag, moe_stream_t stream) {
+  const int r = check_training(p);
+  if (r) return (moe_status)r;
+  if (grouped_rows(*p) == 0) return MOE_OK;
+  if (!xg || !w13 || !masked_m || !offsets || !hg || !gu || !gu_scales || !err_flag) return MOE_ERR_INVALID;
+  if (!aligned16(xg) || !aligned16(w13) || !aligned16(hg) || !aligned16(gu) || !aligned4(gu_scales))
+    return MOE_ERR_UNSUPPORTED;
+  return launched(launch_swiglu_save(*p, xg, w13, masked_m, offsets, hg, gu, gu_scales, err_flag, (cudaStream_t)stream));
+}
+
+moe_status moe_combine_backward(const moe_problem* p, const void* dout, const void* yg, const int32_t* row_of,
+                                const float* w, void* dyg, float* wg, float* dw, moe_stream_t stream) {
+  const int r = check_training(p);
+  if (r) return (moe_status)r;
+  if (p->T == 0) return MOE_OK;
+  if (!dout || !row_of || !w || !dyg || !wg || (dw && !yg)) return MOE_ERR_INVALID;
+  if (!aligned16(dout) || !aligned16(yg) || !aligned16(dyg)) return MOE_ERR_UNSUPPORTED;
+  return launched(launch_combine_backward(*p, dout, yg, row_of, w, dyg, wg, dw, (cudaStream_t)stream));
+}
+
+moe_status moe_grouped_ffn_backward(const moe_problem* p, const void* dyg, const float* wg, const void* xg,
+                                    const void* w13, const void* w2, const uint8_t* gu, const float* gu_scales,
+                                    const int32_t* masked_m, const int32_t* offsets, void* dgu, void* hg, void* dxg, void* dw13, void* dw2,
+                                    int32_t dw_dtype, int32_t accumulate, int32_t* err_flag, moe_stream_t stream) {
+  const int r = check_training(p);
+  if (r) return (moe_status)r;
+  if (!float_dtype(dw_dtype)) return MOE_ERR_INVALID;
+  if (accumulate && dw_dtype != MOE_F32) return MOE_ERR_UNSUPPORTED;
+  if (grouped_rows(*p) > 0) {
+    if (!dyg || !w2 || !gu || !gu_scales || !masked_m || !offsets || !dgu || !hg || !err_flag) return MOE_ERR_INVALID;
+    if ((dxg && !w13) || (dw13 && !xg)) return MOE_ERR_INVALID;
+  }
+  for (const void* q : {dyg, xg, w13, w2, (const void*)gu, (const void*)dgu, (const void*)hg, (const void*)dxg,
+                        (const void*)dw13, (const void*)dw2})
+    if (!aligned16(q)) return MOE_ERR_UNSUPPORTED;
+  if (!aligned4(wg) || !aligned4(gu_scales)) return MOE_ERR_UNSUPPORTED;
+  FfnBackwardArgs a{};
+  a.dyg = dyg, a.wg = wg, a.xg = xg, a.w13 = w13, a.w2 = w2, a.gu = gu, a.gu_scales = gu_scales;
+  a.masked_m = masked_m, a.offsets = offsets, a.dgu = dgu, a.hg = hg, a.dxg = dxg, a.dw13 = dw13, a.dw2 = dw2;
+  a.dw_dtype = dw_dtype, a.accumulate = accumulate != 0, a.err = err_flag;
+  return launched(launch_ffn_backward(*p, a, (cudaStream_t)stream));
+}
+
+moe_status moe_permute_backward(const moe_problem* p, const void* dxg, const int32_t* row_of, void* dx,
+                                moe_stream_t stream) {
+  const int r = check_training(p);
+  if (r) return (moe_status)r;
+  if (p->T == 0) return MOE_OK;
+  if (!dxg || !row_of || !dx) return MOE_ERR_INVALID;
+  if (!aligned16(dxg) || !aligned16(dx)) return MOE_ERR_UNSUPPORTED;
+  return launched(launch_combine(*p, dxg, row_of, nullptr, dx, (cudaStream_t)stream));
+}
+
+moe_status moe_route_backward(const moe_problem* p, int32_t score, const float* logits, const int32_t* ids,
+                              const float* w, const float* dw, int32_t renormalize, float scale, const float* add,
+                              float* dlogits, moe_stream_t stream) {
+  const int r = check_problem(p);
+  if (r) return (moe_status)r;
+  if (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID) return MOE_ERR_INVALID;
+  if (p->T == 0) return MOE_OK;
+  if (!ids || !dw || !dlogits || (score == MOE_SCORE_SOFTMAX ? !w : !logits)) return MOE_ERR_INVALID;
+  return launched(launch_route_backward(*p, score, logits, ids, w, dw, renormalize != 0, scale, add, dlogits,
+                                        (cudaStream_t)stream));
+}
+
 moe_status moe_selftest_bounded_wait(int64_t cycles, int32_t* err_flag, moe_stream_t stream) {
   if (!err_flag || cycles < 1 || cycles > 4000000000LL) return MOE_ERR_INVALID;
   return launched(launch_bounded_wait_selftest((long long)cycles, err_flag, (cudaStream_t)stream));

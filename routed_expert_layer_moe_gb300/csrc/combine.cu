@@ -23,7 +23,7 @@ __global__ void __launch_bounds__(128) combine_kernel(const TY* __restrict__ yg,
   __shared__ float wts[kMaxKS];
   if (threadIdx.x < KS) {
     rows[threadIdx.x] = row_of[(size_t)t * KS + threadIdx.x];
-    wts[threadIdx.x] = (threadIdx.x < K) ? w[(size_t)t * K + threadIdx.x] : 1.0f;
+    wts[threadIdx.x] = (w && threadIdx.x < K) ? w[(size_t)t * K + threadIdx.x] : 1.0f;
   }
   __syncthreads();
   if (c0 >= H) return;

@@ -85,6 +85,7 @@ int launch_eplb_record(const moe_problem& p, const int32_t* masked_m, int64_t pa
 int launch_eplb_rebalance(const moe_problem& p, const int32_t* load_window, int window, const int32_t* p2l,
                           int64_t* logical_load, int32_t* new_p2l, int32_t* err, cudaStream_t st);
 int launch_bounded_wait_selftest(long long cycles, int32_t* err, cudaStream_t st);
+// w null: every record has weight 1.
 int launch_combine(const moe_problem& p, const void* yg, const int32_t* row_of, const float* w, void* out,
                    cudaStream_t st);
 
@@ -140,6 +141,32 @@ struct NormArgs {
 size_t block_norm_workspace_bytes(int T, int H);
 int launch_block_norm(const NormArgs& n, cudaStream_t st);
 int launch_block_norm_backward(const NormArgs& n, float* dw_post, float* dw_pre, cudaStream_t st);
+
+int launch_fp8_quantize(int dtype, int64_t rows, int64_t cols, const void* x, uint8_t* codes, float* scales,
+                        cudaStream_t st);
+int launch_fp8_dequantize(int dtype, int64_t rows, int64_t cols, const uint8_t* codes, const float* scales, void* out,
+                          cudaStream_t st);
+
+// Training of the experts (gemm_train.cu) and the gradients around them (gradient.cu).
+int launch_swiglu_save(const moe_problem& p, const void* xg, const void* w13, const int32_t* masked_m,
+                       const int32_t* offsets, void* hg, uint8_t* gu, float* gu_scales, int32_t* err, cudaStream_t st);
+struct FfnBackwardArgs {
+  const void* dyg;
+  const float* wg;
+  const void *xg, *w13, *w2;
+  const uint8_t* gu;
+  const float* gu_scales;
+  const int32_t *masked_m, *offsets;
+  void *dgu, *hg, *dxg, *dw13, *dw2;  // dxg, dw13, dw2: null where they are not wanted
+  int dw_dtype, accumulate;
+  int32_t* err;
+};
+int launch_ffn_backward(const moe_problem& p, const FfnBackwardArgs& a, cudaStream_t st);
+int launch_combine_backward(const moe_problem& p, const void* dout, const void* yg, const int32_t* row_of,
+                            const float* w, void* dyg, float* wg, float* dw, cudaStream_t st);
+int launch_route_backward(const moe_problem& p, int score, const float* logits, const int32_t* ids, const float* w,
+                          const float* dw, int renorm, float scale, const float* add, float* dlogits,
+                          cudaStream_t st);
 
 enum { MODE_SWIGLU = 0, MODE_DOWN = 1 };
 

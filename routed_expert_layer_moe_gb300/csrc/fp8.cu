@@ -1,0 +1,198 @@
+// Activation checkpoints in 8 bits: rows of E4M3 codes with one fp32 scale per 128 values, and back.
+//
+//   s = max |x| * fp32(1 / 448) over the group,  code = E4M3(x / s),  value = code * s
+//
+// The code is that of the exact quotient.  x * (1 / s) is within two units in the last place of it, so only a product
+// that close to the middle between two codes (whose low 19 mantissa bits are zero) can round to the wrong one: about
+// one in 2^16 takes the slow way, the IEEE quotient and the sign of its remainder.  A division for every value would
+// cost more than the memory does.
+#include "fp8.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+
+__device__ __noinline__ float exact_quotient(float x, float s) {
+  const float q = __fdiv_rn(x, s);
+  const uint32_t b = __float_as_uint(q);
+  if ((b & 0x7FFFFu) || (b & 0x7FFFFFFFu) < 0x3A800000u) return q;  // no middle of two codes (the least is 2^-10)
+  const double r = (double)x - (double)q * (double)s;               // exact: 24 x 24 bits
+  if (r == 0.0) return q;
+  return __uint_as_float((r > 0.0) == (q > 0.0f) ? b + 1u : b - 1u);  // one step to the side of the exact quotient
+}
+
+// A number with the exact quotient's E4M3 code.  inv = 1 / s, or 0 where that overflows or loses bits.
+__device__ __forceinline__ float quotient(float x, float s, float inv) {
+  const float q = x * inv;
+  const bool near_middle = ((__float_as_uint(q) + 4u) & 0x7FFFFu) < 8u && fabsf(q) > 0x1p-11f;
+  return near_middle || inv == 0.0f ? exact_quotient(x, s) : q;
+}
+
+__device__ __forceinline__ float inverse(float s) {
+  return s > 0x1p-100f && s < 0x1p100f ? __frcp_rn(s) : 0.0f;
+}
+
+template <typename T>
+__device__ __forceinline__ void load8(const T* x, float (&v)[8]) {
+  if constexpr (sizeof(T) == 4) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(x)), b = __ldg(reinterpret_cast<const float4*>(x) + 1);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  } else {
+    const uint4 raw = __ldg(reinterpret_cast<const uint4*>(x));
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&raw);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __bfloat1622float2(h[i]);
+      v[2 * i] = f.x, v[2 * i + 1] = f.y;
+    }
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ T to_type(float v) {
+  if constexpr (sizeof(T) == 4)
+    return v;
+  else
+    return __float2bfloat16_rn(v);
+}
+
+// Rows of whole groups, 16-byte aligned: the groups of all rows lie one after the other.  Eight values a thread,
+// 16 threads a group; n8 is a multiple of 16, so a group's threads are all in range or all out of it.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) quantize_kernel(const T* __restrict__ x, long long n8,
+                                                            uint8_t* __restrict__ codes, float* __restrict__ scales) {
+  const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
+  float v[8], amax = 0.0f;
+  if (i < n8) {
+    load8(x + 8 * i, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) amax = fp8_amax(amax, v[j]);
+  }
+#pragma unroll
+  for (int off = 8; off > 0; off >>= 1) amax = fp8_amax(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+  if (i >= n8) return;
+  const float s = fp8_scale(amax), inv = inverse(s);
+  uint2 c = make_uint2(0u, 0u);
+  if (s == s) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = quotient(v[j], s, inv);
+    c.x = fp8_pair(v[0], v[1]) | fp8_pair(v[2], v[3]) << 16;
+    c.y = fp8_pair(v[4], v[5]) | fp8_pair(v[6], v[7]) << 16;
+  }
+  reinterpret_cast<uint2*>(codes)[i] = c;
+  if ((i & 15) == 0) scales[i >> 4] = s;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) dequantize_kernel(const uint8_t* __restrict__ codes,
+                                                              const float* __restrict__ scales, long long n8,
+                                                              T* __restrict__ out) {
+  const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
+  if (i >= n8) return;
+  const uint2 c = __ldg(reinterpret_cast<const uint2*>(codes) + i);
+  const float s = __ldg(scales + (i >> 4));
+  float v[8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 f = fp8_unpair((j < 2 ? c.x : c.y) >> (16 * (j & 1)));
+    v[2 * j] = f.x * s, v[2 * j + 1] = f.y * s;
+  }
+  if constexpr (sizeof(T) == 4) {
+    reinterpret_cast<float4*>(out)[2 * i] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(out)[2 * i + 1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    uint4 raw;
+    __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&raw);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) h[j] = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+    reinterpret_cast<uint4*>(out)[i] = raw;
+  }
+}
+
+// Rows of any length and alignment: a warp per group, four values a lane, 32 apart.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) quantize_any_kernel(const T* __restrict__ x, long long groups, int per_row,
+                                                                long long cols, uint8_t* __restrict__ codes,
+                                                                float* __restrict__ scales) {
+  const long long gr = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  if (gr >= groups) return;
+  const int lane = threadIdx.x & 31;
+  const long long row = gr / per_row, col = (gr - row * per_row) * FP8_GROUP;
+  const int n = (int)min((long long)FP8_GROUP, cols - col);
+  const long long at = row * cols + col;
+  float v[4], amax = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v[j] = lane + 32 * j < n ? (float)x[at + lane + 32 * j] : 0.0f;
+    amax = fp8_amax(amax, v[j]);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) amax = fp8_amax(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+  const float s = fp8_scale(amax), inv = inverse(s);
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (lane + 32 * j < n)
+      codes[at + lane + 32 * j] = s == s ? (uint8_t)fp8_pair(quotient(v[j], s, inv), 0.0f) : (uint8_t)0;
+  if (lane == 0) scales[gr] = s;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) dequantize_any_kernel(const uint8_t* __restrict__ codes,
+                                                                  const float* __restrict__ scales, long long groups,
+                                                                  int per_row, long long cols, T* __restrict__ out) {
+  const long long gr = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  if (gr >= groups) return;
+  const int lane = threadIdx.x & 31;
+  const long long row = gr / per_row, col = (gr - row * per_row) * FP8_GROUP;
+  const int n = (int)min((long long)FP8_GROUP, cols - col);
+  const long long at = row * cols + col;
+  const float s = __ldg(scales + gr);
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (lane + 32 * j < n) out[at + lane + 32 * j] = to_type<T>(fp8_unpair(codes[at + lane + 32 * j]).x * s);
+}
+
+template <typename T>
+int quantize(int64_t rows, int64_t cols, const T* x, uint8_t* codes, float* scales, cudaStream_t st) {
+  if (cols % FP8_GROUP == 0 && aligned16(x) && (reinterpret_cast<uintptr_t>(codes) & 7u) == 0) {
+    const long long n8 = rows * cols / 8;
+    quantize_kernel<<<(unsigned)((n8 + kThreads - 1) / kThreads), kThreads, 0, st>>>(x, n8, codes, scales);
+  } else {
+    const long long per_row = (cols + FP8_GROUP - 1) / FP8_GROUP, groups = rows * per_row;
+    quantize_any_kernel<<<(unsigned)((groups + kThreads / 32 - 1) / (kThreads / 32)), kThreads, 0, st>>>(
+        x, groups, (int)per_row, cols, codes, scales);
+  }
+  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+template <typename T>
+int dequantize(int64_t rows, int64_t cols, const uint8_t* codes, const float* scales, T* out, cudaStream_t st) {
+  if (cols % FP8_GROUP == 0 && aligned16(out) && (reinterpret_cast<uintptr_t>(codes) & 7u) == 0) {
+    const long long n8 = rows * cols / 8;
+    dequantize_kernel<<<(unsigned)((n8 + kThreads - 1) / kThreads), kThreads, 0, st>>>(codes, scales, n8, out);
+  } else {
+    const long long per_row = (cols + FP8_GROUP - 1) / FP8_GROUP, groups = rows * per_row;
+    dequantize_any_kernel<<<(unsigned)((groups + kThreads / 32 - 1) / (kThreads / 32)), kThreads, 0, st>>>(
+        codes, scales, groups, (int)per_row, cols, out);
+  }
+  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+}  // namespace
+
+int launch_fp8_quantize(int dtype, int64_t rows, int64_t cols, const void* x, uint8_t* codes, float* scales,
+                        cudaStream_t st) {
+  if (rows == 0 || cols == 0) return MOE_OK;
+  return dtype == MOE_F32 ? quantize(rows, cols, static_cast<const float*>(x), codes, scales, st)
+                          : quantize(rows, cols, static_cast<const __nv_bfloat16*>(x), codes, scales, st);
+}
+
+int launch_fp8_dequantize(int dtype, int64_t rows, int64_t cols, const uint8_t* codes, const float* scales, void* out,
+                          cudaStream_t st) {
+  if (rows == 0 || cols == 0) return MOE_OK;
+  return dtype == MOE_F32 ? dequantize(rows, cols, codes, scales, static_cast<float*>(out), st)
+                          : dequantize(rows, cols, codes, scales, static_cast<__nv_bfloat16*>(out), st);
+}
+
+}  // namespace moe

@@ -1,0 +1,818 @@
+// The products that train the experts (bf16), grouped by expert over ragged row counts.
+//
+//   UP   g, u = xg W13^T                 h = silu(g) u; g and u kept in 8 bits (e4m3, a scale per 128)
+//   DH   dh = w dyg W2                   dg = dh u s (1 + g (1 - s)), du = dh g s, w h = w g s u, s = sigmoid(g),
+//                                        with g and u as the checkpoint holds them, w the row's weight
+//   DX   dxg = dgu W13
+//   WG   dW[m][n] = sum over the rows of a slot of a[row][m] b[row][n]     (dW13 = dgu^T xg, dW2 = dyg^T (w h))
+//
+// One kernel form for all four: clusters of two CTAs (SM pairs) whose tensor cores work on one tile of 256 x 256
+// fp32 accumulators (cta_group::2, M = 256), each CTA staging 128 rows of either operand per 64 values of the reduced
+// dimension: 32 KB a stage for 256 x 256 x 64 multiply-adds a pair.  Persistent; two accumulators in tensor
+// memory, so a tile's epilogue runs beside the next tile's products.
+//
+// Every operand is read in the order it is stored, by TMA with the 128-byte swizzle:
+//   * reduced dimension contiguous (xg, dyg, dgu, and W13 in UP): a stage is rows of 64 values, K-major.
+//   * reduced dimension the outer one (W2 in DH, W13 in DX, both operands of WG): a stage is 64 rows of k with 64
+//     columns in each of two boxes, MN-major; the tensor core transposes.
+// So no weight is kept twice, and no operand is transposed in memory.
+//
+// Ragged rows.  Where the rows are the M side (UP, DH, DX), a chunk of up to 256 rows loads whole boxes: rows behind a
+// slot's last one give accumulator rows that are not stored.  Where they are the reduced dimension (WG), the last 64 of
+// a slot may hold rows of the next one, or padding, which may be NaN: MMAs of K = 16 stop behind the last row, and a
+// warp writes zeros over the up to 15 rows between in shared memory, of both operands.
+//
+// Roles of a CTA: warp 0 TMA producer, warp 1 MMAs (leader CTA), warp 2 the zeros of WG, warps 4-11 epilogue.  Every
+// wait is bounded; on expiry the CTA drains its copies and MMAs, frees tensor memory, reports MOE_FLAG_TIMEOUT and
+// returns.
+#include <algorithm>
+
+#include "fp8.cuh"
+
+namespace moe {
+namespace {
+
+enum { UP = 0, DH = 1, DX = 2, WG = 3 };
+
+constexpr int KB = 64;                    // reduced values of a stage: 128 bytes of a K-major row
+constexpr int HALF = 128;                 // rows of an operand that one CTA stages
+constexpr int OP_BYTES = HALF * KB * 2;   // one operand of a stage
+constexpr int BOX_BYTES = OP_BYTES / 2;   // MN-major: 64 k rows of 64 columns
+constexpr int STAGE = 2 * OP_BYTES;
+constexpr int MAX_STAGES = 6;
+constexpr int THREADS = 384;
+constexpr int EPI_WARP0 = 4, EPI_WARPS = 8;
+constexpr int EPI_BUF = 2048;             // 32 rows of 64 bytes a warp
+constexpr uint32_t TMEM_COLS = 512, ACC_COLS = 256;
+constexpr int GROUP_M = 8;                // M tiles that neighbouring units share an N tile with
+constexpr long long TIMEOUT = 4000000000LL;  // SM cycles, about 2 s
+constexpr int NUM_BOXES = 3;              // row boxes of 32, 64 and 128
+__host__ __device__ constexpr int box_rows(int i) { return 32 << i; }
+__host__ __device__ constexpr int box_of(int rows) { return rows <= 32 ? 0 : rows <= 64 ? 1 : 2; }
+
+struct Maps {
+  CUtensorMap a[NUM_BOXES];  // WG: the first alone
+  CUtensorMap b;
+};
+
+struct Params {
+  int nslots, masked, M_max;
+  long long rows_total;
+  int kb;            // stages of the reduced dimension (WG: by the slot's rows)
+  int mt, nt;        // WG: M tiles; N tiles
+  int b_rows;        // rows of one slot in the weights
+  int ncols;         // columns of the output: UP, DH: I; DX: H; WG: N
+  int m_rows;        // WG: rows of the output a slot
+  int stages;
+  int accumulate;    // WG, fp32: add to what is there
+  const int32_t* masked_m;
+  const int32_t* offsets;
+  void* out;         // UP, DH: h (DH: times w) bf16 [rows][I]; DX: dxg bf16 [rows][H]; WG: dW [slots][m_rows][N]
+  void* out2;        // UP: codes [rows][2 I]; DH: dgu bf16 [rows][2 I]
+  float* out2_s;     // UP: scales [rows][2 I / 128]
+  const uint8_t* gu;   // DH: codes and scales of the checkpoint
+  const float* gu_s;
+  const float* wg;     // DH: weights of the rows, or null
+  int32_t* err;
+  uint32_t epi_off, ex_off, pre_off, bar_off, misc_off;
+};
+
+struct Unit {
+  int slot, mi, j;   // slot, M tile (WG) or chunk, N tile
+  int row;           // UP, DH, DX: first row of this CTA's part of the chunk; WG: first row of the slot
+  int nvalid, most;  // rows of this CTA's part, the larger of the pair's parts; WG: rows of the slot, both
+  int kb;            // stages
+};
+
+template <int MODE>
+__device__ __forceinline__ Unit decode(const Params& p, const int* prefix, const int* srows, const int* sbase, int u,
+                                       uint32_t rank) {
+  int lo = 0, hi = p.nslots;  // prefix[lo] <= u < prefix[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (prefix[mid] <= u)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  Unit U;
+  U.slot = lo;
+  const int r = u - prefix[lo], m = srows[lo];
+  const int nm = MODE == WG ? p.mt : (m + 2 * HALF - 1) / (2 * HALF);
+  // groups of GROUP_M tiles of M, the M tile the fastest within one: a wave of pairs shares operands through L2
+  const int g = r / (GROUP_M * p.nt), first = g * GROUP_M;
+  const int size = min(GROUP_M, nm - first), rr = r - first * p.nt;
+  U.mi = first + rr % size;
+  U.j = rr / size;
+  if constexpr (MODE == WG) {
+    U.row = sbase[lo];
+    U.nvalid = U.most = m;
+    U.kb = (m + KB - 1) / KB;
+  } else {
+    const int base = m / nm, extra = m - base * nm;  // near-equal chunks
+    const int n = base + (U.mi < extra ? 1 : 0), n0 = (n + 1) >> 1;
+    U.row = sbase[lo] + U.mi * base + min(U.mi, extra) + (rank ? n0 : 0);
+    U.nvalid = rank ? n - n0 : n0;
+    U.most = n0;
+    U.kb = p.kb;
+  }
+  return U;
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n"
+      "  .reg .pred p;\n"
+      "  elect.sync _|p, 0xffffffff;\n"
+      "  selp.u32 %0, 1, 0, p;\n"
+      "}\n"
+      : "=r"(one));
+  return one;
+}
+
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n"
+      "  .reg .pred p;\n"
+      "  setp.ne.b32 p, %4, 0;\n"
+      "  tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n"
+      "}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Arrival on an mbarrier of the cluster that other CTAs' reads of this CTA's shared memory are ordered by.
+__device__ __forceinline__ void arrive_cluster(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// Shared-memory matrix descriptor of an MN-major tile: boxes of 64 k rows x 128 bytes (64 columns) written with the
+// 128-byte swizzle.  Eight k rows are 1024 bytes (stride byte offset), the next 64 columns a box further (leading one).
+__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(BOX_BYTES >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+
+template <int MODE>
+__device__ constexpr uint32_t instruction_desc() {
+  uint32_t d = mma_idesc<false>(2 * HALF, 2 * HALF);
+  if (MODE == WG) d |= 1u << 15;              // A: MN-major
+  if (MODE != UP) d |= 1u << 16;              // B: MN-major
+  return d;
+}
+
+__device__ __forceinline__ void tmem_load32(uint32_t taddr, float (&v)[32]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
+                 "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+               : "r"(taddr)
+               : "memory");
+}
+
+// Wait for this thread's loads from tensor memory; v is what one of them wrote.
+__device__ __forceinline__ void tmem_loaded32(float (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]),
+                 "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])
+               :
+               : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// 64 bytes of each lane's row to global memory, through the warp's shared buffer so that four lanes write a row's 64
+// bytes together: dst is the first row's address, `rows` of the 32 are written.  ADD: added to the fp32 values there.
+template <bool ADD = false>
+__device__ __forceinline__ void store_rows(uint8_t* buf, int lane, const uint32_t (&v)[16], uint8_t* dst,
+                                           size_t stride, int rows) {
+  __syncwarp();  // the buffer's last use has been read
+#pragma unroll
+  for (int c = 0; c < 4; ++c)  // 16-byte pieces in an order that keeps eight lanes on different banks
+    *reinterpret_cast<uint4*>(buf + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) =
+        make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 8 * i + (lane >> 2), c = lane & 3;
+    if (r < rows) {
+      uint4 x = *reinterpret_cast<const uint4*>(buf + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+      uint4* at = reinterpret_cast<uint4*>(dst + (size_t)r * stride + 16 * c);
+      if constexpr (ADD) {
+        const uint4 y = *at;
+        x.x = __float_as_uint(__uint_as_float(x.x) + __uint_as_float(y.x));
+        x.y = __float_as_uint(__uint_as_float(x.y) + __uint_as_float(y.y));
+        x.z = __float_as_uint(__uint_as_float(x.z) + __uint_as_float(y.z));
+        x.w = __float_as_uint(__uint_as_float(x.w) + __uint_as_float(y.w));
+      }
+      *at = x;
+    }
+  }
+}
+
+// The epilogue of one tile, warp `ew` of the eight: lanes 32 (ew & 3) .. of the CTA's 128 accumulator rows, columns
+// 128 (ew >> 2) .. of its 256 (UP: 64 of the gate's and the same 64 of the up's).  acc: the warp's lanes and the
+// tile's first column; `zero`: there is no accumulator, the tile is zeros (WG without rows).
+template <int MODE, typename OUT>
+__device__ __forceinline__ void epilogue(const Params& p, const Unit& U, uint32_t rank, int ew, int lane, uint32_t acc,
+                                         uint8_t* buf, float* ex, bool zero) {
+  const int quad = ew & 3, half = ew >> 2;
+  const int r0 = 32 * quad;                    // the warp's first row in the CTA's 128
+  if constexpr (MODE == UP) {
+    const size_t row0 = (size_t)U.row + r0, row = row0 + lane;
+    const int rows = min(32, U.nvalid - r0), I = p.ncols, c0 = U.j * HALF + 64 * half;
+    float g[32], u[32];
+    float ag = 0.0f, au = 0.0f;
+#pragma unroll
+    for (int c = 0; c < 64; c += 32) {
+      tmem_load32(acc + 64 * half + c, g);
+      tmem_load32(acc + HALF + 64 * half + c, u);
+      tmem_loaded32(g);
+      tmem_loaded32(u);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) ag = fp8_amax(ag, g[i]), au = fp8_amax(au, u[i]);
+    }
+    // a group's other 64 columns are with the warp of the same rows in the other half
+    float2* mine = reinterpret_cast<float2*>(ex) + (half * HALF + r0 + lane);
+    *mine = make_float2(ag, au);
+    asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory");
+    const float2 other = reinterpret_cast<float2*>(ex)[(half ^ 1) * HALF + r0 + lane];
+    const float sg = fp8_scale(fp8_amax(ag, other.x)), su = fp8_scale(fp8_amax(au, other.y));
+    // one division a group; the codes' inputs are fp32 sums, so a reciprocal's last bit is within their own error
+    const float ig = sg == sg ? 1.0f / sg : 0.0f, iu = su == su ? 1.0f / su : 0.0f;
+    if (half == 0 && lane < rows) {
+      p.out2_s[row * (2 * I / FP8_GROUP) + U.j] = sg;
+      p.out2_s[row * (2 * I / FP8_GROUP) + I / FP8_GROUP + U.j] = su;
+    }
+#pragma unroll
+    for (int c = 0; c < 64; c += 32) {
+      tmem_load32(acc + 64 * half + c, g);
+      tmem_load32(acc + HALF + 64 * half + c, u);
+      tmem_loaded32(g);
+      tmem_loaded32(u);
+      uint32_t v[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = pack2(silu(g[2 * i]) * u[2 * i], silu(g[2 * i + 1]) * u[2 * i + 1]);
+      store_rows(buf, lane, v, static_cast<uint8_t*>(p.out) + (row0 * I + c0 + c) * 2, (size_t)I * 2, rows);
+      if (lane < rows) {
+        uint8_t* code = static_cast<uint8_t*>(p.out2) + row * 2 * I + c0 + c;
+        const bool bad_g = sg != sg, bad_u = su != su;
+        uint32_t q[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          q[i] = bad_g ? 0u : fp8_pair(g[4 * i] * ig, g[4 * i + 1] * ig) | fp8_pair(g[4 * i + 2] * ig, g[4 * i + 3] * ig) << 16;
+        reinterpret_cast<uint4*>(code)[0] = make_uint4(q[0], q[1], q[2], q[3]);
+        reinterpret_cast<uint4*>(code)[1] = make_uint4(q[4], q[5], q[6], q[7]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          q[i] = bad_u ? 0u : fp8_pair(u[4 * i] * iu, u[4 * i + 1] * iu) | fp8_pair(u[4 * i + 2] * iu, u[4 * i + 3] * iu) << 16;
+        reinterpret_cast<uint4*>(code + I)[0] = make_uint4(q[0], q[1], q[2], q[3]);
+        reinterpret_cast<uint4*>(code + I)[1] = make_uint4(q[4], q[5], q[6], q[7]);
+      }
+    }
+  } else if constexpr (MODE == DH) {
+    const size_t row0 = (size_t)U.row + r0, row = row0 + lane;
+    const int rows = min(32, U.nvalid - r0), I = p.ncols, c0 = U.j * 2 * HALF + HALF * half;
+    if (c0 >= I || rows <= 0) return;
+    const int n = 2 * I / FP8_GROUP;
+    float sg = 0.0f, su = 0.0f, w = 1.0f;
+    if (lane < rows) {
+      if (p.wg) w = p.wg[row];
+      sg = p.gu_s[row * n + c0 / FP8_GROUP];
+      su = p.gu_s[row * n + (I + c0) / FP8_GROUP];
+    }
+#pragma unroll 1
+    for (int c = 0; c < HALF; c += 32) {
+      uint4 qg[2] = {}, qu[2] = {};
+      if (lane < rows) {
+        const uint4* code = reinterpret_cast<const uint4*>(p.gu + row * 2 * I + c0 + c);
+        qg[0] = __ldg(code), qg[1] = __ldg(code + 1);
+        code = reinterpret_cast<const uint4*>(p.gu + row * 2 * I + I + c0 + c);
+        qu[0] = __ldg(code), qu[1] = __ldg(code + 1);
+      }
+      float d[32];
+      tmem_load32(acc + HALF * half + c, d);
+      tmem_loaded32(d);
+      uint32_t vg[16], vu[16], vh[16];
+      const uint32_t* wg = reinterpret_cast<const uint32_t*>(qg);
+      const uint32_t* wu = reinterpret_cast<const uint32_t*>(qu);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float2 cg = fp8_unpair(wg[i >> 1] >> (16 * (i & 1))), cu = fp8_unpair(wu[i >> 1] >> (16 * (i & 1)));
+        float dg[2], du[2], h[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float g = (e ? cg.y : cg.x) * sg, u = (e ? cu.y : cu.x) * su, x = w * d[2 * i + e];
+          const float s = __fdividef(1.0f, 1.0f + __expf(-g));
+          const float gs = g * s;
+          h[e] = w * (gs * u);
+          du[e] = x * gs;
+          dg[e] = x * u * fmaf(gs, 1.0f - s, s);
+        }
+        vg[i] = pack2(dg[0], dg[1]);
+        vu[i] = pack2(du[0], du[1]);
+        vh[i] = pack2(h[0], h[1]);
+      }
+      uint8_t* dgu = static_cast<uint8_t*>(p.out2) + (row0 * 2 * I + c0 + c) * 2;
+      store_rows(buf, lane, vg, dgu, (size_t)I * 4, rows);
+      store_rows(buf, lane, vu, dgu + (size_t)I * 2, (size_t)I * 4, rows);
+      store_rows(buf, lane, vh, static_cast<uint8_t*>(p.out) + (row0 * I + c0 + c) * 2, (size_t)I * 2, rows);
+    }
+  } else {
+    // DX: rows of the chunk; WG: rows of the slot's gradient, whole tiles of 128
+    const int N = p.ncols, c0 = U.j * 2 * HALF + HALF * half;
+    const int rows = MODE == WG ? 32 : min(32, U.nvalid - r0);
+    const size_t row0 = MODE == WG ? (size_t)U.slot * p.m_rows + U.mi * 2 * HALF + rank * HALF + r0
+                                   : (size_t)U.row + r0;
+    if (c0 >= N || rows <= 0) return;
+    if (MODE == WG && U.mi * 2 * HALF + (int)rank * HALF >= p.m_rows) return;
+    uint8_t* dst = static_cast<uint8_t*>(p.out) + (row0 * N + c0) * sizeof(OUT);
+#pragma unroll 1
+    for (int c = 0; c < HALF; c += 32) {
+      float d[32];
+      if (zero) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) d[i] = 0.0f;
+      } else {
+        tmem_load32(acc + HALF * half + c, d);
+        tmem_loaded32(d);
+      }
+      uint32_t v[16];
+      if constexpr (sizeof(OUT) == 2) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = pack2(d[2 * i], d[2 * i + 1]);
+        store_rows(buf, lane, v, dst + c * 2, (size_t)N * 2, rows);
+      } else {
+#pragma unroll
+        for (int o = 0; o < 32; o += 16) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(d[o + i]);
+          if (p.accumulate)
+            store_rows<true>(buf, lane, v, dst + (c + o) * 4, (size_t)N * 4, rows);
+          else
+            store_rows(buf, lane, v, dst + (c + o) * 4, (size_t)N * 4, rows);
+        }
+      }
+    }
+  }
+}
+
+// Whether both warps that meet at hardware barrier `id` (64 threads) are ok.
+__device__ __forceinline__ bool both_ok(int id, bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n"
+      "  .reg .pred p, q;\n"
+      "  setp.ne.b32 q, %1, 0;\n"
+      "  bar.red.and.pred p, %2, 64, q;\n"
+      "  selp.u32 %0, 1, 0, p;\n"
+      "}\n"
+      : "=r"(r)
+      : "r"((uint32_t)ok), "r"(id)
+      : "memory");
+  return r;
+}
+
+template <int MODE, typename OUT>
+__global__ void __launch_bounds__(THREADS, 1)
+    train_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
+  float* ex = reinterpret_cast<float*>(smem + p.ex_off);   // UP: [2 tiles][2 halves][128 rows] (gate, up) magnitudes
+  int* prefix = reinterpret_cast<int*>(smem + p.pre_off);  // [nslots + 1] unit prefix
+  int* srows = prefix + p.nslots + 1;
+  int* sbase = srows + p.nslots;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + p.bar_off);
+  uint64_t* empty = full + MAX_STAGES;
+  uint64_t* landed = empty + MAX_STAGES;  // WG: this CTA's copies of a last stage that needs zeros
+  uint64_t* fixed = landed + MAX_STAGES;  // WG: both CTAs have written them
+  uint64_t* tfull = fixed + MAX_STAGES;   // [2] accumulators written
+  uint64_t* tempty = tfull + 2;           // [2] read
+  uint64_t* drain = tempty + 2;
+  uint64_t* fin = drain + 1;              // the peer CTA is done with this CTA's memory
+  uint32_t* tmem_base_smem = reinterpret_cast<uint32_t*>(smem + p.misc_off);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + p.misc_off + 4);
+
+  const int tid = threadIdx.x;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int unit0 = (int)cluster_id_x(), ustride = (int)nclusters_x();
+  const int stages = p.stages;
+
+  if (tid == 0) {
+    for (int i = 0; i < MAX_STAGES; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+      mbar_init(&landed[i], 1);
+      mbar_init(&fixed[i], 2);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&tfull[i], 1);
+      mbar_init(&tempty[i], 2 * EPI_WARPS);
+    }
+    mbar_init(drain, 1);
+    mbar_init(fin, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc<true>(tmem_base_smem, TMEM_COLS);
+    tmem_relinquish<true>();
+  }
+  // launched while the kernel before it in the stream may still run: nothing global is read or written before this
+  grid_dependency_wait();
+  grid_dependents_launch();
+  for (int s = tid; s < p.nslots; s += THREADS) {
+    long long base = p.masked ? (long long)s * p.M_max : (long long)__ldcg(p.offsets + s);
+    int m = __ldcg(p.masked_m + s);
+    if (p.masked) m = min(m, p.M_max);
+    if (base < 0 || base > p.rows_total) base = p.rows_total;  // no counts may lead outside the buffers
+    m = (int)max(0LL, min((long long)m, p.rows_total - base));
+    srows[s] = m;
+    sbase[s] = (int)base;
+    prefix[s + 1] = MODE == WG ? (m == 0 && p.accumulate ? 0 : p.mt * p.nt) : (m + 2 * HALF - 1) / (2 * HALF) * p.nt;
+  }
+  if (tid == 0) prefix[0] = 0;
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 0) {
+    int run = 0;
+    for (int base = 1; base <= p.nslots; base += 32) {
+      const int i = base + lane;
+      int v = (i <= p.nslots) ? prefix[i] : 0;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int n = __shfl_up_sync(0xffffffffu, v, off);
+        if (lane >= off) v += n;
+      }
+      if (i <= p.nslots) prefix[i] = run + v;
+      run += __shfl_sync(0xffffffffu, v, 31);
+    }
+  }
+  __syncthreads();
+  cluster_sync_all();  // both CTAs' barriers are initialised before either CTA touches the other's
+  tc_fence_after_sync();
+  const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_base_smem, 0);
+  const int total = prefix[p.nslots];
+  auto unit = [&](int u) { return decode<MODE>(p, prefix, srows, sbase, u, rank); };
+  // rows of a slot's last stage that are in its last MMA's 16 but behind the last row
+  auto ragged = [](const Unit& U) { return MODE == WG && U.kb > 0 && (U.nvalid & 15) != 0; };
+
+  if (warp == 0) {
+    // -------------------------------------------------------------- producer
+    if (lane == 0) {
+      const CUtensorMap* mb = &maps.b;
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int u = unit0; ok && u < total; u += ustride) {
+        const Unit U = unit(u);
+        const int bx = MODE == WG ? 0 : box_of(U.most);
+        const CUtensorMap* ma = &maps.a[bx];
+        const uint32_t a_bytes = MODE == WG ? OP_BYTES : (uint32_t)box_rows(bx) * KB * 2;
+        const uint32_t bytes = a_bytes + OP_BYTES;
+        const int am = MODE == WG ? U.mi * 2 * HALF + (int)rank * HALF : 0;
+        const int bn = U.j * (MODE == UP ? HALF : 2 * HALF) + (MODE == UP ? 0 : (int)rank * HALF);
+        const int brow = MODE == UP ? U.slot * p.b_rows + (int)rank * p.ncols + bn : U.slot * p.b_rows;
+        for (int kb = 0; kb < U.kb; ++kb) {
+          if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, TIMEOUT)) {
+            ok = false;
+            break;
+          }
+          uint8_t* sa = smem + (size_t)stage * STAGE;
+          uint8_t* sb = sa + OP_BYTES;
+          const int k = kb * KB;
+          if (kb == U.kb - 1 && ragged(U)) {
+            // counted on this CTA's own barrier: warp 2 has to see them land here
+            mbar_arrive_expect_tx(&landed[stage], bytes);
+            if (leader) mbar_arrive(&full[stage]);
+            for (int h = 0; h < 2; ++h) {
+              tma_load_2d(sa + h * BOX_BYTES, ma, &landed[stage], am + 64 * h, U.row + k);
+              tma_load_2d(sb + h * BOX_BYTES, mb, &landed[stage], bn + 64 * h, U.row + k);
+            }
+          } else {
+            // the leader's barrier counts both CTAs' copies
+            if (leader) mbar_arrive_expect_tx(&full[stage], 2 * bytes);
+            const uint32_t bar = mapa_shared(&full[stage], 0);
+            if constexpr (MODE == WG) {
+              for (int h = 0; h < 2; ++h) tma_load_2d_pair(sa + h * BOX_BYTES, ma, bar, am + 64 * h, U.row + k);
+            } else {
+              tma_load_2d_pair(sa, ma, bar, k, U.row);
+            }
+            if constexpr (MODE == UP) {
+              tma_load_2d_pair(sb, mb, bar, k, brow);
+            } else {
+              const int y = MODE == WG ? U.row + k : brow + k;
+              for (int h = 0; h < 2; ++h) tma_load_2d_pair(sb + h * BOX_BYTES, mb, bar, bn + 64 * h, y);
+            }
+          }
+          if (++stage == stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // -------------------------------------------------------------- MMAs: a converged warp, one elected lane
+    const uint32_t s0 = smem_u32(smem);
+    const uint64_t da0 = MODE == WG ? desc_mn(s0) : smem_desc_sw128(s0);
+    const uint64_t db0 = MODE == UP ? smem_desc_sw128(s0 + OP_BYTES) : desc_mn(s0 + OP_BYTES);
+    // 16 values of k: 32 bytes of a K-major row, 16 rows of an MN-major box
+    constexpr uint32_t STEP_A = MODE == WG ? 16 * 128 / 16 : 2, STEP_B = MODE == UP ? 2 : 16 * 128 / 16;
+    constexpr uint32_t idesc = instruction_desc<MODE>();
+    int stage = 0;
+    uint32_t phase = 0, fphase = 0, it = 0;  // fphase: a bit per stage
+    bool ok = true, any = false;
+    for (int u = unit0; ok && leader && u < total; u += ustride) {
+      const Unit U = unit(u);
+      const int nkb = __shfl_sync(0xffffffffu, U.kb, 0), rows = __shfl_sync(0xffffffffu, U.nvalid, 0);
+      if (MODE == WG && nkb == 0) continue;
+      const uint32_t d = tmem_base + (it & 1u) * ACC_COLS;
+      ok = __all_sync(0xffffffffu, mbar_wait<true>(&tempty[it & 1u], ((it >> 1) & 1u) ^ 1u, abort_flag, TIMEOUT));
+      if (!ok) break;
+      tc_fence_after_sync();
+      for (int kb = 0; kb < nkb; ++kb) {
+        ok = __all_sync(0xffffffffu, mbar_wait<true>(&full[stage], phase, abort_flag, TIMEOUT));
+        if (!ok) break;
+        int steps = KB / 16;
+        if (MODE == WG && kb == nkb - 1) {
+          steps = (rows - kb * KB + 15) / 16;
+          if (rows & 15) {
+            ok = __all_sync(0xffffffffu, mbar_wait<true>(&fixed[stage], (fphase >> stage) & 1u, abort_flag, TIMEOUT));
+            if (!ok) break;
+            fphase ^= 1u << stage;
+          }
+        }
+        tc_fence_after_sync();
+        const uint64_t da = da0 + (uint32_t)stage * (STAGE >> 4), db = db0 + (uint32_t)stage * (STAGE >> 4);
+        if (elect_one()) {
+#pragma unroll
+          for (int ks = 0; ks < KB / 16; ++ks)
+            if (MODE != WG || ks < steps) mma_pair(d, da + ks * STEP_A, db + ks * STEP_B, idesc, kb > 0 || ks > 0);
+          tc_commit_pair(&empty[stage], 3);
+        }
+        __syncwarp();
+        any = true;
+        if (++stage == stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (ok && elect_one()) tc_commit_pair(&tfull[it & 1u], 3);
+      __syncwarp();
+      ++it;
+    }
+    if (!ok && any && elect_one()) {
+      // all MMAs issued by this thread must finish before tensor memory is freed
+      tc_commit_pair(drain, 1);
+      const long long t0 = clock64();
+      while (!mbar_try_wait(drain, 0) && clock64() - t0 < TIMEOUT) {
+      }
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // -------------------------------------------------------------- WG: zeros behind a slot's last row
+    if constexpr (MODE == WG) {
+      int stage = 0;
+      uint32_t lphase = 0;
+      bool ok = true;
+      for (int u = unit0; ok && u < total; u += ustride) {
+        const Unit U = unit(u);
+        if (U.kb == 0) continue;
+        const int last = (stage + U.kb - 1) % stages;
+        if (ragged(U)) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&landed[last], (lphase >> last) & 1u, abort_flag, TIMEOUT));
+          if (!ok) break;
+          lphase ^= 1u << last;
+          const int v = U.nvalid - (U.kb - 1) * KB, n = ((v + 15) & ~15) - v;  // rows v .. v + n - 1 of the stage
+          uint8_t* at = smem + (size_t)last * STAGE + v * 128;
+          for (int i = lane; i < n * 8 * 4; i += 32)  // eight 16-byte pieces a row, four boxes
+            *reinterpret_cast<uint4*>(at + (i & 3) * BOX_BYTES + (i >> 2) * 16) = make_uint4(0u, 0u, 0u, 0u);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the tensor cores read them
+          __syncwarp();
+          if (lane == 0) arrive_cluster(mapa_shared(&fixed[last], 0));
+        }
+        stage = (stage + U.kb) % stages;
+      }
+    }
+  } else if (warp >= EPI_WARP0) {
+    // -------------------------------------------------------------- epilogue
+    const int ew = warp - EPI_WARP0;
+    uint8_t* buf = smem + p.epi_off + (size_t)ew * EPI_BUF;
+    uint32_t it = 0;
+    for (int u = unit0; u < total; u += ustride) {
+      const Unit U = unit(u);
+      if (MODE == WG && U.kb == 0) {
+        epilogue<MODE, OUT>(p, U, rank, ew, lane, 0u, buf, ex, true);
+        continue;
+      }
+      const uint32_t b = it & 1u;
+      bool ok = __all_sync(0xffffffffu, mbar_wait<true>(&tfull[b], (it >> 1) & 1u, abort_flag, TIMEOUT));
+      if constexpr (MODE == UP) ok = both_ok(1 + (ew & 3), ok);  // the two warps of a row go on or give up together
+      if (!ok) break;
+      tc_fence_after_sync();
+      const uint32_t acc = tmem_base + b * ACC_COLS + ((uint32_t)(32 * (ew & 3)) << 16);
+      epilogue<MODE, OUT>(p, U, rank, ew, lane, acc, buf, ex + b * 4 * HALF, false);
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(mapa_shared(&tempty[b], 0));
+      ++it;
+    }
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  // Neither CTA frees its tensor memory or leaves while the other may still use it: the leader's MMAs read the peer's
+  // shared memory and write its tensor memory, the peer's copies and arrivals land on the leader's barriers.
+  if (tid == 0) {
+    if (*abort_flag) {  // let copies in flight land before shared memory is released
+      const uint64_t t0 = global_timer_ns();
+      while (global_timer_ns() - t0 < 200000u) {
+      }
+    }
+    mbar_arrive_remote(mapa_shared(fin, rank ^ 1u));
+    const long long t0 = clock64();
+    while (!mbar_try_wait<true>(fin, 0)) {
+      if (clock64() - t0 > TIMEOUT) {
+        *abort_flag = 1;
+        break;
+      }
+    }
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc<true>(tmem_base, TMEM_COLS);
+  }
+  if (tid == 0 && *abort_flag) atomicOr(p.err, MOE_FLAG_TIMEOUT);
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+
+// Shared memory of a launch: as many stages as fit.
+int lay_out(Params& prm, size_t* smem) {
+  for (int st = MAX_STAGES; st >= 2; --st) {
+    size_t off = (size_t)st * STAGE;
+    auto carve = [&](size_t bytes, size_t align) {
+      off = align_up(off, align);
+      const size_t at = off;
+      off += bytes;
+      return (uint32_t)at;
+    };
+    prm.epi_off = carve((size_t)EPI_WARPS * EPI_BUF, 128);
+    prm.ex_off = carve(2 * 2 * HALF * 2 * sizeof(float), 16);
+    prm.pre_off = carve((3 * (size_t)prm.nslots + 1) * 4, 16);
+    prm.bar_off = carve((4 * MAX_STAGES + 6) * 8, 8);
+    prm.misc_off = carve(16, 16);
+    if ((int)(off + 1024) <= device_info().max_smem_optin) {
+      prm.stages = st;
+      *smem = off + 1024;
+      return MOE_OK;
+    }
+  }
+  return MOE_ERR_UNSUPPORTED;
+}
+
+void cluster_attribute(cudaLaunchAttribute* a) {
+  a->id = cudaLaunchAttributeClusterDimension;
+  a->val.clusterDim.x = 2;
+  a->val.clusterDim.y = 1;
+  a->val.clusterDim.z = 1;
+}
+
+template <int MODE, typename OUT>
+int launch(Params prm, const Maps& maps, cudaStream_t st) {
+  auto kern = train_gemm_kernel<MODE, OUT>;
+  static bool attr_set[64] = {};
+  static int clusters[64] = {};  // clusters of two that the device keeps resident at once
+  size_t smem = 0;
+  const int r = lay_out(prm, &smem);
+  if (r) return r;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64) return MOE_ERR_UNSUPPORTED;
+  if (!attr_set[dev]) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, device_info().max_smem_optin) !=
+        cudaSuccess)
+      return MOE_ERR_CUDA;
+    attr_set[dev] = true;
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  cluster_attribute(&attr[0]);
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (clusters[dev] == 0) {
+    cfg.gridDim = dim3(2 * (device_info().sm_count / 2));
+    int c = 0;
+    if (cudaOccupancyMaxActiveClusters(&c, kern, &cfg) != cudaSuccess || c <= 0) return MOE_ERR_CUDA;
+    clusters[dev] = std::min(c, device_info().sm_count / 2);
+  }
+  cfg.gridDim = dim3(2 * clusters[dev]);
+  attr[1] = overlap_attribute();
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, maps, prm) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+bool map_of(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint32_t box) {
+  return encode_tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, cols, rows, cols * 2, KB, box, base) == CUDA_SUCCESS;
+}
+
+Params common_params(const moe_problem& p, const int32_t* masked_m, const int32_t* offsets, int32_t* err) {
+  Params prm{};
+  prm.nslots = p.P + p.has_shared;
+  prm.masked = p.layout == MOE_LAYOUT_MASKED;
+  prm.M_max = p.M_max;
+  prm.rows_total = grouped_rows(p);
+  prm.masked_m = masked_m;
+  prm.offsets = offsets;
+  prm.err = err;
+  return prm;
+}
+
+// Rows of the M side [rows][K] times the weights [slots][b_rows][b_cols].
+template <int MODE>
+int launch_rows(Params prm, const void* a, int K, const void* w, int b_rows, int b_cols, int ncols, cudaStream_t st) {
+  Maps maps;
+  for (int i = 0; i < NUM_BOXES; ++i)
+    if (!map_of(&maps.a[i], a, K, (uint64_t)prm.rows_total, box_rows(i))) return MOE_ERR_CUDA;
+  if (!map_of(&maps.b, w, b_cols, (uint64_t)prm.nslots * b_rows, MODE == UP ? HALF : KB)) return MOE_ERR_CUDA;
+  prm.kb = K / KB;
+  prm.b_rows = b_rows;
+  prm.ncols = ncols;
+  prm.nt = MODE == UP ? ncols / HALF : (ncols + 2 * HALF - 1) / (2 * HALF);
+  return launch<MODE, __nv_bfloat16>(prm, maps, st);
+}
+
+// a [rows][M], b [rows][N] -> dw [slots][M][N].
+int launch_weight_grad(Params prm, const void* a, int M, const void* b, int N, void* dw, int dw_dtype, int accumulate,
+                       cudaStream_t st) {
+  Maps maps{};
+  if (!map_of(&maps.a[0], a, M, (uint64_t)prm.rows_total, KB)) return MOE_ERR_CUDA;
+  if (!map_of(&maps.b, b, N, (uint64_t)prm.rows_total, KB)) return MOE_ERR_CUDA;
+  prm.m_rows = M;
+  prm.ncols = N;
+  prm.mt = (M + 2 * HALF - 1) / (2 * HALF);
+  prm.nt = (N + 2 * HALF - 1) / (2 * HALF);
+  prm.out = dw;
+  prm.accumulate = accumulate;
+  return dw_dtype == MOE_F32 ? launch<WG, float>(prm, maps, st) : launch<WG, __nv_bfloat16>(prm, maps, st);
+}
+
+}  // namespace
+
+int launch_swiglu_save(const moe_problem& p, const void* xg, const void* w13, const int32_t* masked_m,
+                       const int32_t* offsets, void* hg, uint8_t* gu, float* gu_scales, int32_t* err,
+                       cudaStream_t st) {
+  if (grouped_rows(p) == 0) return MOE_OK;
+  Params prm = common_params(p, masked_m, offsets, err);
+  prm.out = hg;
+  prm.out2 = gu;
+  prm.out2_s = gu_scales;
+  return launch_rows<UP>(prm, xg, p.H, w13, 2 * p.I, p.H, p.I, st);
+}
+
+int launch_ffn_backward(const moe_problem& p, const FfnBackwardArgs& a, cudaStream_t st) {
+  const Params prm = common_params(p, a.masked_m, a.offsets, a.err);
+  const size_t nslots = prm.nslots, es = a.dw_dtype == MOE_F32 ? 4 : 2;
+  if (prm.rows_total == 0) {  // no rows: the weights' gradients are zeros
+    for (void* dw : {a.dw13, a.dw2}) {
+      const size_t n = nslots * p.H * p.I * (dw == a.dw13 ? 2 : 1) * es;
+      if (dw && !a.accumulate && cudaMemsetAsync(dw, 0, n, st) != cudaSuccess) return MOE_ERR_CUDA;
+    }
+    return MOE_OK;
+  }
+  Params dh = prm;
+  dh.out = a.hg;
+  dh.out2 = a.dgu;
+  dh.gu = a.gu;
+  dh.gu_s = a.gu_scales;
+  dh.wg = a.wg;
+  int r = launch_rows<DH>(dh, a.dyg, p.H, a.w2, p.H, p.I, p.I, st);
+  if (r) return r;
+  if (a.dw2) {
+    r = launch_weight_grad(prm, a.dyg, p.H, a.hg, p.I, a.dw2, a.dw_dtype, a.accumulate, st);
+    if (r) return r;
+  }
+  if (a.dw13) {
+    r = launch_weight_grad(prm, a.dgu, 2 * p.I, a.xg, p.H, a.dw13, a.dw_dtype, a.accumulate, st);
+    if (r) return r;
+  }
+  if (a.dxg) {
+    Params dx = prm;
+    dx.out = a.dxg;
+    r = launch_rows<DX>(dx, a.dgu, 2 * p.I, a.w13, 2 * p.I, p.H, p.H, st);
+  }
+  return r;
+}
+
+}  // namespace moe

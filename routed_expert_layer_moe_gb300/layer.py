@@ -21,10 +21,15 @@ class MoeLayer:
     or e2m1 weights the grouped activations xg, hg are e4m3 with 1x128 scales.
     mxfp4: uint8 codes, two to a byte, w13 [P+S, 2I, H/2], w2 [P+S, H, I/2], with a
     scale byte per 32 codes, w13_s [P+S, 2I, H/32], w2_s [P+S, H, I/32] (as
-    moe_mx_quantize writes them); xg and hg have the same form."""
+    moe_mx_quantize writes them); xg and hg have the same form.
+
+    train (bf16 experts): the buffers of a training pass too.  forward(x, logits, save=True) keeps g and u of the
+    experts in 8 bits, and backward(dout) gives the gradients of that pass.  What it reads (ids, w, row_of, masked_m,
+    offsets, xg, yg, gu, gu_s) is overwritten by the layer's next forward pass: where other passes come between a
+    forward and its gradient (micro-batches), take a MoeLayer for each, on the same weights."""
 
     def __init__(self, problem: L.Problem, act: str, wt: str, out: str, w13, w2, w13_s=None, w2_s=None,
-                 phys_to_log=None, device="cuda"):
+                 phys_to_log=None, device="cuda", train=False):
         self.p = problem
         self.act, self.wt, self.out_dt = act, wt, out
         st = L.moe_check_problem(problem)
@@ -56,6 +61,16 @@ class MoeLayer:
         self.hg_s = torch.empty((rows, p.I // group), dtype=sd, device=dev) if f8 or mx else None
         self.out = torch.empty((p.T, p.H), dtype=TORCH_DTYPE[out], device=dev)
         self.err = torch.zeros(1, **i32)
+        self.train = bool(train)
+        if train:
+            if wt != "bf16":
+                raise L.MoeError(L.MOE_ERR_UNSUPPORTED, "training of %s experts" % wt)
+            bf16 = dict(dtype=torch.bfloat16, device=dev)
+            self.gu = torch.empty((rows, 2 * p.I), dtype=torch.uint8, device=dev)
+            self.gu_s = torch.empty((rows, 2 * p.I // L.FP8_GROUP), dtype=torch.float32, device=dev)
+            self.dyg, self.dxg = (torch.empty((rows, p.H), **bf16) for _ in range(2))
+            self.dgu = torch.empty((rows, 2 * p.I), **bf16)
+            self.wg = torch.empty(rows, dtype=torch.float32, device=dev)
         nbytes = max(L.moe_workspace_bytes(p), 256)
         self.ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
 
@@ -75,6 +90,12 @@ class MoeLayer:
     def swiglu(self, stream=None):
         L.moe_grouped_swiglu_gemm(self.p, self.xg, self.xg_s, self.w13, self.w13_s, self.masked_m, self.offsets,
                                   self.hg, self.hg_s, self.err, self.ws, stream)
+
+    def swiglu_save(self, stream=None):
+        """swiglu() that keeps g and u in 8 bits for backward(): gu, gu_s."""
+        self._training("swiglu_save()")
+        L.moe_grouped_swiglu_gemm_save(self.p, self.xg, self.w13, self.masked_m, self.offsets, self.hg, self.gu,
+                                       self.gu_s, self.err, stream)
 
     def down(self, stream=None):
         L.moe_grouped_down_gemm(self.p, self.hg, self.hg_s, self.w2, self.w2_s, self.masked_m, self.offsets,
@@ -100,9 +121,15 @@ class MoeLayer:
                           self.offsets, self.row_of, self.w, self.hg, self.hg_s, self.yg, self.out, self.err, self.ws,
                           stream)
 
-    def forward(self, x, logits, stream=None, fused=False):
+    def forward(self, x, logits, stream=None, fused=False, save=False):
         """route -> permute -> gate/up -> down -> combine; returns self.out.  fused=True makes the
-        same pass with the fused calls: route_permute() and ffn_combine()."""
+        same pass with the fused calls: route_permute() and ffn_combine().  save=True (a layer with train=True):
+        gate/up keeps what backward() needs."""
+        if save:
+            self._training("forward(save=True)")
+            self.route_permute(logits, x, stream)
+            self.ffn_save(stream)
+            return self.out
         if fused:
             self.route_permute(logits, x, stream)
             self.ffn_combine(stream)
@@ -113,3 +140,43 @@ class MoeLayer:
         self.down(stream)
         self.combine(stream)
         return self.out
+
+    # -- training ---------------------------------------------------------------
+    def _training(self, what):
+        if not self.train:
+            raise ValueError("%s: the layer was made without train=True" % what)
+
+    def ffn_save(self, stream=None):
+        """ffn_combine() of a training pass: gate/up that keeps g and u, down, combine."""
+        self.swiglu_save(stream)
+        self.down(stream)
+        self.combine(stream)
+
+    def backward(self, dout, dw13=None, dw2=None, accumulate=False, weights=True, score="softmax", logits=None,
+                 renormalize=True, scale=1.0, add=None, stream=None):
+        """Gradients of the last forward(save=True) from dout, the gradient of its output: (dx, dlogits, dw13, dw2).
+        dw13, dw2: tensors for the weights' gradients, like w13 and w2 (bf16) or in float32; None: new ones like
+        the weights; accumulate: added to the ones given (float32); weights=False: none, both are None.  score: the
+        router of that pass, "softmax" (route) or "sigmoid" (route_grouped, with its logits, renormalize and scale).
+        add [T, E]: added to dlogits, for instance the balance loss's gradient.  New tensors are allocated on the
+        stream of the call."""
+        self._training("backward()")
+        if accumulate and (not weights or dw13 is None or dw2 is None):
+            raise ValueError("accumulate: expected dw13 and dw2 to add to")
+        p = self.p
+        f32 = dict(dtype=torch.float32, device=self.out.device)
+        with L._allocate_on(stream):
+            dx = torch.empty_like(self.out)
+            dlogits, dw = torch.empty((p.T, p.E), **f32), torch.empty((p.T, p.K), **f32)
+            if weights:
+                dw13 = torch.empty_like(self.w13) if dw13 is None else dw13
+                dw2 = torch.empty_like(self.w2) if dw2 is None else dw2
+            else:
+                dw13 = dw2 = None
+        L.moe_combine_backward(p, dout, self.yg, self.row_of, self.w, self.dyg, self.wg, dw, stream)
+        L.moe_grouped_ffn_backward(p, self.dyg, self.wg, self.xg, self.w13, self.w2, self.gu, self.gu_s, 
+                                   self.masked_m, self.offsets, self.dgu, self.hg, self.dxg, dw13, dw2, self.err,
+                                   accumulate, stream)
+        L.moe_permute_backward(p, self.dxg, self.row_of, dx, stream)
+        L.moe_route_backward(p, score, logits, self.ids, self.w, dw, dlogits, add, renormalize, scale, stream)
+        return dx, dlogits, dw13, dw2
