@@ -546,21 +546,21 @@ moe_status moe_combine_backward(const moe_problem* p, const void* dout, const vo
  *   dxg[row] = W13[s]^T . dgu[row]
  * and for every slot, summed over its valid rows,
  *   dw13[s] = dgu^T xg [2I][H],  dw2[s] = dyg^T hg [H][I].
- * dgu [rows][2I], hg [rows][I] and dxg [rows][H] are bf16 (written; products
- * take them in that form).  wg NULL: every row has weight 1.  dw13, dw2: dw_dtype BF16 or F32; `accumulate` (F32
+ * dgu [rows][2I] and hg [rows][I] are bf16 (written; products take them in that
+ * form), dxg [rows][H] is fp32 (a token's rows of it are still to be added).  wg NULL: every row has weight 1.  dw13, dw2: dw_dtype BF16 or F32; `accumulate` (F32
  * alone, else MOE_ERR_UNSUPPORTED) adds to what they hold, otherwise every
  * element is written, zeros for a slot without rows.  dxg, dw13 and dw2 may each
  * be NULL where they are not wanted (then w13, xg are not read).  All but wg and
  * gu_scales 16-byte aligned; outputs overlap no input and no other output. */
 moe_status moe_grouped_ffn_backward(const moe_problem* p, const void* dyg, const float* wg, const void* xg,
                                     const void* w13, const void* w2, const uint8_t* gu, const float* gu_scales,
-                                    const int32_t* masked_m, const int32_t* offsets, void* dgu, void* hg, void* dxg, void* dw13, void* dw2,
+                                    const int32_t* masked_m, const int32_t* offsets, void* dgu, void* hg, float* dxg, void* dw13, void* dw2,
                                     int32_t dw_dtype, int32_t accumulate, int32_t* err_flag, moe_stream_t stream);
 
 /* Gradient of the dispatch: dx[t] = sum over the token's placed records of
  * dxg[row], in fp32 in k order (the shared expert's last), rounded once.  dxg
- * [rows][H], dx [T][H] bf16, 16-byte aligned. */
-moe_status moe_permute_backward(const moe_problem* p, const void* dxg, const int32_t* row_of, void* dx,
+ * [rows][H] fp32, dx [T][H] bf16, 16-byte aligned. */
+moe_status moe_permute_backward(const moe_problem* p, const float* dxg, const int32_t* row_of, void* dx,
                                 moe_stream_t stream);
 
 /* Gradient of the router's weights with the choice held constant; any problem

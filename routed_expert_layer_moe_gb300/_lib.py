@@ -499,7 +499,7 @@ def moe_grouped_ffn_backward(p: Problem, dyg, wg, xg, w13, w2, gu, gu_scales, ma
         _arg(gu, "gu", _U8, (rows, 2 * p.I)), _arg(gu_scales, "gu_scales", _F32, (rows, 2 * p.I // FP8_GROUP)),
         _arg(masked_m, "masked_m", _I32, (n,)), _arg(offsets, "offsets", _I32, (n + 1,)),
         _arg(dgu, "dgu", _BF16, (rows, 2 * p.I)), _arg(hg, "hg", _BF16, (rows, p.I)),
-        _arg(dxg, "dxg", _BF16, (rows, p.H)), _arg(dw13, "dw13", dt, (n, 2 * p.I, p.H)),
+        _arg(dxg, "dxg", _F32, (rows, p.H)), _arg(dw13, "dw13", dt, (n, 2 * p.I, p.H)),
         _arg(dw2, "dw2", dt, (n, p.H, p.I)), _FLOAT_DTYPES[dt], int(bool(accumulate)), _ptr(err_flag),
         _stream(stream)), "moe_grouped_ffn_backward")
 
@@ -508,7 +508,7 @@ def moe_permute_backward(p: Problem, dxg, row_of, dx, stream=None) -> None:
     """Gradient of the dispatch: dx [T, H] = the sum of a token's rows of dxg."""
     rows, _ = _train_sizes(p)
     _check(lib().moe_permute_backward(
-        ctypes.byref(p), _arg(dxg, "dxg", _BF16, (rows, p.H)),
+        ctypes.byref(p), _arg(dxg, "dxg", _F32, (rows, p.H)),
         _arg(row_of, "row_of", _I32, (p.T, p.K + p.has_shared)), _arg(dx, "dx", _BF16, (p.T, p.H)), _stream(stream)),
         "moe_permute_backward")
 

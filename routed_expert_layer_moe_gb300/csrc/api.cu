@@ -521,7 +521,7 @@ moe_status moe_combine_backward(const moe_problem* p, const void* dout, const vo
 
 moe_status moe_grouped_ffn_backward(const moe_problem* p, const void* dyg, const float* wg, const void* xg,
                                     const void* w13, const void* w2, const uint8_t* gu, const float* gu_scales,
-                                    const int32_t* masked_m, const int32_t* offsets, void* dgu, void* hg, void* dxg, void* dw13, void* dw2,
+                                    const int32_t* masked_m, const int32_t* offsets, void* dgu, void* hg, float* dxg, void* dw13, void* dw2,
                                     int32_t dw_dtype, int32_t accumulate, int32_t* err_flag, moe_stream_t stream) {
   const int r = check_training(p);
   if (r) return (moe_status)r;
@@ -542,14 +542,14 @@ moe_status moe_grouped_ffn_backward(const moe_problem* p, const void* dyg, const
   return launched(launch_ffn_backward(*p, a, (cudaStream_t)stream));
 }
 
-moe_status moe_permute_backward(const moe_problem* p, const void* dxg, const int32_t* row_of, void* dx,
+moe_status moe_permute_backward(const moe_problem* p, const float* dxg, const int32_t* row_of, void* dx,
                                 moe_stream_t stream) {
   const int r = check_training(p);
   if (r) return (moe_status)r;
   if (p->T == 0) return MOE_OK;
   if (!dxg || !row_of || !dx) return MOE_ERR_INVALID;
   if (!aligned16(dxg) || !aligned16(dx)) return MOE_ERR_UNSUPPORTED;
-  return launched(launch_combine(*p, dxg, row_of, nullptr, dx, (cudaStream_t)stream));
+  return launched(launch_permute_backward(*p, dxg, row_of, dx, (cudaStream_t)stream));
 }
 
 moe_status moe_route_backward(const moe_problem* p, int32_t score, const float* logits, const int32_t* ids,

@@ -83,6 +83,17 @@ __global__ void __launch_bounds__(128) combine_kernel(const TY* __restrict__ yg,
 
 }  // namespace
 
+// The dispatch's gradient: every record with weight 1, rows of fp32.
+int launch_permute_backward(const moe_problem& p, const float* dxg, const int32_t* row_of, void* dx,
+                            cudaStream_t st) {
+  if (p.T == 0) return MOE_OK;
+  const int threads = 128;
+  const dim3 grid(p.T, (p.H / 4 + threads - 1) / threads);
+  combine_kernel<float, __nv_bfloat16, 4><<<grid, threads, 0, st>>>(dxg, row_of, nullptr, (__nv_bfloat16*)dx, p.H, p.K,
+                                                                     p.K + p.has_shared);
+  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
 int launch_combine(const moe_problem& p, const void* yg, const int32_t* row_of, const float* w, void* out,
                    cudaStream_t st) {
   if (p.T == 0) return MOE_OK;

@@ -85,7 +85,6 @@ int launch_eplb_record(const moe_problem& p, const int32_t* masked_m, int64_t pa
 int launch_eplb_rebalance(const moe_problem& p, const int32_t* load_window, int window, const int32_t* p2l,
                           int64_t* logical_load, int32_t* new_p2l, int32_t* err, cudaStream_t st);
 int launch_bounded_wait_selftest(long long cycles, int32_t* err, cudaStream_t st);
-// w null: every record has weight 1.
 int launch_combine(const moe_problem& p, const void* yg, const int32_t* row_of, const float* w, void* out,
                    cudaStream_t st);
 
@@ -164,6 +163,7 @@ struct FfnBackwardArgs {
 int launch_ffn_backward(const moe_problem& p, const FfnBackwardArgs& a, cudaStream_t st);
 int launch_combine_backward(const moe_problem& p, const void* dout, const void* yg, const int32_t* row_of,
                             const float* w, void* dyg, float* wg, float* dw, cudaStream_t st);
+int launch_permute_backward(const moe_problem& p, const float* dxg, const int32_t* row_of, void* dx, cudaStream_t st);
 int launch_route_backward(const moe_problem& p, int score, const float* logits, const int32_t* ids, const float* w,
                           const float* dw, int renorm, float scale, const float* add, float* dlogits,
                           cudaStream_t st);

@@ -3,7 +3,7 @@
 //   UP   g, u = xg W13^T                 h = silu(g) u; g and u kept in 8 bits (e4m3, a scale per 128)
 //   DH   dh = w dyg W2                   dg = dh u s (1 + g (1 - s)), du = dh g s, w h = w g s u, s = sigmoid(g),
 //                                        with g and u as the checkpoint holds them, w the row's weight
-//   DX   dxg = dgu W13
+//   DX   dxg = dgu W13                  in fp32: a token's rows of it are still added up
 //   WG   dW[m][n] = sum over the rows of a slot of a[row][m] b[row][n]     (dW13 = dgu^T xg, dW2 = dyg^T (w h))
 //
 // One kernel form for all four: clusters of two CTAs (SM pairs) whose tensor cores work on one tile of 256 x 256
@@ -67,7 +67,7 @@ struct Params {
   int accumulate;    // WG, fp32: add to what is there
   const int32_t* masked_m;
   const int32_t* offsets;
-  void* out;         // UP, DH: h (DH: times w) bf16 [rows][I]; DX: dxg bf16 [rows][H]; WG: dW [slots][m_rows][N]
+  void* out;         // UP, DH: h (DH: times w) bf16 [rows][I]; DX: dxg fp32 [rows][H]; WG: dW [slots][m_rows][N]
   void* out2;        // UP: codes [rows][2 I]; DH: dgu bf16 [rows][2 I]
   float* out2_s;     // UP: scales [rows][2 I / 128]
   const uint8_t* gu;   // DH: codes and scales of the checkpoint
@@ -350,7 +350,7 @@ __device__ __forceinline__ void epilogue(const Params& p, const Unit& U, uint32_
         for (int o = 0; o < 32; o += 16) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(d[o + i]);
-          if (p.accumulate)
+          if (MODE == WG && p.accumulate)
             store_rows<true>(buf, lane, v, dst + (c + o) * 4, (size_t)N * 4, rows);
           else
             store_rows(buf, lane, v, dst + (c + o) * 4, (size_t)N * 4, rows);
@@ -740,7 +740,7 @@ Params common_params(const moe_problem& p, const int32_t* masked_m, const int32_
 }
 
 // Rows of the M side [rows][K] times the weights [slots][b_rows][b_cols].
-template <int MODE>
+template <int MODE, typename OUT = __nv_bfloat16>
 int launch_rows(Params prm, const void* a, int K, const void* w, int b_rows, int b_cols, int ncols, cudaStream_t st) {
   Maps maps;
   for (int i = 0; i < NUM_BOXES; ++i)
@@ -750,7 +750,7 @@ int launch_rows(Params prm, const void* a, int K, const void* w, int b_rows, int
   prm.b_rows = b_rows;
   prm.ncols = ncols;
   prm.nt = MODE == UP ? ncols / HALF : (ncols + 2 * HALF - 1) / (2 * HALF);
-  return launch<MODE, __nv_bfloat16>(prm, maps, st);
+  return launch<MODE, OUT>(prm, maps, st);
 }
 
 // a [rows][M], b [rows][N] -> dw [slots][M][N].
@@ -810,7 +810,7 @@ int launch_ffn_backward(const moe_problem& p, const FfnBackwardArgs& a, cudaStre
   if (a.dxg) {
     Params dx = prm;
     dx.out = a.dxg;
-    r = launch_rows<DX>(dx, a.dgu, 2 * p.I, a.w13, 2 * p.I, p.H, p.H, st);
+    r = launch_rows<DX, float>(dx, a.dgu, 2 * p.I, a.w13, 2 * p.I, p.H, p.H, st);
   }
   return r;
 }

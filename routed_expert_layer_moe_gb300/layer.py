@@ -68,7 +68,8 @@ class MoeLayer:
             bf16 = dict(dtype=torch.bfloat16, device=dev)
             self.gu = torch.empty((rows, 2 * p.I), dtype=torch.uint8, device=dev)
             self.gu_s = torch.empty((rows, 2 * p.I // L.FP8_GROUP), dtype=torch.float32, device=dev)
-            self.dyg, self.dxg = (torch.empty((rows, p.H), **bf16) for _ in range(2))
+            self.dyg = torch.empty((rows, p.H), **bf16)
+            self.dxg = torch.empty((rows, p.H), dtype=torch.float32, device=dev)
             self.dgu = torch.empty((rows, 2 * p.I), **bf16)
             self.wg = torch.empty(rows, dtype=torch.float32, device=dev)
         nbytes = max(L.moe_workspace_bytes(p), 256)

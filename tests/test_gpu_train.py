@@ -86,7 +86,7 @@ class Case:
 
     def backward(self, gu, gs, dtype=torch.bfloat16, dw=None, accumulate=False, dyg=None, xg=None, want=(1, 1, 1)):
         E, H, I = len(self.counts), self.H, self.I
-        dgu, hg, dxg = self.out(2 * I), self.out(I), self.out(H)
+        dgu, hg, dxg = self.out(2 * I), self.out(I), self.out(H, torch.float32)
         dw13, dw2 = dw or (torch.full((E, 2 * I, H), 5.0, dtype=dtype, device="cuda"),
                            torch.full((E, H, I), 5.0, dtype=dtype, device="cuda"))
         a = [t if k else None for k, t in zip(want, (dxg, dw13, dw2))]
@@ -163,7 +163,7 @@ def test_ffn_backward(counts, H, I, layout, dtype):
         for got, v, k in ((dgu[s][:, :I], want[0], u.abs() * (1 + g.abs())), (dgu[s][:, I:], want[1], g.abs())):
             assert ((d(got) - v).abs() <= HALF * v.abs() + (1 + HALF) * k * (off + 2.0 ** -17 * dh.abs())).all()
         da, hh, n = d(dgu[s]), d(hg[s]), c.counts[e]
-        for got, a, b, k, half in ((dxg[s], da, w13, 2 * I, HALF), (dw13[e], da.T, x, n, w_half),
+        for got, a, b, k, half in ((dxg[s], da, w13, 2 * I, 2.0 ** -24), (dw13[e], da.T, x, n, w_half),
                                    (dw2[e], dy.T, hh, n, w_half)):
             v = a @ b
             assert ((d(got) - v).abs() <= half * v.abs() + (1 + half) * sums(k) * (a.abs() @ b.abs())).all()
@@ -249,7 +249,7 @@ def test_no_rows():
         dw = torch.full((2, 256, 128), 5.0, device="cuda"), torch.full((2, 128, 128), 5.0, device="cuda")
         moe.moe_grouped_ffn_backward(p, z(c.rows, 128), None, z(c.rows, 128), c.w13.cuda(), c.w2.cuda(),
                                      z(c.rows, 256, dt=torch.uint8), z(c.rows, 2, dt=torch.float32), c.masked_m,
-                                     c.offsets, z(c.rows, 256), z(c.rows, 128), z(c.rows, 128), *dw, c.err)
+                                     c.offsets, z(c.rows, 256), z(c.rows, 128), z(c.rows, 128, dt=torch.float32), *dw, c.err)
         assert not dw[0].any() and not dw[1].any() and int(c.err) == 0
         moe.moe_grouped_swiglu_gemm_save(p, z(c.rows, 128), c.w13.cuda(), c.masked_m, c.offsets, z(c.rows, 128),
                                          z(c.rows, 256, dt=torch.uint8), z(c.rows, 2, dt=torch.float32), c.err)
@@ -304,9 +304,10 @@ def test_gradients_around_the_experts(T, H, E, K, shared):
     assert torch.equal(dyg, again[0])
     # the dispatch's gradient
     dx = torch.empty(T, H, device="cuda").bfloat16()
-    moe.moe_permute_backward(p, a[1], a[2], dx)
+    dxg = r(rows, H)
+    moe.moe_permute_backward(p, dxg.cuda(), a[2], dx)
     for t in range(T):
-        parts = torch.stack([yg[int(at)].double() if at >= 0 else torch.zeros(H).double() for at in row_of[t]])
+        parts = torch.stack([dxg[int(at)].double() if at >= 0 else torch.zeros(H).double() for at in row_of[t]])
         v = parts.sum(0)
         assert ((dx[t].cpu().double() - v).abs() <= HALF * v.abs() + (1 + HALF) * (K + 1) * 2.0 ** -24 * parts.abs().sum(0)).all()
 
