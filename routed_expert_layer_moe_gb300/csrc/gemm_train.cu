@@ -42,7 +42,6 @@ constexpr int STAGE = 2 * OP_BYTES;
 constexpr int MAX_STAGES = 6;
 constexpr int THREADS = 384;
 constexpr int EPI_WARP0 = 4, EPI_WARPS = 8;
-constexpr int EPI_BUF = 2048;             // 32 rows of 64 bytes a warp
 constexpr uint32_t TMEM_COLS = 512, ACC_COLS = 256;
 constexpr int GROUP_M = 8;                // M tiles that neighbouring units share an N tile with
 constexpr long long TIMEOUT = 4000000000LL;  // SM cycles, about 2 s
@@ -63,8 +62,10 @@ struct Params {
   int b_rows;        // rows of one slot in the weights
   int ncols;         // columns of the output: UP, DH: I; DX: H; WG: N
   int m_rows;        // WG: rows of the output a slot
+  uint64_t group_inv;  // ceil(2^64 / (GROUP_M nt))
   int stages;
   int accumulate;    // WG, fp32: add to what is there
+  int wide;          // the outputs are 32-byte aligned
   const int32_t* masked_m;
   const int32_t* offsets;
   void* out;         // UP, DH: h (DH: times w) bf16 [rows][I]; DX: dxg fp32 [rows][H]; WG: dW [slots][m_rows][N]
@@ -74,50 +75,58 @@ struct Params {
   const float* gu_s;
   const float* wg;     // DH: weights of the rows, or null
   int32_t* err;
-  uint32_t epi_off, ex_off, pre_off, bar_off, misc_off;
+  uint32_t ex_off, pre_off, bar_off, misc_off;
 };
 
 struct Unit {
   int slot, mi, j;   // slot, M tile (WG) or chunk, N tile
   int row;           // UP, DH, DX: first row of this CTA's part of the chunk; WG: first row of the slot
-  int nvalid, most;  // rows of this CTA's part, the larger of the pair's parts; WG: rows of the slot, both
+  int nvalid, nall;  // rows of this CTA's part, of both parts; WG: rows of the slot
   int kb;            // stages
 };
 
+// ceil(2^32 / n) for n = 2 .. GROUP_M: r / n = umulhi(r, it) for r < 2^29.
+__constant__ uint32_t kInverse[GROUP_M + 1] = {0,          0,          0x80000000u, 0x55555556u, 0x40000000u,
+                                               0x33333334u, 0x2AAAAAABu, 0x24924925u, 0x20000000u};
+
+// A role's walk over its units, u0, u0 + stride, ..: the slot is carried along and nothing is divided, since a look-up
+// stands between the last copies or products of one unit and the first of the next.
 template <int MODE>
-__device__ __forceinline__ Unit decode(const Params& p, const int* prefix, const int* srows, const int* sbase, int u,
-                                       uint32_t rank) {
-  int lo = 0, hi = p.nslots;  // prefix[lo] <= u < prefix[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (prefix[mid] <= u)
-      lo = mid;
-    else
-      hi = mid;
+struct Walk {
+  const Params& p;
+  const int *prefix, *srows, *sbase;
+  uint32_t rank;
+  int slot;
+
+  __device__ __forceinline__ void seek(int u) {
+    while (prefix[slot + 1] <= u) ++slot;
   }
-  Unit U;
-  U.slot = lo;
-  const int r = u - prefix[lo], m = srows[lo];
-  const int nm = MODE == WG ? p.mt : (m + 2 * HALF - 1) / (2 * HALF);
-  // groups of GROUP_M tiles of M, the M tile the fastest within one: a wave of pairs shares operands through L2
-  const int g = r / (GROUP_M * p.nt), first = g * GROUP_M;
-  const int size = min(GROUP_M, nm - first), rr = r - first * p.nt;
-  U.mi = first + rr % size;
-  U.j = rr / size;
-  if constexpr (MODE == WG) {
-    U.row = sbase[lo];
-    U.nvalid = U.most = m;
-    U.kb = (m + KB - 1) / KB;
-  } else {
-    const int base = m / nm, extra = m - base * nm;  // near-equal chunks
-    const int n = base + (U.mi < extra ? 1 : 0), n0 = (n + 1) >> 1;
-    U.row = sbase[lo] + U.mi * base + min(U.mi, extra) + (rank ? n0 : 0);
-    U.nvalid = rank ? n - n0 : n0;
-    U.most = n0;
-    U.kb = p.kb;
+
+  __device__ __forceinline__ Unit at(int u) {
+    seek(u);
+    Unit U;
+    U.slot = slot;
+    const int r = u - prefix[slot], m = srows[slot];
+    const int nm = MODE == WG ? p.mt : (m + 2 * HALF - 1) / (2 * HALF);
+    // groups of GROUP_M tiles of M, the M tile the fastest within one: a wave of pairs shares operands through L2
+    const int first = (int)__umul64hi((uint64_t)r, p.group_inv) * GROUP_M;
+    const int size = min(GROUP_M, nm - first), rr = r - first * p.nt;
+    U.j = size == 1 ? rr : (int)__umulhi((uint32_t)rr, kInverse[size]);
+    U.mi = first + rr - U.j * size;
+    if constexpr (MODE == WG) {
+      U.row = sbase[slot];
+      U.nvalid = U.nall = m;
+      U.kb = (m + KB - 1) / KB;
+    } else {
+      // whole parts of 128 rows as far as they go
+      U.nall = min(2 * HALF, m - U.mi * 2 * HALF);
+      U.nvalid = rank ? max(U.nall - HALF, 0) : min(U.nall, HALF);
+      U.row = sbase[slot] + U.mi * 2 * HALF + (int)rank * HALF;
+      U.kb = p.kb;
+    }
+    return U;
   }
-  return U;
-}
+};
 
 __device__ __forceinline__ bool elect_one() {
   uint32_t one;
@@ -179,36 +188,44 @@ __device__ __forceinline__ void tmem_loaded32(float (&v)[32]) {
                : "memory");
 }
 
+// N (32 or 64) columns of this thread's lane of tensor memory.
+template <int N>
+__device__ __forceinline__ void tmem_load(uint32_t taddr, float (&v)[N]) {
+  float a[32];
+  tmem_load32(taddr, a);
+  if constexpr (N == 64) {
+    float b[32];
+    tmem_load32(taddr + 32, b);
+    tmem_loaded32(b);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[32 + i] = b[i];
+  }
+  tmem_loaded32(a);
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = a[i];
+}
+
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// 64 bytes of each lane's row to global memory, through the warp's shared buffer so that four lanes write a row's 64
-// bytes together: dst is the first row's address, `rows` of the 32 are written.  ADD: added to the fp32 values there.
-template <bool ADD = false>
-__device__ __forceinline__ void store_rows(uint8_t* buf, int lane, const uint32_t (&v)[16], uint8_t* dst,
-                                           size_t stride, int rows) {
-  __syncwarp();  // the buffer's last use has been read
+// N words of a lane's row to memory, 32 bytes (a whole sector) at a time; wide: 32-byte aligned.  Results go straight from
+// the registers: through shared memory, coalesced or by TMA, the stores are fewer cycles of the memory pipe but take
+// them from the MMAs, whose operands come from shared memory at half its rate (dW13 + dW2 of 2 experts of 4096 x 14336,
+// 1024 rows each: 250 + 126 us without stores, 268 + 139 so, 279 + 147 with coalesced 16-byte stores, 284 + 150 by TMA).
+template <int N>
+__device__ __forceinline__ void store_row(void* dst, const uint32_t (&v)[N], bool wide) {
+  uint4* q = static_cast<uint4*>(dst);
 #pragma unroll
-  for (int c = 0; c < 4; ++c)  // 16-byte pieces in an order that keeps eight lanes on different banks
-    *reinterpret_cast<uint4*>(buf + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) =
-        make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
-  __syncwarp();
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = 8 * i + (lane >> 2), c = lane & 3;
-    if (r < rows) {
-      uint4 x = *reinterpret_cast<const uint4*>(buf + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
-      uint4* at = reinterpret_cast<uint4*>(dst + (size_t)r * stride + 16 * c);
-      if constexpr (ADD) {
-        const uint4 y = *at;
-        x.x = __float_as_uint(__uint_as_float(x.x) + __uint_as_float(y.x));
-        x.y = __float_as_uint(__uint_as_float(x.y) + __uint_as_float(y.y));
-        x.z = __float_as_uint(__uint_as_float(x.z) + __uint_as_float(y.z));
-        x.w = __float_as_uint(__uint_as_float(x.w) + __uint_as_float(y.w));
-      }
-      *at = x;
+  for (int i = 0; i < N / 8; ++i) {
+    const uint4 a = make_uint4(v[8 * i], v[8 * i + 1], v[8 * i + 2], v[8 * i + 3]);
+    const uint4 b = make_uint4(v[8 * i + 4], v[8 * i + 5], v[8 * i + 6], v[8 * i + 7]);
+    if (wide) {
+      st_global_v8(q + 2 * i, a, b);
+    } else {
+      q[2 * i] = a;
+      q[2 * i + 1] = b;
     }
   }
 }
@@ -218,12 +235,11 @@ __device__ __forceinline__ void store_rows(uint8_t* buf, int lane, const uint32_
 // tile's first column; `zero`: there is no accumulator, the tile is zeros (WG without rows).
 template <int MODE, typename OUT>
 __device__ __forceinline__ void epilogue(const Params& p, const Unit& U, uint32_t rank, int ew, int lane, uint32_t acc,
-                                         uint8_t* buf, float* ex, bool zero) {
+                                         float* ex, bool zero) {
   const int quad = ew & 3, half = ew >> 2;
-  const int r0 = 32 * quad;                    // the warp's first row in the CTA's 128
+  const int r = 32 * quad + lane;  // the lane's row in the CTA's 128
   if constexpr (MODE == UP) {
-    const size_t row0 = (size_t)U.row + r0, row = row0 + lane;
-    const int rows = min(32, U.nvalid - r0), I = p.ncols, c0 = U.j * HALF + 64 * half;
+    const int I = p.ncols, c0 = U.j * HALF + 64 * half;
     float g[32], u[32];
     float ag = 0.0f, au = 0.0f;
 #pragma unroll
@@ -236,14 +252,16 @@ __device__ __forceinline__ void epilogue(const Params& p, const Unit& U, uint32_
       for (int i = 0; i < 32; ++i) ag = fp8_amax(ag, g[i]), au = fp8_amax(au, u[i]);
     }
     // a group's other 64 columns are with the warp of the same rows in the other half
-    float2* mine = reinterpret_cast<float2*>(ex) + (half * HALF + r0 + lane);
-    *mine = make_float2(ag, au);
+    reinterpret_cast<float2*>(ex)[half * HALF + r] = make_float2(ag, au);
     asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory");
-    const float2 other = reinterpret_cast<float2*>(ex)[(half ^ 1) * HALF + r0 + lane];
+    if (U.nvalid <= 32 * quad) return;
+    const float2 other = reinterpret_cast<float2*>(ex)[(half ^ 1) * HALF + r];
     const float sg = fp8_scale(fp8_amax(ag, other.x)), su = fp8_scale(fp8_amax(au, other.y));
     // one division a group; the codes' inputs are fp32 sums, so a reciprocal's last bit is within their own error
-    const float ig = sg == sg ? 1.0f / sg : 0.0f, iu = su == su ? 1.0f / su : 0.0f;
-    if (half == 0 && lane < rows) {
+    const float ig = 1.0f / sg, iu = 1.0f / su;
+    const bool live = r < U.nvalid;
+    const size_t row = (size_t)U.row + r;
+    if (half == 0 && live) {
       p.out2_s[row * (2 * I / FP8_GROUP) + U.j] = sg;
       p.out2_s[row * (2 * I / FP8_GROUP) + I / FP8_GROUP + U.j] = su;
     }
@@ -253,55 +271,45 @@ __device__ __forceinline__ void epilogue(const Params& p, const Unit& U, uint32_
       tmem_load32(acc + HALF + 64 * half + c, u);
       tmem_loaded32(g);
       tmem_loaded32(u);
-      uint32_t v[16];
+      uint32_t h[16], qg[8], qu[8];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = pack2(silu(g[2 * i]) * u[2 * i], silu(g[2 * i + 1]) * u[2 * i + 1]);
-      store_rows(buf, lane, v, static_cast<uint8_t*>(p.out) + (row0 * I + c0 + c) * 2, (size_t)I * 2, rows);
-      if (lane < rows) {
+      for (int i = 0; i < 16; ++i) h[i] = pack2(silu(g[2 * i]) * u[2 * i], silu(g[2 * i + 1]) * u[2 * i + 1]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {  // a group without a scale has codes 0
+        qg[i] = sg != sg ? 0u : fp8_pair(g[4 * i] * ig, g[4 * i + 1] * ig) | fp8_pair(g[4 * i + 2] * ig, g[4 * i + 3] * ig) << 16;
+        qu[i] = su != su ? 0u : fp8_pair(u[4 * i] * iu, u[4 * i + 1] * iu) | fp8_pair(u[4 * i + 2] * iu, u[4 * i + 3] * iu) << 16;
+      }
+      if (live) {
+        store_row(static_cast<__nv_bfloat16*>(p.out) + row * I + c0 + c, h, p.wide);
         uint8_t* code = static_cast<uint8_t*>(p.out2) + row * 2 * I + c0 + c;
-        const bool bad_g = sg != sg, bad_u = su != su;
-        uint32_t q[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          q[i] = bad_g ? 0u : fp8_pair(g[4 * i] * ig, g[4 * i + 1] * ig) | fp8_pair(g[4 * i + 2] * ig, g[4 * i + 3] * ig) << 16;
-        reinterpret_cast<uint4*>(code)[0] = make_uint4(q[0], q[1], q[2], q[3]);
-        reinterpret_cast<uint4*>(code)[1] = make_uint4(q[4], q[5], q[6], q[7]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          q[i] = bad_u ? 0u : fp8_pair(u[4 * i] * iu, u[4 * i + 1] * iu) | fp8_pair(u[4 * i + 2] * iu, u[4 * i + 3] * iu) << 16;
-        reinterpret_cast<uint4*>(code + I)[0] = make_uint4(q[0], q[1], q[2], q[3]);
-        reinterpret_cast<uint4*>(code + I)[1] = make_uint4(q[4], q[5], q[6], q[7]);
+        store_row(code, qg, p.wide);
+        store_row(code + I, qu, p.wide);
       }
     }
   } else if constexpr (MODE == DH) {
-    const size_t row0 = (size_t)U.row + r0, row = row0 + lane;
-    const int rows = min(32, U.nvalid - r0), I = p.ncols, c0 = U.j * 2 * HALF + HALF * half;
-    if (c0 >= I || rows <= 0) return;
+    const int I = p.ncols, c0 = U.j * 2 * HALF + HALF * half;
+    if (c0 >= I || U.nvalid <= 32 * quad) return;
+    const bool live = r < U.nvalid;
+    const size_t row = (size_t)U.row + (live ? r : 0);  // a lane without a row reads the first one's
     const int n = 2 * I / FP8_GROUP;
-    float sg = 0.0f, su = 0.0f, w = 1.0f;
-    if (lane < rows) {
-      if (p.wg) w = p.wg[row];
-      sg = p.gu_s[row * n + c0 / FP8_GROUP];
-      su = p.gu_s[row * n + (I + c0) / FP8_GROUP];
-    }
+    const float w = p.wg ? p.wg[row] : 1.0f;
+    const float sg = p.gu_s[row * n + c0 / FP8_GROUP], su = p.gu_s[row * n + (I + c0) / FP8_GROUP];
+    const uint4* code = reinterpret_cast<const uint4*>(p.gu + row * 2 * I + c0);
+    __nv_bfloat16* dgu = static_cast<__nv_bfloat16*>(p.out2) + row * 2 * I + c0;
+    __nv_bfloat16* hg = static_cast<__nv_bfloat16*>(p.out) + row * I + c0;
 #pragma unroll 1
     for (int c = 0; c < HALF; c += 32) {
-      uint4 qg[2] = {}, qu[2] = {};
-      if (lane < rows) {
-        const uint4* code = reinterpret_cast<const uint4*>(p.gu + row * 2 * I + c0 + c);
-        qg[0] = __ldg(code), qg[1] = __ldg(code + 1);
-        code = reinterpret_cast<const uint4*>(p.gu + row * 2 * I + I + c0 + c);
-        qu[0] = __ldg(code), qu[1] = __ldg(code + 1);
-      }
+      const uint4 g0 = __ldg(code + c / 16), g1 = __ldg(code + c / 16 + 1);
+      const uint4 u0 = __ldg(code + (I + c) / 16), u1 = __ldg(code + (I + c) / 16 + 1);
+      const uint32_t qg[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
+      const uint32_t qu[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
       float d[32];
-      tmem_load32(acc + HALF * half + c, d);
+      tmem_load32(acc + HALF * half + (uint32_t)c, d);
       tmem_loaded32(d);
       uint32_t vg[16], vu[16], vh[16];
-      const uint32_t* wg = reinterpret_cast<const uint32_t*>(qg);
-      const uint32_t* wu = reinterpret_cast<const uint32_t*>(qu);
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const float2 cg = fp8_unpair(wg[i >> 1] >> (16 * (i & 1))), cu = fp8_unpair(wu[i >> 1] >> (16 * (i & 1)));
+        const float2 cg = fp8_unpair(qg[i >> 1] >> (16 * (i & 1))), cu = fp8_unpair(qu[i >> 1] >> (16 * (i & 1)));
         float dg[2], du[2], h[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -316,46 +324,46 @@ __device__ __forceinline__ void epilogue(const Params& p, const Unit& U, uint32_
         vu[i] = pack2(du[0], du[1]);
         vh[i] = pack2(h[0], h[1]);
       }
-      uint8_t* dgu = static_cast<uint8_t*>(p.out2) + (row0 * 2 * I + c0 + c) * 2;
-      store_rows(buf, lane, vg, dgu, (size_t)I * 4, rows);
-      store_rows(buf, lane, vu, dgu + (size_t)I * 2, (size_t)I * 4, rows);
-      store_rows(buf, lane, vh, static_cast<uint8_t*>(p.out) + (row0 * I + c0 + c) * 2, (size_t)I * 2, rows);
+      if (live) {
+        store_row(dgu + c, vg, p.wide);
+        store_row(dgu + I + c, vu, p.wide);
+        store_row(hg + c, vh, p.wide);
+      }
     }
   } else {
     // DX: rows of the chunk; WG: rows of the slot's gradient, whole tiles of 128
     const int N = p.ncols, c0 = U.j * 2 * HALF + HALF * half;
-    const int rows = MODE == WG ? 32 : min(32, U.nvalid - r0);
-    const size_t row0 = MODE == WG ? (size_t)U.slot * p.m_rows + U.mi * 2 * HALF + rank * HALF + r0
-                                   : (size_t)U.row + r0;
-    if (c0 >= N || rows <= 0) return;
-    if (MODE == WG && U.mi * 2 * HALF + (int)rank * HALF >= p.m_rows) return;
-    uint8_t* dst = static_cast<uint8_t*>(p.out) + (row0 * N + c0) * sizeof(OUT);
+    if (c0 >= N || (MODE == WG ? U.mi * 2 * HALF + (int)rank * HALF >= p.m_rows : U.nvalid <= 32 * quad)) return;
+    const bool live = MODE == WG || r < U.nvalid;
+    const size_t row = MODE == WG ? (size_t)U.slot * p.m_rows + U.mi * 2 * HALF + rank * HALF + r : (size_t)U.row + r;
+    OUT* dst = static_cast<OUT*>(p.out) + row * N + c0;
+    constexpr int COLS = 128 / sizeof(OUT);  // 128 bytes of a row at a time
 #pragma unroll 1
-    for (int c = 0; c < HALF; c += 32) {
-      float d[32];
+    for (int c = 0; c < HALF; c += COLS) {
+      float d[COLS];
       if (zero) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) d[i] = 0.0f;
+        for (int i = 0; i < COLS; ++i) d[i] = 0.0f;
       } else {
-        tmem_load32(acc + HALF * half + c, d);
-        tmem_loaded32(d);
+        tmem_load<COLS>(acc + HALF * half + (uint32_t)c, d);
       }
-      uint32_t v[16];
+      uint32_t v[32];
       if constexpr (sizeof(OUT) == 2) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = pack2(d[2 * i], d[2 * i + 1]);
-        store_rows(buf, lane, v, dst + c * 2, (size_t)N * 2, rows);
+        for (int i = 0; i < 32; ++i) v[i] = pack2(d[2 * i], d[2 * i + 1]);
       } else {
+        if (MODE == WG && p.accumulate) {
+          const float4* old = reinterpret_cast<const float4*>(dst + c);
 #pragma unroll
-        for (int o = 0; o < 32; o += 16) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(d[o + i]);
-          if (MODE == WG && p.accumulate)
-            store_rows<true>(buf, lane, v, dst + (c + o) * 4, (size_t)N * 4, rows);
-          else
-            store_rows(buf, lane, v, dst + (c + o) * 4, (size_t)N * 4, rows);
+          for (int i = 0; i < 8; ++i) {
+            const float4 f = old[i];
+            d[4 * i] += f.x, d[4 * i + 1] += f.y, d[4 * i + 2] += f.z, d[4 * i + 3] += f.w;
+          }
         }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(d[i]);
       }
+      if (live) store_row(dst + c, v, p.wide);
     }
   }
 }
@@ -458,7 +466,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc_fence_after_sync();
   const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_base_smem, 0);
   const int total = prefix[p.nslots];
-  auto unit = [&](int u) { return decode<MODE>(p, prefix, srows, sbase, u, rank); };
+  Walk<MODE> walk{p, prefix, srows, sbase, rank, 0};
   // rows of a slot's last stage that are in its last MMA's 16 but behind the last row
   auto ragged = [](const Unit& U) { return MODE == WG && U.kb > 0 && (U.nvalid & 15) != 0; };
 
@@ -470,11 +478,12 @@ __global__ void __launch_bounds__(THREADS, 1)
       uint32_t phase = 0;
       bool ok = true;
       for (int u = unit0; ok && u < total; u += ustride) {
-        const Unit U = unit(u);
-        const int bx = MODE == WG ? 0 : box_of(U.most);
-        const CUtensorMap* ma = &maps.a[bx];
-        const uint32_t a_bytes = MODE == WG ? OP_BYTES : (uint32_t)box_rows(bx) * KB * 2;
-        const uint32_t bytes = a_bytes + OP_BYTES;
+        const Unit U = walk.at(u);
+        const CUtensorMap* ma = &maps.a[MODE == WG ? 0 : box_of(U.nvalid)];
+        auto row_bytes = [](int rows) { return rows > 0 ? (uint32_t)box_rows(box_of(rows)) * KB * 2 : 0u; };
+        // of both CTAs; a part without rows copies none
+        const uint32_t bytes = MODE == WG ? 2 * STAGE
+                                          : row_bytes(min(U.nall, HALF)) + row_bytes(U.nall - HALF) + 2 * OP_BYTES;
         const int am = MODE == WG ? U.mi * 2 * HALF + (int)rank * HALF : 0;
         const int bn = U.j * (MODE == UP ? HALF : 2 * HALF) + (MODE == UP ? 0 : (int)rank * HALF);
         const int brow = MODE == UP ? U.slot * p.b_rows + (int)rank * p.ncols + bn : U.slot * p.b_rows;
@@ -488,7 +497,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           const int k = kb * KB;
           if (kb == U.kb - 1 && ragged(U)) {
             // counted on this CTA's own barrier: warp 2 has to see them land here
-            mbar_arrive_expect_tx(&landed[stage], bytes);
+            mbar_arrive_expect_tx(&landed[stage], STAGE);
             if (leader) mbar_arrive(&full[stage]);
             for (int h = 0; h < 2; ++h) {
               tma_load_2d(sa + h * BOX_BYTES, ma, &landed[stage], am + 64 * h, U.row + k);
@@ -496,11 +505,11 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
           } else {
             // the leader's barrier counts both CTAs' copies
-            if (leader) mbar_arrive_expect_tx(&full[stage], 2 * bytes);
+            if (leader) mbar_arrive_expect_tx(&full[stage], bytes);
             const uint32_t bar = mapa_shared(&full[stage], 0);
             if constexpr (MODE == WG) {
               for (int h = 0; h < 2; ++h) tma_load_2d_pair(sa + h * BOX_BYTES, ma, bar, am + 64 * h, U.row + k);
-            } else {
+            } else if (U.nvalid > 0) {
               tma_load_2d_pair(sa, ma, bar, k, U.row);
             }
             if constexpr (MODE == UP) {
@@ -528,10 +537,14 @@ __global__ void __launch_bounds__(THREADS, 1)
     int stage = 0;
     uint32_t phase = 0, fphase = 0, it = 0;  // fphase: a bit per stage
     bool ok = true, any = false;
+    int nkb = p.kb, rows = 0;
     for (int u = unit0; ok && leader && u < total; u += ustride) {
-      const Unit U = unit(u);
-      const int nkb = __shfl_sync(0xffffffffu, U.kb, 0), rows = __shfl_sync(0xffffffffu, U.nvalid, 0);
-      if (MODE == WG && nkb == 0) continue;
+      if constexpr (MODE == WG) {
+        walk.seek(u);
+        rows = __shfl_sync(0xffffffffu, srows[walk.slot], 0);
+        nkb = (rows + KB - 1) / KB;
+        if (nkb == 0) continue;
+      }
       const uint32_t d = tmem_base + (it & 1u) * ACC_COLS;
       ok = __all_sync(0xffffffffu, mbar_wait<true>(&tempty[it & 1u], ((it >> 1) & 1u) ^ 1u, abort_flag, TIMEOUT));
       if (!ok) break;
@@ -582,7 +595,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       uint32_t lphase = 0;
       bool ok = true;
       for (int u = unit0; ok && u < total; u += ustride) {
-        const Unit U = unit(u);
+        const Unit U = walk.at(u);
         if (U.kb == 0) continue;
         const int last = (stage + U.kb - 1) % stages;
         if (ragged(U)) {
@@ -593,7 +606,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           uint8_t* at = smem + (size_t)last * STAGE + v * 128;
           for (int i = lane; i < n * 8 * 4; i += 32)  // eight 16-byte pieces a row, four boxes
             *reinterpret_cast<uint4*>(at + (i & 3) * BOX_BYTES + (i >> 2) * 16) = make_uint4(0u, 0u, 0u, 0u);
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the tensor cores read them
+          fence_proxy_async_shared();  // the tensor cores read them
           __syncwarp();
           if (lane == 0) arrive_cluster(mapa_shared(&fixed[last], 0));
         }
@@ -603,12 +616,11 @@ __global__ void __launch_bounds__(THREADS, 1)
   } else if (warp >= EPI_WARP0) {
     // -------------------------------------------------------------- epilogue
     const int ew = warp - EPI_WARP0;
-    uint8_t* buf = smem + p.epi_off + (size_t)ew * EPI_BUF;
     uint32_t it = 0;
     for (int u = unit0; u < total; u += ustride) {
-      const Unit U = unit(u);
+      const Unit U = walk.at(u);
       if (MODE == WG && U.kb == 0) {
-        epilogue<MODE, OUT>(p, U, rank, ew, lane, 0u, buf, ex, true);
+        epilogue<MODE, OUT>(p, U, rank, ew, lane, 0u, ex, true);
         continue;
       }
       const uint32_t b = it & 1u;
@@ -617,7 +629,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (!ok) break;
       tc_fence_after_sync();
       const uint32_t acc = tmem_base + b * ACC_COLS + ((uint32_t)(32 * (ew & 3)) << 16);
-      epilogue<MODE, OUT>(p, U, rank, ew, lane, acc, buf, ex + b * 4 * HALF, false);
+      epilogue<MODE, OUT>(p, U, rank, ew, lane, acc, ex + b * 4 * HALF, false);
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive_remote(mapa_shared(&tempty[b], 0));
@@ -656,7 +668,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 // ---------------------------------------------------------------------------
 
 // Shared memory of a launch: as many stages as fit.
-int lay_out(Params& prm, size_t* smem) {
+int lay_out(Params& prm, int mode, size_t* smem) {
   for (int st = MAX_STAGES; st >= 2; --st) {
     size_t off = (size_t)st * STAGE;
     auto carve = [&](size_t bytes, size_t align) {
@@ -665,8 +677,7 @@ int lay_out(Params& prm, size_t* smem) {
       off += bytes;
       return (uint32_t)at;
     };
-    prm.epi_off = carve((size_t)EPI_WARPS * EPI_BUF, 128);
-    prm.ex_off = carve(2 * 2 * HALF * 2 * sizeof(float), 16);
+    prm.ex_off = carve(mode == UP ? 2 * 2 * HALF * 2 * sizeof(float) : 0, 16);
     prm.pre_off = carve((3 * (size_t)prm.nslots + 1) * 4, 16);
     prm.bar_off = carve((4 * MAX_STAGES + 6) * 8, 8);
     prm.misc_off = carve(16, 16);
@@ -688,11 +699,13 @@ void cluster_attribute(cudaLaunchAttribute* a) {
 
 template <int MODE, typename OUT>
 int launch(Params prm, const Maps& maps, cudaStream_t st) {
+  prm.wide = ((reinterpret_cast<uintptr_t>(prm.out) | reinterpret_cast<uintptr_t>(prm.out2)) & 31u) == 0;
+  prm.group_inv = ~0ull / (uint64_t)(GROUP_M * prm.nt) + 1;  // the divisor is at least 8: no overflow
   auto kern = train_gemm_kernel<MODE, OUT>;
   static bool attr_set[64] = {};
   static int clusters[64] = {};  // clusters of two that the device keeps resident at once
   size_t smem = 0;
-  const int r = lay_out(prm, &smem);
+  const int r = lay_out(prm, MODE, &smem);
   if (r) return r;
   int dev = 0;
   cudaGetDevice(&dev);
@@ -742,7 +755,7 @@ Params common_params(const moe_problem& p, const int32_t* masked_m, const int32_
 // Rows of the M side [rows][K] times the weights [slots][b_rows][b_cols].
 template <int MODE, typename OUT = __nv_bfloat16>
 int launch_rows(Params prm, const void* a, int K, const void* w, int b_rows, int b_cols, int ncols, cudaStream_t st) {
-  Maps maps;
+  Maps maps{};
   for (int i = 0; i < NUM_BOXES; ++i)
     if (!map_of(&maps.a[i], a, K, (uint64_t)prm.rows_total, box_rows(i))) return MOE_ERR_CUDA;
   if (!map_of(&maps.b, w, b_cols, (uint64_t)prm.nslots * b_rows, MODE == UP ? HALF : KB)) return MOE_ERR_CUDA;
