@@ -20,7 +20,9 @@
 // Ragged rows.  Where the rows are the M side (UP, DH, DX), a chunk of up to 256 rows loads whole boxes: rows behind a
 // slot's last one give accumulator rows that are not stored.  Where they are the reduced dimension (WG), the last 64 of
 // a slot may hold rows of the next one, or padding, which may be NaN: MMAs of K = 16 stop behind the last row, and a
-// warp writes zeros over the up to 15 rows between in shared memory, of both operands.
+// warp writes zeros over the up to 15 rows between in shared memory, of both operands.  Such a last stage has a place of
+// its own beside the ring of stages and is loaded early, so that the zeros are there when its turn comes; in the
+// ring, the MMAs waited for them at the end of every tile (dW13 of 8 experts of 4096 x 14336, about 1024 rows each: 1330 us).
 //
 // Roles of a CTA: warp 0 TMA producer, warp 1 MMAs (leader CTA), warp 2 the zeros of WG, warps 4-11 epilogue.  Every
 // wait is bounded; on expiry the CTA drains its copies and MMAs, frees tensor memory, reports MOE_FLAG_TIMEOUT and
@@ -86,7 +88,7 @@ struct Unit {
 };
 
 // ceil(2^32 / n) for n = 2 .. GROUP_M: r / n = umulhi(r, it) for r < 2^29.
-__constant__ uint32_t kInverse[GROUP_M + 1] = {0,          0,          0x80000000u, 0x55555556u, 0x40000000u,
+__constant__ uint32_t kInverse[9] = {0,          0,          0x80000000u, 0x55555556u, 0x40000000u,
                                                0x33333334u, 0x2AAAAAABu, 0x24924925u, 0x20000000u};
 
 // A role's walk over its units, u0, u0 + stride, ..: the slot is carried along and nothing is divided, since a look-up
@@ -395,9 +397,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   int* sbase = srows + p.nslots;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + p.bar_off);
   uint64_t* empty = full + MAX_STAGES;
-  uint64_t* landed = empty + MAX_STAGES;  // WG: this CTA's copies of a last stage that needs zeros
-  uint64_t* fixed = landed + MAX_STAGES;  // WG: both CTAs have written them
-  uint64_t* tfull = fixed + MAX_STAGES;   // [2] accumulators written
+  uint64_t* landed = empty + MAX_STAGES;  // WG, the last stage that needs zeros: this CTA's copies are there
+  uint64_t* fixed = landed + 1;           // both CTAs have written the zeros
+  uint64_t* last_empty = fixed + 1;       // the MMAs have read it
+  uint64_t* tfull = last_empty + 1;       // [2] accumulators written
   uint64_t* tempty = tfull + 2;           // [2] read
   uint64_t* drain = tempty + 2;
   uint64_t* fin = drain + 1;              // the peer CTA is done with this CTA's memory
@@ -415,9 +418,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int i = 0; i < MAX_STAGES; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
-      mbar_init(&landed[i], 1);
-      mbar_init(&fixed[i], 2);
     }
+    mbar_init(landed, 1);
+    mbar_init(fixed, 2);
+    mbar_init(last_empty, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tfull[i], 1);
       mbar_init(&tempty[i], 2 * EPI_WARPS);
@@ -475,7 +479,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (lane == 0) {
       const CUtensorMap* mb = &maps.b;
       int stage = 0;
-      uint32_t phase = 0;
+      uint32_t phase = 0, lphase = 0;
       bool ok = true;
       for (int u = unit0; ok && u < total; u += ustride) {
         const Unit U = walk.at(u);
@@ -487,7 +491,24 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int am = MODE == WG ? U.mi * 2 * HALF + (int)rank * HALF : 0;
         const int bn = U.j * (MODE == UP ? HALF : 2 * HALF) + (MODE == UP ? 0 : (int)rank * HALF);
         const int brow = MODE == UP ? U.slot * p.b_rows + (int)rank * p.ncols + bn : U.slot * p.b_rows;
-        for (int kb = 0; kb < U.kb; ++kb) {
+        const int whole = ragged(U) ? U.kb - 1 : U.kb;  // stages that go through the ring
+        for (int kb = 0; ok && kb <= whole; ++kb) {
+          // the last stage's place is free at the latest when the ring has gone round once in this tile
+          if (whole < U.kb && kb == min(whole, stages)) {
+            if (!mbar_wait(last_empty, lphase ^ 1u, abort_flag, TIMEOUT)) {
+              ok = false;
+              break;
+            }
+            lphase ^= 1u;
+            mbar_arrive_expect_tx(landed, STAGE);  // counted here: warp 2 has to see this CTA's copies land
+            uint8_t* sa = smem + (size_t)stages * STAGE;
+            const int y = U.row + whole * KB;
+            for (int h = 0; h < 2; ++h) {
+              tma_load_2d(sa + h * BOX_BYTES, ma, landed, am + 64 * h, y);
+              tma_load_2d(sa + OP_BYTES + h * BOX_BYTES, mb, landed, bn + 64 * h, y);
+            }
+          }
+          if (kb == whole) break;
           if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, TIMEOUT)) {
             ok = false;
             break;
@@ -495,29 +516,19 @@ __global__ void __launch_bounds__(THREADS, 1)
           uint8_t* sa = smem + (size_t)stage * STAGE;
           uint8_t* sb = sa + OP_BYTES;
           const int k = kb * KB;
-          if (kb == U.kb - 1 && ragged(U)) {
-            // counted on this CTA's own barrier: warp 2 has to see them land here
-            mbar_arrive_expect_tx(&landed[stage], STAGE);
-            if (leader) mbar_arrive(&full[stage]);
-            for (int h = 0; h < 2; ++h) {
-              tma_load_2d(sa + h * BOX_BYTES, ma, &landed[stage], am + 64 * h, U.row + k);
-              tma_load_2d(sb + h * BOX_BYTES, mb, &landed[stage], bn + 64 * h, U.row + k);
-            }
+          // the leader's barrier counts both CTAs' copies
+          if (leader) mbar_arrive_expect_tx(&full[stage], bytes);
+          const uint32_t bar = mapa_shared(&full[stage], 0);
+          if constexpr (MODE == WG) {
+            for (int h = 0; h < 2; ++h) tma_load_2d_pair(sa + h * BOX_BYTES, ma, bar, am + 64 * h, U.row + k);
+          } else if (U.nvalid > 0) {
+            tma_load_2d_pair(sa, ma, bar, k, U.row);
+          }
+          if constexpr (MODE == UP) {
+            tma_load_2d_pair(sb, mb, bar, k, brow);
           } else {
-            // the leader's barrier counts both CTAs' copies
-            if (leader) mbar_arrive_expect_tx(&full[stage], bytes);
-            const uint32_t bar = mapa_shared(&full[stage], 0);
-            if constexpr (MODE == WG) {
-              for (int h = 0; h < 2; ++h) tma_load_2d_pair(sa + h * BOX_BYTES, ma, bar, am + 64 * h, U.row + k);
-            } else if (U.nvalid > 0) {
-              tma_load_2d_pair(sa, ma, bar, k, U.row);
-            }
-            if constexpr (MODE == UP) {
-              tma_load_2d_pair(sb, mb, bar, k, brow);
-            } else {
-              const int y = MODE == WG ? U.row + k : brow + k;
-              for (int h = 0; h < 2; ++h) tma_load_2d_pair(sb + h * BOX_BYTES, mb, bar, bn + 64 * h, y);
-            }
+            const int y = MODE == WG ? U.row + k : brow + k;
+            for (int h = 0; h < 2; ++h) tma_load_2d_pair(sb + h * BOX_BYTES, mb, bar, bn + 64 * h, y);
           }
           if (++stage == stages) {
             stage = 0;
@@ -535,7 +546,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     constexpr uint32_t STEP_A = MODE == WG ? 16 * 128 / 16 : 2, STEP_B = MODE == UP ? 2 : 16 * 128 / 16;
     constexpr uint32_t idesc = instruction_desc<MODE>();
     int stage = 0;
-    uint32_t phase = 0, fphase = 0, it = 0;  // fphase: a bit per stage
+    uint32_t phase = 0, fphase = 0, it = 0;
     bool ok = true, any = false;
     int nkb = p.kb, rows = 0;
     for (int u = unit0; ok && leader && u < total; u += ustride) {
@@ -549,32 +560,34 @@ __global__ void __launch_bounds__(THREADS, 1)
       ok = __all_sync(0xffffffffu, mbar_wait<true>(&tempty[it & 1u], ((it >> 1) & 1u) ^ 1u, abort_flag, TIMEOUT));
       if (!ok) break;
       tc_fence_after_sync();
-      for (int kb = 0; kb < nkb; ++kb) {
-        ok = __all_sync(0xffffffffu, mbar_wait<true>(&full[stage], phase, abort_flag, TIMEOUT));
-        if (!ok) break;
-        int steps = KB / 16;
-        if (MODE == WG && kb == nkb - 1) {
-          steps = (rows - kb * KB + 15) / 16;
-          if (rows & 15) {
-            ok = __all_sync(0xffffffffu, mbar_wait<true>(&fixed[stage], (fphase >> stage) & 1u, abort_flag, TIMEOUT));
-            if (!ok) break;
-            fphase ^= 1u << stage;
-          }
-        }
+      // one stage's MMAs, of `steps` times 16 values of k
+      auto multiply = [&](int at, int steps, bool first, uint64_t* done) {
         tc_fence_after_sync();
-        const uint64_t da = da0 + (uint32_t)stage * (STAGE >> 4), db = db0 + (uint32_t)stage * (STAGE >> 4);
+        const uint64_t da = da0 + (uint32_t)at * (STAGE >> 4), db = db0 + (uint32_t)at * (STAGE >> 4);
         if (elect_one()) {
 #pragma unroll
           for (int ks = 0; ks < KB / 16; ++ks)
-            if (MODE != WG || ks < steps) mma_pair(d, da + ks * STEP_A, db + ks * STEP_B, idesc, kb > 0 || ks > 0);
-          tc_commit_pair(&empty[stage], 3);
+            if (MODE != WG || ks < steps) mma_pair(d, da + ks * STEP_A, db + ks * STEP_B, idesc, !first || ks > 0);
+          tc_commit_pair(done, 3);
         }
         __syncwarp();
         any = true;
+      };
+      const int whole = MODE == WG && (rows & 15) ? nkb - 1 : nkb;
+      for (int kb = 0; kb < whole; ++kb) {
+        ok = __all_sync(0xffffffffu, mbar_wait<true>(&full[stage], phase, abort_flag, TIMEOUT));
+        if (!ok) break;
+        multiply(stage, MODE == WG && kb == nkb - 1 ? (rows - kb * KB) / 16 : KB / 16, kb == 0, &empty[stage]);
         if (++stage == stages) {
           stage = 0;
           phase ^= 1u;
         }
+      }
+      if (MODE == WG && ok && whole < nkb) {
+        ok = __all_sync(0xffffffffu, mbar_wait<true>(fixed, fphase, abort_flag, TIMEOUT));
+        if (!ok) break;
+        fphase ^= 1u;
+        multiply(stages, (rows - whole * KB + 15) / 16, whole == 0, last_empty);
       }
       if (ok && elect_one()) tc_commit_pair(&tfull[it & 1u], 3);
       __syncwarp();
@@ -591,26 +604,20 @@ __global__ void __launch_bounds__(THREADS, 1)
   } else if (warp == 2) {
     // -------------------------------------------------------------- WG: zeros behind a slot's last row
     if constexpr (MODE == WG) {
-      int stage = 0;
       uint32_t lphase = 0;
-      bool ok = true;
-      for (int u = unit0; ok && u < total; u += ustride) {
-        const Unit U = walk.at(u);
-        if (U.kb == 0) continue;
-        const int last = (stage + U.kb - 1) % stages;
-        if (ragged(U)) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&landed[last], (lphase >> last) & 1u, abort_flag, TIMEOUT));
-          if (!ok) break;
-          lphase ^= 1u << last;
-          const int v = U.nvalid - (U.kb - 1) * KB, n = ((v + 15) & ~15) - v;  // rows v .. v + n - 1 of the stage
-          uint8_t* at = smem + (size_t)last * STAGE + v * 128;
-          for (int i = lane; i < n * 8 * 4; i += 32)  // eight 16-byte pieces a row, four boxes
-            *reinterpret_cast<uint4*>(at + (i & 3) * BOX_BYTES + (i >> 2) * 16) = make_uint4(0u, 0u, 0u, 0u);
-          fence_proxy_async_shared();  // the tensor cores read them
-          __syncwarp();
-          if (lane == 0) arrive_cluster(mapa_shared(&fixed[last], 0));
-        }
-        stage = (stage + U.kb) % stages;
+      for (int u = unit0; u < total; u += ustride) {
+        walk.seek(u);
+        const int m = srows[walk.slot];
+        if ((m & 15) == 0) continue;
+        if (!__all_sync(0xffffffffu, mbar_wait(landed, lphase, abort_flag, TIMEOUT))) break;
+        lphase ^= 1u;
+        const int v = m % KB, n = 16 - (v & 15);  // rows v .. v + n - 1 of the stage
+        uint8_t* at = smem + (size_t)stages * STAGE + v * 128;
+        for (int i = lane; i < n * 8 * 4; i += 32)  // eight 16-byte pieces a row, four boxes
+          *reinterpret_cast<uint4*>(at + (i & 3) * BOX_BYTES + (i >> 2) * 16) = make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_shared();  // the tensor cores read them
+        __syncwarp();
+        if (lane == 0) arrive_cluster(mapa_shared(fixed, 0));
       }
     }
   } else if (warp >= EPI_WARP0) {
@@ -670,7 +677,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 // Shared memory of a launch: as many stages as fit.
 int lay_out(Params& prm, int mode, size_t* smem) {
   for (int st = MAX_STAGES; st >= 2; --st) {
-    size_t off = (size_t)st * STAGE;
+    size_t off = (size_t)(mode == WG ? st + 1 : st) * STAGE;  // WG: and the last stage's place
     auto carve = [&](size_t bytes, size_t align) {
       off = align_up(off, align);
       const size_t at = off;
@@ -679,7 +686,7 @@ int lay_out(Params& prm, int mode, size_t* smem) {
     };
     prm.ex_off = carve(mode == UP ? 2 * 2 * HALF * 2 * sizeof(float) : 0, 16);
     prm.pre_off = carve((3 * (size_t)prm.nslots + 1) * 4, 16);
-    prm.bar_off = carve((4 * MAX_STAGES + 6) * 8, 8);
+    prm.bar_off = carve((2 * MAX_STAGES + 9) * 8, 8);
     prm.misc_off = carve(16, 16);
     if ((int)(off + 1024) <= device_info().max_smem_optin) {
       prm.stages = st;
