@@ -577,6 +577,19 @@ moe_status moe_route_backward(const moe_problem* p, int32_t score, const float* 
                               const float* w, const float* dw, int32_t renormalize, float scale, const float* add,
                               float* dlogits, moe_stream_t stream);
 
+/* The four calls of the gradient in one, three launches and the products' two:
+ * moe_combine_backward with moe_route_backward in the same launch,
+ * moe_grouped_ffn_backward and moe_permute_backward; the same arguments and the
+ * same results.  dyg, wg, dgu, hg and dxg are buffers between the steps, written as by
+ * those calls; dw [T][K] is written too.  dw13 and dw2 may each be NULL. */
+moe_status moe_layer_backward(const moe_problem* p, const void* dout, const void* yg, const int32_t* row_of,
+                              const int32_t* ids, const float* w, const void* xg, const void* w13, const void* w2,
+                              const uint8_t* gu, const float* gu_scales, const int32_t* masked_m,
+                              const int32_t* offsets, int32_t score, const float* logits, int32_t renormalize,
+                              float scale, const float* add, void* dyg, float* wg, void* dgu, void* hg, float* dxg,
+                              float* dw, void* dx, float* dlogits, void* dw13, void* dw2, int32_t dw_dtype,
+                              int32_t accumulate, int32_t* err_flag, moe_stream_t stream);
+
 /* Diagnostic, an addition of this library (the pages describe none): runs the
  * bounded wait that every kernel here uses on an mbarrier that nothing
  * completes, with a limit of `cycles` SM cycles (1 .. 4e9), so that the expiry

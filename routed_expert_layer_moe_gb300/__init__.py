@@ -12,7 +12,7 @@ from ._lib import (EXPORTS, LIB_PATH, MOE_E2M1, MOE_E4M3, MOE_BF16, MOE_F32, MOE
                    moe_balance_loss, moe_balance_loss_backward, moe_balance_workspace_bytes, moe_block_norm,
                    moe_block_norm_backward, moe_block_norm_workspace_bytes, moe_mx_dequantize, moe_mx_quantize,
                    moe_combine_backward, moe_fp8_dequantize, moe_fp8_quantize, moe_grouped_ffn_backward,
-                   moe_grouped_swiglu_gemm_save, moe_permute_backward, moe_route_backward,
+                   moe_grouped_swiglu_gemm_save, moe_layer_backward, moe_permute_backward, moe_route_backward,
                    moe_grouped_down_gemm, moe_grouped_ffn, moe_grouped_rows, moe_grouped_swiglu_gemm, moe_permute,
                    moe_permute_no_workspace, moe_route_grouped_topk, moe_route_permute, moe_route_topk, moe_selftest_bounded_wait,
                    moe_version,

@@ -37,7 +37,7 @@ EXPORTS = ["moe_version", "moe_status_string", "moe_grouped_rows", "moe_workspac
            "moe_balance_workspace_bytes", "moe_balance_loss", "moe_balance_loss_backward",
            "moe_block_norm_workspace_bytes", "moe_block_norm", "moe_block_norm_backward",
            "moe_fp8_quantize", "moe_fp8_dequantize", "moe_grouped_swiglu_gemm_save", "moe_combine_backward",
-           "moe_grouped_ffn_backward", "moe_permute_backward", "moe_route_backward",
+           "moe_grouped_ffn_backward", "moe_permute_backward", "moe_route_backward", "moe_layer_backward",
            "moe_eplb_record", "moe_eplb_rebalance", "moe_eplb_invert", "moe_selftest_bounded_wait"]
 
 
@@ -141,6 +141,8 @@ def lib():
     L.moe_permute_backward.restype = i32
     L.moe_route_backward.argtypes = [pp, i32] + [vp] * 4 + [i32, f32] + [vp] * 3
     L.moe_route_backward.restype = i32
+    L.moe_layer_backward.argtypes = [pp] + [vp] * 12 + [i32, vp, i32, f32] + [vp] * 11 + [i32, i32, vp, vp]
+    L.moe_layer_backward.restype = i32
     L.moe_selftest_bounded_wait.argtypes = [i64, vp, vp]
     L.moe_selftest_bounded_wait.restype = i32
     L.moe_eplb_invert.argtypes = [i32, i32, vp, i32, vp, vp]
@@ -432,8 +434,9 @@ def _fp8_args(values, codes, scales, name: str):
     d, addr = _values(values, name)
     if values.dim() < 1:
         raise ValueError("%s: expected rows of values" % name)
-    *lead, cols = values.shape
-    return (d, torch.Size(lead).numel(), cols, addr, _arg(codes, "codes", torch.uint8, values.shape),
+    shape = values.shape
+    lead, cols = shape[:-1], shape[-1]
+    return (d, lead.numel(), cols, addr, _arg(codes, "codes", torch.uint8, shape),
             _arg(scales, "scales", torch.float32, (*lead, -(-cols // FP8_GROUP))))
 
 
@@ -522,6 +525,32 @@ def moe_route_backward(p: Problem, score: str, logits, ids, w, dw, dlogits, add=
         _arg(w, "w", _F32, (p.T, p.K)), _arg(dw, "dw", _F32, (p.T, p.K)), int(bool(renormalize)), float(scale),
         _arg(add, "add", _F32, (p.T, p.E)), _arg(dlogits, "dlogits", _F32, (p.T, p.E)), _stream(stream)),
         "moe_route_backward")
+
+
+def moe_layer_backward(p: Problem, dout, yg, row_of, ids, w, xg, w13, w2, gu, gu_scales, masked_m, offsets, dyg, wg,
+                       dgu, hg, dxg, dw, dx, dlogits, dw13, dw2, err_flag, score="softmax", logits=None,
+                       renormalize=True, scale: float = 1.0, add=None, accumulate=False, stream=None) -> None:
+    """moe_combine_backward, moe_route_backward, moe_grouped_ffn_backward and moe_permute_backward in one call (moe.h).
+    dyg, wg, dgu, hg, dxg: buffers between the steps, as those calls write them."""
+    rows, n = _train_sizes(p)
+    T, H, I, K = p.T, p.H, p.I, p.K
+    R = (rows, H)
+    TK, TE, TH = (T, K), (T, p.E), (T, H)
+    dt = (dw13 if dw13 is not None else dw2).dtype if dw13 is not None or dw2 is not None else _BF16
+    if dt not in _FLOAT_DTYPES:
+        raise ValueError("dw13, dw2: expected float32 or bfloat16, got %s" % dt)
+    _check(lib().moe_layer_backward(
+        ctypes.byref(p), _arg(dout, "dout", _BF16, TH), _arg(yg, "yg", _BF16, R),
+        _arg(row_of, "row_of", _I32, (T, K + p.has_shared)), _arg(ids, "ids", _I32, TK), _arg(w, "w", _F32, TK),
+        _arg(xg, "xg", _BF16, R), _arg(w13, "w13", _BF16, (n, 2 * I, H)), _arg(w2, "w2", _BF16, (n, H, I)),
+        _arg(gu, "gu", _U8, (rows, 2 * I)), _arg(gu_scales, "gu_scales", _F32, (rows, 2 * I // FP8_GROUP)),
+        _arg(masked_m, "masked_m", _I32, (n,)), _arg(offsets, "offsets", _I32, (n + 1,)), SCORES[score],
+        _arg(logits, "logits", _F32, TE), int(bool(renormalize)), scale, _arg(add, "add", _F32, TE),
+        _arg(dyg, "dyg", _BF16, R), _arg(wg, "wg", _F32, (rows,)), _arg(dgu, "dgu", _BF16, (rows, 2 * I)),
+        _arg(hg, "hg", _BF16, (rows, I)), _arg(dxg, "dxg", _F32, R), _arg(dw, "dw", _F32, TK),
+        _arg(dx, "dx", _BF16, TH), _arg(dlogits, "dlogits", _F32, TE), _arg(dw13, "dw13", dt, (n, 2 * I, H)),
+        _arg(dw2, "dw2", dt, (n, H, I)), _FLOAT_DTYPES[dt], int(bool(accumulate)), _ptr(err_flag), _stream(stream)),
+        "moe_layer_backward")
 
 
 def moe_eplb_record(p: Problem, masked_m, pass_index: int, window: int, load_window, stream=None) -> None:

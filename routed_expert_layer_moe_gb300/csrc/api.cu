@@ -519,26 +519,32 @@ moe_status moe_combine_backward(const moe_problem* p, const void* dout, const vo
   return launched(launch_combine_backward(*p, dout, yg, row_of, w, dyg, wg, dw, (cudaStream_t)stream));
 }
 
+static int check_ffn_backward(const moe_problem& p, const FfnBackwardArgs& a) {
+  if (!float_dtype(a.dw_dtype)) return MOE_ERR_INVALID;
+  if (a.accumulate && a.dw_dtype != MOE_F32) return MOE_ERR_UNSUPPORTED;
+  if (grouped_rows(p) > 0) {
+    if (!a.dyg || !a.w2 || !a.gu || !a.gu_scales || !a.masked_m || !a.offsets || !a.dgu || !a.hg || !a.err)
+      return MOE_ERR_INVALID;
+    if ((a.dxg && !a.w13) || (a.dw13 && !a.xg)) return MOE_ERR_INVALID;
+  }
+  for (const void* q : {a.dyg, a.xg, a.w13, a.w2, (const void*)a.gu, (const void*)a.dgu, (const void*)a.hg,
+                        (const void*)a.dxg, (const void*)a.dw13, (const void*)a.dw2})
+    if (!aligned16(q)) return MOE_ERR_UNSUPPORTED;
+  if (!aligned4(a.wg) || !aligned4(a.gu_scales)) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
 moe_status moe_grouped_ffn_backward(const moe_problem* p, const void* dyg, const float* wg, const void* xg,
                                     const void* w13, const void* w2, const uint8_t* gu, const float* gu_scales,
-                                    const int32_t* masked_m, const int32_t* offsets, void* dgu, void* hg, float* dxg, void* dw13, void* dw2,
-                                    int32_t dw_dtype, int32_t accumulate, int32_t* err_flag, moe_stream_t stream) {
-  const int r = check_training(p);
+                                    const int32_t* masked_m, const int32_t* offsets, void* dgu, void* hg, float* dxg,
+                                    void* dw13, void* dw2, int32_t dw_dtype, int32_t accumulate, int32_t* err_flag,
+                                    moe_stream_t stream) {
+  int r = check_training(p);
   if (r) return (moe_status)r;
-  if (!float_dtype(dw_dtype)) return MOE_ERR_INVALID;
-  if (accumulate && dw_dtype != MOE_F32) return MOE_ERR_UNSUPPORTED;
-  if (grouped_rows(*p) > 0) {
-    if (!dyg || !w2 || !gu || !gu_scales || !masked_m || !offsets || !dgu || !hg || !err_flag) return MOE_ERR_INVALID;
-    if ((dxg && !w13) || (dw13 && !xg)) return MOE_ERR_INVALID;
-  }
-  for (const void* q : {dyg, xg, w13, w2, (const void*)gu, (const void*)dgu, (const void*)hg, (const void*)dxg,
-                        (const void*)dw13, (const void*)dw2})
-    if (!aligned16(q)) return MOE_ERR_UNSUPPORTED;
-  if (!aligned4(wg) || !aligned4(gu_scales)) return MOE_ERR_UNSUPPORTED;
-  FfnBackwardArgs a{};
-  a.dyg = dyg, a.wg = wg, a.xg = xg, a.w13 = w13, a.w2 = w2, a.gu = gu, a.gu_scales = gu_scales;
-  a.masked_m = masked_m, a.offsets = offsets, a.dgu = dgu, a.hg = hg, a.dxg = dxg, a.dw13 = dw13, a.dw2 = dw2;
-  a.dw_dtype = dw_dtype, a.accumulate = accumulate != 0, a.err = err_flag;
+  const FfnBackwardArgs a{dyg, wg, xg, w13, w2, gu, gu_scales, masked_m, offsets, dgu, hg, dxg, dw13, dw2, dw_dtype,
+                          accumulate != 0, err_flag};
+  r = check_ffn_backward(*p, a);
+  if (r) return (moe_status)r;
   return launched(launch_ffn_backward(*p, a, (cudaStream_t)stream));
 }
 
@@ -560,8 +566,35 @@ moe_status moe_route_backward(const moe_problem* p, int32_t score, const float* 
   if (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID) return MOE_ERR_INVALID;
   if (p->T == 0) return MOE_OK;
   if (!ids || !dw || !dlogits || (score == MOE_SCORE_SOFTMAX ? !w : !logits)) return MOE_ERR_INVALID;
-  return launched(launch_route_backward(*p, score, logits, ids, w, dw, renormalize != 0, scale, add, dlogits,
-                                        (cudaStream_t)stream));
+  const RouteBackward route{score, logits, ids, renormalize != 0, scale, add, dlogits};
+  return launched(launch_route_backward(*p, route, w, dw, (cudaStream_t)stream));
+}
+
+moe_status moe_layer_backward(const moe_problem* p, const void* dout, const void* yg, const int32_t* row_of,
+                              const int32_t* ids, const float* w, const void* xg, const void* w13, const void* w2,
+                              const uint8_t* gu, const float* gu_scales, const int32_t* masked_m,
+                              const int32_t* offsets, int32_t score, const float* logits, int32_t renormalize,
+                              float scale, const float* add, void* dyg, float* wg, void* dgu, void* hg, float* dxg,
+                              float* dw, void* dx, float* dlogits, void* dw13, void* dw2, int32_t dw_dtype,
+                              int32_t accumulate, int32_t* err_flag, moe_stream_t stream) {
+  int r = check_training(p);
+  if (r) return (moe_status)r;
+  if (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID) return MOE_ERR_INVALID;
+  const FfnBackwardArgs a{dyg, wg, xg, w13, w2, gu, gu_scales, masked_m, offsets, dgu, hg, dxg, dw13, dw2, dw_dtype,
+                          accumulate != 0, err_flag};
+  r = check_ffn_backward(*p, a);
+  if (r) return (moe_status)r;
+  if (p->T > 0) {
+    if (!dout || !yg || !row_of || !ids || !w || !dyg || !wg || !dw || !dxg || !dx || !dlogits) return MOE_ERR_INVALID;
+    if (score == MOE_SCORE_SIGMOID && !logits) return MOE_ERR_INVALID;
+    if (!aligned16(dout) || !aligned16(yg) || !aligned16(dx)) return MOE_ERR_UNSUPPORTED;
+  }
+  const cudaStream_t st = (cudaStream_t)stream;
+  const RouteBackward route{score, logits, ids, renormalize != 0, scale, add, dlogits};
+  r = launch_combine_backward(*p, dout, yg, row_of, w, dyg, wg, dw, st, &route);
+  if (!r) r = launch_ffn_backward(*p, a, st);
+  if (!r) r = launch_permute_backward(*p, dxg, row_of, dx, st);
+  return launched(r);
 }
 
 moe_status moe_selftest_bounded_wait(int64_t cycles, int32_t* err_flag, moe_stream_t stream) {

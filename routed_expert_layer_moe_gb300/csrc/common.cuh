@@ -156,16 +156,27 @@ struct FfnBackwardArgs {
   const uint8_t* gu;
   const float* gu_scales;
   const int32_t *masked_m, *offsets;
-  void *dgu, *hg, *dxg, *dw13, *dw2;  // dxg, dw13, dw2: null where they are not wanted
+  void *dgu, *hg;
+  float* dxg;
+  void *dw13, *dw2;  // dxg, dw13, dw2: null where they are not wanted
   int dw_dtype, accumulate;
   int32_t* err;
 };
 int launch_ffn_backward(const moe_problem& p, const FfnBackwardArgs& a, cudaStream_t st);
+struct RouteBackward {
+  int score;
+  const float* logits;
+  const int32_t* ids;
+  int renorm;
+  float scale;
+  const float* add;
+  float* dlogits;
+};
 int launch_combine_backward(const moe_problem& p, const void* dout, const void* yg, const int32_t* row_of,
-                            const float* w, void* dyg, float* wg, float* dw, cudaStream_t st);
+                            const float* w, void* dyg, float* wg, float* dw, cudaStream_t st,
+                            const RouteBackward* route = nullptr);  // route: dlogits in the same launch
 int launch_permute_backward(const moe_problem& p, const float* dxg, const int32_t* row_of, void* dx, cudaStream_t st);
-int launch_route_backward(const moe_problem& p, int score, const float* logits, const int32_t* ids, const float* w,
-                          const float* dw, int renorm, float scale, const float* add, float* dlogits,
+int launch_route_backward(const moe_problem& p, const RouteBackward& route, const float* w, const float* dw,
                           cudaStream_t st);
 
 enum { MODE_SWIGLU = 0, MODE_DOWN = 1 };

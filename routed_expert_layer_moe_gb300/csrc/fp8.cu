@@ -2,10 +2,11 @@
 //
 //   s = max |x| * fp32(1 / 448) over the group,  code = E4M3(x / s),  value = code * s
 //
-// The code is that of the exact quotient.  x * (1 / s) is within two units in the last place of it, so only a product
-// that close to the middle between two codes (whose low 19 mantissa bits are zero) can round to the wrong one; there the
-// sign of x - middle * s, exact in one fused multiply-add, says which side the quotient is on.  bf16 values hit such
-// middles often: with an IEEE division and a 64-bit remainder for them 8192 x 4096 took 99 us to quantise.
+// The code is that of the exact quotient.  x * (1 / s) is within two units in the last place of it.  Where two codes
+// meet, the low 19 mantissa bits are zero; so the nearest multiple m of eight units, moved by four units to the side of
+// x - m s (exact in one fused multiply-add), lies between the same two codes as the quotient.  Eight instructions a value;
+// with an IEEE division and its remainder in 64 bits where a middle is near, which bf16 values hit often, 8192 x 4096
+// took 99 us to quantise, with this step taken only there 31.
 #include "fp8.cuh"
 
 namespace moe {
@@ -24,32 +25,32 @@ __device__ __noinline__ float quotient_by_division(float x, float s) {
 }
 
 // A number with the exact quotient's E4M3 code.  inv = 1 / s, or 0 for a scale that is not within [2^-80, 2^100]: in
-// between, a remainder is a multiple of 2^-136 and loses nothing.
+// between, the remainder of a quotient that has a code other than 0 loses nothing.
 __device__ __forceinline__ float quotient(float x, float s, float inv) {
-  const float q = x * inv;
-  const uint32_t b = __float_as_uint(q) + 4u;
-  if ((b & 0x7FFFFu) < 8u && fabsf(q) > 0x1p-11f) {
-    const uint32_t mid = b & ~0x7FFFFu;
-    const float m = __uint_as_float(mid), r = fmaf(-m, s, x);
-    return __uint_as_float(r == 0.0f ? mid : (r > 0.0f) == (m > 0.0f) ? mid + 1u : mid - 1u);
-  }
-  return q;
+  const uint32_t m = (__float_as_uint(x * inv) + 4u) & ~7u;
+  const float r = fmaf(-__uint_as_float(m), s, x);
+  const int side = (int)(__float_as_uint(r) ^ m) >= 0 ? 4 : -4;  // the same sign as m: further from zero
+  return __uint_as_float(r == 0.0f ? m : m + side);
 }
 
 __device__ __forceinline__ float inverse(float s) {
   return s >= 0x1p-80f && s <= 0x1p100f ? __frcp_rn(s) : 0.0f;
 }
 
+// Sixteen consecutive values of a 16-byte aligned array.
 template <typename T>
-__device__ __forceinline__ void load8(const T* x, float (&v)[8]) {
+__device__ __forceinline__ void load16(const T* x, float (&v)[16]) {
   if constexpr (sizeof(T) == 4) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(x)), b = __ldg(reinterpret_cast<const float4*>(x) + 1);
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  } else {
-    const uint4 raw = __ldg(reinterpret_cast<const uint4*>(x));
-    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&raw);
+    float4 a[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 4; ++i) a[i] = __ldg(reinterpret_cast<const float4*>(x) + i);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[4 * i] = a[i].x, v[4 * i + 1] = a[i].y, v[4 * i + 2] = a[i].z, v[4 * i + 3] = a[i].w;
+  } else {
+    const uint4 raw[2] = {__ldg(reinterpret_cast<const uint4*>(x)), __ldg(reinterpret_cast<const uint4*>(x) + 1)};
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(raw);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
       const float2 f = __bfloat1622float2(h[i]);
       v[2 * i] = f.x, v[2 * i + 1] = f.y;
     }
@@ -64,61 +65,71 @@ __device__ __forceinline__ T to_type(float v) {
     return __float2bfloat16_rn(v);
 }
 
-// Rows of whole groups, 16-byte aligned: the groups of all rows lie one after the other.  Eight values a thread,
-// 16 threads a group; n8 is a multiple of 16, so a group's threads are all in range or all out of it.
+// Rows of whole groups, 16-byte aligned: the groups of all rows lie one after the other.  Sixteen values a thread, eight
+// threads a group; n16 is a multiple of 8, so a group's threads are all in range or all out of it.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) quantize_kernel(const T* __restrict__ x, long long n8,
+__global__ void __launch_bounds__(kThreads) quantize_kernel(const T* __restrict__ x, long long n16,
                                                             uint8_t* __restrict__ codes, float* __restrict__ scales) {
   const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
-  float v[8], amax = 0.0f;
-  if (i < n8) {
-    load8(x + 8 * i, v);
+  float v[16], amax = 0.0f;
+  if (i < n16) {
+    load16(x + 16 * i, v);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) amax = fp8_amax(amax, v[j]);
+    for (int j = 0; j < 16; ++j) amax = fp8_amax(amax, v[j]);
   }
 #pragma unroll
-  for (int off = 8; off > 0; off >>= 1) amax = fp8_amax(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-  if (i >= n8) return;
+  for (int off = 4; off > 0; off >>= 1) amax = fp8_amax(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+  if (i >= n16) return;
   const float s = fp8_scale(amax), inv = inverse(s);
-  uint2 c = make_uint2(0u, 0u);
+  uint32_t c[4] = {0u, 0u, 0u, 0u};
   if (s == s) {
     if (inv != 0.0f) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = quotient(v[j], s, inv);
+      for (int j = 0; j < 16; ++j) v[j] = quotient(v[j], s, inv);
     } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = quotient_by_division(v[j], s);
+#pragma unroll 1
+      for (int j = 0; j < 16; ++j) v[j] = quotient_by_division(v[j], s);
     }
-    c.x = fp8_pair(v[0], v[1]) | fp8_pair(v[2], v[3]) << 16;
-    c.y = fp8_pair(v[4], v[5]) | fp8_pair(v[6], v[7]) << 16;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c[j] = fp8_pair(v[4 * j], v[4 * j + 1]) | fp8_pair(v[4 * j + 2], v[4 * j + 3]) << 16;
   }
-  reinterpret_cast<uint2*>(codes)[i] = c;
-  if ((i & 15) == 0) scales[i >> 4] = s;
+  reinterpret_cast<uint4*>(codes)[i] = make_uint4(c[0], c[1], c[2], c[3]);
+  if ((i & 7) == 0) scales[i >> 3] = s;
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) dequantize_kernel(const uint8_t* __restrict__ codes,
-                                                              const float* __restrict__ scales, long long n8,
-                                                              T* __restrict__ out) {
+                                                              const float* __restrict__ scales, long long n16,
+                                                              T* __restrict__ out, bool wide) {
   const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
-  if (i >= n8) return;
-  const uint2 c = __ldg(reinterpret_cast<const uint2*>(codes) + i);
-  const float s = __ldg(scales + (i >> 4));
-  float v[8];
+  if (i >= n16) return;
+  const uint4 raw = __ldg(reinterpret_cast<const uint4*>(codes) + i);
+  const uint32_t c[4] = {raw.x, raw.y, raw.z, raw.w};
+  const float s = __ldg(scales + (i >> 3));
+  float v[16];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float2 f = fp8_unpair((j < 2 ? c.x : c.y) >> (16 * (j & 1)));
+  for (int j = 0; j < 8; ++j) {
+    const float2 f = fp8_unpair(c[j >> 1] >> (16 * (j & 1)));
     v[2 * j] = f.x * s, v[2 * j + 1] = f.y * s;
   }
+  constexpr int N = sizeof(T);  // 16-byte pieces
+  uint4 o[N];
   if constexpr (sizeof(T) == 4) {
-    reinterpret_cast<float4*>(out)[2 * i] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(out)[2 * i + 1] = make_float4(v[4], v[5], v[6], v[7]);
-  } else {
-    uint4 raw;
-    __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&raw);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) h[j] = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-    reinterpret_cast<uint4*>(out)[i] = raw;
+    for (int j = 0; j < 16; ++j) reinterpret_cast<float*>(o)[j] = v[j];
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) reinterpret_cast<__nv_bfloat162*>(o)[j] = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+  }
+  uint4* dst = reinterpret_cast<uint4*>(out) + N * i;
+#pragma unroll
+  for (int j = 0; j < N; j += 2) {
+    if (wide) {
+      st_global_v8(dst + j, o[j], o[j + 1]);
+    } else {
+      dst[j] = o[j];
+      dst[j + 1] = o[j + 1];
+    }
   }
 }
 
@@ -169,9 +180,9 @@ __global__ void __launch_bounds__(kThreads) dequantize_any_kernel(const uint8_t*
 
 template <typename T>
 int quantize(int64_t rows, int64_t cols, const T* x, uint8_t* codes, float* scales, cudaStream_t st) {
-  if (cols % FP8_GROUP == 0 && aligned16(x) && (reinterpret_cast<uintptr_t>(codes) & 7u) == 0) {
-    const long long n8 = rows * cols / 8;
-    quantize_kernel<<<(unsigned)((n8 + kThreads - 1) / kThreads), kThreads, 0, st>>>(x, n8, codes, scales);
+  if (cols % FP8_GROUP == 0 && aligned16(x) && aligned16(codes)) {
+    const long long n16 = rows * cols / 16;
+    quantize_kernel<<<(unsigned)((n16 + kThreads - 1) / kThreads), kThreads, 0, st>>>(x, n16, codes, scales);
   } else {
     const long long per_row = (cols + FP8_GROUP - 1) / FP8_GROUP, groups = rows * per_row;
     quantize_any_kernel<<<(unsigned)((groups + kThreads / 32 - 1) / (kThreads / 32)), kThreads, 0, st>>>(
@@ -182,9 +193,10 @@ int quantize(int64_t rows, int64_t cols, const T* x, uint8_t* codes, float* scal
 
 template <typename T>
 int dequantize(int64_t rows, int64_t cols, const uint8_t* codes, const float* scales, T* out, cudaStream_t st) {
-  if (cols % FP8_GROUP == 0 && aligned16(out) && (reinterpret_cast<uintptr_t>(codes) & 7u) == 0) {
-    const long long n8 = rows * cols / 8;
-    dequantize_kernel<<<(unsigned)((n8 + kThreads - 1) / kThreads), kThreads, 0, st>>>(codes, scales, n8, out);
+  if (cols % FP8_GROUP == 0 && aligned16(out) && aligned16(codes)) {
+    const long long n16 = rows * cols / 16;
+    dequantize_kernel<<<(unsigned)((n16 + kThreads - 1) / kThreads), kThreads, 0, st>>>(
+        codes, scales, n16, out, (reinterpret_cast<uintptr_t>(out) & 31u) == 0);
   } else {
     const long long per_row = (cols + FP8_GROUP - 1) / FP8_GROUP, groups = rows * per_row;
     dequantize_any_kernel<<<(unsigned)((groups + kThreads / 32 - 1) / (kThreads / 32)), kThreads, 0, st>>>(

@@ -6,7 +6,8 @@
 //   DX   dxg = dgu W13                  in fp32: a token's rows of it are still added up
 //   WG   dW[m][n] = sum over the rows of a slot of a[row][m] b[row][n]     (dW13 = dgu^T xg, dW2 = dyg^T (w h))
 //
-// One kernel form for all four: clusters of two CTAs (SM pairs) whose tensor cores work on one tile of 256 x 256
+// Three launches: UP in the forward pass; DH and then DX with WG (GRAD), which need nothing of each other, in the backward
+// pass.  One kernel form for all: clusters of two CTAs (SM pairs) whose tensor cores work on one tile of 256 x 256
 // fp32 accumulators (cta_group::2, M = 256), each CTA staging 128 rows of either operand per 64 values of the reduced
 // dimension: 32 KB a stage for 256 x 256 x 64 multiply-adds a pair.  Persistent; two accumulators in tensor
 // memory, so a tile's epilogue runs beside the next tile's products.
@@ -28,13 +29,15 @@
 // wait is bounded; on expiry the CTA drains its copies and MMAs, frees tensor memory, reports MOE_FLAG_TIMEOUT and
 // returns.
 #include <algorithm>
+#include <type_traits>
 
 #include "fp8.cuh"
 
 namespace moe {
 namespace {
 
-enum { UP = 0, DH = 1, DX = 2, WG = 3 };
+enum { UP = 0, DH = 1, GRAD = 2 };     // launches; GRAD: DX and WG
+enum { ROWS = 0, W13 = 1, W2 = 2 };    // what a unit is a tile of: rows' results (UP, DH, DX) or a gradient of weights
 
 constexpr int KB = 64;                    // reduced values of a stage: 128 bytes of a K-major row
 constexpr int HALF = 128;                 // rows of an operand that one CTA stages
@@ -47,32 +50,44 @@ constexpr int EPI_WARP0 = 4, EPI_WARPS = 8;
 constexpr uint32_t TMEM_COLS = 512, ACC_COLS = 256;
 constexpr int GROUP_M = 8;                // M tiles that neighbouring units share an N tile with
 constexpr long long TIMEOUT = 4000000000LL;  // SM cycles, about 2 s
+// GRAD: stages from which on lanes store their own rows.  Short tiles are bound by their stores, which want whole lines
+// (dW13 + dW2 of 64 rows, 4864 x 4096: 22.9 + 15.7 us own, 19.5 + 12.2 exchanged; 512 rows 35 + 21, 33.5 + 20); beside long
+// ones the exchange's shuffles take shared memory's cycles from the MMAs (1024 rows: 51.6 + 29.0 own, 54 + 30 exchanged).
+constexpr int OWN_ROWS_KB = 12;
 constexpr int NUM_BOXES = 3;              // row boxes of 32, 64 and 128
 __host__ __device__ constexpr int box_rows(int i) { return 32 << i; }
 __host__ __device__ constexpr int box_of(int rows) { return rows <= 32 ? 0 : rows <= 64 ? 1 : 2; }
 
 struct Maps {
-  CUtensorMap a[NUM_BOXES];  // WG: the first alone
-  CUtensorMap b;
+  CUtensorMap a[NUM_BOXES];  // rows, by box
+  CUtensorMap b;             // weights
+  CUtensorMap wa[2], wb[2];  // GRAD: operands of dW13 and dW2
+};
+
+struct WeightGrad {    // dW [slots][rows][cols]
+  int rows, cols;
+  int mt, nt, units;   // tiles; units of a slot: mt * nt, or 0 where the gradient is not wanted
+  uint64_t group_inv;  // ceil(2^64 / (GROUP_M nt))
+  void* out;
 };
 
 struct Params {
   int nslots, masked, M_max;
   long long rows_total;
-  int kb;            // stages of the reduced dimension (WG: by the slot's rows)
-  int mt, nt;        // WG: M tiles; N tiles
-  int b_rows;        // rows of one slot in the weights
-  int ncols;         // columns of the output: UP, DH: I; DX: H; WG: N
-  int m_rows;        // WG: rows of the output a slot
+  int kb;              // UP, DH, DX: stages of the reduced dimension
+  int nt;              // N tiles; GRAD: 0 where dxg is not wanted
   uint64_t group_inv;  // ceil(2^64 / (GROUP_M nt))
+  int b_rows;          // rows of one slot in the weights
+  int ncols;           // columns of the output: UP, DH: I; DX: H
+  WeightGrad w[2];     // GRAD
   int stages;
-  int accumulate;    // WG, fp32: add to what is there
-  int wide;          // the outputs are 32-byte aligned
+  int accumulate;      // dW, fp32: add to what is there
+  int wide;            // the outputs are 32-byte aligned
   const int32_t* masked_m;
   const int32_t* offsets;
-  void* out;         // UP, DH: h (DH: times w) bf16 [rows][I]; DX: dxg fp32 [rows][H]; WG: dW [slots][m_rows][N]
-  void* out2;        // UP: codes [rows][2 I]; DH: dgu bf16 [rows][2 I]
-  float* out2_s;     // UP: scales [rows][2 I / 128]
+  void* out;           // UP, DH: h (DH: times w) bf16 [rows][I]; DX: dxg fp32 [rows][H]
+  void* out2;          // UP: codes [rows][2 I]; DH: dgu bf16 [rows][2 I]
+  float* out2_s;       // UP: scales [rows][2 I / 128]
   const uint8_t* gu;   // DH: codes and scales of the checkpoint
   const float* gu_s;
   const float* wg;     // DH: weights of the rows, or null
@@ -81,58 +96,116 @@ struct Params {
 };
 
 struct Unit {
-  int slot, mi, j;   // slot, M tile (WG) or chunk, N tile
-  int row;           // UP, DH, DX: first row of this CTA's part of the chunk; WG: first row of the slot
-  int nvalid, nall;  // rows of this CTA's part, of both parts; WG: rows of the slot
-  int kb;            // stages
+  int kind, slot, mi, j;  // slot, chunk of rows (weights: M tile), N tile
+  int row;                // first row of this CTA's part of the chunk; weights: first row of the slot
+  int nvalid, nall;       // rows of this CTA's part, of both parts; weights: rows of the slot
+  int kb;                 // stages
 };
 
 // ceil(2^32 / n) for n = 2 .. GROUP_M: r / n = umulhi(r, it) for r < 2^29.
 __constant__ uint32_t kInverse[9] = {0,          0,          0x80000000u, 0x55555556u, 0x40000000u,
                                                0x33333334u, 0x2AAAAAABu, 0x24924925u, 0x20000000u};
 
-// A role's walk over its units: the slot is carried along and nothing is divided, since a look-up
-// stands between the last copies or products of one unit and the first of the next.
+// The slots of a launch in shared memory, by place (GRAD: by descending row count, else their own order).
+struct Slots {
+  int *prefix, *wprefix;  // units before a place: of rows, of weights (GRAD)
+  int *rows, *base;       // rows, first row
+  int* order;             // GRAD: the slot at a place
+};
+
+// A role's walk over its units.  The place is carried along and nothing is divided on the way: a look-up stands between
+// the last copies or products of one unit and the first of the next.
+//
+// Units of rows, all of one cost, are dealt in rounds over the pairs of CTAs.  GRAD goes on with those of weights, the
+// most rows first: to the pairs that the last, partial round of rows left out as many as one unit of rows is worth,
+// then to all, every other round backwards, so that the sums of what each is dealt differ by little (64 experts with 200
+// to 4000 rows: the longest 1.01 to 1.05 of the mean; 1.07 to 1.3 in the slots' own order, always forwards).
 template <int MODE>
 struct Walk {
   const Params& p;
-  const int *prefix, *srows, *sbase, *order;
+  const Slots& s;
   uint32_t rank;
-  int i0, stride;   // this pair of CTAs among all
-  int slot, round;  // the slot's place; units taken so far
+  int i, pairs;           // this pair of CTAs among all
+  int wtotal, mine;       // units of weights; units of rows that are this pair's
+  int first, nlag, ahead, extra;  // pairs from `first` on, nlag of them, get `ahead` units of weights; this one gets `extra`
+  int place, round, u;
+  bool weights;
 
-  // The next unit's number, or one that is not below the total.  WG: slots come in descending order of their rows,
-  // and every other round goes through the pairs backwards, so that the sums of what each is dealt differ by little
-  // (64 experts with 200 to 4000 rows: the longest 1.01 to 1.05 of the mean; 1.07 to 1.3 in the slots' own order).
-  __device__ __forceinline__ int next() {
-    const int k = round++;
-    return k * stride + (MODE == WG && (k & 1) ? stride - 1 - i0 : i0);
+  __device__ __forceinline__ Walk(const Params& p_, const Slots& s_, uint32_t rank_)
+      : p(p_), s(s_), rank(rank_), i((int)cluster_id_x()), pairs((int)nclusters_x()), place(0), round(0), weights(false) {
+    const int total = s.prefix[p.nslots], whole = total / pairs;
+    first = total - whole * pairs;
+    mine = whole + (i < first);
+    wtotal = nlag = ahead = extra = 0;
+    if constexpr (MODE == GRAD) {
+      wtotal = s.wprefix[p.nslots];
+      if (first > 0) {
+        nlag = pairs - first;
+        ahead = (p.kb + 3) / ((s.rows[0] + KB - 1) / KB + 3);  // a tile costs about three stages beside its own
+        if (i >= first) extra = ahead;
+      }
+    }
   }
 
-  __device__ __forceinline__ void seek(int u) {
-    while (prefix[slot + 1] <= u) ++slot;
+  // Goes on to the next unit, number u of its kind; false behind the last.
+  __device__ __forceinline__ bool next() {
+    int k = round++;
+    if (k < mine) {
+      u = k * pairs + i;
+      return true;
+    }
+    if constexpr (MODE != GRAD) return false;
+    if (!weights) {
+      weights = true;
+      place = 0;
+    }
+    k -= mine;
+    if (k < extra) {
+      u = k * nlag + i - first;
+    } else {
+      k -= extra;
+      u = ahead * nlag + k * pairs + (k & 1 ? pairs - 1 - i : i);
+    }
+    return u < wtotal;
   }
 
-  __device__ __forceinline__ Unit at(int u) {
-    seek(u);
+  __device__ __forceinline__ void seek() {
+    const int* prefix = MODE == GRAD && weights ? s.wprefix : s.prefix;
+    while (prefix[place + 1] <= u) ++place;
+  }
+
+  __device__ __forceinline__ Unit unit() {
+    seek();
     Unit U;
-    U.slot = MODE == WG ? order[slot] : slot;
-    const int r = u - prefix[slot], m = srows[slot];
-    const int nm = MODE == WG ? p.mt : (m + 2 * HALF - 1) / (2 * HALF);
+    U.slot = MODE == GRAD ? s.order[place] : place;
+    const int m = s.rows[place];
+    int r = u, nm, nt;
+    uint64_t inv;
+    if (MODE == GRAD && weights) {
+      r -= s.wprefix[place];
+      U.kind = r < p.w[0].units ? W13 : W2;
+      if (U.kind == W2) r -= p.w[0].units;
+      const WeightGrad& w = p.w[U.kind - W13];
+      nm = w.mt, nt = w.nt, inv = w.group_inv;
+    } else {
+      r -= s.prefix[place];
+      U.kind = ROWS;
+      nm = (m + 2 * HALF - 1) / (2 * HALF), nt = p.nt, inv = p.group_inv;
+    }
     // groups of GROUP_M tiles of M, the M tile the fastest within one: a wave of pairs shares operands through L2
-    const int first = (int)__umul64hi((uint64_t)r, p.group_inv) * GROUP_M;
-    const int size = min(GROUP_M, nm - first), rr = r - first * p.nt;
+    const int group = (int)__umul64hi((uint64_t)r, inv) * GROUP_M;
+    const int size = min(GROUP_M, nm - group), rr = r - group * nt;
     U.j = size == 1 ? rr : (int)__umulhi((uint32_t)rr, kInverse[size]);
-    U.mi = first + rr - U.j * size;
-    if constexpr (MODE == WG) {
-      U.row = sbase[slot];
+    U.mi = group + rr - U.j * size;
+    if (U.kind != ROWS) {
+      U.row = s.base[place];
       U.nvalid = U.nall = m;
       U.kb = (m + KB - 1) / KB;
     } else {
       // whole parts of 128 rows as far as they go
       U.nall = min(2 * HALF, m - U.mi * 2 * HALF);
       U.nvalid = rank ? max(U.nall - HALF, 0) : min(U.nall, HALF);
-      U.row = sbase[slot] + U.mi * 2 * HALF + (int)rank * HALF;
+      U.row = s.base[place] + U.mi * 2 * HALF + (int)rank * HALF;
       U.kb = p.kb;
     }
     return U;
@@ -174,12 +247,9 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t saddr) {
          (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 
-template <int MODE>
-__device__ constexpr uint32_t instruction_desc() {
-  uint32_t d = mma_idesc<false>(2 * HALF, 2 * HALF);
-  if (MODE == WG) d |= 1u << 15;              // A: MN-major
-  if (MODE != UP) d |= 1u << 16;              // B: MN-major
-  return d;
+// a_mn, b_mn: the operand is MN-major.
+__host__ __device__ constexpr uint32_t instruction_desc(bool a_mn, bool b_mn) {
+  return mma_idesc<false>(2 * HALF, 2 * HALF) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
 }
 
 __device__ __forceinline__ void tmem_load32(uint32_t taddr, float (&v)[32]) {
@@ -221,29 +291,90 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// N words of a lane's row to memory, 32 bytes (a whole sector) at a time; wide: 32-byte aligned.  Results go straight from
-// the registers: through shared memory, coalesced or by TMA, the stores are fewer cycles of the memory pipe but take
-// them from the MMAs, whose operands come from shared memory at half its rate (dW13 + dW2 of 2 experts of 4096 x 14336,
-// 1024 rows each: 250 + 126 us without stores, 268 + 139 so, 279 + 147 with coalesced 16-byte stores, 284 + 150 by TMA).
+// Transposes pieces of eight words among L = N / 8 neighbouring lanes: piece j of lane i of them becomes piece i of lane j.
 template <int N>
-__device__ __forceinline__ void store_row(void* dst, const uint32_t (&v)[N], bool wide) {
-  uint4* q = static_cast<uint4*>(dst);
+__device__ __forceinline__ void exchange_pieces(uint32_t (&v)[N], int lane) {
+  constexpr int L = N / 8;
 #pragma unroll
-  for (int i = 0; i < N / 8; ++i) {
-    const uint4 a = make_uint4(v[8 * i], v[8 * i + 1], v[8 * i + 2], v[8 * i + 3]);
-    const uint4 b = make_uint4(v[8 * i + 4], v[8 * i + 5], v[8 * i + 6], v[8 * i + 7]);
-    if (wide) {
-      st_global_v8(q + 2 * i, a, b);
-    } else {
-      q[2 * i] = a;
-      q[2 * i + 1] = b;
+  for (int d = 1; d < L; d *= 2) {
+    const bool up = lane & d;
+#pragma unroll
+    for (int j = 0; j < L; ++j)
+      if (!(j & d)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          uint32_t &lo = v[8 * j + i], &hi = v[8 * (j + d) + i];
+          const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? lo : hi, d);
+          if (up)
+            lo = got;
+          else
+            hi = got;
+        }
+      }
+  }
+}
+
+// N words of each lane's row to memory, without shared memory: through it, coalesced or by TMA, the stores take cycles
+// of it from the MMAs, whose operands come from there at half its rate.  A lane storing its own row would touch 32 lines
+// an instruction (4.3 TB/s for whole tiles, 5.4 with whole lines); so L = N / 8 lanes first exchange their pieces of 32
+// bytes, after which each holds one piece of L rows, and L lanes store 32 L bytes of a row together.
+// first: the warp's first row; rows: how many of the 32 are written; add: to the fp32 values there; wide: 32-byte aligned.
+// own: without the exchange.
+template <int N>
+__device__ __forceinline__ void store_rows(void* first, size_t stride, int lane, uint32_t (&v)[N], int rows, bool wide,
+                                           bool add = false, bool own = false) {
+  constexpr int L = N / 8;
+  if (!own) exchange_pieces(v, lane);
+  // piece j of the lane: of row r0 + j, or of the lane's own row
+  const int r0 = own ? lane : lane / L * L;
+  const size_t step = own ? 32 : stride;
+  uint8_t* at = static_cast<uint8_t*>(first) + (size_t)r0 * stride + (own ? 0 : 32 * (lane % L));
+#pragma unroll
+  for (int j = 0; j < L; ++j) {
+    if (r0 + (own ? 0 : j) < rows) {
+      uint4* q = reinterpret_cast<uint4*>(at + j * step);
+      uint32_t* x = &v[8 * j];
+      if (add) {
+        const float4 f = reinterpret_cast<const float4*>(q)[0], g = reinterpret_cast<const float4*>(q)[1];
+        const float old[8] = {f.x, f.y, f.z, f.w, g.x, g.y, g.z, g.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) + old[i]);
+      }
+      const uint4 a = make_uint4(x[0], x[1], x[2], x[3]), b = make_uint4(x[4], x[5], x[6], x[7]);
+      if (wide) {
+        st_global_v8(q, a, b);
+      } else {
+        q[0] = a;
+        q[1] = b;
+      }
     }
+  }
+}
+
+// 128 columns of a warp's 32 accumulator rows to memory; zero: zeros in their place.
+template <typename OUT>
+__device__ __forceinline__ void store_tile(OUT* first, int cols, int lane, uint32_t acc, int rows, bool zero, bool add,
+                                           bool wide, bool own) {
+  constexpr int COLS = 128 / sizeof(OUT);  // 128 bytes of a row at a time
+#pragma unroll 1
+  for (int c = 0; c < HALF; c += COLS) {
+    uint32_t v[32];
+    if (zero) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = 0u;
+    } else {
+      float d[COLS];
+      tmem_load<COLS>(acc + (uint32_t)c, d);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = sizeof(OUT) == 2 ? pack2(d[(2 * i) % COLS], d[(2 * i + 1) % COLS]) : __float_as_uint(d[i]);
+    }
+    store_rows(first + c, (size_t)cols * sizeof(OUT), lane, v, rows, wide, sizeof(OUT) == 4 && add, own);
   }
 }
 
 // The epilogue of one tile, warp `ew` of the eight: lanes 32 (ew & 3) .. of the CTA's 128 accumulator rows, columns
 // 128 (ew >> 2) .. of its 256 (UP: 64 of the gate's and the same 64 of the up's).  acc: the warp's lanes and the
-// tile's first column; `zero`: there is no accumulator, the tile is zeros (WG without rows).
+// tile's first column; `zero`: there is no accumulator, the tile is zeros (dW of a slot without rows).
 template <int MODE, typename OUT>
 __device__ __forceinline__ void epilogue(const Params& p, const Unit& U, uint32_t rank, int ew, int lane, uint32_t acc,
                                          float* ex, bool zero) {
@@ -270,44 +401,44 @@ __device__ __forceinline__ void epilogue(const Params& p, const Unit& U, uint32_
     const float sg = fp8_scale(fp8_amax(ag, other.x)), su = fp8_scale(fp8_amax(au, other.y));
     // one division a group; the codes' inputs are fp32 sums, so a reciprocal's last bit is within their own error
     const float ig = 1.0f / sg, iu = 1.0f / su;
-    const bool live = r < U.nvalid;
     const size_t row = (size_t)U.row + r;
-    if (half == 0 && live) {
+    if (half == 0 && r < U.nvalid) {
       p.out2_s[row * (2 * I / FP8_GROUP) + U.j] = sg;
       p.out2_s[row * (2 * I / FP8_GROUP) + I / FP8_GROUP + U.j] = su;
     }
+    const int rows = U.nvalid - 32 * quad;
+    const size_t row0 = (size_t)U.row + 32 * quad;
+    uint32_t qg[16], qu[16];
 #pragma unroll
     for (int c = 0; c < 64; c += 32) {
       tmem_load32(acc + 64 * half + c, g);
       tmem_load32(acc + HALF + 64 * half + c, u);
       tmem_loaded32(g);
       tmem_loaded32(u);
-      uint32_t h[16], qg[8], qu[8];
+      uint32_t h[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) h[i] = pack2(silu(g[2 * i]) * u[2 * i], silu(g[2 * i + 1]) * u[2 * i + 1]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {  // a group without a scale has codes 0
-        qg[i] = sg != sg ? 0u : fp8_pair(g[4 * i] * ig, g[4 * i + 1] * ig) | fp8_pair(g[4 * i + 2] * ig, g[4 * i + 3] * ig) << 16;
-        qu[i] = su != su ? 0u : fp8_pair(u[4 * i] * iu, u[4 * i + 1] * iu) | fp8_pair(u[4 * i + 2] * iu, u[4 * i + 3] * iu) << 16;
+        qg[c / 4 + i] = sg != sg ? 0u : fp8_pair(g[4 * i] * ig, g[4 * i + 1] * ig) | fp8_pair(g[4 * i + 2] * ig, g[4 * i + 3] * ig) << 16;
+        qu[c / 4 + i] = su != su ? 0u : fp8_pair(u[4 * i] * iu, u[4 * i + 1] * iu) | fp8_pair(u[4 * i + 2] * iu, u[4 * i + 3] * iu) << 16;
       }
-      if (live) {
-        store_row(static_cast<__nv_bfloat16*>(p.out) + row * I + c0 + c, h, p.wide);
-        uint8_t* code = static_cast<uint8_t*>(p.out2) + row * 2 * I + c0 + c;
-        store_row(code, qg, p.wide);
-        store_row(code + I, qu, p.wide);
-      }
+      store_rows(static_cast<__nv_bfloat16*>(p.out) + row0 * I + c0 + c, (size_t)I * 2, lane, h, rows, p.wide);
     }
+    uint8_t* code = static_cast<uint8_t*>(p.out2) + row0 * 2 * I + c0;
+    store_rows(code, (size_t)I * 2, lane, qg, rows, p.wide);
+    store_rows(code + I, (size_t)I * 2, lane, qu, rows, p.wide);
   } else if constexpr (MODE == DH) {
     const int I = p.ncols, c0 = U.j * 2 * HALF + HALF * half;
     if (c0 >= I || U.nvalid <= 32 * quad) return;
-    const bool live = r < U.nvalid;
-    const size_t row = (size_t)U.row + (live ? r : 0);  // a lane without a row reads the first one's
+    const int rows = U.nvalid - 32 * quad;
+    const size_t row0 = (size_t)U.row + 32 * quad, row = row0 + (lane < rows ? lane : 0);
     const int n = 2 * I / FP8_GROUP;
     const float w = p.wg ? p.wg[row] : 1.0f;
     const float sg = p.gu_s[row * n + c0 / FP8_GROUP], su = p.gu_s[row * n + (I + c0) / FP8_GROUP];
     const uint4* code = reinterpret_cast<const uint4*>(p.gu + row * 2 * I + c0);
-    __nv_bfloat16* dgu = static_cast<__nv_bfloat16*>(p.out2) + row * 2 * I + c0;
-    __nv_bfloat16* hg = static_cast<__nv_bfloat16*>(p.out) + row * I + c0;
+    __nv_bfloat16* dgu = static_cast<__nv_bfloat16*>(p.out2) + row0 * 2 * I + c0;
+    __nv_bfloat16* hg = static_cast<__nv_bfloat16*>(p.out) + row0 * I + c0;
 #pragma unroll 1
     for (int c = 0; c < HALF; c += 32) {
       const uint4 g0 = __ldg(code + c / 16), g1 = __ldg(code + c / 16 + 1);
@@ -335,46 +466,25 @@ __device__ __forceinline__ void epilogue(const Params& p, const Unit& U, uint32_
         vu[i] = pack2(du[0], du[1]);
         vh[i] = pack2(h[0], h[1]);
       }
-      if (live) {
-        store_row(dgu + c, vg, p.wide);
-        store_row(dgu + I + c, vu, p.wide);
-        store_row(hg + c, vh, p.wide);
-      }
+      store_rows(dgu + c, (size_t)I * 4, lane, vg, rows, p.wide);
+      store_rows(dgu + I + c, (size_t)I * 4, lane, vu, rows, p.wide);
+      store_rows(hg + c, (size_t)I * 2, lane, vh, rows, p.wide);
     }
   } else {
-    // DX: rows of the chunk; WG: rows of the slot's gradient, whole tiles of 128
-    const int N = p.ncols, c0 = U.j * 2 * HALF + HALF * half;
-    if (c0 >= N || (MODE == WG ? U.mi * 2 * HALF + (int)rank * HALF >= p.m_rows : U.nvalid <= 32 * quad)) return;
-    const bool live = MODE == WG || r < U.nvalid;
-    const size_t row = MODE == WG ? (size_t)U.slot * p.m_rows + U.mi * 2 * HALF + rank * HALF + r : (size_t)U.row + r;
-    OUT* dst = static_cast<OUT*>(p.out) + row * N + c0;
-    constexpr int COLS = 128 / sizeof(OUT);  // 128 bytes of a row at a time
-#pragma unroll 1
-    for (int c = 0; c < HALF; c += COLS) {
-      float d[COLS];
-      if (zero) {
-#pragma unroll
-        for (int i = 0; i < COLS; ++i) d[i] = 0.0f;
-      } else {
-        tmem_load<COLS>(acc + HALF * half + (uint32_t)c, d);
-      }
-      uint32_t v[32];
-      if constexpr (sizeof(OUT) == 2) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = pack2(d[2 * i], d[2 * i + 1]);
-      } else {
-        if (MODE == WG && p.accumulate) {
-          const float4* old = reinterpret_cast<const float4*>(dst + c);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float4 f = old[i];
-            d[4 * i] += f.x, d[4 * i + 1] += f.y, d[4 * i + 2] += f.z, d[4 * i + 3] += f.w;
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(d[i]);
-      }
-      if (live) store_row(dst + c, v, p.wide);
+    const int c0 = U.j * 2 * HALF + HALF * half;
+    acc += HALF * half;
+    const bool own = U.kb >= OWN_ROWS_KB;
+    if (U.kind == ROWS) {
+      const int rows = U.nvalid - 32 * quad;
+      if (c0 < p.ncols && rows > 0)
+        store_tile(static_cast<float*>(p.out) + ((size_t)U.row + 32 * quad) * p.ncols + c0, p.ncols, lane, acc, rows,
+                   false, false, p.wide, own);
+    } else {
+      const WeightGrad& w = p.w[U.kind - W13];
+      const int m = U.mi * 2 * HALF + (int)rank * HALF;  // whole tiles of 128 rows and columns
+      if (c0 < w.cols && m < w.rows)
+        store_tile(static_cast<OUT*>(w.out) + ((size_t)U.slot * w.rows + m + 32 * quad) * w.cols + c0, w.cols, lane, acc,
+                   32, zero, p.accumulate, p.wide, own);
     }
   }
 }
@@ -401,13 +511,15 @@ __global__ void __launch_bounds__(THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
   float* ex = reinterpret_cast<float*>(smem + p.ex_off);   // UP: [2 tiles][2 halves][128 rows] (gate, up) magnitudes
-  int* prefix = reinterpret_cast<int*>(smem + p.pre_off);  // [nslots + 1] unit prefix
-  int* srows = prefix + p.nslots + 1;
-  int* sbase = srows + p.nslots;
-  int* order = sbase + p.nslots;  // WG: slots by descending row count; srows, sbase and prefix go by place in it
+  Slots S;
+  S.prefix = reinterpret_cast<int*>(smem + p.pre_off);
+  S.rows = S.prefix + p.nslots + 1;
+  S.base = S.rows + p.nslots;
+  S.order = S.base + p.nslots;
+  S.wprefix = S.order + p.nslots;  // GRAD: [nslots + 1]
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + p.bar_off);
   uint64_t* empty = full + MAX_STAGES;
-  uint64_t* landed = empty + MAX_STAGES;  // WG, the last stage that needs zeros: this CTA's copies are there
+  uint64_t* landed = empty + MAX_STAGES;  // weights, the last stage that needs zeros: this CTA's copies are there
   uint64_t* fixed = landed + 1;           // both CTAs have written the zeros
   uint64_t* last_empty = fixed + 1;       // the MMAs have read it
   uint64_t* tfull = last_empty + 1;       // [2] accumulators written
@@ -453,38 +565,41 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (p.masked) m = min(m, p.M_max);
     if (base < 0 || base > p.rows_total) base = p.rows_total;  // no counts may lead outside the buffers
     m = (int)max(0LL, min((long long)m, p.rows_total - base));
-    if constexpr (MODE == WG) {
-      order[s] = m;  // the row counts, until they are in order
+    if constexpr (MODE == GRAD) {
+      S.order[s] = m;  // the row counts, until they are in order
     } else {
-      srows[s] = m;
-      sbase[s] = (int)base;
-      prefix[s + 1] = (m + 2 * HALF - 1) / (2 * HALF) * p.nt;
+      S.rows[s] = m;
+      S.base[s] = (int)base;
+      S.prefix[s + 1] = (m + 2 * HALF - 1) / (2 * HALF) * p.nt;
     }
   }
-  if constexpr (MODE == WG) {
+  if constexpr (MODE == GRAD) {
     __syncthreads();
-    int place[3];  // of this thread's slots: at most 1024 of them
+    int place[3];  // of this thread's slots: there are at most 1024
     int i = 0;
     for (int s = tid; s < p.nslots; s += THREADS, ++i) {
-      const int m = order[s];
+      const int m = S.order[s];
       int n = 0;
-      for (int t = 0; t < p.nslots; ++t) n += order[t] > m || (order[t] == m && t < s);
+      for (int t = 0; t < p.nslots; ++t) n += S.order[t] > m || (S.order[t] == m && t < s);
       place[i] = n;
-      srows[n] = m;
-      prefix[n + 1] = m == 0 && p.accumulate ? 0 : p.mt * p.nt;
+      S.rows[n] = m;
+      S.prefix[n + 1] = (m + 2 * HALF - 1) / (2 * HALF) * p.nt;
+      S.wprefix[n + 1] = m == 0 && p.accumulate ? 0 : p.w[0].units + p.w[1].units;
     }
     __syncthreads();
     i = 0;
     for (int s = tid; s < p.nslots; s += THREADS, ++i) {
-      order[place[i]] = s;
+      S.order[place[i]] = s;
       const long long base = p.masked ? (long long)s * p.M_max : (long long)__ldcg(p.offsets + s);
-      sbase[place[i]] = (int)(base < 0 || base > p.rows_total ? p.rows_total : base);
+      S.base[place[i]] = (int)(base < 0 || base > p.rows_total ? p.rows_total : base);
     }
   }
-  if (tid == 0) prefix[0] = 0;
+  if (tid == 0) S.prefix[0] = 0;
+  if (MODE == GRAD && tid == 0) S.wprefix[0] = 0;
   tc_fence_before_sync();
   __syncthreads();
-  if (warp == 0) {
+  if (warp == 0 || (MODE == GRAD && warp == 1)) {
+    int* prefix = warp == 0 ? S.prefix : S.wprefix;
     int run = 0;
     for (int base = 1; base <= p.nslots; base += 32) {
       const int i = base + lane;
@@ -502,28 +617,28 @@ __global__ void __launch_bounds__(THREADS, 1)
   cluster_sync_all();  // both CTAs' barriers are initialised before either CTA touches the other's
   tc_fence_after_sync();
   const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_base_smem, 0);
-  const int total = prefix[p.nslots];
-  Walk<MODE> walk{p, prefix, srows, sbase, order, rank, (int)cluster_id_x(), (int)nclusters_x(), 0, 0};
+  Walk<MODE> walk(p, S, rank);
   // rows of a slot's last stage that are in its last MMA's 16 but behind the last row
-  auto ragged = [](const Unit& U) { return MODE == WG && U.kb > 0 && (U.nvalid & 15) != 0; };
+  auto ragged = [](const Unit& U) { return MODE == GRAD && U.kind != ROWS && (U.nvalid & 15) != 0; };
 
   if (warp == 0) {
     // -------------------------------------------------------------- producer
     if (lane == 0) {
-      const CUtensorMap* mb = &maps.b;
       int stage = 0;
       uint32_t phase = 0, lphase = 0;
       bool ok = true;
-      for (int u; ok && (u = walk.next()) < total;) {
-        const Unit U = walk.at(u);
-        const CUtensorMap* ma = &maps.a[MODE == WG ? 0 : box_of(U.nvalid)];
+      while (ok && walk.next()) {
+        const Unit U = walk.unit();
+        const bool weights = MODE == GRAD && U.kind != ROWS;
+        const CUtensorMap* ma = weights ? &maps.wa[U.kind - W13] : &maps.a[box_of(U.nvalid)];
+        const CUtensorMap* mb = weights ? &maps.wb[U.kind - W13] : &maps.b;
         auto row_bytes = [](int rows) { return rows > 0 ? (uint32_t)box_rows(box_of(rows)) * KB * 2 : 0u; };
         // of both CTAs; a part without rows copies none
-        const uint32_t bytes = MODE == WG ? 2 * STAGE
-                                          : row_bytes(min(U.nall, HALF)) + row_bytes(U.nall - HALF) + 2 * OP_BYTES;
-        const int am = MODE == WG ? U.mi * 2 * HALF + (int)rank * HALF : 0;
+        const uint32_t bytes = weights ? 2 * STAGE
+                                       : row_bytes(min(U.nall, HALF)) + row_bytes(U.nall - HALF) + 2 * OP_BYTES;
+        const int am = U.mi * 2 * HALF + (int)rank * HALF;
         const int bn = U.j * (MODE == UP ? HALF : 2 * HALF) + (MODE == UP ? 0 : (int)rank * HALF);
-        const int brow = MODE == UP ? U.slot * p.b_rows + (int)rank * p.ncols + bn : U.slot * p.b_rows;
+        const int brow = weights ? U.row : U.slot * p.b_rows + (MODE == UP ? (int)rank * p.ncols + bn : 0);
         const int whole = ragged(U) ? U.kb - 1 : U.kb;  // stages that go through the ring
         for (int kb = 0; ok && kb <= whole; ++kb) {
           // the last stage's place is free at the latest when the ring has gone round once in this tile
@@ -552,7 +667,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           // the leader's barrier counts both CTAs' copies
           if (leader) mbar_arrive_expect_tx(&full[stage], bytes);
           const uint32_t bar = mapa_shared(&full[stage], 0);
-          if constexpr (MODE == WG) {
+          if (weights) {
             for (int h = 0; h < 2; ++h) tma_load_2d_pair(sa + h * BOX_BYTES, ma, bar, am + 64 * h, U.row + k);
           } else if (U.nvalid > 0) {
             tma_load_2d_pair(sa, ma, bar, k, U.row);
@@ -560,8 +675,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           if constexpr (MODE == UP) {
             tma_load_2d_pair(sb, mb, bar, k, brow);
           } else {
-            const int y = MODE == WG ? U.row + k : brow + k;
-            for (int h = 0; h < 2; ++h) tma_load_2d_pair(sb + h * BOX_BYTES, mb, bar, bn + 64 * h, y);
+            for (int h = 0; h < 2; ++h) tma_load_2d_pair(sb + h * BOX_BYTES, mb, bar, bn + 64 * h, brow + k);
           }
           if (++stage == stages) {
             stage = 0;
@@ -573,25 +687,22 @@ __global__ void __launch_bounds__(THREADS, 1)
   } else if (warp == 1) {
     // -------------------------------------------------------------- MMAs: a converged warp, one elected lane
     const uint32_t s0 = smem_u32(smem);
-    const uint64_t da0 = MODE == WG ? desc_mn(s0) : smem_desc_sw128(s0);
-    const uint64_t db0 = MODE == UP ? smem_desc_sw128(s0 + OP_BYTES) : desc_mn(s0 + OP_BYTES);
-    // 16 values of k: 32 bytes of a K-major row, 16 rows of an MN-major box
-    constexpr uint32_t STEP_A = MODE == WG ? 16 * 128 / 16 : 2, STEP_B = MODE == UP ? 2 : 16 * 128 / 16;
-    constexpr uint32_t idesc = instruction_desc<MODE>();
     int stage = 0;
     uint32_t phase = 0, fphase = 0, it = 0;
     bool ok = true, any = false;
-    int nkb = p.kb, rows = 0;
-    for (int u; ok && leader && (u = walk.next()) < total;) {
-      if constexpr (MODE == WG) {
-        walk.seek(u);
-        rows = __shfl_sync(0xffffffffu, srows[walk.slot], 0);
-        nkb = (rows + KB - 1) / KB;
-        if (nkb == 0) continue;
-      }
+    // The MMAs of a unit of nkb stages.  WEIGHTS: of a slot's `rows`, the reduced dimension.  The two kinds are code of
+    // their own, so that all that an MMA takes but the stage is a constant.
+    auto products = [&](auto weights_, int nkb, int rows) {
+      constexpr bool WEIGHTS = decltype(weights_)::value;
+      const uint64_t da0 = WEIGHTS ? desc_mn(s0) : smem_desc_sw128(s0);
+      const uint64_t db0 = MODE == UP ? smem_desc_sw128(s0 + OP_BYTES) : desc_mn(s0 + OP_BYTES);
+      // 16 values of k: 32 bytes of a K-major row, 16 rows of an MN-major box
+      constexpr uint32_t STEP_K = 2, STEP_MN = 16 * 128 / 16;
+      constexpr uint32_t STEP_A = WEIGHTS ? STEP_MN : STEP_K, STEP_B = MODE == UP ? STEP_K : STEP_MN;
+      constexpr uint32_t idesc = instruction_desc(WEIGHTS, MODE != UP);
       const uint32_t d = tmem_base + (it & 1u) * ACC_COLS;
       ok = __all_sync(0xffffffffu, mbar_wait<true>(&tempty[it & 1u], ((it >> 1) & 1u) ^ 1u, abort_flag, TIMEOUT));
-      if (!ok) break;
+      if (!ok) return;
       tc_fence_after_sync();
       // one stage's MMAs, of `steps` times 16 values of k
       auto multiply = [&](int at, int steps, bool first, uint64_t* done) {
@@ -600,31 +711,40 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (elect_one()) {
 #pragma unroll
           for (int ks = 0; ks < KB / 16; ++ks)
-            if (MODE != WG || ks < steps) mma_pair(d, da + ks * STEP_A, db + ks * STEP_B, idesc, !first || ks > 0);
+            if (!WEIGHTS || ks < steps) mma_pair(d, da + ks * STEP_A, db + ks * STEP_B, idesc, !first || ks > 0);
           tc_commit_pair(done, 3);
         }
         __syncwarp();
         any = true;
       };
-      const int whole = MODE == WG && (rows & 15) ? nkb - 1 : nkb;
+      const int whole = WEIGHTS && (rows & 15) ? nkb - 1 : nkb;
       for (int kb = 0; kb < whole; ++kb) {
         ok = __all_sync(0xffffffffu, mbar_wait<true>(&full[stage], phase, abort_flag, TIMEOUT));
-        if (!ok) break;
-        multiply(stage, MODE == WG && kb == nkb - 1 ? (rows - kb * KB) / 16 : KB / 16, kb == 0, &empty[stage]);
+        if (!ok) return;
+        multiply(stage, WEIGHTS && kb == nkb - 1 ? (rows - kb * KB) / 16 : KB / 16, kb == 0, &empty[stage]);
         if (++stage == stages) {
           stage = 0;
           phase ^= 1u;
         }
       }
-      if (MODE == WG && ok && whole < nkb) {
+      if (WEIGHTS && whole < nkb) {
         ok = __all_sync(0xffffffffu, mbar_wait<true>(fixed, fphase, abort_flag, TIMEOUT));
-        if (!ok) break;
+        if (!ok) return;
         fphase ^= 1u;
         multiply(stages, (rows - whole * KB + 15) / 16, whole == 0, last_empty);
       }
-      if (ok && elect_one()) tc_commit_pair(&tfull[it & 1u], 3);
+      if (elect_one()) tc_commit_pair(&tfull[it & 1u], 3);
       __syncwarp();
       ++it;
+    };
+    while (ok && leader && walk.next()) {
+      if (MODE != GRAD || !walk.weights) {
+        products(std::false_type{}, p.kb, 0);
+      } else {
+        walk.seek();
+        const int rows = __shfl_sync(0xffffffffu, S.rows[walk.place], 0);
+        if (rows > 0) products(std::true_type{}, (rows + KB - 1) / KB, rows);
+      }
     }
     if (!ok && any && elect_one()) {
       // all MMAs issued by this thread must finish before tensor memory is freed
@@ -635,12 +755,13 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     __syncwarp();
   } else if (warp == 2) {
-    // -------------------------------------------------------------- WG: zeros behind a slot's last row
-    if constexpr (MODE == WG) {
+    // -------------------------------------------------------------- weights: zeros behind a slot's last row
+    if constexpr (MODE == GRAD) {
       uint32_t lphase = 0;
-      for (int u; (u = walk.next()) < total;) {
-        walk.seek(u);
-        const int m = srows[walk.slot];
+      while (walk.next()) {
+        if (!walk.weights) continue;
+        walk.seek();
+        const int m = S.rows[walk.place];
         if ((m & 15) == 0) continue;
         if (!__all_sync(0xffffffffu, mbar_wait(landed, lphase, abort_flag, TIMEOUT))) break;
         lphase ^= 1u;
@@ -657,9 +778,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     // -------------------------------------------------------------- epilogue
     const int ew = warp - EPI_WARP0;
     uint32_t it = 0;
-    for (int u; (u = walk.next()) < total;) {
-      const Unit U = walk.at(u);
-      if (MODE == WG && U.kb == 0) {
+    while (walk.next()) {
+      const Unit U = walk.unit();
+      if (MODE == GRAD && U.kb == 0) {
         epilogue<MODE, OUT>(p, U, rank, ew, lane, 0u, ex, true);
         continue;
       }
@@ -707,10 +828,12 @@ __global__ void __launch_bounds__(THREADS, 1)
 // Host side
 // ---------------------------------------------------------------------------
 
-// Shared memory of a launch: as many stages as fit.
+// Shared memory of a launch: as many stages as fit, but one less in GRAD, whose last stages have a place of their own:
+// what a launch leaves of the SM's memory is the L1 that stores go through (dW13 + dW2 of 64 experts of 2048 x 1024:
+// 380 + 209 us with six and that place, 370 + 196 with five).
 int lay_out(Params& prm, int mode, size_t* smem) {
-  for (int st = MAX_STAGES; st >= 2; --st) {
-    size_t off = (size_t)(mode == WG ? st + 1 : st) * STAGE;  // WG: and the last stage's place
+  for (int st = mode == GRAD ? MAX_STAGES - 1 : MAX_STAGES; st >= 2; --st) {
+    size_t off = (size_t)(mode == GRAD ? st + 1 : st) * STAGE;  // GRAD: and the place of a slot's last stage
     auto carve = [&](size_t bytes, size_t align) {
       off = align_up(off, align);
       const size_t at = off;
@@ -718,7 +841,7 @@ int lay_out(Params& prm, int mode, size_t* smem) {
       return (uint32_t)at;
     };
     prm.ex_off = carve(mode == UP ? 2 * 2 * HALF * 2 * sizeof(float) : 0, 16);
-    prm.pre_off = carve((4 * (size_t)prm.nslots + 1) * 4, 16);
+    prm.pre_off = carve((5 * (size_t)prm.nslots + 2) * 4, 16);
     prm.bar_off = carve((2 * MAX_STAGES + 9) * 8, 8);
     prm.misc_off = carve(16, 16);
     if ((int)(off + 1024) <= device_info().max_smem_optin) {
@@ -739,8 +862,9 @@ void cluster_attribute(cudaLaunchAttribute* a) {
 
 template <int MODE, typename OUT>
 int launch(Params prm, const Maps& maps, cudaStream_t st) {
-  prm.wide = ((reinterpret_cast<uintptr_t>(prm.out) | reinterpret_cast<uintptr_t>(prm.out2)) & 31u) == 0;
-  prm.group_inv = ~0ull / (uint64_t)(GROUP_M * prm.nt) + 1;  // the divisor is at least 8: no overflow
+  prm.wide = 1;
+  for (const void* q : {(const void*)prm.out, (const void*)prm.out2, (const void*)prm.w[0].out, (const void*)prm.w[1].out})
+    if (reinterpret_cast<uintptr_t>(q) & 31u) prm.wide = 0;
   auto kern = train_gemm_kernel<MODE, OUT>;
   static bool attr_set[64] = {};
   static int clusters[64] = {};  // clusters of two that the device keeps resident at once
@@ -792,33 +916,35 @@ Params common_params(const moe_problem& p, const int32_t* masked_m, const int32_
   return prm;
 }
 
+// ceil(2^64 / (GROUP_M nt)): the divisor is at least 8, so it does not overflow.
+uint64_t group_inverse(int nt) { return nt ? ~0ull / ((uint64_t)GROUP_M * nt) + 1 : 0; }
+
 // Rows of the M side [rows][K] times the weights [slots][b_rows][b_cols].
-template <int MODE, typename OUT = __nv_bfloat16>
-int launch_rows(Params prm, const void* a, int K, const void* w, int b_rows, int b_cols, int ncols, cudaStream_t st) {
-  Maps maps{};
+int plan_rows(int mode, Params& prm, Maps& maps, const void* a, int K, const void* w, int b_rows, int b_cols, int ncols) {
   for (int i = 0; i < NUM_BOXES; ++i)
     if (!map_of(&maps.a[i], a, K, (uint64_t)prm.rows_total, box_rows(i))) return MOE_ERR_CUDA;
-  if (!map_of(&maps.b, w, b_cols, (uint64_t)prm.nslots * b_rows, MODE == UP ? HALF : KB)) return MOE_ERR_CUDA;
+  if (!map_of(&maps.b, w, b_cols, (uint64_t)prm.nslots * b_rows, mode == UP ? HALF : KB)) return MOE_ERR_CUDA;
   prm.kb = K / KB;
   prm.b_rows = b_rows;
   prm.ncols = ncols;
-  prm.nt = MODE == UP ? ncols / HALF : (ncols + 2 * HALF - 1) / (2 * HALF);
-  return launch<MODE, OUT>(prm, maps, st);
+  prm.nt = mode == UP ? ncols / HALF : (ncols + 2 * HALF - 1) / (2 * HALF);
+  prm.group_inv = group_inverse(prm.nt);
+  return MOE_OK;
 }
 
 // a [rows][M], b [rows][N] -> dw [slots][M][N].
-int launch_weight_grad(Params prm, const void* a, int M, const void* b, int N, void* dw, int dw_dtype, int accumulate,
-                       cudaStream_t st) {
-  Maps maps{};
-  if (!map_of(&maps.a[0], a, M, (uint64_t)prm.rows_total, KB)) return MOE_ERR_CUDA;
-  if (!map_of(&maps.b, b, N, (uint64_t)prm.rows_total, KB)) return MOE_ERR_CUDA;
-  prm.m_rows = M;
-  prm.ncols = N;
-  prm.mt = (M + 2 * HALF - 1) / (2 * HALF);
-  prm.nt = (N + 2 * HALF - 1) / (2 * HALF);
-  prm.out = dw;
-  prm.accumulate = accumulate;
-  return dw_dtype == MOE_F32 ? launch<WG, float>(prm, maps, st) : launch<WG, __nv_bfloat16>(prm, maps, st);
+int plan_weights(Params& prm, Maps& maps, int i, const void* a, int M, const void* b, int N, void* dw) {
+  if (!map_of(&maps.wa[i], a, M, (uint64_t)prm.rows_total, KB) || !map_of(&maps.wb[i], b, N, (uint64_t)prm.rows_total, KB))
+    return MOE_ERR_CUDA;
+  WeightGrad& w = prm.w[i];
+  w.rows = M;
+  w.cols = N;
+  w.mt = (M + 2 * HALF - 1) / (2 * HALF);
+  w.nt = (N + 2 * HALF - 1) / (2 * HALF);
+  w.units = w.mt * w.nt;
+  w.group_inv = group_inverse(w.nt);
+  w.out = dw;
+  return MOE_OK;
 }
 
 }  // namespace
@@ -831,7 +957,9 @@ int launch_swiglu_save(const moe_problem& p, const void* xg, const void* w13, co
   prm.out = hg;
   prm.out2 = gu;
   prm.out2_s = gu_scales;
-  return launch_rows<UP>(prm, xg, p.H, w13, 2 * p.I, p.H, p.I, st);
+  Maps maps{};
+  const int r = plan_rows(UP, prm, maps, xg, p.H, w13, 2 * p.I, p.H, p.I);
+  return r ? r : launch<UP, __nv_bfloat16>(prm, maps, st);
 }
 
 int launch_ffn_backward(const moe_problem& p, const FfnBackwardArgs& a, cudaStream_t st) {
@@ -850,22 +978,18 @@ int launch_ffn_backward(const moe_problem& p, const FfnBackwardArgs& a, cudaStre
   dh.gu = a.gu;
   dh.gu_s = a.gu_scales;
   dh.wg = a.wg;
-  int r = launch_rows<DH>(dh, a.dyg, p.H, a.w2, p.H, p.I, p.I, st);
+  Maps maps{};
+  int r = plan_rows(DH, dh, maps, a.dyg, p.H, a.w2, p.H, p.I, p.I);
+  if (!r) r = launch<DH, __nv_bfloat16>(dh, maps, st);
+  if (r || !(a.dxg || a.dw13 || a.dw2)) return r;
+  Params g = prm;
+  g.out = a.dxg;
+  g.accumulate = a.accumulate;
+  if (a.dxg) r = plan_rows(GRAD, g, maps, a.dgu, 2 * p.I, a.w13, 2 * p.I, p.H, p.H);
+  if (!r && a.dw13) r = plan_weights(g, maps, 0, a.dgu, 2 * p.I, a.xg, p.H, a.dw13);
+  if (!r && a.dw2) r = plan_weights(g, maps, 1, a.dyg, p.H, a.hg, p.I, a.dw2);
   if (r) return r;
-  if (a.dw2) {
-    r = launch_weight_grad(prm, a.dyg, p.H, a.hg, p.I, a.dw2, a.dw_dtype, a.accumulate, st);
-    if (r) return r;
-  }
-  if (a.dw13) {
-    r = launch_weight_grad(prm, a.dgu, 2 * p.I, a.xg, p.H, a.dw13, a.dw_dtype, a.accumulate, st);
-    if (r) return r;
-  }
-  if (a.dxg) {
-    Params dx = prm;
-    dx.out = a.dxg;
-    r = launch_rows<DX, float>(dx, a.dgu, 2 * p.I, a.w13, 2 * p.I, p.H, p.H, st);
-  }
-  return r;
+  return a.dw_dtype == MOE_F32 ? launch<GRAD, float>(g, maps, st) : launch<GRAD, __nv_bfloat16>(g, maps, st);
 }
 
 }  // namespace moe

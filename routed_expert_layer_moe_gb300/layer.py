@@ -72,6 +72,7 @@ class MoeLayer:
             self.dxg = torch.empty((rows, p.H), dtype=torch.float32, device=dev)
             self.dgu = torch.empty((rows, 2 * p.I), **bf16)
             self.wg = torch.empty(rows, dtype=torch.float32, device=dev)
+            self.dw = torch.empty((p.T, p.K), dtype=torch.float32, device=dev)
         nbytes = max(L.moe_workspace_bytes(p), 256)
         self.ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
 
@@ -165,19 +166,16 @@ class MoeLayer:
         if accumulate and (not weights or dw13 is None or dw2 is None):
             raise ValueError("accumulate: expected dw13 and dw2 to add to")
         p = self.p
-        f32 = dict(dtype=torch.float32, device=self.out.device)
         with L._allocate_on(stream):
             dx = torch.empty_like(self.out)
-            dlogits, dw = torch.empty((p.T, p.E), **f32), torch.empty((p.T, p.K), **f32)
+            dlogits = torch.empty((p.T, p.E), dtype=torch.float32, device=self.out.device)
             if weights:
                 dw13 = torch.empty_like(self.w13) if dw13 is None else dw13
                 dw2 = torch.empty_like(self.w2) if dw2 is None else dw2
             else:
                 dw13 = dw2 = None
-        L.moe_combine_backward(p, dout, self.yg, self.row_of, self.w, self.dyg, self.wg, dw, stream)
-        L.moe_grouped_ffn_backward(p, self.dyg, self.wg, self.xg, self.w13, self.w2, self.gu, self.gu_s, 
-                                   self.masked_m, self.offsets, self.dgu, self.hg, self.dxg, dw13, dw2, self.err,
-                                   accumulate, stream)
-        L.moe_permute_backward(p, self.dxg, self.row_of, dx, stream)
-        L.moe_route_backward(p, score, logits, self.ids, self.w, dw, dlogits, add, renormalize, scale, stream)
+        L.moe_layer_backward(p, dout, self.yg, self.row_of, self.ids, self.w, self.xg, self.w13, self.w2, self.gu,
+                             self.gu_s, self.masked_m, self.offsets, self.dyg, self.wg, self.dgu, self.hg, self.dxg,
+                             self.dw, dx, dlogits, dw13, dw2, self.err, score, logits, renormalize, scale, add,
+                             accumulate, stream)
         return dx, dlogits, dw13, dw2

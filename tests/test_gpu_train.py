@@ -490,3 +490,33 @@ def test_layer_backward(T, K, shared, layout):
         assert rel <= 4 * HALF, (name, rel)
     again = layer.backward(dout)  # nothing of the pass is used up
     assert all(torch.equal(a, b) for a, b in zip(grads, again))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_one_call_gives_what_the_four_give(score):
+    layer, r = make_layer(45, 256, 128, 6, 3, 1)
+    x, logits, dout, add = r(45, 256).bfloat16(), r(45, 6), r(45, 256).bfloat16(), r(45, 6)
+    how = dict(renormalize=True, scale=2.5)
+    if score == "sigmoid":
+        layer.route_grouped(logits, 2, 1, None, True, 2.5)
+        layer.permute(x)
+        layer.ffn_save()
+    else:
+        layer.forward(x, logits, save=True)
+    got = layer.backward(dout, score=score, logits=logits, add=add, **how)
+    p = layer.p
+    dyg, dgu, hg = (torch.empty_like(t) for t in (layer.yg, layer.dgu, layer.hg))
+    wg, dw, dxg = torch.empty_like(layer.wg), torch.empty_like(layer.w), torch.empty_like(layer.dxg)
+    dx, dl = torch.empty_like(x), torch.empty_like(logits)
+    dw13, dw2 = torch.empty_like(layer.w13), torch.empty_like(layer.w2)
+    moe.moe_combine_backward(p, dout, layer.yg, layer.row_of, layer.w, dyg, wg, dw)
+    moe.moe_grouped_ffn_backward(p, dyg, wg, layer.xg, layer.w13, layer.w2, layer.gu, layer.gu_s, layer.masked_m,
+                                 layer.offsets, dgu, hg, dxg, dw13, dw2, layer.err)
+    moe.moe_permute_backward(p, dxg, layer.row_of, dx)
+    moe.moe_route_backward(p, score, logits, layer.ids, layer.w, dw, dl, add, **how)
+    for a, b in zip(got, (dx, dl, dw13, dw2)):
+        assert torch.equal(a, b)
+    assert torch.equal(layer.dw, dw) and int(layer.err) == 0
+    want = layer_reference(layer, dout, score, logits, **{"renorm": True, "scale": 2.5})
+    for a, v in zip((dx, dl - add, dw13, dw2), want):
+        assert float((d(a) - v).norm() / v.norm()) <= 4 * HALF
