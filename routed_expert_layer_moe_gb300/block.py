@@ -11,6 +11,13 @@ With sigmoid scores and groups of experts the router's call comes between:
     block.layer.route_grouped(logits, n_group, topk_group, bias, scale=2.5)
     y, xn_next = block.leave(x, logits, routed=True)
 
+Training, with a layer of bf16 experts made with train=True: leave(x, logits, save=True), and
+
+    dx, dout, dgate, dw_post, dw_next = block.leave_backward(x, dy, dxn_next)
+    dxn, dlogits, dw13, dw2 = block.layer.backward(dout, add=block.balance_backward(logits, dloss))
+    dxn = dxn + (dlogits @ W_g.T).to(dxn.dtype)   # the router's product is the caller's
+    dx, dw_pre = block.enter_backward(x, dxn, dx)
+
 The buffers of the forward calls and of the loss are allocated once and every call only enqueues kernels on the
 stream, so a step is graph-capturable after a first eager one.  leave_backward() and enter_backward() return new
 tensors, allocated on the stream of the call: a caller that uses them on another stream orders the two streams, and
@@ -19,7 +26,9 @@ calls record_stream on what it drops there, as with any tensor of another stream
 What one pass leaves for its gradients is overwritten by the next one: layer.out and layer.ids by any forward pass of
 the layer (of another block on it too), the results of a method of the block by its next call.  Where another
 pass comes between a forward and its gradients (micro-batches, two blocks on one layer), keep copies and hand
-them in: ids to balance(), counts and tokens to balance_backward(), out to leave_backward().  Calls that use each
+them in: ids to balance(), counts and tokens to balance_backward(), out to leave_backward(), as it is or in 8 bits as
+keep_out() leaves it.  What layer.backward() reads stays with the layer: micro-batches in flight take a layer each, on the
+same weights (layer.py).  Calls that use each
 other's results are ordered by the caller if they run on different streams, and so are two calls of one method."""
 from __future__ import annotations
 
@@ -56,15 +65,19 @@ class MoeBlock:
         L.moe_block_norm(x, None, None, None, self.w_pre, self.res_scale, self.eps, None, self.xn, stream)
         return self.xn
 
-    def leave(self, x, logits, stream=None, routed=False):
+    def leave(self, x, logits, stream=None, routed=False, save=False):
         """The layer on enter()'s result, and the norm after it: (y, the next block's normed input or None).  The layer
         routes by softmax top-k of the logits; routed: it takes the ids and weights that it holds, of a routing
-        that the caller made (layer.route_grouped, or any that writes layer.ids and layer.w)."""
+        that the caller made (layer.route_grouped, or any that writes layer.ids and layer.w).  save: the layer keeps what
+        layer.backward() needs (bf16 experts, train=True)."""
         if routed:
             self.layer.permute(self.xn, stream)
-            self.layer.ffn_combine(stream)
+            if save:
+                self.layer.ffn_save(stream)
+            else:
+                self.layer.ffn_combine(stream)
         else:
-            self.layer.forward(self.xn, logits, stream, fused=True)
+            self.layer.forward(self.xn, logits, stream, fused=True, save=save)
         L.moe_block_norm(x, self.layer.out, self.gate, self.w_post, self.w_next, self.res_scale, self.eps, self.y,
                          self.xn_next, stream)
         return self.y, self.xn_next
@@ -90,16 +103,32 @@ class MoeBlock:
         return self.dlogits
 
     # -- gradients of the norms -------------------------------------------------
+    def keep_out(self, stream=None):
+        """The layer's output as an 8-bit checkpoint, (codes, scales), half its size: leave_backward() takes it as out when
+        other passes have overwritten the output itself."""
+        out = self.layer.out
+        with L._allocate_on(stream):
+            codes = torch.empty(out.shape, dtype=torch.uint8, device=out.device)
+            scales = torch.empty((out.shape[0], -(-out.shape[1] // L.FP8_GROUP)), dtype=torch.float32, device=out.device)
+        L.moe_fp8_quantize(out, codes, scales, stream)
+        return codes, scales
+
     def leave_backward(self, x, dy, dxn_next, stream=None, out=None):
         """Gradients of leave()'s norm: of x, of the layer's output, of gate, w_post and w_next (fp32).  dxn_next is
-        None without w_next.  out: the layer's output in that leave(), if it is not the layer's last one any more."""
+        None without w_next.  out: the layer's output in that leave(), if it is not the layer's last one any more, or what
+        keep_out() made of it."""
         f32 = dict(dtype=torch.float32, device=x.device)
         with L._allocate_on(stream):
             dx, dout = torch.empty_like(x), torch.empty_like(x)
             dgate = None if self.gate is None else torch.empty(self.gate.shape, **f32)
             dw_post = torch.empty(self.w_post.shape, **f32)
             dw_next = None if self.w_next is None else torch.empty(self.w_next.shape, **f32)
-        L.moe_block_norm_backward(x, self.layer.out if out is None else out, self.gate, self.w_post, self.w_next,
+            kept, out = out, self.layer.out if out is None else out
+            if isinstance(kept, tuple):
+                out = torch.empty_like(self.layer.out)
+        if isinstance(kept, tuple):
+            L.moe_fp8_dequantize(*kept, out, stream)
+        L.moe_block_norm_backward(x, out, self.gate, self.w_post, self.w_next,
                                   self.res_scale, self.eps, dy, dxn_next, dx, dout, dgate, dw_post, dw_next,
                                   self.ws_leave, stream)
         return dx, dout, dgate, dw_post, dw_next

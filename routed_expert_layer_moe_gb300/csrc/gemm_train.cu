@@ -400,7 +400,9 @@ __device__ __forceinline__ void epilogue(const Params& p, const Unit& U, uint32_
     const float2 other = reinterpret_cast<float2*>(ex)[(half ^ 1) * HALF + r];
     const float sg = fp8_scale(fp8_amax(ag, other.x)), su = fp8_scale(fp8_amax(au, other.y));
     // one division a group; the codes' inputs are fp32 sums, so a reciprocal's last bit is within their own error
-    const float ig = 1.0f / sg, iu = 1.0f / su;
+    // (scales whose reciprocal would overflow: both sides times 2^100)
+    const bool tiny_g = sg < 0x1p-100f, tiny_u = su < 0x1p-100f;
+    const float ig = 1.0f / (tiny_g ? sg * 0x1p100f : sg), iu = 1.0f / (tiny_u ? su * 0x1p100f : su);
     const size_t row = (size_t)U.row + r;
     if (half == 0 && r < U.nvalid) {
       p.out2_s[row * (2 * I / FP8_GROUP) + U.j] = sg;
@@ -418,6 +420,14 @@ __device__ __forceinline__ void epilogue(const Params& p, const Unit& U, uint32_
       uint32_t h[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) h[i] = pack2(silu(g[2 * i]) * u[2 * i], silu(g[2 * i + 1]) * u[2 * i + 1]);
+      if (tiny_g) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) g[i] *= 0x1p100f;
+      }
+      if (tiny_u) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) u[i] *= 0x1p100f;
+      }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {  // a group without a scale has codes 0
         qg[c / 4 + i] = sg != sg ? 0u : fp8_pair(g[4 * i] * ig, g[4 * i + 1] * ig) | fp8_pair(g[4 * i + 2] * ig, g[4 * i + 3] * ig) << 16;

@@ -151,7 +151,8 @@ class MoeLayer:
     def ffn_save(self, stream=None):
         """ffn_combine() of a training pass: gate/up that keeps g and u, down, combine."""
         self.swiglu_save(stream)
-        self.down(stream)
+        if self.rows:  # the down call takes no empty buffers
+            self.down(stream)
         self.combine(stream)
 
     def backward(self, dout, dw13=None, dw2=None, accumulate=False, weights=True, score="softmax", logits=None,

@@ -520,3 +520,20 @@ def test_one_call_gives_what_the_four_give(score):
     want = layer_reference(layer, dout, score, logits, **{"renorm": True, "scale": 2.5})
     for a, v in zip((dx, dl - add, dw13, dw2), want):
         assert float((d(a) - v).norm() / v.norm()) <= 4 * HALF
+
+
+@pytest.mark.parametrize("size", [1e-18, 3e-20, 1e17])
+def test_checkpoint_of_tiny_and_huge_products(size):
+    """g and u next to the ends of fp32: scales below the smallest normal number, whose reciprocal overflows, and large ones."""
+    c = Case([19, 3], 128, 128, "contig")
+    c.w13 = (c.w13.double() * size).bfloat16()
+    x = (c.x.double() * size).bfloat16()
+    hg, gu, gs = c.save(x)
+    values = torch.from_numpy(ref.fp8_values(gu.cpu().numpy(), gs.cpu().numpy()))
+    for e, s in enumerate(c.slot):
+        a, w = d(x[s]), d(c.w13[e])
+        g, off = a @ w.T, sums(128) * (a.abs() @ w.abs().T) + 128 * 2.0 ** -126  # products below 2^-126 may be lost
+        sc = d(gs[s]).repeat_interleave(128, 1)
+        assert torch.isfinite(values[s]).all()
+        # half a step of E4M3 (of the smallest binade below it), an off sum, and the scale's own rounding (2^-149 steps)
+        assert ((values[s] - g).abs() <= (2.0 ** -4 + 2.0 ** -10) * g.abs() + 2.0 ** -9 * sc + 2 * off + 448 * 2.0 ** -148).all()
