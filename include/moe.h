@@ -486,7 +486,8 @@ moe_status moe_block_norm_backward(int32_t dtype, int32_t T, int32_t H, const vo
  * ------------------------------------------------------------------------- */
 
 /* x [rows][cols] (dtype F32 or BF16, any alignment of the type's own size) ->
- * codes [rows][cols], scales [rows][ceil(cols / 128)]. */
+ * codes [rows][cols], scales [rows][ceil(cols / 128)].  rows, cols <= 2^33,
+ * rows * cols <= 2^40, fewer than 2^32 groups. */
 moe_status moe_fp8_quantize(int32_t dtype, int64_t rows, int64_t cols, const void* x, uint8_t* codes, float* scales,
                             moe_stream_t stream);
 

@@ -465,7 +465,7 @@ static int check_fp8(int32_t dtype, int64_t rows, int64_t cols, const void* valu
                      const void* scales) {
   // groups of all rows, a warp each, and the values' index
   if (!float_dtype(dtype) || rows < 0 || cols < 0 || rows > (1LL << 33) || cols > (1LL << 33) ||
-      (cols > 0 && rows > (1LL << 40) / cols) || rows * ((cols + 127) / 128) > (1LL << 33))
+      (cols > 0 && rows > (1LL << 40) / cols) || rows * ((cols + 127) / 128) >= (1LL << 32))
     return MOE_ERR_INVALID;
   if (rows == 0 || cols == 0) return MOE_OK;
   if (!values || !codes || !scales) return MOE_ERR_INVALID;

@@ -367,7 +367,7 @@ def test_route_backward_at_the_edges():
 # ---------------------------------------------------------------------------------------------- 8-bit checkpoints
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
-@pytest.mark.parametrize("rows,cols,offset", [(1, 1, 0), (3, 127, 0), (2, 128, 0), (5, 128, 1), (7, 129, 0), (33, 300, 3),
+@pytest.mark.parametrize("rows,cols,offset", [(1, 1, 0), (3, 127, 0), (2, 128, 0), (5, 128, 1), (7, 129, 0), (33, 300, 3), (9, 130, 0), (6, 260, 2), (11, 252, 4),
                                               (2, 4096, 0), (200, 384, 0), (1, 16384, 8)])
 def test_fp8_checkpoint(rows, cols, offset, dtype):
     g = torch.Generator().manual_seed(rows * cols)
