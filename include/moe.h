@@ -482,7 +482,7 @@ moe_status moe_block_norm_backward(int32_t dtype, int32_t T, int32_t H, const vo
  * E4M3(x / s), the nearest to the exact quotient with ties to the even code,
  * saturating at 448; the sign of a zero is kept.  A group that holds a NaN or an infinity gets a NaN scale and
  * codes 0.  Value = code * s, rounded once; it is within 2^-4 of x, relative,
- * where |x| >= 2^-6 s, and within 2^-10 s below that.
+ * where |x| >= 2^-6 s, and within 2^-10 s below that.  Outputs overlap no input.
  * ------------------------------------------------------------------------- */
 
 /* x [rows][cols] (dtype F32 or BF16, any alignment of the type's own size) ->
@@ -517,6 +517,7 @@ moe_status moe_fp8_dequantize(int32_t dtype, int64_t rows, int64_t cols, const u
  * not placed (row_of = -1) contributes nothing and has dw = 0.  Weights'
  * gradients are per slot: replicas of one expert each have their own.  Sums are
  * fp32 in a fixed order: the same inputs give the same bits.  No workspace.
+ * Counts and offsets that lead outside the grouped buffers are cut to them.
  * ------------------------------------------------------------------------- */
 
 /* Step 3 that also keeps g and u for the gradient: with (g, u) the products of
@@ -578,10 +579,9 @@ moe_status moe_route_backward(const moe_problem* p, int32_t score, const float* 
                               const float* w, const float* dw, int32_t renormalize, float scale, const float* add,
                               float* dlogits, moe_stream_t stream);
 
-/* The four calls of the gradient in one, three launches and the products' two:
- * moe_combine_backward with moe_route_backward in the same launch,
- * moe_grouped_ffn_backward and moe_permute_backward; the same arguments and the
- * same results.  dyg, wg, dgu, hg and dxg are buffers between the steps, written as by
+/* The four calls of the gradient in one, four launches: moe_combine_backward and
+ * moe_route_backward in one, the two of moe_grouped_ffn_backward,
+ * moe_permute_backward; the same arguments and the same results.  dyg, wg, dgu, hg and dxg are buffers between the steps, written as by
  * those calls; dw [T][K] is written too.  dw13 and dw2 may each be NULL. */
 moe_status moe_layer_backward(const moe_problem* p, const void* dout, const void* yg, const int32_t* row_of,
                               const int32_t* ids, const float* w, const void* xg, const void* w13, const void* w2,

@@ -28,6 +28,13 @@
 // Roles of a CTA: warp 0 TMA producer, warp 1 MMAs (leader CTA), warp 2 the zeros of WG, warps 4-11 epilogue.  Every
 // wait is bounded; on expiry the CTA drains its copies and MMAs, frees tensor memory, reports MOE_FLAG_TIMEOUT and
 // returns.
+//
+// What bounds it.  A stage moves 32 KB into each SM for 512 cycles of MMAs, 64 bytes a cycle: next to what the way from
+// L2 gives, so operands are never staged twice and results leave without touching shared memory.  Long products run
+// at 2.0 PFLOP/s for some milliseconds (dxg, 9728 rows of 4096 x 9728: 771 us) and at the power limit's clocks after
+// that.  Experts' last chunks of less than 256 rows are whole tiles: 4.5 chunks for 1024 rows on average.  Measured (burst):
+// 8 experts of 4096 x 14336, 4096 tokens of 2 records: UP 1090 us (1.76 PFLOP/s), DH 610 (1.58), DX 1120 (1.72), dW13 1130
+// (1.70), dW2 650 (1.48); 512 experts of 4096 x 1024, 160 rows each: UP 1400 us, 6.8 TB/s.
 #include <algorithm>
 #include <type_traits>
 
@@ -773,7 +780,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         walk.seek();
         const int m = S.rows[walk.place];
         if ((m & 15) == 0) continue;
-        if (!__all_sync(0xffffffffu, mbar_wait(landed, lphase, abort_flag, TIMEOUT))) break;
+        // the first of these waits lasts through all units of rows: 16 limits, about half a minute
+        if (!__all_sync(0xffffffffu, mbar_wait(landed, lphase, abort_flag, 16 * TIMEOUT))) break;
         lphase ^= 1u;
         const int v = m % KB, n = 16 - (v & 15);  // rows v .. v + n - 1 of the stage
         uint8_t* at = smem + (size_t)stages * STAGE + v * 128;

@@ -25,8 +25,9 @@ class MoeLayer:
 
     train (bf16 experts): the buffers of a training pass too.  forward(x, logits, save=True) keeps g and u of the
     experts in 8 bits, and backward(dout) gives the gradients of that pass.  What it reads (ids, w, row_of, masked_m,
-    offsets, xg, yg, gu, gu_s) is overwritten by the layer's next forward pass: where other passes come between a
-    forward and its gradient (micro-batches), take a MoeLayer for each, on the same weights."""
+    offsets, xg, yg, gu, gu_s) is overwritten by the layer's next forward pass, with or without save: where other
+    passes come between a forward and its gradient (micro-batches), take a MoeLayer for each, on the same weights.
+    backward() itself overwrites hg and its own buffers (dyg, wg, dgu, dxg, dw)."""
 
     def __init__(self, problem: L.Problem, act: str, wt: str, out: str, w13, w2, w13_s=None, w2_s=None,
                  phys_to_log=None, device="cuda", train=False):
@@ -126,7 +127,7 @@ class MoeLayer:
     def forward(self, x, logits, stream=None, fused=False, save=False):
         """route -> permute -> gate/up -> down -> combine; returns self.out.  fused=True makes the
         same pass with the fused calls: route_permute() and ffn_combine().  save=True (a layer with train=True):
-        gate/up keeps what backward() needs."""
+        gate/up keeps what backward() needs; route_permute() and ffn_save(), whatever fused is."""
         if save:
             self._training("forward(save=True)")
             self.route_permute(logits, x, stream)
