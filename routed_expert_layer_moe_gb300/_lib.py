@@ -427,6 +427,7 @@ def moe_block_norm_backward(x, block, gate, w_post, w_pre, res_scale: float, eps
 
 
 FP8_GROUP = 128  # values that share a scale of an 8-bit checkpoint
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
 
 def _fp8_args(values, codes, scales, name: str):
@@ -435,9 +436,14 @@ def _fp8_args(values, codes, scales, name: str):
     if values.dim() < 1:
         raise ValueError("%s: expected rows of values" % name)
     shape = values.shape
-    lead, cols = shape[:-1], shape[-1]
-    return (d, lead.numel(), cols, addr, _arg(codes, "codes", torch.uint8, shape),
-            _arg(scales, "scales", torch.float32, (*lead, -(-cols // FP8_GROUP))))
+    cols = shape[-1]
+    if len(shape) == 2:
+        rows = shape[0]
+        groups = (rows, -(-cols // FP8_GROUP))
+    else:
+        rows = shape[:-1].numel()
+        groups = (*shape[:-1], -(-cols // FP8_GROUP))
+    return (d, rows, cols, addr, _arg(codes, "codes", _U8, shape), _arg(scales, "scales", _F32, groups))
 
 
 def moe_fp8_quantize(x, codes, scales, stream=None) -> None:
@@ -450,9 +456,6 @@ def moe_fp8_dequantize(codes, scales, out, stream=None) -> None:
     """E4M3 codes and scales -> the values they stand for, out [..., cols] (float32 or bfloat16)."""
     d, rows, cols, po, pc, ps = _fp8_args(out, codes, scales, "out")
     _check(lib().moe_fp8_dequantize(d, rows, cols, pc, ps, po, _stream(stream)), "moe_fp8_dequantize")
-
-
-_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
 
 def _train_sizes(p: Problem):
@@ -493,18 +496,15 @@ def moe_grouped_ffn_backward(p: Problem, dyg, wg, xg, w13, w2, gu, gu_scales, ma
     dw13 [slots, 2I, H] and dw2 [slots, H, I] are both bfloat16 or both float32; accumulate (float32): added to what
     they hold."""
     rows, n = _train_sizes(p)
-    dt = next((t.dtype for t in (dw13, dw2) if t is not None), _BF16)
-    if dt not in _FLOAT_DTYPES:
-        raise ValueError("dw13, dw2: expected float32 or bfloat16, got %s" % dt)
+    d, a13, a2 = _weight_grads(p, n, dw13, dw2)
     _check(lib().moe_grouped_ffn_backward(
         ctypes.byref(p), _arg(dyg, "dyg", _BF16, (rows, p.H)), _arg(wg, "wg", _F32, (rows,)), _arg(xg, "xg", _BF16, (rows, p.H)),
         _arg(w13, "w13", _BF16, (n, 2 * p.I, p.H)), _arg(w2, "w2", _BF16, (n, p.H, p.I)),
         _arg(gu, "gu", _U8, (rows, 2 * p.I)), _arg(gu_scales, "gu_scales", _F32, (rows, 2 * p.I // FP8_GROUP)),
         _arg(masked_m, "masked_m", _I32, (n,)), _arg(offsets, "offsets", _I32, (n + 1,)),
         _arg(dgu, "dgu", _BF16, (rows, 2 * p.I)), _arg(hg, "hg", _BF16, (rows, p.I)),
-        _arg(dxg, "dxg", _F32, (rows, p.H)), _arg(dw13, "dw13", dt, (n, 2 * p.I, p.H)),
-        _arg(dw2, "dw2", dt, (n, p.H, p.I)), _FLOAT_DTYPES[dt], int(bool(accumulate)), _ptr(err_flag),
-        _stream(stream)), "moe_grouped_ffn_backward")
+        _arg(dxg, "dxg", _F32, (rows, p.H)), a13, a2, d, int(bool(accumulate)), _ptr(err_flag), _stream(stream)),
+        "moe_grouped_ffn_backward")
 
 
 def moe_permute_backward(p: Problem, dxg, row_of, dx, stream=None) -> None:
@@ -527,6 +527,27 @@ def moe_route_backward(p: Problem, score: str, logits, ids, w, dw, dlogits, add=
         "moe_route_backward")
 
 
+def _weight_grads(p: Problem, n: int, dw13, dw2):
+    """moe_dtype and addresses of the weights' gradients."""
+    dt = dw13.dtype if dw13 is not None else dw2.dtype if dw2 is not None else _BF16
+    if dt not in _FLOAT_DTYPES:
+        raise ValueError("dw13, dw2: expected float32 or bfloat16, got %s" % dt)
+    return (_FLOAT_DTYPES[dt], _arg(dw13, "dw13", dt, (n, 2 * p.I, p.H)), _arg(dw2, "dw2", dt, (n, p.H, p.I)))
+
+
+def _layer_backward(p: Problem, state, between, dout, dx, dlogits, dw13, dw2, err_flag, score, logits, renormalize, scale,
+                    add, accumulate, stream) -> None:
+    """The call, with the addresses of what the forward pass left (yg, row_of, ids, w, xg, w13, w2, gu, gu_scales,
+    masked_m, offsets) and of the buffers between the steps (dyg, wg, dgu, hg, dxg, dw)."""
+    TE, TH = (p.T, p.E), (p.T, p.H)
+    d, a13, a2 = _weight_grads(p, p.P + p.has_shared, dw13, dw2)
+    _check(lib().moe_layer_backward(
+        ctypes.byref(p), _arg(dout, "dout", _BF16, TH), *state, SCORES[score], _arg(logits, "logits", _F32, TE),
+        int(bool(renormalize)), scale, _arg(add, "add", _F32, TE), *between, _arg(dx, "dx", _BF16, TH),
+        _arg(dlogits, "dlogits", _F32, TE), a13, a2, d, int(bool(accumulate)), _ptr(err_flag), _stream(stream)),
+        "moe_layer_backward")
+
+
 def moe_layer_backward(p: Problem, dout, yg, row_of, ids, w, xg, w13, w2, gu, gu_scales, masked_m, offsets, dyg, wg,
                        dgu, hg, dxg, dw, dx, dlogits, dw13, dw2, err_flag, score="softmax", logits=None,
                        renormalize=True, scale: float = 1.0, add=None, accumulate=False, stream=None) -> None:
@@ -534,23 +555,16 @@ def moe_layer_backward(p: Problem, dout, yg, row_of, ids, w, xg, w13, w2, gu, gu
     dyg, wg, dgu, hg, dxg: buffers between the steps, as those calls write them."""
     rows, n = _train_sizes(p)
     T, H, I, K = p.T, p.H, p.I, p.K
-    R = (rows, H)
-    TK, TE, TH = (T, K), (T, p.E), (T, H)
-    dt = (dw13 if dw13 is not None else dw2).dtype if dw13 is not None or dw2 is not None else _BF16
-    if dt not in _FLOAT_DTYPES:
-        raise ValueError("dw13, dw2: expected float32 or bfloat16, got %s" % dt)
-    _check(lib().moe_layer_backward(
-        ctypes.byref(p), _arg(dout, "dout", _BF16, TH), _arg(yg, "yg", _BF16, R),
-        _arg(row_of, "row_of", _I32, (T, K + p.has_shared)), _arg(ids, "ids", _I32, TK), _arg(w, "w", _F32, TK),
-        _arg(xg, "xg", _BF16, R), _arg(w13, "w13", _BF16, (n, 2 * I, H)), _arg(w2, "w2", _BF16, (n, H, I)),
-        _arg(gu, "gu", _U8, (rows, 2 * I)), _arg(gu_scales, "gu_scales", _F32, (rows, 2 * I // FP8_GROUP)),
-        _arg(masked_m, "masked_m", _I32, (n,)), _arg(offsets, "offsets", _I32, (n + 1,)), SCORES[score],
-        _arg(logits, "logits", _F32, TE), int(bool(renormalize)), scale, _arg(add, "add", _F32, TE),
-        _arg(dyg, "dyg", _BF16, R), _arg(wg, "wg", _F32, (rows,)), _arg(dgu, "dgu", _BF16, (rows, 2 * I)),
-        _arg(hg, "hg", _BF16, (rows, I)), _arg(dxg, "dxg", _F32, R), _arg(dw, "dw", _F32, TK),
-        _arg(dx, "dx", _BF16, TH), _arg(dlogits, "dlogits", _F32, TE), _arg(dw13, "dw13", dt, (n, 2 * I, H)),
-        _arg(dw2, "dw2", dt, (n, H, I)), _FLOAT_DTYPES[dt], int(bool(accumulate)), _ptr(err_flag), _stream(stream)),
-        "moe_layer_backward")
+    R, TK = (rows, H), (T, K)
+    state = (_arg(yg, "yg", _BF16, R), _arg(row_of, "row_of", _I32, (T, K + p.has_shared)), _arg(ids, "ids", _I32, TK),
+             _arg(w, "w", _F32, TK), _arg(xg, "xg", _BF16, R), _arg(w13, "w13", _BF16, (n, 2 * I, H)),
+             _arg(w2, "w2", _BF16, (n, H, I)), _arg(gu, "gu", _U8, (rows, 2 * I)),
+             _arg(gu_scales, "gu_scales", _F32, (rows, 2 * I // FP8_GROUP)), _arg(masked_m, "masked_m", _I32, (n,)),
+             _arg(offsets, "offsets", _I32, (n + 1,)))
+    between = (_arg(dyg, "dyg", _BF16, R), _arg(wg, "wg", _F32, (rows,)), _arg(dgu, "dgu", _BF16, (rows, 2 * I)),
+               _arg(hg, "hg", _BF16, (rows, I)), _arg(dxg, "dxg", _F32, R), _arg(dw, "dw", _F32, TK))
+    _layer_backward(p, state, between, dout, dx, dlogits, dw13, dw2, err_flag, score, logits, renormalize, scale, add,
+                    accumulate, stream)
 
 
 def moe_eplb_record(p: Problem, masked_m, pass_index: int, window: int, load_window, stream=None) -> None:

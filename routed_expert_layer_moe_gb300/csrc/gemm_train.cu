@@ -683,9 +683,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         const CUtensorMap* ma = weights ? &maps.wa[U.kind - W13] : &maps.a[box_of(U.nvalid)];
         const CUtensorMap* mb = weights ? &maps.wb[U.kind - W13] : &maps.b;
         auto row_bytes = [](int rows) { return rows > 0 ? (uint32_t)box_rows(box_of(rows)) * KB * 2 : 0u; };
-        // of both CTAs; a part without rows copies none
-        const uint32_t bytes = weights ? 2 * STAGE
-                                       : row_bytes(min(U.nall, HALF)) + row_bytes(U.nall - HALF) + 2 * OP_BYTES;
+        // of both CTAs; a part without rows copies none, but zeros in UP
+        const uint32_t bytes = weights || MODE == UP
+                                   ? 2 * STAGE
+                                   : row_bytes(min(U.nall, HALF)) + row_bytes(U.nall - HALF) + 2 * OP_BYTES;
         const int am = U.mi * 2 * HALF + (int)rank * HALF;
         const int bn = U.j * (MODE == UP ? HALF : 2 * HALF) + (MODE == UP ? 0 : (int)rank * HALF);
         const int brow = weights ? U.row : U.slot * p.b_rows + (MODE == UP ? (int)rank * p.ncols + bn : 0);
@@ -719,8 +720,19 @@ __global__ void __launch_bounds__(THREADS, 1)
           const uint32_t bar = mapa_shared(&full[stage], 0);
           if (weights) {
             for (int h = 0; h < 2; ++h) tma_load_2d_pair(sa + h * BOX_BYTES, ma, bar, am + 64 * h, U.row + k);
-          } else if (U.nvalid > 0) {
-            tma_load_2d_pair(sa, ma, bar, k, U.row);
+          } else {
+            // The box that holds the part's rows.  UP: and zeros behind it (boxes behind the buffer's end, which read
+            // nothing): MMAs of zeros draw less power than those of what a stage held before, which long runs are bound
+            // by (8 experts of 4096 x 14336: 1368 -> 1354 us; the gradient's products, whose stages turn over faster,
+            // lost 2% by it).
+            const int have = U.nvalid > 0 ? box_rows(box_of(U.nvalid)) : 0;
+            const int end = (int)p.rows_total;
+            if (have > 0) tma_load_2d_pair(sa, ma, bar, k, U.row);
+            if constexpr (MODE == UP) {
+              if (have == 0) tma_load_2d_pair(sa, &maps.a[2], bar, k, end);
+              if (have == 32) tma_load_2d_pair(sa + 32 * KB * 2, &maps.a[0], bar, k, end);
+              if (have == 32 || have == 64) tma_load_2d_pair(sa + 64 * KB * 2, &maps.a[1], bar, k, end);
+            }
           }
           if constexpr (MODE == UP) {
             tma_load_2d_pair(sb, mb, bar, k, brow);

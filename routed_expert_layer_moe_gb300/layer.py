@@ -176,8 +176,10 @@ class MoeLayer:
                 dw2 = torch.empty_like(self.w2) if dw2 is None else dw2
             else:
                 dw13 = dw2 = None
-        L.moe_layer_backward(p, dout, self.yg, self.row_of, self.ids, self.w, self.xg, self.w13, self.w2, self.gu,
-                             self.gu_s, self.masked_m, self.offsets, self.dyg, self.wg, self.dgu, self.hg, self.dxg,
-                             self.dw, dx, dlogits, dw13, dw2, self.err, score, logits, renormalize, scale, add,
-                             accumulate, stream)
+        ptr = L._ptr  # the layer's own buffers, as in its other methods
+        state = (ptr(self.yg), ptr(self.row_of), ptr(self.ids), ptr(self.w), ptr(self.xg), ptr(self.w13), ptr(self.w2),
+                 ptr(self.gu), ptr(self.gu_s), ptr(self.masked_m), ptr(self.offsets))
+        between = (ptr(self.dyg), ptr(self.wg), ptr(self.dgu), ptr(self.hg), ptr(self.dxg), ptr(self.dw))
+        L._layer_backward(p, state, between, dout, dx, dlogits, dw13, dw2, self.err, score, logits, renormalize, scale, add,
+                          accumulate, stream)
         return dx, dlogits, dw13, dw2
