@@ -537,3 +537,25 @@ def test_checkpoint_of_tiny_and_huge_products(size):
         assert torch.isfinite(values[s]).all()
         # half a step of E4M3 (of the smallest binade below it), an off sum, and the scale's own rounding (2^-149 steps)
         assert ((values[s] - g).abs() <= (2.0 ** -4 + 2.0 ** -10) * g.abs() + 2.0 ** -9 * sc + 2 * off + 448 * 2.0 ** -148).all()
+
+
+@pytest.mark.parametrize("shape", [(5,), (2, 3, 130), (2, 2, 2, 128), (0, 128), (4, 0), (0,)], ids=str)
+def test_fp8_shapes(shape):
+    """Leading dimensions are rows; nothing is done where there is nothing."""
+    x = torch.randn(shape, generator=torch.Generator().manual_seed(1))
+    codes = torch.empty(shape, dtype=torch.uint8, device="cuda")
+    scales = torch.empty(*shape[:-1], -(-shape[-1] // 128), device="cuda")
+    out = torch.empty(shape, device="cuda")
+    moe.moe_fp8_quantize(x.cuda(), codes, scales)
+    moe.moe_fp8_dequantize(codes, scales, out)
+    if x.numel():
+        flat = x.reshape(-1, shape[-1])
+        c, s = ref.fp8_quantize(flat.double().numpy())
+        assert np.array_equal(codes.cpu().numpy().reshape(flat.shape), c)
+        assert np.array_equal(scales.cpu().numpy().reshape(s.shape), s)
+        assert np.array_equal(out.cpu().numpy().reshape(flat.shape), ref.fp8_values(c, s).astype(np.float32))
+    with pytest.raises(ValueError):
+        moe.moe_fp8_quantize(x.cuda(), codes, torch.empty(3, 7, 11, device="cuda"))
+    if len(shape) > 1 and x.numel():
+        with pytest.raises(ValueError, match="dense"):
+            moe.moe_fp8_quantize(x.cuda().transpose(0, 1), codes.transpose(0, 1), scales)

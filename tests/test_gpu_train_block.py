@@ -241,7 +241,8 @@ def test_outputs_at_16_bytes():
 
 
 @pytest.mark.parametrize("T,H,I,E,K,shared,layout", [(1, 4096, 2048, 8, 2, 1, "masked"), (700, 1152, 5504, 3, 2, 0, "contig"),
-                                                     (1500, 2048, 1024, 70, 8, 1, "contig"), (400, 7168, 384, 2, 1, 0, "masked")])
+                                                     (1500, 2048, 1024, 70, 8, 1, "contig"), (400, 7168, 384, 2, 1, 0, "masked"),
+                                                     (64, 128, 128, 1000, 2, 1, "contig"), (5, 128, 128, 1023, 3, 1, "masked")])
 def test_larger_sizes(T, H, I, E, K, shared, layout):
     """Several waves of tiles, many slots, long reductions; every stage against 64 bits on the device, by norm.  The
     roundings of operands and results add up in squares: half a step of bf16 is 2^-8 of a value at most, a third of that
@@ -285,3 +286,35 @@ def test_larger_sizes(T, H, I, E, K, shared, layout):
     want = dxg[layer.row_of.long()].sum(1)
     worst["dx"] = float((dx.double() - want).norm() / want.norm())
     assert max(worst.values()) <= HALF, worst
+
+
+def test_elements_past_32_bits():
+    """Grouped rows whose elements pass 2^31: the last rows of the last slot and the first of the first."""
+    T, H, I, E, K = 40000, 128, 14336, 4, 2
+    layer, r = make_layer(T, H, I, E, K)
+    assert layer.dgu.numel() > 1 << 31
+    x, logits, dout = r(T, H).bfloat16(), r(T, E), r(T, H).bfloat16()
+    layer.forward(x, logits, save=True)
+    dx, dlogits, dw13, dw2 = layer.backward(dout)
+    torch.cuda.synchronize()
+    assert int(layer.err) == 0
+    rows = layer.rows
+    for s, part in ((0, slice(0, 40)), (E - 1, slice(rows - 40, rows))):
+        xr, wg, dy = layer.xg[part].double(), layer.wg[part].double()[:, None], layer.dyg[part].double()
+        gu = xr @ layer.w13[s].double().T
+        values = torch.empty(40, 2 * I, device="cuda")
+        moe.moe_fp8_dequantize(layer.gu[part], layer.gu_s[part], values)
+        sc = layer.gu_s[part].double().repeat_interleave(128, 1)
+        assert ((values.double() - gu).abs() <= 2.0 ** -4 * gu.abs() * (1 + 2.0 ** -10) + 2.0 ** -9 * sc).all()
+        leaf = values.double().requires_grad_()
+        h = tref.swiglu(leaf[:, :I], leaf[:, I:])
+        dgu, = torch.autograd.grad(h, leaf, wg * (dy @ layer.w2[s].double()))
+        for got, want in ((layer.hg[part], (wg * h).detach()), (layer.dgu[part], dgu),
+                          (layer.dxg[part], dgu @ layer.w13[s].double())):
+            assert float((got.double() - want).norm() / want.norm()) <= HALF
+    # the last slot's gradients of weights, whose rows lie past 2^31 elements, from what the products were given
+    n = int(layer.masked_m[-1])
+    tail = slice(rows - n, rows)
+    for got, a, b in ((dw13[-1][:256], layer.dgu[tail][:, :256], layer.xg[tail]), (dw2[-1], layer.dyg[tail], layer.hg[tail])):
+        want = a.double().T @ b.double()
+        assert float((got.double() - want).norm() / want.norm()) <= HALF
