@@ -21,6 +21,7 @@ __global__ void __launch_bounds__(128) combine_kernel(const TY* __restrict__ yg,
   const int c0 = (blockIdx.y * blockDim.x + threadIdx.x) * VEC;
   __shared__ int rows[kMaxKS];
   __shared__ float wts[kMaxKS];
+  grid_dependency_wait();  // at once, but in the dispatch's gradient
   if (threadIdx.x < KS) {
     rows[threadIdx.x] = row_of[(size_t)t * KS + threadIdx.x];
     wts[threadIdx.x] = (w && threadIdx.x < K) ? w[(size_t)t * K + threadIdx.x] : 1.0f;
@@ -83,15 +84,23 @@ __global__ void __launch_bounds__(128) combine_kernel(const TY* __restrict__ yg,
 
 }  // namespace
 
-// The dispatch's gradient: every record with weight 1, rows of fp32.
+// The dispatch's gradient: every record with weight 1, rows of fp32.  Launched while the products that write them end.
 int launch_permute_backward(const moe_problem& p, const float* dxg, const int32_t* row_of, void* dx,
                             cudaStream_t st) {
   if (p.T == 0) return MOE_OK;
   const int threads = 128;
-  const dim3 grid(p.T, (p.H / 4 + threads - 1) / threads);
-  combine_kernel<float, __nv_bfloat16, 4><<<grid, threads, 0, st>>>(dxg, row_of, nullptr, (__nv_bfloat16*)dx, p.H, p.K,
-                                                                     p.K + p.has_shared);
-  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(p.T, (p.H / 4 + threads - 1) / threads);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr = overlap_attribute();
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const float* ones = nullptr;
+  return cudaLaunchKernelEx(&cfg, combine_kernel<float, __nv_bfloat16, 4>, dxg, row_of, ones, (__nv_bfloat16*)dx, p.H,
+                            p.K, p.K + p.has_shared) == cudaSuccess
+             ? MOE_OK
+             : MOE_ERR_CUDA;
 }
 
 int launch_combine(const moe_problem& p, const void* yg, const int32_t* row_of, const float* w, void* out,

@@ -85,6 +85,7 @@ __global__ void __launch_bounds__(32 * kWarps)
                             float* __restrict__ wg, float* __restrict__ dw, int nvec, int K, int KS, long long rows,
                             const RouteArgs r) {
   __shared__ float sums[32];
+  grid_dependents_launch();  // the products' CTAs set up meanwhile
   const int t = blockIdx.x, lane = threadIdx.x & 31;
   const uint4* src = reinterpret_cast<const uint4*>(dout) + (size_t)t * nvec;
   for (int k = threadIdx.x >> 5; k < KS; k += blockDim.x >> 5) {
