@@ -34,7 +34,7 @@
 // at 2.0 PFLOP/s for some milliseconds (dxg, 9728 rows of 4096 x 9728: 771 us) and at the power limit's clocks after
 // that.  Experts' last chunks of less than 256 rows are whole tiles: 4.5 chunks for 1024 rows on average.  Measured (burst):
 // 8 experts of 4096 x 14336, 4096 tokens of 2 records: UP 1090 us (1.76 PFLOP/s), DH 610 (1.58), DX 1120 (1.72), dW13 1130
-// (1.70), dW2 650 (1.48); 512 experts of 4096 x 1024, 160 rows each: UP 1400 us, 6.8 TB/s.
+// (1.70), dW2 650 (1.48); 512 experts of 4096 x 1024, 160 rows each: UP 1400 to 1440 us, 6.7 TB/s.
 #include <algorithm>
 #include <type_traits>
 
