@@ -220,6 +220,7 @@ moe_status moe_route_grouped_topk(const moe_problem* p, const float* logits, con
  *   offsets [P+S+1] int32: exclusive prefix sum of masked_m.
  *   row_of [T][K+S] int32: grouped row of record (t,k); column K is the
  *     shared expert's row.  -1 for a record that was not placed (see err_flag).
+ *     The calls that read row_of take any entry outside [0, rows) for -1.
  *   src_of [rows] int32: token of each written row (padding rows untouched).
  *   xg [rows][H], dtype p->wt (e4m3 for E2M1 weights): x[t] copied to its
  *     rows; for e4m3 each row is

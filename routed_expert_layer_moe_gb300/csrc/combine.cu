@@ -16,14 +16,14 @@ constexpr int kMaxKS = 33;
 template <typename TY, typename TO, int VEC>
 __global__ void __launch_bounds__(128) combine_kernel(const TY* __restrict__ yg, const int32_t* __restrict__ row_of,
                                                       const float* __restrict__ w, TO* __restrict__ out, int H,
-                                                      int K, int KS) {
+                                                      int K, int KS, int nrows) {
   const int t = blockIdx.x;
   const int c0 = (blockIdx.y * blockDim.x + threadIdx.x) * VEC;
   __shared__ int rows[kMaxKS];
   __shared__ float wts[kMaxKS];
   grid_dependency_wait();  // at once, but in the dispatch's gradient
   if (threadIdx.x < KS) {
-    rows[threadIdx.x] = row_of[(size_t)t * KS + threadIdx.x];
+    rows[threadIdx.x] = placed_row(row_of[(size_t)t * KS + threadIdx.x], nrows);
     wts[threadIdx.x] = (w && threadIdx.x < K) ? w[(size_t)t * K + threadIdx.x] : 1.0f;
   }
   __syncthreads();
@@ -98,7 +98,7 @@ int launch_permute_backward(const moe_problem& p, const float* dxg, const int32_
   cfg.numAttrs = 1;
   const float* ones = nullptr;
   return cudaLaunchKernelEx(&cfg, combine_kernel<float, __nv_bfloat16, 4>, dxg, row_of, ones, (__nv_bfloat16*)dx, p.H,
-                            p.K, p.K + p.has_shared) == cudaSuccess
+                            p.K, p.K + p.has_shared, (int)grouped_rows(p)) == cudaSuccess
              ? MOE_OK
              : MOE_ERR_CUDA;
 }
@@ -107,15 +107,15 @@ int launch_combine(const moe_problem& p, const void* yg, const int32_t* row_of, 
                    cudaStream_t st) {
   if (p.T == 0) return MOE_OK;
   const int KS = p.K + p.has_shared;
-  const int threads = 128;
+  const int threads = 128, nrows = (int)grouped_rows(p);
   if (p.wt == MOE_F32) {
     const dim3 grid(p.T, (p.H / 4 + threads - 1) / threads);
     combine_kernel<float, float, 4><<<grid, threads, 0, st>>>((const float*)yg, row_of, w, (float*)out, p.H, p.K,
-                                                               KS);
+                                                               KS, nrows);
   } else {
     const dim3 grid(p.T, (p.H / 8 + threads - 1) / threads);
     combine_kernel<__nv_bfloat16, __nv_bfloat16, 8><<<grid, threads, 0, st>>>(
-        (const __nv_bfloat16*)yg, row_of, w, (__nv_bfloat16*)out, p.H, p.K, KS);
+        (const __nv_bfloat16*)yg, row_of, w, (__nv_bfloat16*)out, p.H, p.K, KS, nrows);
   }
   return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

@@ -198,6 +198,9 @@ inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 // Device helpers
 // ---------------------------------------------------------------------------
 
+// An entry of row_of as its readers take it: -1, a record without a place, for whatever lies outside [0, nrows).
+__device__ __forceinline__ int placed_row(int row, int nrows) { return (unsigned)row < (unsigned)nrows ? row : -1; }
+
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }

@@ -1122,7 +1122,7 @@ __global__ void __launch_bounds__(128) splitk_reduce_combine_kernel(
   __shared__ int rws[33];
   __shared__ float wts[33];
   if ((int)threadIdx.x < KS) {
-    rws[threadIdx.x] = row_of[(size_t)t * KS + threadIdx.x];
+    rws[threadIdx.x] = placed_row(row_of[(size_t)t * KS + threadIdx.x], (int)rows);
     wts[threadIdx.x] = ((int)threadIdx.x < K) ? w[(size_t)t * K + threadIdx.x] : 1.0f;
   }
   __syncthreads();
