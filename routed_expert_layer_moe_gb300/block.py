@@ -27,8 +27,8 @@ What one pass leaves for its gradients is overwritten by the next one: layer.out
 the layer (of another block on it too), the results of a method of the block by its next call.  Where another
 pass comes between a forward and its gradients (micro-batches, two blocks on one layer), keep copies and hand
 them in: ids to balance(), counts and tokens to balance_backward(), out to leave_backward(), as it is or in 8 bits as
-keep_out() leaves it.  What layer.backward() reads stays with the layer: micro-batches in flight take a layer each, on the
-same weights (layer.py).  Calls that use each
+keep_out() leaves it.  What layer.backward() reads stays with the layer, and layer.backward() refuses once another pass
+has overwritten it: micro-batches in flight take a layer each, on the same weights (layer.py).  Calls that use each
 other's results are ordered by the caller if they run on different streams, and so are two calls of one method."""
 from __future__ import annotations
 
