@@ -482,8 +482,11 @@ moe_status moe_block_norm_backward(int32_t dtype, int32_t T, int32_t H, const vo
  * largest magnitude * fp32(1/448) (rounded to fp32; 1 where it is 0), code =
  * E4M3(x / s), the nearest to the exact quotient with ties to the even code,
  * saturating at 448; the sign of a zero is kept.  A group that holds a NaN or an infinity gets a NaN scale and
- * codes 0.  Value = code * s, rounded once; it is within 2^-4 of x, relative,
- * where |x| >= 2^-6 s, and within 2^-10 s below that.  Outputs overlap no input.
+ * codes 0.  Value = code * s, rounded once to the output's type; before that it
+ * is within 2^-4 of x, relative, where |x| >= 2^-6 s, and within 2^-10 s below
+ * that.  A scale below 2^-126 (a group of magnitudes below 448 * 2^-126) has
+ * few bits, and codes may saturate: up to 7 * 2^-144 is added to both, which
+ * only fp32 values of a like size notice.  Outputs overlap no input.
  * ------------------------------------------------------------------------- */
 
 /* x [rows][cols] (dtype F32 or BF16, any alignment of the type's own size) ->
