@@ -463,7 +463,7 @@ moe_status moe_block_norm_backward(int32_t dtype, int32_t T, int32_t H, const vo
 
 static int check_fp8(int32_t dtype, int64_t rows, int64_t cols, const void* values, const void* codes,
                      const void* scales) {
-  // groups of all rows, a warp each, and the values' index
+  // the groups of all rows are counted in 32 bits, the values in 64
   if (!float_dtype(dtype) || rows < 0 || cols < 0 || rows > (1LL << 33) || cols > (1LL << 33) ||
       (cols > 0 && rows > (1LL << 40) / cols) || rows * ((cols + 127) / 128) >= (1LL << 32))
     return MOE_ERR_INVALID;

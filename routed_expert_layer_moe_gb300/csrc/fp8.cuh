@@ -12,9 +12,9 @@ __device__ __forceinline__ float fp8_amax(float a, float b) {
   return __uint_as_float(max(__float_as_uint(a) & 0x7FFFFFFFu, __float_as_uint(b) & 0x7FFFFFFFu));
 }
 
-// Scale of a group whose largest magnitude is amax: amax * fp32(1 / 448), a product where a division would do no better
-// (the codes are of the quotient by whatever the scale came out as); 1 where that is zero, NaN for a group with a NaN or
-// an infinity (its codes are 0).
+// Scale of a group whose largest magnitude is amax: the product amax * fp32(1 / 448), rounded once, by definition.  It is
+// an ulp away from the quotient amax / 448 in about half of all groups; the codes are of x over the scale as it came out, so
+// neither is the nearer one to x.  1 where the product is zero, NaN for a group with a NaN or an infinity (its codes are 0).
 __device__ __forceinline__ float fp8_scale(float amax) {
   if (!(amax < __uint_as_float(0x7F800000u))) return __uint_as_float(0x7FC00000u);
   const float s = __fmul_rn(amax, 1.0f / 448.0f);

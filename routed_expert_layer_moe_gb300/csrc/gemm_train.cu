@@ -33,8 +33,10 @@
 // L2 gives, so operands are never staged twice and results leave without touching shared memory.  Long products run
 // at 2.0 PFLOP/s for some milliseconds (dxg, 9728 rows of 4096 x 9728: 771 us) and at the power limit's clocks after
 // that.  Experts' last chunks of less than 256 rows are whole tiles: 4.5 chunks for 1024 rows on average.  Measured (burst):
-// 8 experts of 4096 x 14336, 4096 tokens of 2 records: UP 1090 us (1.76 PFLOP/s), DH 610 (1.58), DX 1120 (1.72), dW13 1130
-// (1.70), dW2 650 (1.48); 512 experts of 4096 x 1024, 160 rows each: UP 1400 to 1440 us, 6.7 TB/s.
+// 8 experts of 4096 x 14336, 4096 tokens of 2 records: UP 1090 to 1120 us (1.72 to 1.76 PFLOP/s), DH 610 to 650 (1.48 to
+// 1.58), GRAD 2730 (1.76; DX alone, as a caller that wants no weights' gradients has it, 1140), with fp32 gradients 2970, added
+// to what is there 4160; 64 experts of 2048 x 1024, 65536 rows: UP 360, DH 230 to 245, GRAD 845, fp32 920, added 1230; 512
+// experts of 4096 x 1024, 160 rows each: UP 1400 to 1480 us, 6.5 to 6.7 TB/s.
 #include <algorithm>
 #include <type_traits>
 
