@@ -27,7 +27,9 @@ class MoeLayer:
     experts in 8 bits, and backward(dout) gives the gradients of that pass.  What it reads (ids, w, row_of, masked_m,
     offsets, xg, yg, gu, gu_s) is overwritten by the layer's next forward pass, with or without save: where other
     passes come between a forward and its gradient (micro-batches), take a MoeLayer for each, on the same weights.
-    backward() itself overwrites hg and its own buffers (dyg, wg, dgu, dxg, dw).
+    backward() itself overwrites hg and its own buffers (dyg, wg, dgu, dxg, dw).  Those five hold nothing between calls:
+    layers of one problem whose backward() calls follow each other on one stream can have them in common, by assigning one
+    layer's to the others.
 
     saved: whether those buffers hold one pass whose g and u were kept; backward() refuses where they do not.  The
     layer's methods keep it up as they are called.  A replay of a captured graph calls none of them, nor does what a

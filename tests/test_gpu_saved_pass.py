@@ -61,3 +61,22 @@ def test_replayed_passes():
         layer.backward(dout)
     layer.saved = True
     assert all(torch.equal(a, b) for a, b in zip(layer.backward(dout), want))
+
+
+def test_scratch_in_common():
+    """Two layers in flight that have the gradient's scratch in common give what they give with their own."""
+    T, H, E = 90, 256, 6
+    a, r = make_layer(T, H, 128, E, 2, 1)
+    b = moe.MoeLayer(a.p, "bf16", "bf16", "bf16", a.w13, a.w2, train=True)
+    data = [(r(T, H).bfloat16(), r(T, E), r(T, H).bfloat16()) for _ in range(2)]
+    want = []
+    for layer, (x, logits, dout) in zip((a, b), data):
+        layer.forward(x, logits, save=True)
+        want.append(layer.backward(dout))
+    for name in ("dyg", "wg", "dgu", "dxg", "dw"):
+        setattr(b, name, getattr(a, name).fill_(float("nan")))
+    for layer, (x, logits, _) in zip((a, b), data):
+        layer.forward(x, logits, save=True)
+    for layer, (_, _, dout), v in list(zip((a, b), data, want))[::-1]:
+        assert all(torch.equal(p, q) for p, q in zip(layer.backward(dout), v))
+    assert int(a.err) == int(b.err) == 0
